@@ -185,7 +185,7 @@ def prepare(case, seed):
         elif case["cache"] == "fp8":
             c = (randn(pool, bs, Hkv, D) / s["scale"]).clamp(-448, 448).to(torch.float8_e4m3fn)
         else:
-            c = _pack(randn(pool * bs, Hkv, D)).view(pool, bs, Hkv, -1)
+            c = _pack(randn(pool * Hkv, bs, D)).view(pool, Hkv, bs, -1)
         caches.append(c)
     s["k_cache"], s["v_cache"] = caches
 
@@ -273,18 +273,21 @@ def _run_plain(s):
             if c["cache"] == "fp8":
                 codes = (x / s["scale"]).clamp(-448, 448).to(torch.float8_e4m3fn)
                 cache.view(torch.uint8)[phys, slot] = codes.view(torch.uint8)
+            elif c["cache"] == "int4":
+                cache[phys, :, slot] = _pack(x)
             else:
-                cache[phys, slot] = _pack(x) if c["cache"] == "int4" else x.to(dt)
+                cache[phys, slot] = x.to(dt)
         if c["op"] == "append":
             out["k_cache"], out["v_cache"] = s["k_cache"], s["v_cache"]
     if c["op"] != "append":
         for name in ("k", "v"):
-            x = s[name + "_cache"].view(torch.uint8)[phys, slot] if c["cache"] == "fp8" else \
-                s[name + "_cache"][phys, slot]
+            cache = s[name + "_cache"]
             if c["cache"] == "fp8":
-                x = x.view(torch.float8_e4m3fn).float() * s["scale"]
+                x = cache.view(torch.uint8)[phys, slot].view(torch.float8_e4m3fn).float() * s["scale"]
             elif c["cache"] == "int4":
-                x = _unpack(x)
+                x = _unpack(cache[phys, :, slot])
+            else:
+                x = cache[phys, slot]
             out[name] = x.to(dt).view(*lead, c["Hkv"], c["D"])
     return out
 
@@ -346,7 +349,7 @@ def _decode_plain(s):
     phys, slot = s["tables"][:, blk].long().clamp(min=0), (t - blk * c["bs"]).expand(B, -1)
     live = t[None, :] < s["lens"][:, None]                                   # [B, L]
     q = s["q"].float().view(B, R, Hkv, G, D).permute(0, 2, 1, 3, 4).reshape(B, Hkv, R * G, D)
-    k = _unpack(s["k_cache"][phys, slot]).permute(0, 2, 3, 1)                # [B, Hkv, D, L]
+    k = _unpack(s["k_cache"][phys, :, slot]).permute(0, 2, 3, 1)                # [B, Hkv, D, L]
     score = torch.matmul(q, k) * D ** -0.5
     del k
     last = s["lens"][:, None] - R + torch.arange(R, device=DEVICE)[None, :]  # [B, R]
@@ -356,7 +359,7 @@ def _decode_plain(s):
     seen = seen[:, None, :, None, :].expand(B, Hkv, R, G, -1).reshape(B, Hkv, R * G, -1)
     score = torch.where(seen, score, torch.full_like(score, -math.inf))
     p = torch.where(seen, (score - score.amax(-1, keepdim=True)).exp(), torch.zeros_like(score))
-    v = _unpack(s["v_cache"][phys, slot])
+    v = _unpack(s["v_cache"][phys, :, slot])
     v = torch.where(live[:, :, None, None], v, torch.zeros_like(v)).transpose(1, 2)
     den = p.sum(-1, keepdim=True)  # 0 for a row that sees no token: its output is zero
     out = torch.matmul(p, v) / torch.where(den > 0, den, torch.ones_like(den))
@@ -378,7 +381,7 @@ def exact(case, seed):
         pos.append(p)
         place.append(tables[b, p // bs] * bs + p % bs)
     pos, place = torch.cat(pos), torch.cat(place)
-    flat = {n: s[n + "_cache"].view(-1, Hkv, s[n + "_cache"].shape[-1]) for n in ("k", "v")}
+    flat = {n: _by_token(s, n) for n in ("k", "v")}
     out, lead = {}, (s["T"],) if case["ragged"] else (B, case["rows"])
     if case["op"] != "gather":
         x = s["qkv"].double().view(s["T"], Hq + 2 * Hkv, D)
@@ -411,6 +414,13 @@ def exact(case, seed):
                 rows = _exact_values(rows)
             out[name] = rows.double().reshape(*lead, Hkv, D)
     return out
+
+
+def _by_token(s, name):
+    """The cache as [slots, Hkv, row]; the pages of a 4-bit cache hold head after head."""
+    c = s[name + "_cache"]
+    c = c.transpose(1, 2) if s["case"]["cache"] == "int4" else c
+    return c.reshape(-1, *c.shape[2:])
 
 
 def _exact_4bit(x):
@@ -454,7 +464,7 @@ def _exact_decode(s, lens):
     G = c["Hq"] // Hkv
     out = torch.zeros((B, R, Hkv, G, D), dtype=torch.float64, device=DEVICE)
     q = s["q"].double().view(B, R, Hkv, G, D)
-    kf, vf = (s[n].view(-1, Hkv, s[n].shape[-1]) for n in ("k_cache", "v_cache"))
+    kf, vf = _by_token(s, "k"), _by_token(s, "v")
     for b, L in enumerate(lens):
         t = torch.arange(L, device=DEVICE)
         place = s["tables"][b, t // bs].long() * bs + t % bs
