@@ -70,9 +70,27 @@ typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1 } pa_dtype;
 /* Element type of the K/V caches in pa_decode_args.kv_dtype. */
 typedef enum pa_kv_dtype {
   PA_KV_AS_DTYPE = 0, /* the caches have the q/out dtype */
-  PA_KV_FP8_E4M3 = 1  /* FP8 E4M3 ("fn": bias 7, no infinities, max 448), one byte per
+  PA_KV_FP8_E4M3 = 1, /* FP8 E4M3 ("fn": bias 7, no infinities, max 448), one byte per
                          element; cache value = stored value * k_scale (K) or v_scale (V) */
+  PA_KV_INT4 = 2      /* 4-bit codes in groups of 32, see PA_INT4_ROW_BYTES */
 } pa_kv_dtype;
+
+/*
+ * A 4-bit cache. The D elements of a row (one token of one KV head) form D / 32 groups
+ * of 32 consecutive elements. Group g has a step and a minimum in fp16, and element d of
+ * it a code n in 0..15; the cache value is (minimum + step * n) * k_scale (K) or v_scale
+ * (V). A row is PA_INT4_ROW_BYTES(D) bytes, 5 bits per element:
+ *   D/2 bytes  codes, as 32-bit little-endian words of eight: the word of elements
+ *              32 g + 8 t .. 32 g + 8 t + 7 (t = 0..3) is word t * (D/32) + g of the row,
+ *              element 32 g + 8 t + j in its bits 4 j .. 4 j + 3
+ *   D/16 bytes steps of the groups, then D/16 bytes minima
+ * The pages hold head after head: k_cache and v_cache are
+ * [num_blocks, Hkv, block_size, PA_INT4_ROW_BYTES(D)], so that a KV head's tokens of a
+ * block are contiguous. pa_append writes such rows: the minimum rounded down and the step
+ * (a fifteenth of the range above it) rounded up to fp16, and the nearest code. A group
+ * that holds a NaN or an infinity reads back as NaN.
+ */
+#define PA_INT4_ROW_BYTES(D) ((D) / 8 * 5)
 
 /* Bits of the device error word (workspace header). */
 #define PA_DEVERR_BLOCK_INDEX 1u /* a live token's block table entry was outside [0, num_blocks) */
@@ -92,15 +110,20 @@ typedef void* pa_stream_t; /* cudaStream_t */
  *           [max(0, L - window), L) (the sliding layers of "vLLM's custom ROCm
  *           paged-attention kernel wins all sixty cells", section 4, scan 1024).
  *           Table entries before the window are not read.
- *   kv_dtype  PA_KV_AS_DTYPE (default) or PA_KV_FP8_E4M3: the caches hold one byte
+ *   kv_dtype  PA_KV_AS_DTYPE (default), PA_KV_FP8_E4M3 or PA_KV_INT4. FP8 caches hold one byte
  *           per element, [num_blocks, block_size, Hkv, D] as before; q and out keep
  *           `dtype`. fp8 K/V are widened exactly to fp16 for the tensor-core
  *           products (the queries are rounded to fp16, so bf16 query elements must
  *           lie within fp16's range, |x| <= 65504; P is kept in fp16) with fp32
  *           accumulation. The pages list an fp8 cache as untested ("vLLM's custom
  *           ROCm paged-attention kernel wins all sixty cells", section 6).
- *   k_scale, v_scale  per-tensor dequantisation scales (finite, > 0) for an fp8
- *           cache; ignored otherwise.
+ *           4-bit caches (layout above): the codes enter the tensor-core products exactly
+ *           as fp16, the queries rounded to fp16 after scaling by a power of two (any
+ *           range), the weights times the steps rounded to fp16, with fp32 accumulation.
+ *           v_scale should leave the larger steps above about 2^-10 (values / v_scale
+ *           around 1): smaller products with weights lose bits to fp16's 2^-24.
+ *   k_scale, v_scale  per-tensor dequantisation scales (finite, > 0) for an fp8 or
+ *           4-bit cache; ignored otherwise.
  *   q_len   query rows per sequence (0 or 1 = single-query decode). With R > 1 rows,
  *           q and out are [B, R, Hq, D]: row i is the query of token L - R + i (the
  *           new tokens of a speculative-decode step or a chunked-prefill tail) and
@@ -269,6 +292,127 @@ pa_status pa_decode_noalloc(const void* q, const void* k_cache, const void* v_ca
                             int B, int Hq, int Hkv, int D, int block_size, int num_blocks,
                             int max_blocks_per_seq, int max_seq_len, float scale,
                             pa_dtype dtype, pa_stream_t stream);
+
+/*
+ * Rotary positions: how a pair of a head's elements turns with its token's position t.
+ * With n = rot_dim / 2 pairs, pair i of the first rot_dim elements is (x[i], x[i + n])
+ * (PA_ROPE_HALF) or (x[2 i], x[2 i + 1]) (PA_ROPE_INTERLEAVED); elements past rot_dim
+ * stay. It turns by the angle t * f_i and is multiplied by the amplitude a:
+ *   (x, y) -> a (x cos - y sin, y cos + x sin)
+ * f_i is held as a fraction of a full turn in units of 2^-64, turns[i] = f_i / 2 pi * 2^64
+ * (modulo 2^64), so that the angle is exact at far positions.
+ */
+typedef enum pa_rope_layout { PA_ROPE_HALF = 0, PA_ROPE_INTERLEAVED = 1 } pa_rope_layout;
+
+/*
+ * Frequencies for contexts longer than the original_max tokens that a model was trained
+ * on, by a factor (>= 1); plain frequencies are f_i = base^(-i / n):
+ *   PA_ROPE_LINEAR  f_i / factor: positions interpolated
+ *   PA_ROPE_NTK     the base becomes base * factor^(rot_dim / (rot_dim - 2)): the slowest
+ *                   pair interpolated, the fastest kept
+ *   PA_ROPE_YARN    pairs that make more than `fast` turns over original_max kept, those
+ *                   that make fewer than `slow` divided by factor, a linear ramp over the
+ *                   pair index between; amplitude 0.1 ln(factor) + 1
+ *   PA_ROPE_BANDED  the same two bands, the ramp linear in the number of turns;
+ *                   amplitude 1
+ */
+typedef enum pa_rope_kind {
+  PA_ROPE_PLAIN = 0, PA_ROPE_LINEAR = 1, PA_ROPE_NTK = 2, PA_ROPE_YARN = 3, PA_ROPE_BANDED = 4
+} pa_rope_kind;
+typedef struct pa_rope_scaling {
+  int32_t kind; /* pa_rope_kind */
+  int32_t original_max;
+  double factor, slow, fast;
+} pa_rope_scaling;
+
+/*
+ * turns[0 .. rot_dim / 2) and the amplitude for a base (> 1) and a scaling (NULL: plain).
+ * rot_dim: a multiple of 16 up to 256. Host arithmetic in fp64; needs no GPU. Callers with
+ * frequencies of their own fill turns themselves.
+ */
+pa_status pa_rope_turns(int rot_dim, double base, const pa_rope_scaling* scaling, uint64_t* turns,
+                        float* amplitude);
+
+/*
+ * Append the keys and values of new tokens to a paged cache, the keys rotated to their
+ * positions, and rotate the queries of the same tokens: what precedes pa_decode in a step,
+ * with the same block_tables and seq_lens.
+ *   q, q_out  queries in and rotated queries out, or both NULL. q_out is dense
+ *             [rows, Hq, D]; it may be q itself when q is dense too
+ *   k, v      [rows, Hkv, D] keys and values (dtype). Row r of q, k, v starts at element
+ *             r * stride (a multiple of 8, e.g. the width of a fused projection whose
+ *             slices they are); the heads of a row are dense
+ *   starts    NULL: every sequence has `rows` new tokens, row b * rows + i is token i of
+ *             sequence b. Else [B + 1] ascending int32 on the device: rows starts[b] to
+ *             starts[b + 1] - 1 belong to sequence b, `rows` is the number of rows in all;
+ *             rows before starts[0] and from starts[B] on are padding, neither read into
+ *             the cache nor written in q_out
+ *   seq_lens  [B] context lengths WITH the new tokens: token i of n has position
+ *             seq_lens[b] - n + i. A row whose position is negative has no token: nothing
+ *             is written to the cache and its q_out row is zero
+ *   k_cache, v_cache, block_tables, block_size, num_blocks, max_blocks_per_seq, kv_dtype
+ *             as for pa_decode; the table entries of the new positions must be filled
+ *   k_scale, v_scale  for fp8 and 4-bit caches: the cache holds value / scale (E4M3
+ *             saturates at +-448, nearest even; 4 bits: see PA_INT4_ROW_BYTES, whose steps
+ *             and minima lie within +-65504)
+ *   rot_dim   elements of a head that turn: 0 (none) or a multiple of 16 up to D
+ * Rotation and quantisation are in fp32, with one rounding to what is stored. A row with
+ * an invalid length or table entry is not written to the cache and raises a PA_DEVERR_*
+ * bit. Two rows of one call that name the same cache slot leave either's values there, or
+ * a mixture. `workspace`: >= PA_WORKSPACE_HEADER_BYTES, 256-byte aligned; only its error
+ * word is used, so it may be the workspace of the decode calls on the stream. Errors as
+ * for pa_decode; q, q_out, k, v and the caches must be 16-byte aligned.
+ */
+typedef struct pa_append_args {
+  const void* q;
+  void* q_out;
+  const void* k;
+  const void* v;
+  void* k_cache;
+  void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* starts;
+  const uint64_t* rope_turns; /* [rot_dim / 2] on the device */
+  int64_t q_stride, k_stride, v_stride;
+  int32_t B, rows, Hq, Hkv, D;
+  int32_t block_size, num_blocks, max_blocks_per_seq;
+  int32_t dtype;    /* pa_dtype */
+  int32_t kv_dtype; /* pa_kv_dtype */
+  float k_scale, v_scale;
+  int32_t rot_dim;
+  int32_t rope_layout; /* pa_rope_layout */
+  float rope_amplitude;
+} pa_append_args;
+
+pa_status pa_append(const pa_append_args* args, void* workspace, size_t workspace_bytes,
+                    pa_stream_t stream);
+
+/*
+ * Read rows back from a paged cache into dense k_out, v_out [rows, Hkv, D] (dtype): the
+ * reverse of pa_append's writing, with the same meaning of rows, starts and seq_lens (the
+ * last n tokens of each sequence; n = seq_lens[b] is the whole context), for attention of a
+ * prompt over its cached prefix. fp8 and 4-bit values are multiplied by k_scale, v_scale
+ * and rounded once; keys stay rotated. A row without a token, or with an invalid length or
+ * table entry, is zero; padding rows are left alone.
+ */
+typedef struct pa_gather_args {
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* starts;
+  void* k_out;
+  void* v_out;
+  int32_t B, rows, Hkv, D;
+  int32_t block_size, num_blocks, max_blocks_per_seq;
+  int32_t dtype;    /* pa_dtype */
+  int32_t kv_dtype; /* pa_kv_dtype */
+  float k_scale, v_scale;
+} pa_gather_args;
+
+pa_status pa_gather(const pa_gather_args* args, void* workspace, size_t workspace_bytes,
+                    pa_stream_t stream);
 
 /* Static text for a status code. */
 const char* pa_status_string(pa_status status);

@@ -1,4 +1,5 @@
-"""Python binding of libpa.so: single-query paged-attention decode on GB300.
+"""Python binding of libpa.so: single-query paged-attention decode on GB300, and the
+rows of its paged cache (append with rotary positions, gather).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels behind the C ABI declared in include/pa.h. PyTorch provides device
@@ -8,13 +9,19 @@ missing, every call raises.
     import paged_kv_attention_pa_gb300 as pa
     out = pa.decode(q, k_cache, v_cache, block_tables, seq_lens, scale,
                     max_seq_len=4096)
+
+A decode step of a layer, from the projection's output:
+
+    rope = pa.rope(128, base=10000.0, device="cuda")
+    q = pa.append(k, v, k_cache, v_cache, block_tables, seq_lens, q=q, rope=rope)
+    out = pa.decode(q, k_cache, v_cache, block_tables, seq_lens, scale)
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import threading
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -27,7 +34,8 @@ LIB_PATH = os.path.join(_PKG, "libpa.so")
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA, \
     PA_ERR_OUT_OF_RANGE = range(6)
 PA_F16, PA_BF16 = 0, 1
-PA_KV_AS_DTYPE, PA_KV_FP8_E4M3 = 0, 1
+PA_KV_AS_DTYPE, PA_KV_FP8_E4M3, PA_KV_INT4 = 0, 1, 2
+PA_ROPE_HALF, PA_ROPE_INTERLEAVED = 0, 1
 PA_DEVERR_BLOCK_INDEX, PA_DEVERR_SEQ_LEN = 1, 2
 PA_FLAG_DETERMINISTIC = 1
 PA_WORKSPACE_HEADER_BYTES = 8448
@@ -46,6 +54,9 @@ SIGNATURES = {
                           [_c.c_float, _c.c_int, _c.c_void_p]),
     "pa_decode_plan": (_c.c_int, [_c.c_void_p, _c.c_int, _c.c_void_p, _c.c_void_p]),
     "pa_decode_kernel_count": (_c.c_int, [_c.c_void_p, _c.c_void_p]),
+    "pa_append": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "pa_gather": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "pa_rope_turns": (_c.c_int, [_c.c_int, _c.c_double, _c.c_void_p, _c.c_void_p, _c.c_void_p]),
     "pa_workspace_init": (_c.c_int, [_c.c_void_p, _c.c_size_t, _c.c_void_p]),
     "pa_read_device_errors": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p]),
     "pa_set_device": (_c.c_int, [_c.c_int]),
@@ -67,6 +78,39 @@ class DecodeArgs(ctypes.Structure):
         ("k_scale", _c.c_float), ("v_scale", _c.c_float), ("q_len", _c.c_int32),
         ("flags", _c.c_uint32), ("total_tokens", _c.c_int64),
     ]
+
+
+class AppendArgs(ctypes.Structure):
+    """Mirror of pa_append_args (include/pa.h)."""
+    _fields_ = [
+        ("q", _c.c_void_p), ("q_out", _c.c_void_p), ("k", _c.c_void_p), ("v", _c.c_void_p),
+        ("k_cache", _c.c_void_p), ("v_cache", _c.c_void_p), ("block_tables", _c.c_void_p),
+        ("seq_lens", _c.c_void_p), ("starts", _c.c_void_p), ("rope_turns", _c.c_void_p),
+        ("q_stride", _c.c_int64), ("k_stride", _c.c_int64), ("v_stride", _c.c_int64),
+        ("B", _c.c_int32), ("rows", _c.c_int32), ("Hq", _c.c_int32), ("Hkv", _c.c_int32),
+        ("D", _c.c_int32), ("block_size", _c.c_int32), ("num_blocks", _c.c_int32),
+        ("max_blocks_per_seq", _c.c_int32), ("dtype", _c.c_int32), ("kv_dtype", _c.c_int32),
+        ("k_scale", _c.c_float), ("v_scale", _c.c_float), ("rot_dim", _c.c_int32),
+        ("rope_layout", _c.c_int32), ("rope_amplitude", _c.c_float),
+    ]
+
+
+class GatherArgs(ctypes.Structure):
+    """Mirror of pa_gather_args (include/pa.h)."""
+    _fields_ = [
+        ("k_cache", _c.c_void_p), ("v_cache", _c.c_void_p), ("block_tables", _c.c_void_p),
+        ("seq_lens", _c.c_void_p), ("starts", _c.c_void_p), ("k_out", _c.c_void_p),
+        ("v_out", _c.c_void_p), ("B", _c.c_int32), ("rows", _c.c_int32), ("Hkv", _c.c_int32),
+        ("D", _c.c_int32), ("block_size", _c.c_int32), ("num_blocks", _c.c_int32),
+        ("max_blocks_per_seq", _c.c_int32), ("dtype", _c.c_int32), ("kv_dtype", _c.c_int32),
+        ("k_scale", _c.c_float), ("v_scale", _c.c_float),
+    ]
+
+
+class RopeScaling(ctypes.Structure):
+    """Mirror of pa_rope_scaling (include/pa.h)."""
+    _fields_ = [("kind", _c.c_int32), ("original_max", _c.c_int32), ("factor", _c.c_double),
+                ("slow", _c.c_double), ("fast", _c.c_double)]
 
 
 class PAError(RuntimeError):
@@ -123,6 +167,31 @@ def _stream_handle(device: torch.device, stream) -> int:
     return int(s.cuda_stream)
 
 
+def int4_row_bytes(D: int) -> int:
+    """Bytes of one row (token and KV head) of a 4-bit cache: 5 bits per element."""
+    return D // 8 * 5
+
+
+def _cache_shape(k_cache, v_cache, dtype):
+    """(kv_dtype, num_blocks, block_size, Hkv, D) of a pair of caches: [num_blocks,
+    block_size, Hkv, D] in the q dtype or float8_e4m3fn, or 4 bits as uint8
+    [num_blocks, Hkv, block_size, int4_row_bytes(D)]."""
+    if k_cache.dim() != 4 or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("k_cache and v_cache must be four-dimensional and of one shape")
+    if v_cache.dtype != k_cache.dtype or \
+            k_cache.dtype not in (dtype, torch.float8_e4m3fn, torch.uint8):
+        raise TypeError("the caches must both have the 16-bit dtype of the call, or both be "
+                        "float8_e4m3fn, or both uint8 (4-bit rows)")
+    if k_cache.dtype == torch.uint8:
+        nb, hkv, bs, row = k_cache.shape
+        if row % 5 != 0:
+            raise ValueError("a 4-bit cache row has int4_row_bytes(D) bytes (80 or 160)")
+        return PA_KV_INT4, nb, bs, hkv, row // 5 * 8
+    nb, bs, hkv, D = k_cache.shape
+    return (PA_KV_FP8_E4M3 if k_cache.dtype == torch.float8_e4m3fn else PA_KV_AS_DTYPE,
+            nb, bs, hkv, D)
+
+
 def make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale: float,
               max_seq_len: Optional[int] = None, splits: int = 0, window: int = 0,
               k_scale: float = 1.0, v_scale: float = 1.0,
@@ -131,19 +200,17 @@ def make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale: float,
     [B, R, Hq, D] for R causal query rows per sequence."""
     if q.dim() not in (3, 4) or k_cache.dim() != 4 or v_cache.dim() != 4:
         raise ValueError("q must be [B, Hq, D] or [B, R, Hq, D] and the caches "
-                         "[num_blocks, block_size, Hkv, D]")
+                         "[num_blocks, block_size, Hkv, D] (4 bits: [num_blocks, Hkv, "
+                         "block_size, int4_row_bytes(D)])")
     if q.dim() == 4:
         B, R, Hq, D = q.shape
     else:
         (B, Hq, D), R = q.shape, 1
-    nb, bs, Hkv, Dk = k_cache.shape
-    if tuple(v_cache.shape) != tuple(k_cache.shape) or Dk != D:
+    if q.dtype not in _DT or out.dtype != q.dtype:
+        raise TypeError("q and out must be float16 or bfloat16")
+    kv, nb, bs, Hkv, Dk = _cache_shape(k_cache, v_cache, q.dtype)
+    if Dk != D:
         raise ValueError("k_cache / v_cache / q shapes disagree")
-    fp8 = k_cache.dtype == torch.float8_e4m3fn
-    if q.dtype not in _DT or out.dtype != q.dtype or v_cache.dtype != k_cache.dtype or \
-            (k_cache.dtype != q.dtype and not fp8):
-        raise TypeError("q and out must be float16 or bfloat16; the caches must have their "
-                        "dtype or both be float8_e4m3fn")
     if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise TypeError("block_tables and seq_lens must be int32")
     if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(seq_lens.shape) != (B,):
@@ -170,15 +237,30 @@ def make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale: float,
     a.splits = int(splits)
     a.window = int(window)
     a.q_len = R
-    a.kv_dtype = PA_KV_FP8_E4M3 if fp8 else PA_KV_AS_DTYPE
-    a.k_scale, a.v_scale = (float(k_scale), float(v_scale)) if fp8 else (1.0, 1.0)
+    a.kv_dtype = kv
+    a.k_scale, a.v_scale = (1.0, 1.0) if kv == PA_KV_AS_DTYPE else (float(k_scale), float(v_scale))
     a.flags = PA_FLAG_DETERMINISTIC if deterministic else 0
     a.total_tokens = int(total_tokens)
     return a
 
 
-# one workspace per (device, stream); grown on demand, zero-filled when made
+# One workspace per (device, stream); grown on demand, zero-filled when made. Workspaces that
+# were outgrown stay allocated: a captured graph may still write to them when it is replayed.
+# Graphs that may be replayed at the same time need workspaces of their own.
 _workspaces = {}
+_outgrown = []
+
+
+def _workspace(need: int, device: torch.device, stream_handle: int) -> torch.Tensor:
+    key = (device.index, stream_handle)
+    ws = _workspaces.get(key)
+    if ws is None or ws.numel() < need:
+        if ws is not None:
+            _outgrown.append(ws)
+            need = max(need, 2 * ws.numel())
+        ws = torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
+        _workspaces[key] = ws
+    return ws
 
 
 def workspace_for(args: DecodeArgs, device: torch.device, stream_handle: int) -> torch.Tensor:
@@ -186,12 +268,7 @@ def workspace_for(args: DecodeArgs, device: torch.device, stream_handle: int) ->
     need = lib.pa_decode_ex_workspace_bytes(ctypes.byref(args))
     if need == 0:
         raise PAError(PA_ERR_INVALID_ARG, "pa_decode_ex_workspace_bytes")
-    key = (device.index, stream_handle)
-    ws = _workspaces.get(key)
-    if ws is None or ws.numel() < need:
-        ws = torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
-        _workspaces[key] = ws
-    return ws
+    return _workspace(need, device, stream_handle)
 
 
 def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -207,7 +284,8 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     bounds seq_lens (pass it: it sets the split plan; None means the table's
     capacity). splits > 0 forces at most that many context splits. window > 0
     attends to the last `window` tokens only. float8_e4m3fn caches are read as
-    stored value * k_scale / v_scale. deterministic=True keeps fixed context splits, so
+    stored value * k_scale / v_scale, and so are 4-bit caches, uint8 [num_blocks, Hkv,
+    block_size, int4_row_bytes(D)] as append() writes them. deterministic=True keeps fixed context splits, so
     that repeated calls are bitwise identical (by default the splits of a long context
     share out its tail as they finish, and the last bit may vary from call to call).
     total_tokens, the sum of seq_lens when the caller knows it on the host, helps the
@@ -267,12 +345,198 @@ def decode_noalloc(q, k_cache, v_cache, block_tables, seq_lens, scale, out=None,
     return out
 
 
+class Rope(NamedTuple):
+    """Rotary positions: `turns` is int64 [rot_dim / 2] on the device, the angle of each pair
+    per token as a fraction of a turn in units of 2^-64 (see include/pa.h)."""
+    turns: torch.Tensor
+    interleaved: bool = False
+    amplitude: float = 1.0
+
+
+_ROPE_KINDS = {"linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
+
+
+def rope(rot_dim: int, base: float = 10000.0, interleaved: bool = False,
+         scaling: Optional[str] = None, factor: float = 1.0, original_max: int = 0,
+         slow: float = 1.0, fast: float = 32.0, device="cuda") -> Rope:
+    """Rotary positions of the first rot_dim elements of a head, with frequencies
+    base^(-2i / rot_dim), scaled for long contexts by "linear", "ntk", "yarn" or "banded"
+    (include/pa.h, pa_rope_kind). interleaved: pairs (2i, 2i + 1) instead of
+    (i, i + rot_dim / 2). Made once and kept."""
+    lib = load()
+    if scaling is not None and scaling not in _ROPE_KINDS:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_KINDS)}")
+    turns = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.int64)
+    amp = ctypes.c_float(1.0)
+    s = RopeScaling(_ROPE_KINDS.get(scaling, 0), int(original_max), float(factor), float(slow),
+                    float(fast))
+    rc = lib.pa_rope_turns(int(rot_dim), float(base), ctypes.byref(s), turns.data_ptr() or None,
+                           ctypes.byref(amp))
+    if rc != PA_OK:
+        raise PAError(rc, "pa_rope_turns")
+    return Rope(turns.to(device), bool(interleaved), amp.value)
+
+
+def _rows_shape(name, t, B, starts):
+    """(rows argument, row stride in elements) of a [B, H, D], [B, R, H, D] or, with starts,
+    [rows, H, D] tensor whose heads are dense and whose rows are evenly spaced."""
+    H, D = t.shape[-2:]
+    if t.dim() not in ((3,) if starts is not None else (3, 4)) or \
+            (starts is None and t.shape[0] != B):
+        raise ValueError(f"{name} must be [B, H, D] or [B, R, H, D], or [rows, H, D] with starts")
+    if t.numel() and (t.stride(-1) != 1 or (H > 1 and t.stride(-2) != D)):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    if t.dim() == 3:
+        return (t.shape[0] if starts is not None else 1), (t.stride(0) if t.shape[0] > 1 else H * D)
+    R = t.shape[1]
+    if R == 1:
+        return 1, (t.stride(0) if t.shape[0] > 1 else H * D)
+    if t.shape[0] > 1 and t.stride(0) != R * t.stride(1):
+        raise ValueError(f"the rows of {name} must be evenly spaced")
+    return R, t.stride(1)
+
+
+def _check_rows_call(device, block_tables, seq_lens, starts, tensors):
+    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32 or \
+            (starts is not None and starts.dtype != torch.int32):
+        raise TypeError("block_tables, seq_lens and starts must be int32")
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    if B < 0 or block_tables.dim() != 2 or block_tables.shape[0] != B or \
+            (starts is not None and tuple(starts.shape) != (B + 1,)):
+        raise ValueError("block_tables must be [B, max_blocks], seq_lens [B] and starts [B + 1]")
+    dense = [("block_tables", block_tables), ("seq_lens", seq_lens), ("starts", starts)]
+    for name, t, contiguous in [(n, t, True) for n, t in dense] + tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the caches on {device}")
+        if contiguous and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    return B
+
+
+def append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+           block_tables: torch.Tensor, seq_lens: torch.Tensor,
+           q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+           starts: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+           k_scale: float = 1.0, v_scale: float = 1.0,
+           workspace: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Write the keys (rotated) and values of new tokens into a paged cache, and rotate the
+    queries of the same tokens; returns the rotated queries (None without q).
+
+    k, v [B, Hkv, D], or [B, R, Hkv, D] for R new tokens per sequence, or [rows, Hkv, D] packed
+    with starts [B + 1] int32 (rows starts[b] to starts[b + 1] - 1 belong to sequence b; others
+    are padding). q likewise with Hq heads. They may be slices of one projection: the heads of
+    a row contiguous, the rows evenly spaced. seq_lens [B] counts the new tokens: token i of n
+    has position seq_lens[b] - n + i and lies where block_tables puts it. The caches are as in
+    decode(): 16-bit, float8_e4m3fn or 4-bit uint8; the last two hold value / k_scale
+    (v_scale). q_out must be contiguous and may be q itself when that is contiguous.
+    Asynchronous on the current (or given) stream.
+    """
+    lib = load()
+    if k.dtype not in _DT or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise TypeError("q, k and v must be float16 or bfloat16, all the same")
+    kv, nb, bs, Hkv, D = _cache_shape(k_cache, v_cache, k.dtype)
+    if q is None and q_out is not None:
+        raise ValueError("q_out needs q")
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    turns = rope.turns if rope is not None else None
+    B = _check_rows_call(k_cache.device, block_tables, seq_lens, starts, [
+        ("k", k, False), ("v", v, False), ("k_cache", k_cache, True), ("v_cache", v_cache, True),
+        ("q", q, False), ("q_out", q_out, True), ("rope.turns", turns, True)])
+    if k.dim() < 3 or tuple(v.shape) != tuple(k.shape) or tuple(k.shape[-2:]) != (Hkv, D):
+        raise ValueError("k and v must have one shape ending in the caches' [Hkv, D]")
+    if turns is not None and (turns.dtype != torch.int64 or turns.dim() != 1):
+        raise TypeError("rope.turns must be int64 [rot_dim / 2]")
+    a = AppendArgs()
+    a.rows, a.k_stride = _rows_shape("k", k, B, starts)
+    _, a.v_stride = _rows_shape("v", v, B, starts)
+    a.k, a.v, a.k_cache, a.v_cache = (t.data_ptr() for t in (k, v, k_cache, v_cache))
+    a.Hkv, a.D = Hkv, D
+    if q is not None:
+        if q.dim() != k.dim() or tuple(q.shape[:-2]) != tuple(k.shape[:-2]) or q.shape[-1] != D:
+            raise ValueError("q must have k's rows and head_dim")
+        if tuple(q_out.shape) != tuple(q.shape) or q_out.dtype != q.dtype:
+            raise ValueError("q_out must have q's shape and dtype")
+        _, a.q_stride = _rows_shape("q", q, B, starts)
+        a.q, a.q_out, a.Hq = q.data_ptr(), q_out.data_ptr(), q.shape[-2]
+    a.block_tables, a.seq_lens = block_tables.data_ptr(), seq_lens.data_ptr()
+    a.starts = starts.data_ptr() if starts is not None else None
+    a.B, a.block_size, a.num_blocks = B, bs, nb
+    a.max_blocks_per_seq = block_tables.shape[1]
+    a.dtype, a.kv_dtype = _DT[k.dtype], kv
+    a.k_scale, a.v_scale = float(k_scale), float(v_scale)
+    if rope is not None:
+        a.rope_turns, a.rot_dim = turns.data_ptr(), 2 * turns.shape[0]
+        a.rope_layout = PA_ROPE_INTERLEAVED if rope.interleaved else PA_ROPE_HALF
+        a.rope_amplitude = float(rope.amplitude)
+    device = k_cache.device
+    _ensure_device(lib, device.index)
+    sh = _stream_handle(device, stream)
+    ws = workspace if workspace is not None else _workspace(PA_WORKSPACE_HEADER_BYTES, device, sh)
+    rc = lib.pa_append(ctypes.byref(a), ws.data_ptr(), ws.numel(), sh)
+    if rc != PA_OK:
+        raise PAError(rc, "pa_append")
+    return q_out
+
+
+def gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+           seq_lens: torch.Tensor, rows: int, starts: Optional[torch.Tensor] = None,
+           dtype: Optional[torch.dtype] = None, k_out: Optional[torch.Tensor] = None,
+           v_out: Optional[torch.Tensor] = None, k_scale: float = 1.0, v_scale: float = 1.0,
+           workspace: Optional[torch.Tensor] = None,
+           stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Read the last tokens of each sequence back from a paged cache, contiguous and in 16
+    bits: (k, v) [B, rows, Hkv, D], the last `rows` tokens of every sequence, or with starts
+    [B + 1] int32 packed [rows, Hkv, D], of which rows starts[b] to starts[b + 1] - 1 are the
+    last tokens of sequence b and others are left alone (zero in tensors made here). Keys
+    stay rotated. dtype is that of the rows (float16 or bfloat16; needed for fp8 and 4-bit
+    caches, whose values are multiplied by k_scale, v_scale). A row without a token is zero.
+    """
+    lib = load()
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else k_cache.dtype
+    if dtype not in _DT:
+        raise TypeError("dtype must be float16 or bfloat16")
+    kv, nb, bs, Hkv, D = _cache_shape(k_cache, v_cache, dtype)
+    device = k_cache.device
+    if rows < 0:
+        raise ValueError("rows must not be negative")
+    shape = (rows, Hkv, D) if starts is not None else (seq_lens.shape[0], rows, Hkv, D)
+    make = torch.zeros if starts is not None else torch.empty
+    outs = [make(shape, dtype=dtype, device=device) if t is None else t for t in (k_out, v_out)]
+    B = _check_rows_call(device, block_tables, seq_lens, starts, [
+        ("k_cache", k_cache, True), ("v_cache", v_cache, True), ("k_out", outs[0], True),
+        ("v_out", outs[1], True)])
+    for t in outs:
+        if tuple(t.shape) != shape or t.dtype != dtype:
+            raise ValueError(f"k_out and v_out must be {dtype} {list(shape)}")
+    a = GatherArgs()
+    a.k_cache, a.v_cache, a.k_out, a.v_out = (t.data_ptr() for t in (k_cache, v_cache, *outs))
+    a.block_tables, a.seq_lens = block_tables.data_ptr(), seq_lens.data_ptr()
+    a.starts = starts.data_ptr() if starts is not None else None
+    a.B, a.rows, a.Hkv, a.D = B, rows, Hkv, D
+    a.block_size, a.num_blocks, a.max_blocks_per_seq = bs, nb, block_tables.shape[1]
+    a.dtype, a.kv_dtype = _DT[dtype], kv
+    a.k_scale, a.v_scale = float(k_scale), float(v_scale)
+    _ensure_device(lib, device.index)
+    sh = _stream_handle(device, stream)
+    ws = workspace if workspace is not None else _workspace(PA_WORKSPACE_HEADER_BYTES, device, sh)
+    rc = lib.pa_gather(ctypes.byref(a), ws.data_ptr(), ws.numel(), sh)
+    if rc != PA_OK:
+        raise PAError(rc, "pa_gather")
+    return outs[0], outs[1]
+
+
 def plan(B: int, Hq: int, Hkv: int, D: int, block_size: int, max_seq_len: int,
          splits: int = 0, sm_count: int = 0, window: int = 0,
-         kv_fp8: bool = False, total_tokens: int = 0) -> Tuple[int, int]:
+         kv_fp8: bool = False, total_tokens: int = 0, kv_int4: bool = False) -> Tuple[int, int]:
     """(splits, tokens per split) the library would launch with. sm_count <= 0 asks
     the current device; a positive sm_count needs no GPU. kv_fp8: FP8 E4M3 caches
-    (their warp tile is 32 tokens, so splits are multiples of 32)."""
+    (their warp tile is 32 tokens, so splits are multiples of 32). kv_int4: 4-bit caches."""
     lib = load()
     a = DecodeArgs()
     a.B, a.Hq, a.Hkv, a.D = B, Hq, Hkv, D
@@ -282,8 +546,8 @@ def plan(B: int, Hq: int, Hkv: int, D: int, block_size: int, max_seq_len: int,
     a.dtype = PA_BF16
     a.splits = splits
     a.window = window
-    if kv_fp8:
-        a.kv_dtype, a.k_scale, a.v_scale = PA_KV_FP8_E4M3, 1.0, 1.0
+    if kv_fp8 or kv_int4:
+        a.kv_dtype, a.k_scale, a.v_scale = PA_KV_INT4 if kv_int4 else PA_KV_FP8_E4M3, 1.0, 1.0
     a.total_tokens = int(total_tokens)
     S, P = ctypes.c_int(0), ctypes.c_int(0)
     rc = lib.pa_decode_plan(ctypes.byref(a), int(sm_count), ctypes.byref(S), ctypes.byref(P))

@@ -59,9 +59,9 @@ bool plan_for(int64_t S_req, int64_t max_len, int64_t p_max, bool floor_p, int64
   return true;
 }
 
-bool make_plan(int sm_count, int64_t B, int64_t Hkv, int64_t D, int64_t kv_elem_bytes,
-               int64_t max_len, int requested, int64_t quantum, int64_t total_tokens,
-               Plan* out) {
+bool make_plan(int sm_count, int64_t B, int64_t Hkv, int D, pa::KvKind kv, int64_t max_len,
+               int requested, int64_t total_tokens, Plan* out) {
+  const int64_t quantum = pa::tile_tokens(D, kv);
   if (max_len <= 0) {
     *out = {1, (int)quantum};
     return true;
@@ -89,11 +89,11 @@ bool make_plan(int sm_count, int64_t B, int64_t Hkv, int64_t D, int64_t kv_elem_
   // An fp8 CTA is bound by its SM's instruction issue, so its time follows all its
   // tiles: no rounding there (rounded, the fp8 grid and hybrid steps lost 0.5-1%).
   const int64_t round_tokens =
-      quantum * (PA_PLAN_BALANCED && kv_elem_bytes == 2 ? pa::warps_per_cta((int)D, false) : 1);
+      quantum * (PA_PLAN_BALANCED && kv == pa::kKv16 ? pa::warps_per_cta(D, kv) : 1);
   auto consider = [&](const Plan& pl) {
     const int64_t waves = ceil_div(live_ctas(pl), sm);
     // the fixed cost in tokens of this cache: K + V bytes per token per KV head
-    const int64_t overhead_tokens = kSplitOverheadBytes / (2 * D * kv_elem_bytes);
+    const int64_t overhead_tokens = kSplitOverheadBytes / (2 * pa::kv_row_bytes(D, kv));
     const int64_t cost = waves * (round_up(pl.P, round_tokens) + overhead_tokens);
     if (!found || cost < best_cost || (cost == best_cost && pl.S < out->S)) {
       *out = pl;
@@ -137,23 +137,6 @@ WsLayout ws_layout(int64_t B, int64_t Hkv, int64_t G, int64_t D, int64_t S) {
   return w;
 }
 
-int current_sm_count() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    return -1;
-  }
-  static int cache[64] = {0};
-  if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return -1;
-  }
-  if (dev >= 0 && dev < 64) cache[dev] = n;
-  return n;
-}
-
 // Size checks shared by the size query, the plan and the launch.
 pa_status check_sizes(const pa_decode_args* a, int64_t* max_len) {
   if (a->B < 0) return PA_ERR_INVALID_ARG;
@@ -172,10 +155,11 @@ pa_status check_sizes(const pa_decode_args* a, int64_t* max_len) {
     if (cols > (a->D == 128 ? 32 : 16)) return PA_ERR_UNSUPPORTED;    // (rows x group) per CTA
     if ((int64_t)a->Hq * rows > 65535) return PA_ERR_INVALID_ARG;     // merge grid limit
   }
-  if (a->kv_dtype != PA_KV_AS_DTYPE && a->kv_dtype != PA_KV_FP8_E4M3) return PA_ERR_INVALID_ARG;
+  if (a->kv_dtype != PA_KV_AS_DTYPE && a->kv_dtype != PA_KV_FP8_E4M3 && a->kv_dtype != PA_KV_INT4)
+    return PA_ERR_INVALID_ARG;
   if (a->flags & ~PA_FLAG_DETERMINISTIC) return PA_ERR_INVALID_ARG;
   if (a->total_tokens < 0) return PA_ERR_INVALID_ARG;
-  if (a->kv_dtype == PA_KV_FP8_E4M3 &&
+  if (a->kv_dtype != PA_KV_AS_DTYPE &&
       !(a->k_scale > 0.f && a->v_scale > 0.f && a->k_scale < INFINITY && a->v_scale < INFINITY))
     return PA_ERR_INVALID_ARG;
   if (a->B > 65535 || a->Hkv > 65535) return PA_ERR_INVALID_ARG;  // grid limits
@@ -190,12 +174,10 @@ pa_status check_sizes(const pa_decode_args* a, int64_t* max_len) {
   return PA_OK;
 }
 
-// Bytes of one cache element.
-int64_t kv_elem_bytes(const pa_decode_args* a) { return a->kv_dtype == PA_KV_FP8_E4M3 ? 1 : 2; }
-
-// Tokens per warp tile of the kernel that serves these arguments.
-int64_t tile_tokens(const pa_decode_args* a) {
-  return pa::tile_tokens(a->D, a->kv_dtype == PA_KV_FP8_E4M3);
+// What the caches of a checked call hold.
+pa::KvKind kv_kind(const pa_decode_args* a) {
+  return a->kv_dtype == PA_KV_INT4 ? pa::kKvInt4
+                                   : a->kv_dtype == PA_KV_FP8_E4M3 ? pa::kKvFp8 : pa::kKv16;
 }
 
 // The batch's total context tokens for the planner (0: unknown). A window bounds
@@ -210,6 +192,47 @@ int64_t plan_len(const pa_decode_args* a, int64_t max_len) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
+
+namespace pa {
+
+// Multiprocessors of the current device, -1 on a CUDA error.
+int current_sm_count() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  static int cache[64] = {0};
+  if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  if (dev >= 0 && dev < 64) cache[dev] = n;
+  return n;
+}
+
+// Division by the block size as a multiply-high and a shift (division by invariant
+// integers using multiplication, Granlund and Montgomery, 1994): for d not a power
+// of two, with l = ceil(log2 d), s = l - 1 and m = ceil(2^(32+s) / d) < 2^32,
+// floor(n m / 2^(32+s)) = floor(n / d) for every 0 <= n < 2^31, since the error
+// n (m d - 2^(32+s)) / (d 2^(32+s)) < 2^31 d / (d 2^(32+s)) <= 1/d.
+void set_block_division(int d, uint32_t* magic, int* shift) {
+  int l = 0;
+  while ((1ll << l) < d) ++l;  // ceil(log2 d)
+  if ((1ll << l) == d) {       // a power of two: a shift
+    *magic = 0;
+    *shift = l;
+    return;
+  }
+  const int s = l - 1;
+  const unsigned long long num = 1ull << (32 + s);
+  *magic = (uint32_t)((num + (unsigned long long)d - 1) / (unsigned long long)d);
+  *shift = s;
+}
+
+}  // namespace pa
 
 extern "C" {
 
@@ -235,36 +258,17 @@ pa_status pa_set_device(int device) {
   return PA_OK;
 }
 
-// Division by the block size as a multiply-high and a shift (division by invariant
-// integers using multiplication, Granlund and Montgomery, 1994): for d not a power
-// of two, with l = ceil(log2 d), s = l - 1 and m = ceil(2^(32+s) / d) < 2^32,
-// floor(n m / 2^(32+s)) = floor(n / d) for every 0 <= n < 2^31, since the error
-// n (m d - 2^(32+s)) / (d 2^(32+s)) < 2^31 d / (d 2^(32+s)) <= 1/d.
-static void set_block_division(int d, uint32_t* magic, int* shift) {
-  int l = 0;
-  while ((1ll << l) < d) ++l;  // ceil(log2 d)
-  if ((1ll << l) == d) {       // a power of two: a shift
-    *magic = 0;
-    *shift = l;
-    return;
-  }
-  const int s = l - 1;
-  const unsigned long long num = 1ull << (32 + s);
-  *magic = (uint32_t)((num + (unsigned long long)d - 1) / (unsigned long long)d);
-  *shift = s;
-}
-
 pa_status pa_decode_plan(const pa_decode_args* a, int sm_count, int* splits,
                          int* partition_tokens) {
   if (!a || !splits || !partition_tokens) return PA_ERR_INVALID_ARG;
   int64_t max_len = 0;
   const pa_status st = check_sizes(a, &max_len);
   if (st != PA_OK) return st;
-  if (sm_count <= 0) sm_count = current_sm_count();
+  if (sm_count <= 0) sm_count = pa::current_sm_count();
   if (sm_count <= 0) return PA_ERR_CUDA;
   Plan plan{};
-  if (!make_plan(sm_count, a->B, a->Hkv, a->D, kv_elem_bytes(a), plan_len(a, max_len), a->splits,
-                 tile_tokens(a), plan_tokens(a), &plan))
+  if (!make_plan(sm_count, a->B, a->Hkv, a->D, kv_kind(a), plan_len(a, max_len), a->splits,
+                 plan_tokens(a), &plan))
     return PA_ERR_UNSUPPORTED;
   *splits = plan.S;
   *partition_tokens = plan.P;
@@ -338,11 +342,11 @@ static pa_status decode_ex(const pa_decode_args* a, void* workspace, size_t work
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PA_ERR_WORKSPACE;
   }
 
-  const int sm = current_sm_count();
+  const int sm = pa::current_sm_count();
   if (sm <= 0) return PA_ERR_CUDA;
   Plan plan{};
-  if (!make_plan(sm, a->B, a->Hkv, a->D, kv_elem_bytes(a), plan_len(a, max_len), a->splits,
-                 tile_tokens(a), plan_tokens(a), &plan))
+  const pa::KvKind kv = kv_kind(a);
+  if (!make_plan(sm, a->B, a->Hkv, a->D, kv, plan_len(a, max_len), a->splits, plan_tokens(a), &plan))
     return PA_ERR_UNSUPPORTED;
   const int G = a->Hq / a->Hkv;
   const int rows = a->q_len > 0 ? a->q_len : 1;
@@ -366,7 +370,7 @@ static pa_status decode_ex(const pa_decode_args* a, void* workspace, size_t work
   p.Hkv = a->Hkv;
   p.G = G;
   p.block_size = a->block_size;
-  set_block_division(a->block_size, &p.bs_magic, &p.bs_shift);
+  pa::set_block_division(a->block_size, &p.bs_magic, &p.bs_shift);
   p.num_blocks = a->num_blocks;
   p.max_blocks = a->max_blocks_per_seq;
   p.max_seq_len = (int)max_len;
@@ -374,25 +378,30 @@ static pa_status decode_ex(const pa_decode_args* a, void* workspace, size_t work
   p.P = plan.P;
   // static share per split; the rest of each context is claimed tile by tile
   p.Ps = plan.P;
-  const long long split_bytes = (long long)plan.P * 2 * a->D * (a->kv_dtype == PA_KV_FP8_E4M3 ? 1 : 2);
+  const long long split_bytes = (long long)plan.P * 2 * pa::kv_row_bytes(a->D, kv);
   if (plan.S > 1 && !(a->flags & PA_FLAG_DETERMINISTIC) && pa::kStealDiv > 0 &&
       split_bytes >= pa::kStealMinBytes && (int64_t)a->B * a->Hkv <= pa::kStealUnits) {
-    const int tw = (int)tile_tokens(a);  // static shares stay whole tiles
+    const int tw = pa::tile_tokens(a->D, kv);  // static shares stay whole tiles
     const int shared = (plan.P / pa::kStealDiv) / tw * tw;
     p.Ps = plan.P - shared;
   }
   p.steal = reinterpret_cast<int*>(ws + 256);
   p.window = a->window;
   p.q_len = rows;
-  p.kv_fp8 = a->kv_dtype == PA_KV_FP8_E4M3;
-  p.v_scale = p.kv_fp8 ? a->v_scale : 1.f;
-  // scores live in the exp2 domain; an fp8 K's scale multiplies every score
-  p.scale_log2 = (float)((double)a->scale * 1.4426950408889634 * (p.kv_fp8 ? (double)a->k_scale : 1.0));
+  p.kv = kv;
+  p.v_scale = kv == pa::kKv16 ? 1.f : a->v_scale;
+  // scores live in the exp2 domain; the scale of an fp8 or 4-bit K multiplies every score
+  p.scale_log2 = (float)((double)a->scale * 1.4426950408889634 * (kv == pa::kKv16 ? 1.0 : (double)a->k_scale));
 
   cudaStream_t cs = (cudaStream_t)stream;
   cudaError_t e;
   const bool bf16 = a->dtype == PA_BF16;
-  if (p.kv_fp8) {
+  if (kv == pa::kKvInt4) {
+    if (a->D == 128)
+      e = bf16 ? pa::launch_decode_int4_bf16_d128(p, cs, kernels) : pa::launch_decode_int4_f16_d128(p, cs, kernels);
+    else
+      e = bf16 ? pa::launch_decode_int4_bf16_d256(p, cs, kernels) : pa::launch_decode_int4_f16_d256(p, cs, kernels);
+  } else if (kv == pa::kKvFp8) {
     if (a->D == 128)
       e = bf16 ? pa::launch_decode_fp8_bf16_d128(p, cs, kernels) : pa::launch_decode_fp8_f16_d128(p, cs, kernels);
     else

@@ -41,6 +41,7 @@
 
 #include "pa.h"
 #include "pa_device.cuh"
+#include "pa_int4.cuh"
 #include "pa_params.h"
 
 namespace pa {
@@ -50,18 +51,24 @@ constexpr int kSmemBudget = 224 * 1024;
 #define PA_CLUSTER_MERGE_MAX 8  // largest split count merged in its cluster (2..8)
 #endif
 
-// F8: the cache holds FP8 E4M3 (one byte per element); tiles land in the ring as
-// bytes, and each lane widens the bytes of its MMA fragments in registers.
-template <int D, int NT, bool F8 = false>
+// The kind of cache a kernel's element tag stands for.
+template <typename KV>
+constexpr KvKind kv_kind_of =
+    std::is_same_v<KV, int4g32> ? kKvInt4 : std::is_same_v<KV, fp8e4m3> ? kKvFp8 : kKv16;
+
+// KIND: FP8 E4M3 (one byte per element) and 4-bit tiles land in the ring as bytes, and
+// each lane widens the bytes of its MMA fragments in registers.
+template <int D, int NT, KvKind KIND = kKv16>
 struct Cfg {
-  static constexpr int NW = warps_per_cta(D, F8);  // warps per CTA
+  static constexpr int NW = warps_per_cta(D, KIND);  // warps per CTA
   static constexpr int THREADS = NW * 32;
-  static constexpr int TW = tile_tokens(D, F8);  // tokens per tile
+  static constexpr int TW = tile_tokens(D, KIND);  // tokens per tile
   static_assert(TW % 16 == 0 && TW <= 32, "a tile is whole MMA row blocks, one token per lane");
   static constexpr int GT = 8 * NT;             // heads computed (G padded)
-  static constexpr int KVB = F8 ? 1 : 2;        // bytes per cache element
-  static constexpr int ROWB = D * KVB + 16;     // ring row pitch, padded against bank conflicts
-  static constexpr int CPR = D * KVB / 16;      // 16-byte chunks per row
+  static constexpr int GROW = kv_row_bytes(D, KIND);  // bytes of a cache row
+  // ring row pitch, padded against bank conflicts (4-bit rows need no padding, pa_int4.cuh)
+  static constexpr int ROWB = KIND == kKvInt4 ? GROW : GROW + 16;
+  static constexpr int CPR = GROW / 16;         // 16-byte chunks per row
   static constexpr int TILE_BYTES = TW * ROWB;  // K (or V) half of a slot
   static constexpr int SLOT_BYTES = 2 * TILE_BYTES;
   static constexpr int KS = D / 16;             // k-steps of the score MMA = d-blocks of PV
@@ -85,9 +92,9 @@ __device__ __forceinline__ int div_block(const DecodeParams& p, int t) {
 // split of the cluster and output item of this split's share: at most
 // (items + splits) entries, items = 8 NT columns x D / 8.
 constexpr int kRecvFloats = 12;
-template <int D, int NT, bool F8>
+template <int D, int NT, KvKind KIND>
 __host__ __device__ constexpr bool cluster_merge_fits() {
-  using C = Cfg<D, NT, F8>;
+  using C = Cfg<D, NT, KIND>;
   return (8 * NT * (D + 6) + (8 * NT * (D / 8) + kMaxClusterMerge) * kRecvFloats) * 4 <=
          C::DEPTH * C::SLOT_BYTES;
 }
@@ -105,13 +112,14 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// T: q and out type; KV: cache element type (T, or fp8e4m3 with fp16 MMAs).
+// T: q and out type; KV: cache element type (T, or fp8e4m3 or int4g32 with fp16 MMAs).
 template <typename T, typename KV, int D, int NT, bool WIN>
-__global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
     decode_kernel(const DecodeParams p) {
-  constexpr bool F8 = std::is_same_v<KV, fp8e4m3>;
-  using TM = std::conditional_t<F8, __half, T>;  // MMA operand type
-  using C = Cfg<D, NT, F8>;
+  constexpr KvKind KIND = kv_kind_of<KV>;
+  constexpr bool F8 = KIND == kKvFp8, I4 = KIND == kKvInt4;
+  using TM = std::conditional_t<F8 || I4, __half, T>;  // MMA operand type
+  using C = Cfg<D, NT, KIND>;
   constexpr int GT = C::GT;
   constexpr int kWarps = C::NW;
   constexpr int kThreads = C::THREADS;
@@ -199,6 +207,17 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
           qf[nt][2 * j + 1][0] = v.z;
           qf[nt][2 * j + 1][1] = v.w;
         }
+      } else if constexpr (I4) {
+        // eight consecutive elements of each group, reordered by int4_query below
+#pragma unroll
+        for (int g = 0; g < C::KS / 2; ++g) {
+          const uint4 v = ok ? __ldg(reinterpret_cast<const uint4*>(q32 + rowp) + 4 * g + tig)
+                             : make_uint4(0u, 0u, 0u, 0u);
+          qf[nt][2 * g][0] = v.x;
+          qf[nt][2 * g][1] = v.y;
+          qf[nt][2 * g + 1][0] = v.z;
+          qf[nt][2 * g + 1][1] = v.w;
+        }
       } else {
 #pragma unroll
         for (int kk = 0; kk < C::KS; ++kk) {
@@ -265,8 +284,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
           atomicOr(p.err, PA_DEVERR_BLOCK_INDEX);
           phys = 0;
         }
-        ridx = ((uint32_t)phys * (uint32_t)p.block_size + (uint32_t)off) * (uint32_t)p.Hkv +
-               (uint32_t)kvh;
+        // 4-bit pages hold head after head, the others token after token
+        ridx = I4 ? ((uint32_t)phys * (uint32_t)p.Hkv + (uint32_t)kvh) * (uint32_t)p.block_size +
+                        (uint32_t)off
+                  : ((uint32_t)phys * (uint32_t)p.block_size + (uint32_t)off) * (uint32_t)p.Hkv +
+                        (uint32_t)kvh;
       }
       const uint32_t slot = my_ring_s + (k % C::DEPTH) * C::SLOT_BYTES;
 #pragma unroll
@@ -275,7 +297,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
         const int r = flat / C::CPR, c = flat % C::CPR;
         const uint32_t rr = __shfl_sync(0xffffffffu, ridx, r);
         if (r < nv) {
-          const uint8_t* src = kbase + (size_t)rr * (D * C::KVB) + c * 16;
+          const uint8_t* src = kbase + (size_t)rr * C::GROW + c * 16;
           const uint32_t dst = slot + r * C::ROWB + c * 16;
           cp_async16(dst, src, pol);
           cp_async16(dst + C::TILE_BYTES, src + v_minus_k, pol);
@@ -363,11 +385,29 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
       }
   }
 
+  // 4-bit caches: the query fragments in the codes' order, the group sums for the minima,
+  // and the factors that turn the two parts of a column's scores into log2 units
+  uint32_t qs[NT][2];
+  float cs[NT][2], cm[NT][2];
+  if constexpr (I4) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float f = int4_query<T, D>(qf[nt], qs[nt], tig) * p.scale_log2;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        cm[nt][h] = __shfl_sync(0xffffffffu, f, 4 * (2 * tig + h));
+        cs[nt][h] = cm[nt][h] * 16777216.f;
+      }
+    }
+  }
+
   // running state: this thread's heads are nt*8 + 2*tig + {0, 1}
   float m[NT][2], l[NT][2];
   float o[NT][C::KS][4];
+  float om[NT][4];  // 4-bit caches: the weighted minima
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
+    om[nt][0] = om[nt][1] = om[nt][2] = om[nt][3] = 0.f;
     m[nt][0] = m[nt][1] = -INFINITY;
     l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
@@ -377,8 +417,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
   const uint32_t k_lane = (uint32_t)(((lane & 7) + 8 * ((lane >> 3) & 1)) * C::ROWB + (lane >> 4) * 16);
   const uint32_t v_lane = (uint32_t)(((lane & 7) + 8 * (lane >> 4)) * C::ROWB + ((lane >> 3) & 1) * 16);
   const float sl2 = p.scale_log2;
-  constexpr bool kLazy = F8;                 // see the rescaling in the softmax
-  constexpr float kSlack = kLazy ? 8.f : 0.f;  // log2 units
+  constexpr bool kLazy = F8 || I4;           // see the rescaling in the softmax
+  constexpr float kSlack = F8 ? 8.f : 0.f;     // log2 units
+  constexpr float kMargin = I4 ? 4.f : 0.f;
+  const int trow = I4 ? int4_row_of(gid) : gid;  // token of this lane's score rows (+ 8)
 
   for (int k = 0; tq[0] >= 0; ++k) {  // tile k of the stream: tokens tq[0] ..
     const int entry = next_entry;
@@ -393,7 +435,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
     const int nv = min(C::TW, L - t0);
     const uint32_t kt = my_ring_s + (k % C::DEPTH) * C::SLOT_BYTES;
     const uint32_t vt = kt + C::TILE_BYTES;
-    if constexpr (!F8) {
+    if constexpr (!F8 && !I4) {
       if (nv < C::TW) {
         // rows past seq_len were never loaded: zero them in V so that p = 0 meets 0
         uint8_t* vrow = my_ring + (k % C::DEPTH) * C::SLOT_BYTES + C::TILE_BYTES;
@@ -419,6 +461,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
     // fp8: this lane's K bytes d in [4 KS tig, 4 KS tig + 4 KS) of rows 16mt + gid and
     // 16mt + gid + 8 (rows past seq_len hold stale bytes: their scores become -inf)
     uint4 kw[MT][2][F8 ? C::KS / 4 : 1];
+    if constexpr (I4) {  // s and s2: the two parts of the scores
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        int4_scores<D, NT>(s[mt], s2[mt], kt + 16 * mt * C::ROWB, qf, qs, gid, tig);
+    }
     if constexpr (F8) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -429,7 +476,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
         }
     }
 #pragma unroll
-    for (int kk = 0; kk < C::KS; ++kk) {
+    for (int kk = 0; kk < (I4 ? 0 : C::KS); ++kk) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         uint32_t a[4];
@@ -459,6 +506,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
     uint32_t pb[MT][NT][2];
     float x[NT][MT][4];
     float mx[NT][2];
+    auto score = [&](int nt, int mt, int i) -> float {
+      if constexpr (I4) return fmaf(s[mt][nt][i], cs[nt][i & 1], s2[mt][nt][i] * cm[nt][i & 1]);
+      return (s[mt][nt][i] + s2[mt][nt][i]) * sl2;
+    };
     bool grow = false;  // some column of this lane sees a score above its running max (+ slack)
     if (t0 + C::TW <= L - R + 1) {
       // every token of the tile is below every column's limit (the usual case): no mask
@@ -467,17 +518,17 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[nt][mt][i] = (s[mt][nt][i] + s2[mt][nt][i]) * sl2;
+          for (int i = 0; i < 4; ++i) x[nt][mt][i] = score(nt, mt, i);
     } else {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const int tok0 = t0 + 16 * mt + gid, tok1 = tok0 + 8;
-          x[nt][mt][0] = tok0 < lim[nt][0] ? (s[mt][nt][0] + s2[mt][nt][0]) * sl2 : -INFINITY;
-          x[nt][mt][1] = tok0 < lim[nt][1] ? (s[mt][nt][1] + s2[mt][nt][1]) * sl2 : -INFINITY;
-          x[nt][mt][2] = tok1 < lim[nt][0] ? (s[mt][nt][2] + s2[mt][nt][2]) * sl2 : -INFINITY;
-          x[nt][mt][3] = tok1 < lim[nt][1] ? (s[mt][nt][3] + s2[mt][nt][3]) * sl2 : -INFINITY;
+          const int tok0 = t0 + 16 * mt + trow, tok1 = tok0 + 8;
+          x[nt][mt][0] = tok0 < lim[nt][0] ? score(nt, mt, 0) : -INFINITY;
+          x[nt][mt][1] = tok0 < lim[nt][1] ? score(nt, mt, 1) : -INFINITY;
+          x[nt][mt][2] = tok1 < lim[nt][0] ? score(nt, mt, 2) : -INFINITY;
+          x[nt][mt][3] = tok1 < lim[nt][1] ? score(nt, mt, 3) : -INFINITY;
         }
     }
 #pragma unroll
@@ -500,6 +551,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
     // softmax; m is raised only when a score exceeds it by more than kSlack (weights
     // stay <= 2^kSlack, exact in fp32 and rounded like any weight to fp16), so
     // almost every tile skips the rescaling.
+    // 4-bit caches: the same, but their weights are also multiplied by the values' steps
+    // in fp16, so they stay at most 1: m is raised to kMargin above the maximum whenever a
+    // score exceeds it (a typical largest weight is then 2^-4 to 1).
     const bool rescale = (!kLazy && (D != 128 || NT > 1)) || __any_sync(0xffffffffu, grow);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -512,7 +566,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
           mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o2));
           mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o2));
         }
-        const float mn0 = fmaxf(m[nt][0], mx0), mn1 = fmaxf(m[nt][1], mx1);
+        const float mn0 = fmaxf(m[nt][0], mx0 + kMargin), mn1 = fmaxf(m[nt][1], mx1 + kMargin);
         const float q0 = mn0 == -INFINITY ? 0.f : mn0, q1 = mn1 == -INFINITY ? 0.f : mn1;
         al0 = exp2_approx(m[nt][0] - q0);
         al1 = exp2_approx(m[nt][1] - q1);
@@ -525,6 +579,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
           o[nt][dd][2] *= al0;
           o[nt][dd][3] *= al1;
         }
+        om[nt][0] *= al0;
+        om[nt][1] *= al1;
       }
       const float r0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
       const float r1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
@@ -544,7 +600,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
     }
 
     // ---- O^T[d][head] += V_tile^T . P^T, one MMA per d-block and row block
-    if constexpr (F8) {
+    if constexpr (I4) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        int4_pv<D, NT>(o, om, vt + 16 * mt * C::ROWB, pb[mt], nv - 16 * mt, gid, tig);
+    } else if constexpr (F8) {
       // Rows of the V^T fragments are permuted: in d-block dd, row gid holds
       // d = 2 KS gid + 2dd and row gid + 8 holds d + 1, so that a lane needs bytes
       // [2 KS gid, 2 KS gid + 2 KS) of its tokens 16mt + {2tig, 2tig+1, 2tig+8,
@@ -606,6 +666,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
   cp_async_wait<0>();
 
   if (p.S == 1 || p.cmerge) pdl_launch_dependents();
+  if constexpr (I4) int4_finish<D, NT>(o, om, tig);
 
   // ---- denominators: sum over the 8 lanes that share tig (different tokens)
 #pragma unroll
@@ -643,9 +704,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
       float* a0 = aw + c0 * AP;
 #pragma unroll
       for (int dd = 0; dd < C::KS; ++dd) {
-        // rows gid and gid + 8 of d-block dd (permuted for fp8 caches, see the PV step)
-        const int dlo = F8 ? 2 * C::KS * gid + 2 * dd : dd * 16 + gid;
-        const int dhi = F8 ? dlo + 1 : dlo + 8;
+        // rows gid and gid + 8 of d-block dd (permuted for fp8 and 4-bit caches, see the PV step)
+        const int dlo = I4 ? 32 * (dd / 2) + 4 * gid + dd % 2 : F8 ? 2 * C::KS * gid + 2 * dd : dd * 16 + gid;
+        const int dhi = I4 ? dlo + 2 : F8 ? dlo + 1 : dlo + 8;
         a0[dlo] = o[nt][dd][0];
         a0[AP + dlo] = o[nt][dd][1];
         a0[dhi] = o[nt][dd][2];
@@ -666,7 +727,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
   const int ccount = p.cmerge;
   const int cper = ccount ? (cols * DV + ccount - 1) / ccount : 0;
   float* const recv = wstate(kWarps - 1) + WSTATE;  // [C][cper][kRecvFloats]
-  if constexpr (cluster_merge_fits<D, NT, F8>()) {
+  if constexpr (cluster_merge_fits<D, NT, KIND>()) {
     // every split of the cluster is past its main loop: the receive entries (in ring
     // memory) are free
     if (ccount) cluster_sync_relaxed();  // orders execution: nothing is pending on them
@@ -692,7 +753,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
     }
     // cache values are stored values times v_scale (1 unless fp8); a column whose
     // row sees no token of this split has M = -inf and den = 0
-    if constexpr (cluster_merge_fits<D, NT, F8>()) {
+    if constexpr (cluster_merge_fits<D, NT, KIND>()) {
       if (ccount) {  // this split's state of the item, pushed to the item's owner
         const int owner = it / cper;
         float* e = const_cast<float*>(map_cluster_rank(recv, (uint32_t)owner)) +
@@ -722,7 +783,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>::THREA
       }
     }
   }
-  if constexpr (cluster_merge_fits<D, NT, F8>()) {
+  if constexpr (cluster_merge_fits<D, NT, KIND>()) {
     if (ccount) {
       cluster_sync();  // every push has landed; no split reads another's memory after this
       const int rank = (int)cluster_rank();
@@ -897,7 +958,7 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream
 
 template <typename T, typename KV, int D, int NT, bool WIN>
 cudaError_t launch_decode_nt(const DecodeParams& p, cudaStream_t st, int* kernels) {
-  using C = Cfg<D, NT, std::is_same_v<KV, fp8e4m3>>;
+  using C = Cfg<D, NT, kv_kind_of<KV>>;
   auto kern = decode_kernel<T, KV, D, NT, WIN>;
   // The dynamic shared memory opt-in is per device; remember which devices have it.
   static unsigned long long done_mask = 0ull;
@@ -916,7 +977,7 @@ cudaError_t launch_decode_nt(const DecodeParams& p, cudaStream_t st, int* kernel
   // every cluster of the launch is resident at once (clusters of more than two CTAs
   // pack the SMs less densely, so a launch of several waves keeps the merge grid).
   q.cmerge = 0;
-  if (cluster_merge_fits<D, NT, std::is_same_v<KV, fp8e4m3>>() && q.S >= 2 &&
+  if (cluster_merge_fits<D, NT, kv_kind_of<KV>>() && q.S >= 2 &&
       q.S <= PA_CLUSTER_MERGE_MAX && q.S <= kMaxClusterMerge) {
     if (q.S == 2) {
       q.cmerge = 2;

@@ -28,11 +28,24 @@ constexpr int kPartitionMin = 64;   // tokens: below this a split's fixed cost d
 #ifndef PA_TILE_TOKENS_F8_D256
 #define PA_TILE_TOKENS_F8_D256 32
 #endif
+#ifndef PA_TILE_TOKENS_I4_D128
+#define PA_TILE_TOKENS_I4_D128 32
+#endif
+#ifndef PA_TILE_TOKENS_I4_D256
+#define PA_TILE_TOKENS_I4_D256 16
+#endif
+// What the caches hold: elements of the q/out type, FP8 E4M3, or 4-bit groups.
+enum KvKind { kKv16 = 0, kKvFp8 = 1, kKvInt4 = 2 };
+// Bytes of one cache row (one token of one KV head) of K or V.
+__host__ __device__ constexpr int kv_row_bytes(int D, KvKind kind) {
+  return kind == kKv16 ? 2 * D : kind == kKvFp8 ? D : PA_INT4_ROW_BYTES(D);
+}
 // Per head_dim and cache type: a 256-wide 16-bit row pair is already 1 KB a token;
 // fp8 rows carry half the bytes of a 16-bit row for the same arithmetic.
-constexpr int tile_tokens(int D, bool fp8) {
-  return fp8 ? (D == 128 ? PA_TILE_TOKENS_F8_D128 : PA_TILE_TOKENS_F8_D256)
-             : (D == 128 ? PA_TILE_TOKENS_D128 : PA_TILE_TOKENS_D256);
+constexpr int tile_tokens(int D, KvKind kind) {
+  return kind == kKvInt4  ? (D == 128 ? PA_TILE_TOKENS_I4_D128 : PA_TILE_TOKENS_I4_D256)
+         : kind == kKvFp8 ? (D == 128 ? PA_TILE_TOKENS_F8_D128 : PA_TILE_TOKENS_F8_D256)
+                          : (D == 128 ? PA_TILE_TOKENS_D128 : PA_TILE_TOKENS_D256);
 }
 // Warps per decode CTA, per head_dim and cache type: fp8 tiles cost more math per
 // byte, so the fp8 kernel at head_dim 128 runs more warps.
@@ -48,8 +61,16 @@ constexpr int tile_tokens(int D, bool fp8) {
 #ifndef PA_WARPS_F8_D256
 #define PA_WARPS_F8_D256 4
 #endif
-constexpr int warps_per_cta(int D, bool fp8) {
-  return D == 128 ? (fp8 ? PA_WARPS_F8_D128 : PA_WARPS_D128) : (fp8 ? PA_WARPS_F8_D256 : PA_WARPS_D256);
+#ifndef PA_WARPS_I4_D128
+#define PA_WARPS_I4_D128 8
+#endif
+#ifndef PA_WARPS_I4_D256
+#define PA_WARPS_I4_D256 8
+#endif
+constexpr int warps_per_cta(int D, KvKind kind) {
+  return kind == kKvInt4  ? (D == 128 ? PA_WARPS_I4_D128 : PA_WARPS_I4_D256)
+         : kind == kKvFp8 ? (D == 128 ? PA_WARPS_F8_D128 : PA_WARPS_F8_D256)
+                          : (D == 128 ? PA_WARPS_D128 : PA_WARPS_D256);
 }
 // Work sharing among the splits of a sequence: each split keeps about
 // (1 - 1/kStealDiv) of its P tokens as a static share, and the rest of the context
@@ -95,13 +116,17 @@ struct DecodeParams {
   int Ps;             // static tokens per split (== P: no shared tiles)
   int window;         // > 0: attend to the last `window` tokens only
   int q_len;          // query rows per sequence (causal among themselves)
-  int kv_fp8;         // caches hold FP8 E4M3 (k_scale is folded into scale_log2)
+  KvKind kv;          // what the caches hold (fp8, 4-bit: k_scale is folded into scale_log2)
   int cmerge;         // 0, or C = S: the S splits of each (sequence, KV head) run as one
                       // thread-block cluster and merge in distributed shared memory (set
                       // by the launcher; no merge grid)
   float v_scale;      // cache V value = stored value * v_scale
   float scale_log2;   // scale * log2(e): scores live in the exp2 domain
 };
+
+// Host helpers shared by the entry points (pa_api.cu).
+int current_sm_count();
+void set_block_division(int d, uint32_t* magic, int* shift);
 
 // One launcher per (dtype, head_dim); each dispatches on the GQA group size. With
 // kernels != nullptr nothing is launched: *kernels is set to the number of kernels
@@ -115,5 +140,10 @@ cudaError_t launch_decode_fp8_bf16_d128(const DecodeParams& p, cudaStream_t st, 
 cudaError_t launch_decode_fp8_bf16_d256(const DecodeParams& p, cudaStream_t st, int* kernels = nullptr);
 cudaError_t launch_decode_fp8_f16_d128(const DecodeParams& p, cudaStream_t st, int* kernels = nullptr);
 cudaError_t launch_decode_fp8_f16_d256(const DecodeParams& p, cudaStream_t st, int* kernels = nullptr);
+// 4-bit caches with bf16 / fp16 queries and outputs.
+cudaError_t launch_decode_int4_bf16_d128(const DecodeParams& p, cudaStream_t st, int* kernels = nullptr);
+cudaError_t launch_decode_int4_bf16_d256(const DecodeParams& p, cudaStream_t st, int* kernels = nullptr);
+cudaError_t launch_decode_int4_f16_d128(const DecodeParams& p, cudaStream_t st, int* kernels = nullptr);
+cudaError_t launch_decode_int4_f16_d256(const DecodeParams& p, cudaStream_t st, int* kernels = nullptr);
 
 }  // namespace pa

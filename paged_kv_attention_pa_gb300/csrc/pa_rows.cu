@@ -1,0 +1,680 @@
+// Rows of a paged cache: pa_append writes new tokens' keys (rotated) and values into the
+// pages and rotates their queries on the way; pa_gather reads rows back, contiguous.
+//
+// Row r of a call is new token i of sequence b, at position t = L - n + i of its context
+// (L = seq_lens[b] with the new tokens counted, n new tokens), the token that row i of
+// pa_decode's query rows stands for. Packed rows find b by a 32-way search of `starts`.
+//
+// Rotation. Pair j of a head at position t turns by the angle t * f_j. The angle is kept
+// as a 64-bit fraction of a turn, turns[j] = f_j / 2 pi * 2^64, so that t * turns[j] modulo
+// 2^64 is the fraction at any position, with an error of t * 2^-64 turns; fp32 enters only
+// at the sine of the remaining half turn.
+//
+// Both kernels move bytes: a lane handles 16 elements of a row (two 16-byte words of 16-bit
+// elements), D / 16 lanes a row, all loads of a warp's rows in flight together. What bounds
+// them is HBM for prompts and the chain length -> table entry -> store for single tokens.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "pa.h"
+#include "pa_device.cuh"
+#include "pa_int4.cuh"
+#include "pa_params.h"
+
+namespace pa {
+
+struct RowsParams {
+  const void* q;  // append: queries in; q_out rotated
+  void* q_out;
+  const void* k;  // append: new rows in; gather: unused
+  const void* v;
+  void* k_out;  // gather: rows out
+  void* v_out;
+  void* k_cache;
+  void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* starts;   // [B + 1], or null: `rows` rows per sequence
+  const uint64_t* turns;   // [rot / 2]
+  uint32_t* err;
+  long long q_stride, k_stride, v_stride;  // elements between rows
+  int B, rows, T;          // T rows in all
+  int Hq, Hkv;
+  int block_size, num_blocks, max_blocks, cap;
+  uint32_t bs_magic;       // t / block_size as in DecodeParams
+  int bs_shift;
+  int rot, interleaved;    // rotated elements of a head
+  float amplitude;
+  float k_scale, v_scale;  // append: 1 / scale, gather: scale
+};
+
+constexpr int kRowThreads = 128, kRowWarps = kRowThreads / 32;
+
+// Where row r lives. kind 0: no row of any sequence (left alone); 1: a row without a
+// token (a context shorter than its rows, or an invalid length); 2: token `pos` of b.
+struct Place {
+  int kind, b, pos;
+};
+
+// All lanes of the warp together; r is the same in all of them.
+__device__ __forceinline__ Place find_row(const RowsParams& p, int r, bool report) {
+  Place at{0, 0, 0};
+  long long n, i;
+  if (p.starts == nullptr) {
+    at.b = r / p.rows;
+    n = p.rows;
+    i = r - at.b * p.rows;
+  } else {
+    // the last of starts[0 .. B] at or below r: 32 probes a round
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = p.B + 1;
+    for (;;) {
+      const int step = (len + 31) / 32;
+      const int idx = lane * step;
+      const bool le = idx < len && __ldg(p.starts + lo + idx) <= r;
+      const int k = __popc(__ballot_sync(0xffffffffu, le));
+      if (k == 0) return at;  // before the first row
+      lo += (k - 1) * step;
+      len = min(step, len - (k - 1) * step);
+      if (step == 1) break;
+    }
+    if (lo >= p.B) return at;  // behind the last sequence
+    at.b = lo;
+    const int s0 = __ldg(p.starts + lo);
+    n = (long long)__ldg(p.starts + lo + 1) - s0;
+    i = (long long)r - s0;
+    if (i >= n) return at;  // starts that do not ascend
+  }
+  const int L = __ldg(p.seq_lens + at.b);
+  at.kind = 1;
+  if (L < 0 || L > p.cap) {
+    if (report) atomicOr(p.err, PA_DEVERR_SEQ_LEN);
+    return at;
+  }
+  const long long pos = L - n + i;
+  if (pos < 0) return at;
+  at.kind = 2;
+  at.pos = (int)pos;
+  return at;
+}
+
+// Cache row (without the head) of token pos: block and slot; -1 for a bad table entry.
+__device__ __forceinline__ long long find_block(const RowsParams& p, const Place& at, int* slot,
+                                                bool report) {
+  const int blk = p.bs_magic == 0 ? at.pos >> p.bs_shift
+                                  : (int)(__umulhi((uint32_t)at.pos, p.bs_magic) >> p.bs_shift);
+  *slot = at.pos - blk * p.block_size;
+  const int phys = __ldg(p.block_tables + (size_t)at.b * p.max_blocks + blk);
+  if ((unsigned)phys >= (unsigned)p.num_blocks) {
+    if (report) atomicOr(p.err, PA_DEVERR_BLOCK_INDEX);
+    return -1;
+  }
+  return phys;
+}
+
+template <KvKind KIND>
+__device__ __forceinline__ size_t cache_row(const RowsParams& p, long long phys, int slot, int head) {
+  return KIND == kKvInt4 ? ((size_t)phys * p.Hkv + head) * p.block_size + slot
+                         : ((size_t)phys * p.block_size + slot) * p.Hkv + head;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(float* x, const uint4& w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = unpack2<T>(word_of(w, i));
+    x[2 * i] = v.x;
+    x[2 * i + 1] = v.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]),
+                    pack2<T>(x[6], x[7]));
+}
+
+// (a, b) turned by the angle with cosine cs.x and sine cs.y; each product rounded on its own.
+__device__ __forceinline__ void rotate_pair(float& a, float& b, float2 cs) {
+  const float x = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
+  b = __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
+  a = x;
+}
+
+// Four fp32 values to four E4M3 codes: nearest even, saturating at +-448, NaN kept.
+__device__ __forceinline__ uint32_t e4m3x4(const float* x) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1]), "f"(x[0]));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3]), "f"(x[2]));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+// Half a group (16 consecutive elements; the other half in lane ^ 1) to two words of codes
+// and the group's step and minimum. The minimum is rounded down and the step up, so every
+// element lies between the first and the sixteenth value; the quotient is IEEE division,
+// so exact ties (frequent for 16-bit inputs) go to the even code.
+__device__ __forceinline__ void int4_group(const float (&x)[16], uint32_t (&words)[2], uint16_t* step16,
+                                           uint16_t* min16) {
+  float lo = x[0], hi = x[0];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    lo = fminf(lo, x[i]);
+    hi = fmaxf(hi, x[i]);
+    bad = bad || !(fabsf(x[i]) < INFINITY);
+  }
+  lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
+  hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+  bad = __shfl_xor_sync(0xffffffffu, (int)bad, 1) || bad;
+  const __half mn = __float2half_rd(fminf(fmaxf(lo, -65504.f), 65504.f));
+  const float low = __half2float(mn);
+  const __half st = __float2half_ru(fminf(__fdiv_rn(__fsub_rn(hi, low), 15.f), 65504.f));
+  const float step = __half2float(st);
+  words[0] = words[1] = 0u;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float n = step > 0.f ? rintf(__fdiv_rn(__fsub_rn(x[i], low), step)) : 0.f;
+    const uint32_t c = bad ? 0u : (uint32_t)fminf(fmaxf(n, 0.f), 15.f);
+    words[i / 8] |= c << (4 * (i % 8));
+  }
+  *step16 = bad ? (uint16_t)0x7fffu : __half_as_ushort(st);
+  *min16 = bad ? (uint16_t)0x7fffu : __half_as_ushort(mn);
+}
+
+// One row per CTA column blockIdx.x; its warps (and the parts blockIdx.y) share the row's
+// warp tasks: IPW query heads, then IPW key heads, then IPW value heads at a time.
+template <typename T, KvKind KIND, int D>
+__global__ void __launch_bounds__(kRowThreads) append_kernel(const RowsParams p) {
+  constexpr int LPI = D / 16, IPW = 32 / LPI;  // lanes per row item, items per warp
+  constexpr int ROWB = kv_row_bytes(D, KIND);
+  __shared__ float2 turn[D / 2];
+  __shared__ __align__(16) float stage[KIND == kKvInt4 ? kRowWarps : 1][KIND == kKvInt4 ? IPW * D : 4];
+  __shared__ __align__(16) uint8_t line[KIND == kKvInt4 ? kRowWarps : 1]
+                                       [KIND == kKvInt4 ? IPW * PA_INT4_ROW_BYTES(D) : 16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int item = lane / LPI, li = lane % LPI;
+  const int r = blockIdx.x;
+  const int ntq = (p.Hq + IPW - 1) / IPW, ntk = (p.Hkv + IPW - 1) / IPW;
+  const int tasks = ntq + 2 * ntk, stride = kRowWarps * gridDim.y;
+  const bool half = !p.interleaved && p.rot > 0;
+  const bool turns_lane = li < p.rot / 16;
+
+  // which = 0 query, 1 key, 2 value; the lane's two 8-element chunks of the head
+  struct Task {
+    int which, head;
+    bool live;
+    int c0, c1;
+  };
+  auto task_of = [&](int t) -> Task {
+    Task k;
+    k.which = t < ntq ? 0 : t < ntq + ntk ? 1 : 2;
+    k.head = (t - (k.which == 0 ? 0 : k.which == 1 ? ntq : ntq + ntk)) * IPW + item;
+    k.live = t < tasks && k.head < (k.which == 0 ? p.Hq : p.Hkv);
+    const bool apart = half && k.which < 2 && turns_lane;  // the pair's other half
+    k.c0 = apart ? li : 2 * li;
+    k.c1 = apart ? li + p.rot / 16 : 2 * li + 1;
+    return k;
+  };
+  auto load = [&](const Task& k, uint4* a, uint4* b) {
+    *a = *b = make_uint4(0u, 0u, 0u, 0u);
+    if (!k.live) return;
+    const T* src = k.which == 0   ? static_cast<const T*>(p.q) + (long long)r * p.q_stride
+                   : k.which == 1 ? static_cast<const T*>(p.k) + (long long)r * p.k_stride
+                                  : static_cast<const T*>(p.v) + (long long)r * p.v_stride;
+    const uint4* row = reinterpret_cast<const uint4*>(src + (size_t)k.head * D);
+    *a = __ldcs(row + k.c0);  // read once (and q may be written in place)
+    *b = __ldcs(row + k.c1);
+  };
+
+  pdl_wait();
+  int t = warp + kRowWarps * blockIdx.y;
+  Task cur = task_of(t);
+  uint4 a, b;
+  load(cur, &a, &b);  // independent of where the row goes
+  pdl_launch_dependents();
+
+  const bool report = threadIdx.x == 0 && blockIdx.y == 0;
+  const Place at = find_row(p, r, report);
+  if (at.kind == 0) return;
+  int slot = 0;
+  long long phys = -1;
+  if (at.kind == 2) phys = find_block(p, at, &slot, report);
+  for (int j = threadIdx.x; j < p.rot / 2; j += kRowThreads) {
+    const uint64_t f = __ldg(p.turns + j) * (uint64_t)(uint32_t)at.pos;
+    float s, c;
+    sincospif((float)(int32_t)(f >> 32) * 4.656612873077393e-10f, &s, &c);  // half turns: * 2^-31
+    turn[j] = make_float2(c * p.amplitude, s * p.amplitude);
+  }
+  __syncthreads();
+
+  while (t < tasks) {
+    const int tn = t + stride;
+    const Task next = task_of(tn);
+    uint4 an, bn;
+    load(next, &an, &bn);
+    float x[16];  // chunk c0, chunk c1
+    unpack8<T>(x, a);
+    unpack8<T>(x + 8, b);
+    const bool turned = cur.which < 2 && turns_lane;  // else 16-bit words pass through as they are
+    if (turned) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 cs = turn[8 * li + e];
+        if (half)
+          rotate_pair(x[e], x[e + 8], cs);
+        else
+          rotate_pair(x[2 * e], x[2 * e + 1], cs);
+      }
+    }
+    if (cur.which == 0) {
+      if (cur.live) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) + ((size_t)r * p.Hq + cur.head) * D);
+        const bool zero = at.kind == 1;
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        dst[cur.c0] = zero ? z : turned ? pack8<T>(x) : a;
+        dst[cur.c1] = zero ? z : turned ? pack8<T>(x + 8) : b;
+      }
+    } else if (phys >= 0) {
+      uint8_t* cache = static_cast<uint8_t*>(cur.which == 1 ? p.k_cache : p.v_cache);
+      const float inv = cur.which == 1 ? p.k_scale : p.v_scale;
+      uint8_t* dst = cache + cache_row<KIND>(p, phys, slot, cur.head) * ROWB;
+      if constexpr (KIND == kKv16) {
+        if (cur.live) {
+          reinterpret_cast<uint4*>(dst)[cur.c0] = turned ? pack8<T>(x) : a;
+          reinterpret_cast<uint4*>(dst)[cur.c1] = turned ? pack8<T>(x + 8) : b;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] *= inv;
+        if constexpr (KIND == kKvFp8) {
+          if (cur.live) {
+            reinterpret_cast<uint2*>(dst)[cur.c0] = make_uint2(e4m3x4(x), e4m3x4(x + 4));
+            reinterpret_cast<uint2*>(dst)[cur.c1] = make_uint2(e4m3x4(x + 8), e4m3x4(x + 12));
+          }
+        } else {
+          using R = Int4Row<D>;
+          if (half && cur.which == 1) {
+            // halves of a pair lie apart: exchange through shared memory, so that a lane
+            // holds elements 16 li .. 16 li + 15
+            float4* st = reinterpret_cast<float4*>(stage[warp] + item * D);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              st[2 * cur.c0 + i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+              st[2 * cur.c1 + i] = make_float4(x[8 + 4 * i], x[9 + 4 * i], x[10 + 4 * i], x[11 + 4 * i]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 v = st[4 * li + i];
+              x[4 * i] = v.x;
+              x[4 * i + 1] = v.y;
+              x[4 * i + 2] = v.z;
+              x[4 * i + 3] = v.w;
+            }
+          }
+          uint32_t words[2];
+          uint16_t step16, min16;
+          int4_group(x, words, &step16, &min16);
+          // the row in shared memory, then whole 16-byte words to the page
+          const int g = li >> 1, o = 2 * (li & 1);
+          uint8_t* l = line[warp] + item * R::BYTES;
+          reinterpret_cast<uint32_t*>(l)[o * R::G + g] = words[0];
+          reinterpret_cast<uint32_t*>(l)[(o + 1) * R::G + g] = words[1];
+          if ((li & 1) == 0) {
+            reinterpret_cast<uint16_t*>(l + R::CODES)[g] = step16;
+            reinterpret_cast<uint16_t*>(l + R::MINS)[g] = min16;
+          }
+          __syncwarp();
+          const uint4* lv = reinterpret_cast<const uint4*>(l);
+          if (cur.live)
+            for (int i = li; i < R::BYTES / 16; i += LPI) reinterpret_cast<uint4*>(dst)[i] = lv[i];
+          __syncwarp();
+        }
+      }
+    }
+    t = tn;
+    cur = next;
+    a = an;
+    b = bn;
+  }
+}
+
+// One warp per (row, IPW KV heads): the lane's 16 elements of K and of V.
+template <typename T, KvKind KIND, int D>
+__global__ void __launch_bounds__(kRowThreads) gather_kernel(const RowsParams p) {
+  constexpr int LPI = D / 16, IPW = 32 / LPI;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int item = lane / LPI, li = lane % LPI;
+  const int nk = (p.Hkv + IPW - 1) / IPW;
+  const unsigned id = blockIdx.x * kRowWarps + warp;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (id >= (unsigned)p.T * (unsigned)nk) return;
+  const int r = (int)(id / (unsigned)nk), hk = (int)(id - (unsigned)r * nk);
+  const int head = hk * IPW + item;
+  const bool report = lane == 0 && hk == 0;
+  const Place at = find_row(p, r, report);
+  if (at.kind == 0) return;
+  int slot = 0;
+  long long phys = -1;
+  if (at.kind == 2) phys = find_block(p, at, &slot, report);
+  if (head >= p.Hkv) return;
+  uint4 y[2][2];  // the lane's 16 elements of K and V
+#pragma unroll
+  for (int s = 0; s < 2; ++s) y[s][0] = y[s][1] = make_uint4(0u, 0u, 0u, 0u);
+  if (phys >= 0) {
+    float x[2][16];
+    const size_t row = cache_row<KIND>(p, phys, slot, head);
+    if constexpr (KIND == kKv16) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(s ? p.v_cache : p.k_cache) + row * D);
+        y[s][0] = __ldg(src + 2 * li);
+        y[s][1] = __ldg(src + 2 * li + 1);
+      }
+    } else if constexpr (KIND == kKvFp8) {
+      uint4 w[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        w[s] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(s ? p.v_cache : p.k_cache) + row * D) + li);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t h = e4m3x2_to_half2((uint16_t)(word_of(w[s], i / 2) >> (16 * (i & 1))));
+          const float2 v = unpack2<__half>(h);
+          x[s][2 * i] = v.x;
+          x[s][2 * i + 1] = v.y;
+        }
+    } else {
+      using R = Int4Row<D>;
+      const int g = li >> 1, o = 2 * (li & 1);
+      uint32_t w[2][2];
+      __half st[2], mn[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint8_t* src = static_cast<const uint8_t*>(s ? p.v_cache : p.k_cache) + row * R::BYTES;
+        const uint32_t* c = reinterpret_cast<const uint32_t*>(src);
+        w[s][0] = __ldg(c + o * R::G + g);
+        w[s][1] = __ldg(c + (o + 1) * R::G + g);
+        st[s] = __ushort_as_half(__ldg(reinterpret_cast<const uint16_t*>(src + R::CODES) + g));
+        mn[s] = __ushort_as_half(__ldg(reinterpret_cast<const uint16_t*>(src + R::MINS) + g));
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const float step = __half2float(st[s]), low = __half2float(mn[s]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          x[s][i] = fmaf((float)((w[s][i / 8] >> (4 * (i % 8))) & 15u), step, low);
+      }
+    }
+    if constexpr (KIND != kKv16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        x[0][i] *= p.k_scale;
+        x[1][i] *= p.v_scale;
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        y[s][0] = pack8<T>(x[s]);
+        y[s][1] = pack8<T>(x[s] + 8);
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(s ? p.v_out : p.k_out) + ((size_t)r * p.Hkv + head) * D);
+    dst[2 * li] = y[s][0];
+    dst[2 * li + 1] = y[s][1];
+  }
+}
+
+namespace {
+
+template <typename Kern>
+cudaError_t launch_rows(Kern kern, dim3 grid, cudaStream_t st, const RowsParams& p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <bool APPEND, typename T, KvKind KIND, int D>
+cudaError_t launch_kind(const RowsParams& p, int sms, cudaStream_t st) {
+  constexpr int IPW = 32 / (D / 16);
+  const int nk = (p.Hkv + IPW - 1) / IPW;
+  if constexpr (APPEND) {
+    // few rows: their heads over more CTAs (a warp per task at most); many: a CTA per row
+    const int tasks = (p.Hq + IPW - 1) / IPW + 2 * nk;
+    const int most = (tasks + kRowWarps - 1) / kRowWarps;
+    const int parts = (int)std::min<long long>(most, std::max<long long>(1, 4ll * sms / p.T));
+    return launch_rows(append_kernel<T, KIND, D>, dim3(p.T, std::min(parts, 65535)), st, p);
+  } else {
+    const unsigned ctas = ((unsigned)p.T * (unsigned)nk + kRowWarps - 1) / kRowWarps;
+    return launch_rows(gather_kernel<T, KIND, D>, dim3(ctas), st, p);
+  }
+}
+
+template <bool APPEND>
+cudaError_t launch(const RowsParams& p, int D, bool bf16, KvKind kind, int sms, cudaStream_t st) {
+#define PA_ROWS_KIND(T, DD)                                                           \
+  (kind == kKv16 ? launch_kind<APPEND, T, kKv16, DD>(p, sms, st)                       \
+   : kind == kKvFp8 ? launch_kind<APPEND, T, kKvFp8, DD>(p, sms, st)                   \
+                    : launch_kind<APPEND, T, kKvInt4, DD>(p, sms, st))
+  if (D == 128) return bf16 ? PA_ROWS_KIND(__nv_bfloat16, 128) : PA_ROWS_KIND(__half, 128);
+  return bf16 ? PA_ROWS_KIND(__nv_bfloat16, 256) : PA_ROWS_KIND(__half, 256);
+#undef PA_ROWS_KIND
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool good_scale(float s) { return s > 0.f && s < INFINITY && 1.f / s < INFINITY; }
+
+// The checks that pa_append and pa_gather share. *T: rows in all.
+pa_status check_rows(int B, int rows, const int32_t* starts, int Hkv, int D, int block_size,
+                     int num_blocks, int max_blocks, int dtype, int kv_dtype, float k_scale,
+                     float v_scale, int64_t* T, int* cap) {
+  if (B < 0 || rows < 0 || Hkv <= 0 || Hkv > 65535 || D <= 0) return PA_ERR_INVALID_ARG;
+  if (D != 128 && D != 256) return PA_ERR_UNSUPPORTED;
+  if (block_size <= 0 || num_blocks <= 0 || max_blocks <= 0) return PA_ERR_INVALID_ARG;
+  if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_INVALID_ARG;
+  if (kv_dtype != PA_KV_AS_DTYPE && kv_dtype != PA_KV_FP8_E4M3 && kv_dtype != PA_KV_INT4)
+    return PA_ERR_INVALID_ARG;
+  if (kv_dtype != PA_KV_AS_DTYPE && !(good_scale(k_scale) && good_scale(v_scale)))
+    return PA_ERR_INVALID_ARG;
+  if ((int64_t)num_blocks * block_size * Hkv > (int64_t)UINT32_MAX) return PA_ERR_UNSUPPORTED;
+  const int64_t c = (int64_t)max_blocks * block_size;
+  if (c > INT_MAX) return PA_ERR_OUT_OF_RANGE;
+  *cap = (int)c;
+  *T = B == 0 ? 0 : starts ? (int64_t)rows : (int64_t)B * rows;
+  if (*T > INT_MAX) return PA_ERR_INVALID_ARG;
+  // gather's grid: one warp per row and 32 / (D / 16) heads
+  const int64_t nk = (Hkv + 512 / D - 1) / (512 / D);
+  if (*T * nk > INT_MAX) return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
+pa_status check_workspace(const void* ws, size_t bytes) {
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || bytes < PA_WORKSPACE_HEADER_BYTES)
+    return PA_ERR_WORKSPACE;
+  return PA_OK;
+}
+
+KvKind kind_of(int kv_dtype) {
+  return kv_dtype == PA_KV_INT4 ? kKvInt4 : kv_dtype == PA_KV_FP8_E4M3 ? kKvFp8 : kKv16;
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" {
+
+pa_status pa_append(const pa_append_args* a, void* workspace, size_t workspace_bytes,
+                    pa_stream_t stream) {
+  using namespace pa;
+  if (!a) return PA_ERR_INVALID_ARG;
+  int64_t T = 0;
+  RowsParams p{};
+  pa_status st = check_rows(a->B, a->rows, a->starts, a->Hkv, a->D, a->block_size, a->num_blocks,
+                            a->max_blocks_per_seq, a->dtype, a->kv_dtype, a->k_scale, a->v_scale,
+                            &T, &p.cap);
+  if (st != PA_OK) return st;
+  if ((a->q == nullptr) != (a->q_out == nullptr)) return PA_ERR_INVALID_ARG;
+  const int Hq = a->q ? a->Hq : 0;
+  if (a->q && (a->Hq <= 0 || a->Hq > 65535)) return PA_ERR_INVALID_ARG;
+  if (a->rot_dim < 0 || a->rot_dim > a->D || a->rot_dim % 16 != 0) return PA_ERR_INVALID_ARG;
+  if (a->rope_layout != PA_ROPE_HALF && a->rope_layout != PA_ROPE_INTERLEAVED) return PA_ERR_INVALID_ARG;
+  if (a->rot_dim > 0 && !(std::fabs(a->rope_amplitude) < INFINITY)) return PA_ERR_INVALID_ARG;
+  for (int64_t s : {a->k_stride, a->v_stride, a->q ? a->q_stride : 0})
+    if (s < 0 || s % 8 != 0) return PA_ERR_INVALID_ARG;
+  if (T == 0) return PA_OK;
+  if (!a->k || !a->v || !a->k_cache || !a->v_cache || !a->block_tables || !a->seq_lens ||
+      (a->rot_dim > 0 && !a->rope_turns))
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(a->q) || !aligned16(a->q_out) || !aligned16(a->k) || !aligned16(a->v) ||
+      !aligned16(a->k_cache) || !aligned16(a->v_cache))
+    return PA_ERR_INVALID_ARG;
+  st = check_workspace(workspace, workspace_bytes);
+  if (st != PA_OK) return st;
+  const int sms = current_sm_count();
+  if (sms <= 0) return PA_ERR_CUDA;
+
+  p.q = a->q;
+  p.q_out = a->q_out;
+  p.k = a->k;
+  p.v = a->v;
+  p.k_cache = a->k_cache;
+  p.v_cache = a->v_cache;
+  p.block_tables = a->block_tables;
+  p.seq_lens = a->seq_lens;
+  p.starts = a->starts;
+  p.turns = a->rope_turns;
+  p.err = static_cast<uint32_t*>(workspace);
+  p.q_stride = a->q_stride;
+  p.k_stride = a->k_stride;
+  p.v_stride = a->v_stride;
+  p.B = a->B;
+  p.rows = a->rows;
+  p.T = (int)T;
+  p.Hq = Hq;
+  p.Hkv = a->Hkv;
+  p.block_size = a->block_size;
+  p.num_blocks = a->num_blocks;
+  p.max_blocks = a->max_blocks_per_seq;
+  set_block_division(a->block_size, &p.bs_magic, &p.bs_shift);
+  p.rot = a->rot_dim;
+  p.interleaved = a->rope_layout == PA_ROPE_INTERLEAVED;
+  p.amplitude = a->rope_amplitude;
+  const bool scaled = a->kv_dtype != PA_KV_AS_DTYPE;
+  p.k_scale = scaled ? 1.f / a->k_scale : 1.f;
+  p.v_scale = scaled ? 1.f / a->v_scale : 1.f;
+  if (launch<true>(p, a->D, a->dtype == PA_BF16, kind_of(a->kv_dtype), sms, (cudaStream_t)stream) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return PA_ERR_CUDA;
+  }
+  return PA_OK;
+}
+
+pa_status pa_gather(const pa_gather_args* a, void* workspace, size_t workspace_bytes,
+                    pa_stream_t stream) {
+  using namespace pa;
+  if (!a) return PA_ERR_INVALID_ARG;
+  int64_t T = 0;
+  RowsParams p{};
+  pa_status st = check_rows(a->B, a->rows, a->starts, a->Hkv, a->D, a->block_size, a->num_blocks,
+                            a->max_blocks_per_seq, a->dtype, a->kv_dtype, a->k_scale, a->v_scale,
+                            &T, &p.cap);
+  if (st != PA_OK) return st;
+  if (T == 0) return PA_OK;
+  if (!a->k_out || !a->v_out || !a->k_cache || !a->v_cache || !a->block_tables || !a->seq_lens)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(a->k_out) || !aligned16(a->v_out) || !aligned16(a->k_cache) || !aligned16(a->v_cache))
+    return PA_ERR_INVALID_ARG;
+  st = check_workspace(workspace, workspace_bytes);
+  if (st != PA_OK) return st;
+  const int sms = current_sm_count();
+  if (sms <= 0) return PA_ERR_CUDA;
+
+  p.k_out = a->k_out;
+  p.v_out = a->v_out;
+  p.k_cache = const_cast<void*>(a->k_cache);
+  p.v_cache = const_cast<void*>(a->v_cache);
+  p.block_tables = a->block_tables;
+  p.seq_lens = a->seq_lens;
+  p.starts = a->starts;
+  p.err = static_cast<uint32_t*>(workspace);
+  p.B = a->B;
+  p.rows = a->rows;
+  p.T = (int)T;
+  p.Hkv = a->Hkv;
+  p.block_size = a->block_size;
+  p.num_blocks = a->num_blocks;
+  p.max_blocks = a->max_blocks_per_seq;
+  set_block_division(a->block_size, &p.bs_magic, &p.bs_shift);
+  const bool scaled = a->kv_dtype != PA_KV_AS_DTYPE;
+  p.k_scale = scaled ? a->k_scale : 1.f;
+  p.v_scale = scaled ? a->v_scale : 1.f;
+  if (launch<false>(p, a->D, a->dtype == PA_BF16, kind_of(a->kv_dtype), sms, (cudaStream_t)stream) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return PA_ERR_CUDA;
+  }
+  return PA_OK;
+}
+
+pa_status pa_rope_turns(int rot_dim, double base, const pa_rope_scaling* s, uint64_t* turns,
+                        float* amplitude) {
+  if (!turns || !amplitude) return PA_ERR_INVALID_ARG;
+  if (rot_dim <= 0 || rot_dim > 256 || rot_dim % 16 != 0) return PA_ERR_INVALID_ARG;
+  if (!(base > 1.0 && base < INFINITY)) return PA_ERR_INVALID_ARG;
+  const int kind = s ? s->kind : PA_ROPE_PLAIN;
+  const double factor = kind == PA_ROPE_PLAIN ? 1.0 : s->factor;
+  if (kind < PA_ROPE_PLAIN || kind > PA_ROPE_BANDED) return PA_ERR_INVALID_ARG;
+  if (!(factor >= 1.0 && factor < INFINITY)) return PA_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586;
+  const int n = rot_dim / 2;
+  double low = 0.0, high = 0.0;
+  *amplitude = 1.f;
+  if (kind == PA_ROPE_NTK) {
+    base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+  } else if (kind == PA_ROPE_YARN) {
+    if (s->original_max <= 0 || !(s->slow > 0.0 && s->fast > s->slow && s->fast < INFINITY))
+      return PA_ERR_INVALID_ARG;
+    // the pair that makes `turns` turns over the original context
+    auto pair_of = [&](double t) { return n * std::log(s->original_max / (t * two_pi)) / std::log(base); };
+    low = std::max(std::floor(pair_of(s->fast)), 0.0);
+    high = std::min(std::ceil(pair_of(s->slow)), (double)(rot_dim - 1));
+    *amplitude = (float)(0.1 * std::log(factor) + 1.0);
+  } else if (kind == PA_ROPE_BANDED) {
+    if (s->original_max <= 0 || !(s->slow > 0.0 && s->fast > s->slow && s->fast < INFINITY))
+      return PA_ERR_INVALID_ARG;
+  }
+  for (int i = 0; i < n; ++i) {
+    const double f = std::pow(base, -(double)i / n);
+    double g = f;
+    if (kind == PA_ROPE_LINEAR) {
+      g = f / factor;
+    } else if (kind == PA_ROPE_YARN) {
+      const double ramp = std::min(std::max((i - low) / std::max(high - low, 1e-3), 0.0), 1.0);
+      g = f / factor * ramp + f * (1.0 - ramp);
+    } else if (kind == PA_ROPE_BANDED) {
+      const double t = s->original_max * f / two_pi;  // turns over the original context
+      const double keep = std::min(std::max((t - s->slow) / (s->fast - s->slow), 0.0), 1.0);
+      g = f / factor * (1.0 - keep) + f * keep;
+    }
+    const double turn = g / two_pi;
+    turns[i] = (uint64_t)std::ldexp(turn - std::floor(turn), 64);
+  }
+  return PA_OK;
+}
+
+}  // extern "C"

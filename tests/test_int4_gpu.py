@@ -1,0 +1,222 @@
+"""Decode attention over 4-bit caches against the float64 oracle (GB300 only)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import rows_harness as rh
+from oracle import decode_ref, decode_ref_rows
+
+pytestmark = pytest.mark.gpu
+
+
+def tolerance(out_dtype, K, V, step_max, ref, L):
+    """Absolute bound of an output element's error. Scores: the query's fp16 form is exact for
+    bf16 and for normal fp16 elements, the products with codes are exact, sums are fp32. A
+    weight p <= 1 (with the largest >= 2^-4) is rounded to fp16 (2^-11 of it, or 2^-25), and
+    so is its product with the token's step; the output once to its type.
+      sum p (2^-11 |v| + 2^-11 step n) / sum p <= 2^-11 (Vmax + 15 step_max)
+      L 2^-25 (Vmax + 15 step_max) / 2^-4 for weights below fp16's normal range
+      2^-16 Vmax for scores off by up to 2^-17 (fp32 sums of up to 256 products of size < 16)"""
+    vmax = max(float(np.abs(v).max()) if v.size else 0.0 for v in V)
+    spread = vmax + 15 * step_max
+    return (rh.HALF_STEP[out_dtype] * np.abs(ref) + 2.0 ** -11 * spread +
+            min(2.0 ** -11, L * 2.0 ** -21) * spread + 2.0 ** -16 * vmax)
+
+
+def run_case(pa, lens, Hq, Hkv, D, bs, dtype="bf16", rows=1, seed=0, scale=None, step=0.3, spread=1.0,
+             qmul=1.0, k_scale=1.0, v_scale=1.0, **kw):
+    kc, vc, bt, K, V = rh.random_int4_pool(lens, bs, Hkv, D, seed, step, spread)
+    g = torch.Generator().manual_seed(seed)
+    B = len(lens)
+    shape = (B, Hq, D) if rows == 1 else (B, rows, Hq, D)
+    q = (torch.randn(shape, generator=g) * qmul).to(rh.DT[dtype])
+    scale = float(np.float32(scale if scale is not None else 1 / math.sqrt(D)))
+    ks, vs = float(np.float32(k_scale)), float(np.float32(v_scale))
+    Ks, Vs = [k * ks for k in K], [v * vs for v in V]
+    ref = decode_ref(rh.f64(q), Ks, Vs, scale, window=kw.get("window", 0)) if rows == 1 else \
+        decode_ref_rows(rh.f64(q), Ks, Vs, scale)
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    out = pa.decode(q.cuda(), kc.cuda(), vc.cuda(), bt.cuda(),
+                    torch.tensor(lens, dtype=torch.int32, device="cuda"), scale,
+                    max_seq_len=max(lens + [1]), k_scale=k_scale, v_scale=v_scale, workspace=ws, **kw)
+    got = rh.f64(out)
+    assert pa.read_device_errors(ws) == 0
+    assert np.all(np.isfinite(got))
+    tol = tolerance(dtype, Ks, Vs, vs * step * math.exp(2.5 * spread), ref, max(lens))
+    err = np.abs(got - ref)
+    assert np.all(err <= tol), (float((err / tol).max()), float(err.max()))
+    return float(err.max() / max(np.abs(ref).max(), 1e-30))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("Hq,Hkv,D,bs,lens", [
+    (8, 8, 128, 16, [512]),
+    (8, 8, 128, 16, [0, 1, 15, 16, 17, 31, 32, 33]),
+    (32, 8, 128, 16, [1000, 37, 4097]),
+    (6, 2, 128, 1, [130]),
+    (24, 4, 256, 784, [500, 785, 3000]),
+    (2, 2, 256, 33, [0, 1, 16, 17, 100]),
+    (16, 1, 128, 48, [700]),              # 16 heads per KV head
+    (16, 1, 256, 16, [700, 5]),
+    (12, 1, 128, 7, [63, 64, 65]),
+])
+def test_decode_int4(cuda_lib, dtype, Hq, Hkv, D, bs, lens):
+    run_case(cuda_lib, lens, Hq, Hkv, D, bs, dtype, seed=1)
+
+
+@pytest.mark.parametrize("S", [1, 2, 3, 5, 8, 9, 40])
+@pytest.mark.parametrize("D,bs", [(128, 16), (256, 100)])
+def test_decode_int4_splits(cuda_lib, S, D, bs):
+    # one split, splits merging in their cluster, and a merge grid; with and without shared tails
+    for det in (False, True):
+        run_case(cuda_lib, [2500, 1, 0, 777], 8, 2, D, bs, seed=2, splits=S, deterministic=det)
+
+
+@pytest.mark.parametrize("rows,Hq,Hkv,D", [(2, 8, 8, 128), (4, 32, 8, 128), (8, 8, 2, 128),
+                                           (2, 16, 2, 256), (3, 5, 1, 256)])
+def test_decode_int4_query_rows(cuda_lib, rows, Hq, Hkv, D):
+    for S in (0, 1, 3):
+        run_case(cuda_lib, [600, rows, 1, 0, 33], Hq, Hkv, D, 16, rows=rows, seed=3, splits=S)
+
+
+@pytest.mark.parametrize("W", [1, 17, 1000])
+def test_decode_int4_window(cuda_lib, W):
+    run_case(cuda_lib, [1500, 999, 16, 1], 8, 4, 128, 16, seed=4, window=W)
+    run_case(cuda_lib, [1500, 999, 16, 1], 6, 2, 256, 784, "f16", seed=4, window=W)
+
+
+@pytest.mark.parametrize("qmul", [1e-6, 1e-3, 30.0, 1e4])
+def test_decode_int4_query_range(cuda_lib, qmul):
+    # queries far from 1 (the scale brings the scores back): the fp16 form follows their range
+    run_case(cuda_lib, [300], 8, 2, 128, 16, "bf16", seed=5, qmul=qmul, scale=0.088 / qmul)
+    if qmul >= 1e-3:   # fp16 queries lose bits of their own below its normal range
+        run_case(cuda_lib, [300], 8, 2, 256, 16, "f16", seed=5, qmul=qmul, scale=0.0625 / qmul)
+
+
+@pytest.mark.parametrize("step", [1e-2, 1.0, 50.0])
+def test_decode_int4_value_range(cuda_lib, step):
+    run_case(cuda_lib, [400, 33], 8, 2, 128, 16, seed=6, step=step, scale=0.02 / step)
+
+
+def test_decode_int4_scales(cuda_lib):
+    run_case(cuda_lib, [400, 33], 8, 2, 128, 16, seed=7, k_scale=0.125, v_scale=300.0)
+    run_case(cuda_lib, [400, 33], 8, 2, 256, 784, seed=7, k_scale=3.0, v_scale=1e-3)
+
+
+def test_decode_int4_sharp_scores(cuda_lib):
+    # scores far apart: the running maximum climbs through many tiles, weights underflow
+    for scale in (1.0, 4.0):
+        run_case(cuda_lib, [3000], 4, 1, 128, 16, "f16", seed=8, scale=scale)
+        run_case(cuda_lib, [3000], 4, 1, 256, 16, "f16", seed=8, scale=scale, splits=1)
+
+
+def test_decode_int4_long_context_offsets(cuda_lib):
+    # a table whose live blocks lie at the far end of a pool past 4 GB per cache
+    Hkv, D, bs, L = 8, 128, 16, 200
+    kc4, vc4, bt, K, V = rh.random_int4_pool([L], bs, Hkv, D, 9)
+    nb = (5 << 30) // (Hkv * bs * 80)
+    pool = [torch.zeros((nb, Hkv, bs, 80), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    used = kc4.shape[0]
+    for p, c in zip(pool, (kc4, vc4)):
+        p[nb - used:] = c.cuda()
+    q = torch.randn((1, 8, D), generator=torch.Generator().manual_seed(9)).bfloat16()
+    out = cuda_lib.decode(q.cuda(), pool[0], pool[1], (bt + (nb - used)).cuda(),
+                          torch.tensor([L], dtype=torch.int32, device="cuda"), 0.088, max_seq_len=L)
+    ref = decode_ref(rh.f64(q), K, V, float(np.float32(0.088)))
+    tol = tolerance("bf16", K, V, 0.3 * math.exp(2.5), ref, L)
+    assert np.all(np.abs(rh.f64(out) - ref) <= tol)
+    # append and gather there too
+    k = torch.randn((1, Hkv, D)).bfloat16().cuda()
+    btc, lens = (bt + (nb - used)).cuda(), torch.tensor([L], dtype=torch.int32, device="cuda")
+    cuda_lib.append(k, k, pool[0], pool[1], btc, lens)
+    ko, vo = cuda_lib.gather(pool[0], pool[1], btc, lens, 1, dtype=torch.bfloat16)
+    assert torch.equal(ko, vo) and (ko[0].float() - k.float()).abs().max() < 0.4
+
+
+def test_decode_int4_unused_slots_do_not_matter(cuda_lib):
+    # NaN steps and minima, then arbitrary finite ones, in every slot without a token
+    for lens in ([33], [1, 47, 1000]):
+        kc, vc, bt, K, V = rh.random_int4_pool(lens, 16, 2, 128, 10)
+        q = torch.randn((len(lens), 8, 128), generator=torch.Generator().manual_seed(1)).half().cuda()
+        sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        outs = []
+        for fill in (None, 0x00, 0x7b, 0xfc):   # NaN as made; zero; large; minus infinity
+            c = [kc.clone(), vc.clone()]
+            if fill is not None:
+                live = torch.zeros(kc.shape[0], 16, dtype=torch.bool)
+                for b, L in enumerate(lens):
+                    p = torch.arange(L)
+                    live[bt[b, p // 16].long(), p % 16] = True
+                for t in c:
+                    y = t.transpose(1, 2)
+                    y[~live] = fill
+            outs.append(cuda_lib.decode(q, c[0].cuda(), c[1].cuda(), bt.cuda(), sl, 0.088,
+                                        max_seq_len=max(lens), deterministic=True).cpu())
+        for o in outs[1:]:
+            assert torch.equal(rh.bits(o), rh.bits(outs[0]))
+
+
+def test_decode_int4_nan_group_stays_in_its_elements(cuda_lib):
+    # a poisoned group of a live V row makes its own 32 output elements NaN, and no others
+    kc, vc, bt, K, V = rh.random_int4_pool([40], 16, 1, 128, 11)
+    vc[bt[0, 1], 0, 3, 64 + 2 * 2:64 + 2 * 2 + 2] = 0xFF     # the step of group 2 of token 19
+    q = torch.randn((1, 4, 128)).half().cuda()
+    out = cuda_lib.decode(q, kc.cuda(), vc.cuda(), bt.cuda(),
+                          torch.tensor([40], dtype=torch.int32, device="cuda"), 0.088, max_seq_len=40)
+    bad = torch.isnan(out[0]).cpu()
+    assert bad[:, 64:96].all() and not bad[:, :64].any() and not bad[:, 96:].any()
+
+
+def test_decode_int4_graph_and_streams(cuda_lib):
+    lens = [700, 33]
+    kc, vc, bt, K, V = rh.random_int4_pool(lens, 16, 2, 128, 12)
+    dev = [t.cuda() for t in (kc, vc, bt)]
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = torch.randn((2, 8, 128), device="cuda").bfloat16()
+    want = cuda_lib.decode(q, *dev, sl, 0.088, max_seq_len=700, deterministic=True).cpu()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):   # each graph with its own workspace and output
+        ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(q)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            cuda_lib.decode(q, *dev, sl, 0.088, out=out, max_seq_len=700, deterministic=True, workspace=ws)
+        graphs.append((g, out, ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, out, _, s in graphs:
+            with torch.cuda.stream(s):
+                out.zero_()
+                g.replay()
+        torch.cuda.synchronize()
+        for _, out, _, _ in graphs:
+            assert torch.equal(rh.bits(out), rh.bits(want))
+
+
+def test_decode_int4_refusals(cuda_lib):
+    c = torch.zeros((4, 2, 16, 80), dtype=torch.uint8, device="cuda")
+    bt = torch.zeros((1, 4), dtype=torch.int32, device="cuda")
+    sl = torch.ones(1, dtype=torch.int32, device="cuda")
+    q = torch.zeros((1, 2, 128), dtype=torch.bfloat16, device="cuda")
+    cuda_lib.decode(q, c, c, bt, sl, 0.1)
+    with pytest.raises(ValueError):
+        cuda_lib.decode(torch.zeros((1, 2, 256), dtype=torch.bfloat16, device="cuda"), c, c, bt, sl, 0.1)
+    with pytest.raises(ValueError):
+        cuda_lib.decode(q, c[..., :79].contiguous(), c[..., :79].contiguous(), bt, sl, 0.1)
+    with pytest.raises(TypeError):
+        cuda_lib.decode(q, c, c.view(torch.int8), bt, sl, 0.1)
+    with pytest.raises(cuda_lib.PAError):
+        cuda_lib.decode(q, c, c, bt, sl, 0.1, k_scale=0.0)
+
+
+def test_outgrown_workspaces_stay_allocated(cuda_lib):
+    # a graph captured with the default workspace keeps writing to it after the workspace of
+    # its stream has been replaced by a larger one
+    s = torch.cuda.Stream()
+    dev = torch.device("cuda", torch.cuda.current_device())
+    a = cuda_lib._workspace(1 << 16, dev, s.cuda_stream)
+    b = cuda_lib._workspace(a.numel() + 1, dev, s.cuda_stream)
+    assert b.numel() >= 2 * a.numel() and any(t is a for t in cuda_lib._outgrown)
