@@ -94,6 +94,7 @@ typedef enum pa_kv_dtype {
 
 /* Bits of the device error word (workspace header). */
 #define PA_DEVERR_BLOCK_INDEX 1u /* a live token's block table entry was outside [0, num_blocks) */
+#define PA_DEVERR_COPY 4u /* a copy into shared memory did not complete in two seconds: no meaningful output */
 #define PA_DEVERR_SEQ_LEN 2u     /* a seq_len < 0, > max_seq_len or > max_blocks_per_seq*block_size */
 
 typedef void* pa_stream_t; /* cudaStream_t */

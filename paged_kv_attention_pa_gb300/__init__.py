@@ -36,7 +36,7 @@ PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA, \
 PA_F16, PA_BF16 = 0, 1
 PA_KV_AS_DTYPE, PA_KV_FP8_E4M3, PA_KV_INT4 = 0, 1, 2
 PA_ROPE_HALF, PA_ROPE_INTERLEAVED = 0, 1
-PA_DEVERR_BLOCK_INDEX, PA_DEVERR_SEQ_LEN = 1, 2
+PA_DEVERR_BLOCK_INDEX, PA_DEVERR_SEQ_LEN, PA_DEVERR_COPY = 1, 2, 4
 PA_FLAG_DETERMINISTIC = 1
 PA_WORKSPACE_HEADER_BYTES = 8448
 PA_NOALLOC_SCRATCH_BYTES = 32 << 20

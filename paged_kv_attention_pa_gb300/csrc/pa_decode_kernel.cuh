@@ -41,7 +41,6 @@
 
 #include "pa.h"
 #include "pa_device.cuh"
-#include "pa_int4.cuh"
 #include "pa_params.h"
 
 namespace pa {
@@ -56,19 +55,18 @@ template <typename KV>
 constexpr KvKind kv_kind_of =
     std::is_same_v<KV, int4g32> ? kKvInt4 : std::is_same_v<KV, fp8e4m3> ? kKvFp8 : kKv16;
 
-// KIND: FP8 E4M3 (one byte per element) and 4-bit tiles land in the ring as bytes, and
-// each lane widens the bytes of its MMA fragments in registers.
+// KIND: what the cache holds (FP8 E4M3 tiles land in the ring as bytes, and each lane
+// widens the bytes of its MMA fragments in registers). 4-bit caches: Int4Cfg.
 template <int D, int NT, KvKind KIND = kKv16>
 struct Cfg {
-  static constexpr int NW = warps_per_cta(D, KIND);  // warps per CTA
+  static constexpr int NW = warps_per_cta(D, KIND, NT);  // warps per CTA
   static constexpr int THREADS = NW * 32;
   static constexpr int TW = tile_tokens(D, KIND);  // tokens per tile
   static_assert(TW % 16 == 0 && TW <= 32, "a tile is whole MMA row blocks, one token per lane");
   static constexpr int GT = 8 * NT;             // heads computed (G padded)
-  static constexpr int GROW = kv_row_bytes(D, KIND);  // bytes of a cache row
-  // ring row pitch, padded against bank conflicts (4-bit rows need no padding, pa_int4.cuh)
-  static constexpr int ROWB = KIND == kKvInt4 ? GROW : GROW + 16;
-  static constexpr int CPR = GROW / 16;         // 16-byte chunks per row
+  static constexpr int KVB = KIND == kKvFp8 ? 1 : 2;  // bytes per cache element
+  static constexpr int ROWB = D * KVB + 16;     // ring row pitch, padded against bank conflicts
+  static constexpr int CPR = D * KVB / 16;      // 16-byte chunks per row
   static constexpr int TILE_BYTES = TW * ROWB;  // K (or V) half of a slot
   static constexpr int SLOT_BYTES = 2 * TILE_BYTES;
   static constexpr int KS = D / 16;             // k-steps of the score MMA = d-blocks of PV
@@ -76,7 +74,8 @@ struct Cfg {
   static constexpr int FIXED = 256;
   static constexpr int DEPTH_FIT = (kSmemBudget - FIXED) / (NW * SLOT_BYTES);
   static constexpr int DEPTH = DEPTH_FIT > 12 ? 12 : DEPTH_FIT;  // slots per warp
-  static constexpr int RING = NW * DEPTH * SLOT_BYTES;
+  static constexpr int WARP_RING = DEPTH * SLOT_BYTES;
+  static constexpr int RING = NW * WARP_RING;
   static constexpr int SMEM = RING + FIXED;
   static_assert((TW * CPR) % 32 == 0, "tile shape");
   static_assert(DEPTH >= 2, "need at least two slots per warp");
@@ -92,11 +91,9 @@ __device__ __forceinline__ int div_block(const DecodeParams& p, int t) {
 // split of the cluster and output item of this split's share: at most
 // (items + splits) entries, items = 8 NT columns x D / 8.
 constexpr int kRecvFloats = 12;
-template <int D, int NT, KvKind KIND>
+template <int D, int NT, typename C>
 __host__ __device__ constexpr bool cluster_merge_fits() {
-  using C = Cfg<D, NT, KIND>;
-  return (8 * NT * (D + 6) + (8 * NT * (D / 8) + kMaxClusterMerge) * kRecvFloats) * 4 <=
-         C::DEPTH * C::SLOT_BYTES;
+  return (8 * NT * (D + 6) + (8 * NT * (D / 8) + kMaxClusterMerge) * kRecvFloats) * 4 <= C::WARP_RING;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint64_t pol) {
@@ -112,15 +109,198 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// T: q and out type; KV: cache element type (T, or fp8e4m3 or int4g32 with fp16 MMAs).
+// What follows a CTA's last tile: its warps' states (m, l, o in the fragment layout of the
+// score and PV products) merge, and become the output, a split's partial, or the cluster's
+// output (see the head of this file).
+template <typename T, KvKind KIND, int D, int NT, typename C>
+__device__ __forceinline__ void finish_cta(const DecodeParams& p, uint8_t* ring, int n_splits,
+                                           float (&m)[NT][2], float (&l)[NT][2],
+                                           float (&o)[NT][D / 16][4]) {
+  constexpr int GT = 8 * NT, kWarps = C::NW, kThreads = C::THREADS;
+  const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int G = p.G, R = p.q_len, cols = G * R;
+  T* out = reinterpret_cast<T*>(p.out);
+  auto qrow = [&](int c) -> size_t {  // row of q / out holding column c
+    return ((size_t)b * R + c / G) * p.Hq + (size_t)kvh * G + c % G;
+  };
+
+  // ---- denominators: sum over the 8 lanes that share tig (different tokens)
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int o2 = 4; o2 < 32; o2 <<= 1) l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], o2);
+
+  // ---- merge the warps. Each warp writes its state (m, l, unscaled accumulators)
+  // into its own ring, which only it has used: every one of its copies has landed
+  // and been consumed. After one barrier, the final pass reads all warps' states
+  // and weighs each by 2^(m_w - M) with M the CTA maximum of the column: it sums
+  // 8 consecutive d of one column per item as two 16-byte words per warp and
+  // writes them with one 16-byte store. Accumulator rows are padded by 4 floats,
+  // so that the fragment writes (columns 2 tig + {0, 1}, rows gid) fall in
+  // distinct banks.
+  constexpr int AP = D + 4;
+  constexpr int WSTATE = GT * (AP + 2);  // floats of one warp's state
+  static_assert(WSTATE * 4 <= C::WARP_RING, "a warp's state fits in its ring");
+  auto wstate = [&](int w) { return reinterpret_cast<float*>(ring + w * C::WARP_RING); };
+  {
+    float* mw = wstate(warp);  // [GT] running maxima, [GT] sums, [GT][AP] accumulators
+    float* lw = mw + GT;
+    float* aw = lw + GT;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int c0 = nt * 8 + 2 * tig;
+      if (gid == 0) {
+        mw[c0] = m[nt][0];
+        mw[c0 + 1] = m[nt][1];
+        lw[c0] = l[nt][0];
+        lw[c0 + 1] = l[nt][1];
+      }
+      float* a0 = aw + c0 * AP;
+#pragma unroll
+      for (int dd = 0; dd < D / 16; ++dd) {
+        // rows gid and gid + 8 of d-block dd (permuted for fp8 and 4-bit caches, see their
+        // PV steps)
+        const int dlo = KIND == kKvInt4  ? 32 * (dd / 2) + 4 * gid + dd % 2
+                        : KIND == kKvFp8 ? 2 * (D / 16) * gid + 2 * dd
+                                         : dd * 16 + gid;
+        const int dhi = dlo + (KIND == kKvInt4 ? 2 : KIND == kKvFp8 ? 1 : 8);
+        a0[dlo] = o[nt][dd][0];
+        a0[AP + dlo] = o[nt][dd][1];
+        a0[dhi] = o[nt][dd][2];
+        a0[AP + dhi] = o[nt][dd][3];
+      }
+    }
+  }
+  __syncthreads();
+
+  const bool single = n_splits == 1;
+  const size_t pidx = ((size_t)b * p.Hkv + kvh) * p.S + split;
+  constexpr int DV = D / 8;  // items per column
+  // The cluster merge: the C = p.cmerge splits of this (sequence, KV head) form one
+  // cluster. Split r owns output items [r per, (r + 1) per); every split pushes its
+  // state of each item into the owner's receive entries (distributed shared memory
+  // stores, which need no round trip), and after a cluster barrier every owner
+  // reduces its items from its own shared memory.
+  const int ccount = p.cmerge;
+  const int cper = ccount ? (cols * DV + ccount - 1) / ccount : 0;
+  float* const recv = wstate(kWarps - 1) + WSTATE;  // [C][cper][kRecvFloats]
+  if constexpr (cluster_merge_fits<D, NT, C>()) {
+    // every split of the cluster is past its main loop: the receive entries (in ring
+    // memory) are free
+    if (ccount) cluster_sync_relaxed();  // orders execution: nothing is pending on them
+  }
+  for (int it = threadIdx.x; it < cols * DV; it += kThreads) {
+    const int g = it / DV, d0 = (it % DV) * 8;  // g: column
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wstate(w)[g]);
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float den = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float* st = wstate(w);
+      const float mwg = st[g];
+      // a warp that saw no token of the column (m = -inf) contributes nothing
+      const float f = mwg == -INFINITY ? 0.f : exp2_approx(mwg - M);
+      const float4* src = reinterpret_cast<const float4*>(st + 2 * GT + g * AP + d0);
+      const float4 x = src[0], y = src[1];
+      v[0] += f * x.x; v[1] += f * x.y; v[2] += f * x.z; v[3] += f * x.w;
+      v[4] += f * y.x; v[5] += f * y.y; v[6] += f * y.z; v[7] += f * y.w;
+      den += f * st[GT + g];
+    }
+    // cache values are stored values times v_scale (1 unless fp8); a column whose
+    // row sees no token of this split has M = -inf and den = 0
+    if constexpr (cluster_merge_fits<D, NT, C>()) {
+      if (ccount) {  // this split's state of the item, pushed to the item's owner
+        const int owner = it / cper;
+        float* e = const_cast<float*>(map_cluster_rank(recv, (uint32_t)owner)) +
+                   ((size_t)cluster_rank() * cper + (it - owner * cper)) * kRecvFloats;
+        reinterpret_cast<float4*>(e)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(e)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        reinterpret_cast<float2*>(e)[4] = make_float2(M, den);
+        continue;
+      }
+    }
+    if (single) {
+      const float r = den > 0.f ? p.v_scale / den : 0.f;
+      uint4 pk;
+      pk.x = pack2<T>(v[0] * r, v[1] * r);
+      pk.y = pack2<T>(v[2] * r, v[3] * r);
+      pk.z = pack2<T>(v[4] * r, v[5] * r);
+      pk.w = pack2<T>(v[6] * r, v[7] * r);
+      *reinterpret_cast<uint4*>(out + qrow(g) * D + d0) = pk;
+    } else {
+      const float vs = p.v_scale;
+      float4* dst = reinterpret_cast<float4*>(p.ws_acc + (pidx * cols + g) * D + d0);
+      dst[0] = make_float4(v[0] * vs, v[1] * vs, v[2] * vs, v[3] * vs);
+      dst[1] = make_float4(v[4] * vs, v[5] * vs, v[6] * vs, v[7] * vs);
+      if (d0 == 0) {
+        p.ws_m[pidx * cols + g] = M;
+        p.ws_l[pidx * cols + g] = den;
+      }
+    }
+  }
+  if constexpr (cluster_merge_fits<D, NT, C>()) {
+    if (ccount) {
+      cluster_sync();  // every push has landed; no split reads another's memory after this
+      const int rank = (int)cluster_rank();
+      if (rank == 0 && p.Ps < p.P && threadIdx.x == 0)
+        p.steal[(size_t)b * p.Hkv + kvh] = 0;  // no claims left
+      const int i_lo = rank * cper, i_hi = min(cols * DV, i_lo + cper);
+      for (int it = i_lo + threadIdx.x; it < i_hi; it += kThreads) {
+        const int g = it / DV, d0 = (it % DV) * 8;
+        const float* e0 = recv + (size_t)(it - i_lo) * kRecvFloats;
+        // every entry loaded first, then the reduction
+        float2 ml[kMaxClusterMerge];
+        float4 xc[kMaxClusterMerge], yc[kMaxClusterMerge];
+        float M = -INFINITY;
+#pragma unroll
+        for (int c2 = 0; c2 < kMaxClusterMerge; ++c2) {
+          if (c2 < ccount) {
+            const float* e = e0 + (size_t)c2 * cper * kRecvFloats;
+            xc[c2] = reinterpret_cast<const float4*>(e)[0];
+            yc[c2] = reinterpret_cast<const float4*>(e)[1];
+            ml[c2] = reinterpret_cast<const float2*>(e)[4];
+            M = fmaxf(M, ml[c2].x);
+          }
+        }
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        float den = 0.f;
+#pragma unroll
+        for (int c2 = 0; c2 < kMaxClusterMerge; ++c2) {
+          if (c2 < ccount) {
+            // a split that saw no token of the column (m = -inf) weighs 0
+            const float w = ml[c2].x == -INFINITY ? 0.f : exp2_approx(ml[c2].x - M);
+            const float4 x = xc[c2], y = yc[c2];
+            den += w * ml[c2].y;
+            v[0] += w * x.x; v[1] += w * x.y; v[2] += w * x.z; v[3] += w * x.w;
+            v[4] += w * y.x; v[5] += w * y.y; v[6] += w * y.z; v[7] += w * y.w;
+          }
+        }
+        const float r = den > 0.f ? p.v_scale / den : 0.f;
+        uint4 pk;
+        pk.x = pack2<T>(v[0] * r, v[1] * r);
+        pk.y = pack2<T>(v[2] * r, v[3] * r);
+        pk.z = pack2<T>(v[4] * r, v[5] * r);
+        pk.w = pack2<T>(v[6] * r, v[7] * r);
+        *reinterpret_cast<uint4*>(out + qrow(g) * D + d0) = pk;
+      }
+    }
+  }
+}
+
+// T: q and out type; KV: cache element type (T, or fp8e4m3 with fp16 MMAs).
 template <typename T, typename KV, int D, int NT, bool WIN>
 __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
     decode_kernel(const DecodeParams p) {
   constexpr KvKind KIND = kv_kind_of<KV>;
-  constexpr bool F8 = KIND == kKvFp8, I4 = KIND == kKvInt4;
-  using TM = std::conditional_t<F8 || I4, __half, T>;  // MMA operand type
+  constexpr bool F8 = KIND == kKvFp8;
+  using TM = std::conditional_t<F8, __half, T>;  // MMA operand type
   using C = Cfg<D, NT, KIND>;
-  constexpr int GT = C::GT;
   constexpr int kWarps = C::NW;
   constexpr int kThreads = C::THREADS;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -207,17 +387,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
           qf[nt][2 * j + 1][0] = v.z;
           qf[nt][2 * j + 1][1] = v.w;
         }
-      } else if constexpr (I4) {
-        // eight consecutive elements of each group, reordered by int4_query below
-#pragma unroll
-        for (int g = 0; g < C::KS / 2; ++g) {
-          const uint4 v = ok ? __ldg(reinterpret_cast<const uint4*>(q32 + rowp) + 4 * g + tig)
-                             : make_uint4(0u, 0u, 0u, 0u);
-          qf[nt][2 * g][0] = v.x;
-          qf[nt][2 * g][1] = v.y;
-          qf[nt][2 * g + 1][0] = v.z;
-          qf[nt][2 * g + 1][1] = v.w;
-        }
       } else {
 #pragma unroll
         for (int kk = 0; kk < C::KS; ++kk) {
@@ -284,11 +453,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
           atomicOr(p.err, PA_DEVERR_BLOCK_INDEX);
           phys = 0;
         }
-        // 4-bit pages hold head after head, the others token after token
-        ridx = I4 ? ((uint32_t)phys * (uint32_t)p.Hkv + (uint32_t)kvh) * (uint32_t)p.block_size +
-                        (uint32_t)off
-                  : ((uint32_t)phys * (uint32_t)p.block_size + (uint32_t)off) * (uint32_t)p.Hkv +
-                        (uint32_t)kvh;
+        ridx = ((uint32_t)phys * (uint32_t)p.block_size + (uint32_t)off) * (uint32_t)p.Hkv +
+               (uint32_t)kvh;
       }
       const uint32_t slot = my_ring_s + (k % C::DEPTH) * C::SLOT_BYTES;
 #pragma unroll
@@ -297,7 +463,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
         const int r = flat / C::CPR, c = flat % C::CPR;
         const uint32_t rr = __shfl_sync(0xffffffffu, ridx, r);
         if (r < nv) {
-          const uint8_t* src = kbase + (size_t)rr * C::GROW + c * 16;
+          const uint8_t* src = kbase + (size_t)rr * (D * C::KVB) + c * 16;
           const uint32_t dst = slot + r * C::ROWB + c * 16;
           cp_async16(dst, src, pol);
           cp_async16(dst + C::TILE_BYTES, src + v_minus_k, pol);
@@ -385,29 +551,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
       }
   }
 
-  // 4-bit caches: the query fragments in the codes' order, the group sums for the minima,
-  // and the factors that turn the two parts of a column's scores into log2 units
-  uint32_t qs[NT][2];
-  float cs[NT][2], cm[NT][2];
-  if constexpr (I4) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float f = int4_query<T, D>(qf[nt], qs[nt], tig) * p.scale_log2;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        cm[nt][h] = __shfl_sync(0xffffffffu, f, 4 * (2 * tig + h));
-        cs[nt][h] = cm[nt][h] * 16777216.f;
-      }
-    }
-  }
-
   // running state: this thread's heads are nt*8 + 2*tig + {0, 1}
   float m[NT][2], l[NT][2];
   float o[NT][C::KS][4];
-  float om[NT][4];  // 4-bit caches: the weighted minima
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    om[nt][0] = om[nt][1] = om[nt][2] = om[nt][3] = 0.f;
     m[nt][0] = m[nt][1] = -INFINITY;
     l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
@@ -417,10 +565,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
   const uint32_t k_lane = (uint32_t)(((lane & 7) + 8 * ((lane >> 3) & 1)) * C::ROWB + (lane >> 4) * 16);
   const uint32_t v_lane = (uint32_t)(((lane & 7) + 8 * (lane >> 4)) * C::ROWB + ((lane >> 3) & 1) * 16);
   const float sl2 = p.scale_log2;
-  constexpr bool kLazy = F8 || I4;           // see the rescaling in the softmax
-  constexpr float kSlack = F8 ? 8.f : 0.f;     // log2 units
-  constexpr float kMargin = I4 ? 4.f : 0.f;
-  const int trow = I4 ? int4_row_of(gid) : gid;  // token of this lane's score rows (+ 8)
+  constexpr bool kLazy = F8;                 // see the rescaling in the softmax
+  constexpr float kSlack = kLazy ? 8.f : 0.f;  // log2 units
 
   for (int k = 0; tq[0] >= 0; ++k) {  // tile k of the stream: tokens tq[0] ..
     const int entry = next_entry;
@@ -435,7 +581,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
     const int nv = min(C::TW, L - t0);
     const uint32_t kt = my_ring_s + (k % C::DEPTH) * C::SLOT_BYTES;
     const uint32_t vt = kt + C::TILE_BYTES;
-    if constexpr (!F8 && !I4) {
+    if constexpr (!F8) {
       if (nv < C::TW) {
         // rows past seq_len were never loaded: zero them in V so that p = 0 meets 0
         uint8_t* vrow = my_ring + (k % C::DEPTH) * C::SLOT_BYTES + C::TILE_BYTES;
@@ -461,11 +607,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
     // fp8: this lane's K bytes d in [4 KS tig, 4 KS tig + 4 KS) of rows 16mt + gid and
     // 16mt + gid + 8 (rows past seq_len hold stale bytes: their scores become -inf)
     uint4 kw[MT][2][F8 ? C::KS / 4 : 1];
-    if constexpr (I4) {  // s and s2: the two parts of the scores
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-        int4_scores<D, NT>(s[mt], s2[mt], kt + 16 * mt * C::ROWB, qf, qs, gid, tig);
-    }
     if constexpr (F8) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -476,7 +617,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
         }
     }
 #pragma unroll
-    for (int kk = 0; kk < (I4 ? 0 : C::KS); ++kk) {
+    for (int kk = 0; kk < C::KS; ++kk) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         uint32_t a[4];
@@ -506,10 +647,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
     uint32_t pb[MT][NT][2];
     float x[NT][MT][4];
     float mx[NT][2];
-    auto score = [&](int nt, int mt, int i) -> float {
-      if constexpr (I4) return fmaf(s[mt][nt][i], cs[nt][i & 1], s2[mt][nt][i] * cm[nt][i & 1]);
-      return (s[mt][nt][i] + s2[mt][nt][i]) * sl2;
-    };
     bool grow = false;  // some column of this lane sees a score above its running max (+ slack)
     if (t0 + C::TW <= L - R + 1) {
       // every token of the tile is below every column's limit (the usual case): no mask
@@ -518,17 +655,17 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[nt][mt][i] = score(nt, mt, i);
+          for (int i = 0; i < 4; ++i) x[nt][mt][i] = (s[mt][nt][i] + s2[mt][nt][i]) * sl2;
     } else {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const int tok0 = t0 + 16 * mt + trow, tok1 = tok0 + 8;
-          x[nt][mt][0] = tok0 < lim[nt][0] ? score(nt, mt, 0) : -INFINITY;
-          x[nt][mt][1] = tok0 < lim[nt][1] ? score(nt, mt, 1) : -INFINITY;
-          x[nt][mt][2] = tok1 < lim[nt][0] ? score(nt, mt, 2) : -INFINITY;
-          x[nt][mt][3] = tok1 < lim[nt][1] ? score(nt, mt, 3) : -INFINITY;
+          const int tok0 = t0 + 16 * mt + gid, tok1 = tok0 + 8;
+          x[nt][mt][0] = tok0 < lim[nt][0] ? (s[mt][nt][0] + s2[mt][nt][0]) * sl2 : -INFINITY;
+          x[nt][mt][1] = tok0 < lim[nt][1] ? (s[mt][nt][1] + s2[mt][nt][1]) * sl2 : -INFINITY;
+          x[nt][mt][2] = tok1 < lim[nt][0] ? (s[mt][nt][2] + s2[mt][nt][2]) * sl2 : -INFINITY;
+          x[nt][mt][3] = tok1 < lim[nt][1] ? (s[mt][nt][3] + s2[mt][nt][3]) * sl2 : -INFINITY;
         }
     }
 #pragma unroll
@@ -551,9 +688,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
     // softmax; m is raised only when a score exceeds it by more than kSlack (weights
     // stay <= 2^kSlack, exact in fp32 and rounded like any weight to fp16), so
     // almost every tile skips the rescaling.
-    // 4-bit caches: the same, but their weights are also multiplied by the values' steps
-    // in fp16, so they stay at most 1: m is raised to kMargin above the maximum whenever a
-    // score exceeds it (a typical largest weight is then 2^-4 to 1).
     const bool rescale = (!kLazy && (D != 128 || NT > 1)) || __any_sync(0xffffffffu, grow);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -566,7 +700,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
           mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o2));
           mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o2));
         }
-        const float mn0 = fmaxf(m[nt][0], mx0 + kMargin), mn1 = fmaxf(m[nt][1], mx1 + kMargin);
+        const float mn0 = fmaxf(m[nt][0], mx0), mn1 = fmaxf(m[nt][1], mx1);
         const float q0 = mn0 == -INFINITY ? 0.f : mn0, q1 = mn1 == -INFINITY ? 0.f : mn1;
         al0 = exp2_approx(m[nt][0] - q0);
         al1 = exp2_approx(m[nt][1] - q1);
@@ -579,8 +713,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
           o[nt][dd][2] *= al0;
           o[nt][dd][3] *= al1;
         }
-        om[nt][0] *= al0;
-        om[nt][1] *= al1;
       }
       const float r0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
       const float r1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
@@ -600,11 +732,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
     }
 
     // ---- O^T[d][head] += V_tile^T . P^T, one MMA per d-block and row block
-    if constexpr (I4) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-        int4_pv<D, NT>(o, om, vt + 16 * mt * C::ROWB, pb[mt], nv - 16 * mt, gid, tig);
-    } else if constexpr (F8) {
+    if constexpr (F8) {
       // Rows of the V^T fragments are permuted: in d-block dd, row gid holds
       // d = 2 KS gid + 2dd and row gid + 8 holds d + 1, so that a lane needs bytes
       // [2 KS gid, 2 KS gid + 2 KS) of its tokens 16mt + {2tig, 2tig+1, 2tig+8,
@@ -666,170 +794,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
   cp_async_wait<0>();
 
   if (p.S == 1 || p.cmerge) pdl_launch_dependents();
-  if constexpr (I4) int4_finish<D, NT>(o, om, tig);
 
-  // ---- denominators: sum over the 8 lanes that share tig (different tokens)
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int o2 = 4; o2 < 32; o2 <<= 1) l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], o2);
-
-  // ---- merge the warps. Each warp writes its state (m, l, unscaled accumulators)
-  // into its own ring, which only it has used: every one of its copies has landed
-  // and been consumed. After one barrier, the final pass reads all warps' states
-  // and weighs each by 2^(m_w - M) with M the CTA maximum of the column: it sums
-  // 8 consecutive d of one column per item as two 16-byte words per warp and
-  // writes them with one 16-byte store. Accumulator rows are padded by 4 floats,
-  // so that the fragment writes (columns 2 tig + {0, 1}, rows gid) fall in
-  // distinct banks.
-  constexpr int AP = D + 4;
-  constexpr int WSTATE = GT * (AP + 2);  // floats of one warp's state
-  static_assert(WSTATE * 4 <= C::DEPTH * C::SLOT_BYTES, "a warp's state fits in its ring");
-  auto wstate = [&](int w) { return reinterpret_cast<float*>(ring + w * C::DEPTH * C::SLOT_BYTES); };
-  {
-    float* mw = wstate(warp);  // [GT] running maxima, [GT] sums, [GT][AP] accumulators
-    float* lw = mw + GT;
-    float* aw = lw + GT;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int c0 = nt * 8 + 2 * tig;
-      if (gid == 0) {
-        mw[c0] = m[nt][0];
-        mw[c0 + 1] = m[nt][1];
-        lw[c0] = l[nt][0];
-        lw[c0 + 1] = l[nt][1];
-      }
-      float* a0 = aw + c0 * AP;
-#pragma unroll
-      for (int dd = 0; dd < C::KS; ++dd) {
-        // rows gid and gid + 8 of d-block dd (permuted for fp8 and 4-bit caches, see the PV step)
-        const int dlo = I4 ? 32 * (dd / 2) + 4 * gid + dd % 2 : F8 ? 2 * C::KS * gid + 2 * dd : dd * 16 + gid;
-        const int dhi = I4 ? dlo + 2 : F8 ? dlo + 1 : dlo + 8;
-        a0[dlo] = o[nt][dd][0];
-        a0[AP + dlo] = o[nt][dd][1];
-        a0[dhi] = o[nt][dd][2];
-        a0[AP + dhi] = o[nt][dd][3];
-      }
-    }
-  }
-  __syncthreads();
-
-  const bool single = n_splits == 1;
-  const size_t pidx = ((size_t)b * p.Hkv + kvh) * p.S + split;
-  constexpr int DV = D / 8;  // items per column
-  // The cluster merge: the C = p.cmerge splits of this (sequence, KV head) form one
-  // cluster. Split r owns output items [r per, (r + 1) per); every split pushes its
-  // state of each item into the owner's receive entries (distributed shared memory
-  // stores, which need no round trip), and after a cluster barrier every owner
-  // reduces its items from its own shared memory.
-  const int ccount = p.cmerge;
-  const int cper = ccount ? (cols * DV + ccount - 1) / ccount : 0;
-  float* const recv = wstate(kWarps - 1) + WSTATE;  // [C][cper][kRecvFloats]
-  if constexpr (cluster_merge_fits<D, NT, KIND>()) {
-    // every split of the cluster is past its main loop: the receive entries (in ring
-    // memory) are free
-    if (ccount) cluster_sync_relaxed();  // orders execution: nothing is pending on them
-  }
-  for (int it = threadIdx.x; it < cols * DV; it += kThreads) {
-    const int g = it / DV, d0 = (it % DV) * 8;  // g: column
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wstate(w)[g]);
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    float den = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float* st = wstate(w);
-      const float mwg = st[g];
-      // a warp that saw no token of the column (m = -inf) contributes nothing
-      const float f = mwg == -INFINITY ? 0.f : exp2_approx(mwg - M);
-      const float4* src = reinterpret_cast<const float4*>(st + 2 * GT + g * AP + d0);
-      const float4 x = src[0], y = src[1];
-      v[0] += f * x.x; v[1] += f * x.y; v[2] += f * x.z; v[3] += f * x.w;
-      v[4] += f * y.x; v[5] += f * y.y; v[6] += f * y.z; v[7] += f * y.w;
-      den += f * st[GT + g];
-    }
-    // cache values are stored values times v_scale (1 unless fp8); a column whose
-    // row sees no token of this split has M = -inf and den = 0
-    if constexpr (cluster_merge_fits<D, NT, KIND>()) {
-      if (ccount) {  // this split's state of the item, pushed to the item's owner
-        const int owner = it / cper;
-        float* e = const_cast<float*>(map_cluster_rank(recv, (uint32_t)owner)) +
-                   ((size_t)cluster_rank() * cper + (it - owner * cper)) * kRecvFloats;
-        reinterpret_cast<float4*>(e)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(e)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        reinterpret_cast<float2*>(e)[4] = make_float2(M, den);
-        continue;
-      }
-    }
-    if (single) {
-      const float r = den > 0.f ? p.v_scale / den : 0.f;
-      uint4 pk;
-      pk.x = pack2<T>(v[0] * r, v[1] * r);
-      pk.y = pack2<T>(v[2] * r, v[3] * r);
-      pk.z = pack2<T>(v[4] * r, v[5] * r);
-      pk.w = pack2<T>(v[6] * r, v[7] * r);
-      *reinterpret_cast<uint4*>(out + qrow(g) * D + d0) = pk;
-    } else {
-      const float vs = p.v_scale;
-      float4* dst = reinterpret_cast<float4*>(p.ws_acc + (pidx * cols + g) * D + d0);
-      dst[0] = make_float4(v[0] * vs, v[1] * vs, v[2] * vs, v[3] * vs);
-      dst[1] = make_float4(v[4] * vs, v[5] * vs, v[6] * vs, v[7] * vs);
-      if (d0 == 0) {
-        p.ws_m[pidx * cols + g] = M;
-        p.ws_l[pidx * cols + g] = den;
-      }
-    }
-  }
-  if constexpr (cluster_merge_fits<D, NT, KIND>()) {
-    if (ccount) {
-      cluster_sync();  // every push has landed; no split reads another's memory after this
-      const int rank = (int)cluster_rank();
-      if (rank == 0 && p.Ps < p.P && threadIdx.x == 0)
-        p.steal[(size_t)b * p.Hkv + kvh] = 0;  // no claims left
-      const int i_lo = rank * cper, i_hi = min(cols * DV, i_lo + cper);
-      for (int it = i_lo + threadIdx.x; it < i_hi; it += kThreads) {
-        const int g = it / DV, d0 = (it % DV) * 8;
-        const float* e0 = recv + (size_t)(it - i_lo) * kRecvFloats;
-        // every entry loaded first, then the reduction
-        float2 ml[kMaxClusterMerge];
-        float4 xc[kMaxClusterMerge], yc[kMaxClusterMerge];
-        float M = -INFINITY;
-#pragma unroll
-        for (int c2 = 0; c2 < kMaxClusterMerge; ++c2) {
-          if (c2 < ccount) {
-            const float* e = e0 + (size_t)c2 * cper * kRecvFloats;
-            xc[c2] = reinterpret_cast<const float4*>(e)[0];
-            yc[c2] = reinterpret_cast<const float4*>(e)[1];
-            ml[c2] = reinterpret_cast<const float2*>(e)[4];
-            M = fmaxf(M, ml[c2].x);
-          }
-        }
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        float den = 0.f;
-#pragma unroll
-        for (int c2 = 0; c2 < kMaxClusterMerge; ++c2) {
-          if (c2 < ccount) {
-            // a split that saw no token of the column (m = -inf) weighs 0
-            const float w = ml[c2].x == -INFINITY ? 0.f : exp2_approx(ml[c2].x - M);
-            const float4 x = xc[c2], y = yc[c2];
-            den += w * ml[c2].y;
-            v[0] += w * x.x; v[1] += w * x.y; v[2] += w * x.z; v[3] += w * x.w;
-            v[4] += w * y.x; v[5] += w * y.y; v[6] += w * y.z; v[7] += w * y.w;
-          }
-        }
-        const float r = den > 0.f ? p.v_scale / den : 0.f;
-        uint4 pk;
-        pk.x = pack2<T>(v[0] * r, v[1] * r);
-        pk.y = pack2<T>(v[2] * r, v[3] * r);
-        pk.z = pack2<T>(v[4] * r, v[5] * r);
-        pk.w = pack2<T>(v[6] * r, v[7] * r);
-        *reinterpret_cast<uint4*>(out + qrow(g) * D + d0) = pk;
-      }
-    }
-  }
+  finish_cta<T, KIND, D, NT, C>(p, ring, n_splits, m, l, o);
 }
 
 // Combine the split partials of one (sequence, query head, 64-wide slice of D):
@@ -956,10 +922,18 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// The kernel of a cache type and its configuration (4-bit caches: pa_decode_int4.cuh).
+template <typename T, typename KV, int D, int NT, bool WIN>
+struct DecodeKernel {
+  using C = Cfg<D, NT, kv_kind_of<KV>>;
+  static constexpr auto kernel = decode_kernel<T, KV, D, NT, WIN>;
+};
+
 template <typename T, typename KV, int D, int NT, bool WIN>
 cudaError_t launch_decode_nt(const DecodeParams& p, cudaStream_t st, int* kernels) {
-  using C = Cfg<D, NT, kv_kind_of<KV>>;
-  auto kern = decode_kernel<T, KV, D, NT, WIN>;
+  using Kernel = DecodeKernel<T, KV, D, NT, WIN>;
+  using C = typename Kernel::C;
+  auto kern = Kernel::kernel;
   // The dynamic shared memory opt-in is per device; remember which devices have it.
   static unsigned long long done_mask = 0ull;
   int dev = 0;
@@ -977,7 +951,7 @@ cudaError_t launch_decode_nt(const DecodeParams& p, cudaStream_t st, int* kernel
   // every cluster of the launch is resident at once (clusters of more than two CTAs
   // pack the SMs less densely, so a launch of several waves keeps the merge grid).
   q.cmerge = 0;
-  if (cluster_merge_fits<D, NT, kv_kind_of<KV>>() && q.S >= 2 &&
+  if (cluster_merge_fits<D, NT, C>() && q.S >= 2 &&
       q.S <= PA_CLUSTER_MERGE_MAX && q.S <= kMaxClusterMerge) {
     if (q.S == 2) {
       q.cmerge = 2;

@@ -1,5 +1,5 @@
 // Decode kernels for 4-bit caches with bf16 queries, head_dim 256.
-#include "pa_decode_kernel.cuh"
+#include "pa_decode_int4.cuh"
 
 namespace pa {
 cudaError_t launch_decode_int4_bf16_d256(const DecodeParams& p, cudaStream_t st, int* kernels) {

@@ -18,7 +18,7 @@
 // one more MMA, against the sums of the query over each group (exact to 22 bits as two
 // fp16 terms). V: the weights are multiplied by the steps of their tokens, one packed
 // multiplication per group and token pair; the minima are one more MMA whose rows are
-// the groups.
+// the groups. (Sums from alternating ends of the codes: see int4_pv.)
 //
 // Shared-memory order. Row i of the score MMA (and with it column i of the V MMA) is
 // token row_of(i) of its 16: rows of 80 bytes four apart start 64 bytes apart modulo 128,
@@ -28,11 +28,6 @@
 #include "pa_device.cuh"
 
 namespace pa {
-
-// Tag type of a 4-bit cache with groups of 32 elements.
-struct int4g32 {
-  uint8_t bits;
-};
 
 // Token (0..7) of row i (0..7) of an MMA row block's half; the other half adds 8.
 __device__ __forceinline__ int int4_row_of(int i) { return (i >> 1) + 4 * (i & 1); }
@@ -47,16 +42,23 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-  return v;
+// Two 8x8 16-bit matrices, transposed; lanes 0-7 and 8-15 give their row addresses.
+__device__ __forceinline__ void ldmatrix_x2_trans(uint32_t (&r)[2], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
+               : "=r"(r[0]), "=r"(r[1])
+               : "r"(addr)
+               : "memory");
 }
 __device__ __forceinline__ uint32_t mul2_half(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+__device__ __forceinline__ uint32_t fma2_half(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b),
+                            *reinterpret_cast<__half2*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 // c = a b with a zero accumulator (fp16 in, fp32 out).
 __device__ __forceinline__ void mma16816_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                               uint32_t b1) {
@@ -210,48 +212,76 @@ __device__ __forceinline__ void int4_scores(float (&s)[NT][4], float (&sm)[NT][4
   }
 }
 
-// o += V^T P^T over the 16 tokens at `rows`, of which the first nv are live (rows past
-// them hold anything: their steps and minima are read as 0, and any code is finite).
-// Accumulator o[nt][2g + i]: rows gid and gid + 8 are elements 32 g + 4 gid + i and + 2,
-// times 2^-24 (i = 0) or 2^-20 (i = 1). om[nt][0..1], row gid: the minima's sum of group gid.
-template <int D, int NT>
+// o += V^T P^T over the 16 tokens at `rows` (rows past the context have zero steps and
+// minima there; any code is finite). Accumulator o[nt][2g + i]: rows gid and gid + 8 are
+// elements 32 g + 4 gid + i and + 2, times 2^-24, for i = 0; for i = 1 the A operand is the
+// whole byte (the nibble of i = 1 above that of i = 0), which takes one mask less, so that
+// the accumulator holds 16 times the element's sum plus that of i = 0 until int4_finish.
+//
+// Every other 16 tokens are summed from the other end of the codes (DOWN): value =
+// maximum - step * (15 - n), with 15 - n the complement of the nibble. Summed from the
+// minimum alone, the codes' sums and the minima's grow with the context and cancel, and
+// the truncation of the tensor cores' fp32 sums is not lost in them: 4e-3 of the output
+// over 32K tokens in one split. From alternating ends both sums stay near the result.
+//
+// The steps of two tokens, for the multiplication of the weights, come from a transposing
+// load of the tokens' steps and minima: lane 4 g + tig then holds those of group g and
+// tokens 2 tig, 2 tig + 1 (of the MMA's order), and a shuffle hands them to the others.
+// om[nt][0..1], row gid: the sum of the minima (maxima) of group gid.
+template <int D, int NT, bool DOWN>
 __device__ __forceinline__ void int4_pv(float (&o)[NT][D / 16][4], float (&om)[NT][4], uint32_t rows,
-                                        const uint32_t (&pb)[NT][2], int nv, int gid, int tig) {
+                                        const uint32_t (&pb)[NT][2], int lane) {
   using R = Int4Row<D>;
+  const int gid = lane >> 2, tig = lane & 3;
   uint4 w[4][R::W];
-  uint32_t st[4][R::G / 2], mn[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {  // the tokens of k = 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
-    const int r = tig + 4 * (j & 1) + 8 * (j >> 1);
-    const uint32_t row = rows + r * R::BYTES;
+    const uint32_t row = rows + (tig + 4 * (j & 1) + 8 * (j >> 1)) * R::BYTES;
 #pragma unroll
     for (int i = 0; i < R::W; ++i) w[j][i] = lds128(row + 16 * R::W * (gid >> 1) + 16 * i);
-    int4_meta<D>(st[j], row, R::CODES);
-    mn[j] = lds16(row + R::MINS + 2 * (gid & (R::G - 1)));
-    if (r >= nv) {
-#pragma unroll
-      for (int i = 0; i < R::G / 2; ++i) st[j][i] = 0u;
-      mn[j] = 0u;
+  }
+  uint32_t st[2], mn[2];  // steps and minima of group gid (D 128: gid < 4), tokens of k < 8 and >= 8
+  {
+    const uint32_t row = rows + (int4_row_of(lane & 7) + (lane & 8)) * R::BYTES + R::CODES;
+    if constexpr (D == 128) {
+      ldmatrix_x2_trans(st, row);  // eight 16-bit columns: four steps, four minima
+      mn[0] = __shfl_sync(0xffffffffu, st[0], lane + 16);
+      mn[1] = __shfl_sync(0xffffffffu, st[1], lane + 16);
+    } else {
+      uint32_t m[4];
+      ldmatrix_x4<true>(m, row + (lane & 16));
+      st[0] = m[0];
+      st[1] = m[1];
+      mn[0] = m[2];
+      mn[1] = m[3];
     }
   }
   {
-    const uint32_t a[4] = {__byte_perm(mn[0], mn[1], 0x5410), 0u, __byte_perm(mn[2], mn[3], 0x5410), 0u};
+    const uint32_t a[4] = {DOWN ? fma2_half(st[0], 0x4b804b80u, mn[0]) : mn[0], 0u,  // 15 step + minimum
+                           DOWN ? fma2_half(st[1], 0x4b804b80u, mn[1]) : mn[1], 0u};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) mma16816<__half>(om[nt], a, pb[nt][0], pb[nt][1]);
+  }
+  if (DOWN) {
+    st[0] ^= 0x80008000u;
+    st[1] ^= 0x80008000u;
   }
   const uint32_t sel = (gid & 1) ? 0x7632u : 0x5410u;  // the half of the octet's word
 #pragma unroll
   for (int g = 0; g < R::G; ++g) {
     const uint32_t x0 = __byte_perm(word_of(w[0][g / 4], g % 4), word_of(w[1][g / 4], g % 4), sel);
     const uint32_t x1 = __byte_perm(word_of(w[2][g / 4], g % 4), word_of(w[3][g / 4], g % 4), sel);
-    const uint32_t h0 = x0 >> 8, h1 = x1 >> 8;
-    const uint32_t a0[4] = {x0 & R::LO, h0 & R::LO, x1 & R::LO, h1 & R::LO};
-    const uint32_t a1[4] = {x0 & R::HI, h0 & R::HI, x1 & R::HI, h1 & R::HI};
-    const uint32_t s0 = __byte_perm(st[0][g / 2], st[1][g / 2], (g & 1) ? 0x7632u : 0x5410u);
-    const uint32_t s1 = __byte_perm(st[2][g / 2], st[3][g / 2], (g & 1) ? 0x7632u : 0x5410u);
+    const uint32_t h0 = __byte_perm(x0, 0u, 0x4341), h1 = __byte_perm(x1, 0u, 0x4341);  // upper bytes
+    constexpr uint32_t kBytes = 0x00ff00ffu;
+    auto lo = [](uint32_t x) { return (DOWN ? ~x : x) & R::LO; };
+    const uint32_t a0[4] = {lo(x0), lo(h0), lo(x1), lo(h1)};
+    const uint32_t a1[4] = {(DOWN ? ~x0 : x0) & kBytes, DOWN ? h0 ^ kBytes : h0,
+                            (DOWN ? ~x1 : x1) & kBytes, DOWN ? h1 ^ kBytes : h1};
+    const uint32_t s0 = __shfl_sync(0xffffffffu, st[0], 4 * g + tig);
+    const uint32_t s1 = __shfl_sync(0xffffffffu, st[1], 4 * g + tig);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      // the weights times the steps, rounded to fp16 once more (they are at most 1)
+      // the weights times the steps, rounded to fp16 once more
       const uint32_t b0 = mul2_half(pb[nt][0], s0), b1 = mul2_half(pb[nt][1], s1);
       mma16816<__half>(o[nt][2 * g], a0, b0, b1);
       mma16816<__half>(o[nt][2 * g + 1], a1, b0, b1);
@@ -269,13 +299,12 @@ __device__ __forceinline__ void int4_finish(float (&o)[NT][D / 16][4], const flo
       const float m0 = __shfl_sync(0xffffffffu, om[nt][0], 4 * g + tig);
       const float m1 = __shfl_sync(0xffffffffu, om[nt][1], 4 * g + tig);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float f = i == 0 ? 16777216.f : 1048576.f;
-        float(&a)[4] = o[nt][2 * g + i];
-        a[0] = fmaf(a[0], f, m0);
-        a[1] = fmaf(a[1], f, m1);
-        a[2] = fmaf(a[2], f, m0);
-        a[3] = fmaf(a[3], f, m1);
+      for (int i = 0; i < 4; ++i) {
+        const float lo = o[nt][2 * g][i] * 16777216.f;                   // 2^24
+        const float hi = (o[nt][2 * g + 1][i] - o[nt][2 * g][i]) * 1048576.f;  // 2^20
+        const float mn = (i & 1) ? m1 : m0;
+        o[nt][2 * g][i] = lo + mn;
+        o[nt][2 * g + 1][i] = hi + mn;
       }
     }
 }

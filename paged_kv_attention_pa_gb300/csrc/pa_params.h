@@ -32,7 +32,7 @@ constexpr int kPartitionMin = 64;   // tokens: below this a split's fixed cost d
 #define PA_TILE_TOKENS_I4_D128 32
 #endif
 #ifndef PA_TILE_TOKENS_I4_D256
-#define PA_TILE_TOKENS_I4_D256 16
+#define PA_TILE_TOKENS_I4_D256 32
 #endif
 // What the caches hold: elements of the q/out type, FP8 E4M3, or 4-bit groups.
 enum KvKind { kKv16 = 0, kKvFp8 = 1, kKvInt4 = 2 };
@@ -42,7 +42,7 @@ __host__ __device__ constexpr int kv_row_bytes(int D, KvKind kind) {
 }
 // Per head_dim and cache type: a 256-wide 16-bit row pair is already 1 KB a token;
 // fp8 rows carry half the bytes of a 16-bit row for the same arithmetic.
-constexpr int tile_tokens(int D, KvKind kind) {
+__host__ __device__ constexpr int tile_tokens(int D, KvKind kind) {
   return kind == kKvInt4  ? (D == 128 ? PA_TILE_TOKENS_I4_D128 : PA_TILE_TOKENS_I4_D256)
          : kind == kKvFp8 ? (D == 128 ? PA_TILE_TOKENS_F8_D128 : PA_TILE_TOKENS_F8_D256)
                           : (D == 128 ? PA_TILE_TOKENS_D128 : PA_TILE_TOKENS_D256);
@@ -62,16 +62,26 @@ constexpr int tile_tokens(int D, KvKind kind) {
 #define PA_WARPS_F8_D256 4
 #endif
 #ifndef PA_WARPS_I4_D128
-#define PA_WARPS_I4_D128 8
+#define PA_WARPS_I4_D128 12
+#endif
+#ifndef PA_WARPS_I4_WIDE
+#define PA_WARPS_I4_WIDE 8
 #endif
 #ifndef PA_WARPS_I4_D256
 #define PA_WARPS_I4_D256 8
 #endif
-constexpr int warps_per_cta(int D, KvKind kind) {
-  return kind == kKvInt4  ? (D == 128 ? PA_WARPS_I4_D128 : PA_WARPS_I4_D256)
+__host__ __device__ constexpr int warps_per_cta(int D, KvKind kind, int column_tiles = 1) {
+  return kind == kKvInt4  ? (column_tiles > 2 || (column_tiles > 1 && D > 128) ? 8 : column_tiles > 1 ? PA_WARPS_I4_WIDE : D == 128 ? PA_WARPS_I4_D128 : PA_WARPS_I4_D256)
          : kind == kKvFp8 ? (D == 128 ? PA_WARPS_F8_D128 : PA_WARPS_F8_D256)
                           : (D == 128 ? PA_WARPS_D128 : PA_WARPS_D256);
 }
+// 4-bit caches: bulk copies (one per block and tile) or 16-byte cp.async.
+#ifndef PA_I4_BULK_D128
+#define PA_I4_BULK_D128 0
+#endif
+#ifndef PA_I4_BULK_D256
+#define PA_I4_BULK_D256 1
+#endif
 // Work sharing among the splits of a sequence: each split keeps about
 // (1 - 1/kStealDiv) of its P tokens as a static share, and the rest of the context
 // is claimed tile by tile through one counter per (sequence, KV head) held in the
