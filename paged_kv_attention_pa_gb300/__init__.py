@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import NamedTuple, Optional, Tuple
 
@@ -162,6 +163,16 @@ def _ensure_device(lib, index: int):
         _tls.device = index
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(device: int, stream) -> int:
+    """cudaStream_t of the given stream or the device's current one."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _stream_handle(torch.device("cuda", device), stream)
+
+
 def _stream_handle(device: torch.device, stream) -> int:
     s = torch.cuda.current_stream(device) if stream is None else stream
     return int(s.cuda_stream)
@@ -176,20 +187,87 @@ def _cache_shape(k_cache, v_cache, dtype):
     """(kv_dtype, num_blocks, block_size, Hkv, D) of a pair of caches: [num_blocks,
     block_size, Hkv, D] in the q dtype or float8_e4m3fn, or 4 bits as uint8
     [num_blocks, Hkv, block_size, int4_row_bytes(D)]."""
-    if k_cache.dim() != 4 or tuple(v_cache.shape) != tuple(k_cache.shape):
+    shape, cd = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be four-dimensional and of one shape")
-    if v_cache.dtype != k_cache.dtype or \
-            k_cache.dtype not in (dtype, torch.float8_e4m3fn, torch.uint8):
+    if v_cache.dtype != cd:
+        raise TypeError("k_cache and v_cache must have one dtype")
+    if cd == dtype:
+        return (PA_KV_AS_DTYPE, *shape)
+    if cd == torch.float8_e4m3fn:
+        return (PA_KV_FP8_E4M3, *shape)
+    if cd != torch.uint8:
         raise TypeError("the caches must both have the 16-bit dtype of the call, or both be "
                         "float8_e4m3fn, or both uint8 (4-bit rows)")
-    if k_cache.dtype == torch.uint8:
-        nb, hkv, bs, row = k_cache.shape
-        if row % 5 != 0:
-            raise ValueError("a 4-bit cache row has int4_row_bytes(D) bytes (80 or 160)")
-        return PA_KV_INT4, nb, bs, hkv, row // 5 * 8
-    nb, bs, hkv, D = k_cache.shape
-    return (PA_KV_FP8_E4M3 if k_cache.dtype == torch.float8_e4m3fn else PA_KV_AS_DTYPE,
-            nb, bs, hkv, D)
+    nb, hkv, bs, row = shape
+    if row % 5 != 0:
+        raise ValueError("a 4-bit cache row has int4_row_bytes(D) bytes (80 or 160)")
+    return PA_KV_INT4, nb, bs, hkv, row // 5 * 8
+
+
+# The argument structures are packed in one go: setting their fields one by one costs a
+# call several microseconds.
+_DECODE = struct.Struct("<6Q8if4i2fiI4xq")
+_APPEND = struct.Struct("<10Q3q10i2f2if4x")
+_GATHER = struct.Struct("<7Q9i2f4x")
+assert _DECODE.size == ctypes.sizeof(DecodeArgs) and _APPEND.size == ctypes.sizeof(AppendArgs) \
+    and _GATHER.size == ctypes.sizeof(GatherArgs)
+
+
+def _pack(layout, *values) -> bytes:
+    try:
+        return layout.pack(*values)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"an argument is out of range: {e}") from None
+
+
+def _where(first, tensors) -> int:
+    """The device index all (name, tensor) pairs share with `first`; contiguous tensors only."""
+    dev = first.get_device()
+    for name, t in tensors:
+        d = t.get_device()
+        if d != dev or d < 0:
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+            raise ValueError(f"{name} is on {t.device}, another tensor of the call on {first.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    return dev
+
+
+def _decode_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale, max_seq_len, splits,
+                 window, k_scale, v_scale, deterministic, total_tokens):
+    """Check shapes / dtypes / devices; the packed pa_decode_args and the device index."""
+    shape = q.shape
+    if len(shape) == 3:
+        (B, Hq, D), R = shape, 1
+    elif len(shape) == 4:
+        B, R, Hq, D = shape
+    else:
+        raise ValueError("q must be [B, Hq, D] or [B, R, Hq, D]")
+    dtype = _DT.get(q.dtype)
+    if dtype is None or out.dtype != q.dtype:
+        raise TypeError("q and out must be float16 or bfloat16")
+    kv, nb, bs, Hkv, Dk = _cache_shape(k_cache, v_cache, q.dtype)
+    if Dk != D:
+        raise ValueError("k_cache / v_cache / q shapes disagree")
+    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        raise TypeError("block_tables and seq_lens must be int32")
+    bts = block_tables.shape
+    if len(bts) != 2 or bts[0] != B or seq_lens.shape != (B,):
+        raise ValueError("block_tables must be [B, max_blocks] and seq_lens [B]")
+    if out.shape != shape:
+        raise ValueError("out must have q's shape")
+    dev = _where(q, (("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
+                     ("block_tables", block_tables), ("seq_lens", seq_lens), ("out", out)))
+    if kv == PA_KV_AS_DTYPE:
+        k_scale = v_scale = 1.0
+    return dev, _pack(
+        _DECODE, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), out.data_ptr(), B, Hq, Hkv, D, bs, nb, bts[1],
+        0 if max_seq_len is None else int(max_seq_len), float(scale), dtype, int(splits),
+        int(window), kv, float(k_scale), float(v_scale), R,
+        PA_FLAG_DETERMINISTIC if deterministic else 0, int(total_tokens))
 
 
 def make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale: float,
@@ -198,50 +276,9 @@ def make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale: float,
               deterministic: bool = False, total_tokens: int = 0) -> DecodeArgs:
     """Check shapes / dtypes / devices and fill a pa_decode_args. q is [B, Hq, D], or
     [B, R, Hq, D] for R causal query rows per sequence."""
-    if q.dim() not in (3, 4) or k_cache.dim() != 4 or v_cache.dim() != 4:
-        raise ValueError("q must be [B, Hq, D] or [B, R, Hq, D] and the caches "
-                         "[num_blocks, block_size, Hkv, D] (4 bits: [num_blocks, Hkv, "
-                         "block_size, int4_row_bytes(D)])")
-    if q.dim() == 4:
-        B, R, Hq, D = q.shape
-    else:
-        (B, Hq, D), R = q.shape, 1
-    if q.dtype not in _DT or out.dtype != q.dtype:
-        raise TypeError("q and out must be float16 or bfloat16")
-    kv, nb, bs, Hkv, Dk = _cache_shape(k_cache, v_cache, q.dtype)
-    if Dk != D:
-        raise ValueError("k_cache / v_cache / q shapes disagree")
-    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
-        raise TypeError("block_tables and seq_lens must be int32")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(seq_lens.shape) != (B,):
-        raise ValueError("block_tables must be [B, max_blocks] and seq_lens [B]")
-    if tuple(out.shape) != tuple(q.shape):
-        raise ValueError("out must have q's shape")
-    for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
-                    ("block_tables", block_tables), ("seq_lens", seq_lens), ("out", out)):
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
-        if t.device != q.device:
-            raise ValueError(f"{name} is on {t.device}, q on {q.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    a = DecodeArgs()
-    a.q, a.k_cache, a.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
-    a.block_tables, a.seq_lens, a.out = block_tables.data_ptr(), seq_lens.data_ptr(), out.data_ptr()
-    a.B, a.Hq, a.Hkv, a.D = B, Hq, Hkv, D
-    a.block_size, a.num_blocks = bs, nb
-    a.max_blocks_per_seq = block_tables.shape[1]
-    a.max_seq_len = 0 if max_seq_len is None else int(max_seq_len)
-    a.scale = float(scale)
-    a.dtype = _DT[q.dtype]
-    a.splits = int(splits)
-    a.window = int(window)
-    a.q_len = R
-    a.kv_dtype = kv
-    a.k_scale, a.v_scale = (1.0, 1.0) if kv == PA_KV_AS_DTYPE else (float(k_scale), float(v_scale))
-    a.flags = PA_FLAG_DETERMINISTIC if deterministic else 0
-    a.total_tokens = int(total_tokens)
-    return a
+    return DecodeArgs.from_buffer_copy(_decode_args(
+        q, k_cache, v_cache, block_tables, seq_lens, out, scale, max_seq_len, splits, window,
+        k_scale, v_scale, deterministic, total_tokens)[1])
 
 
 # One workspace per (device, stream); grown on demand, zero-filled when made. Workspaces that
@@ -264,8 +301,7 @@ def _workspace(need: int, device: torch.device, stream_handle: int) -> torch.Ten
 
 
 def workspace_for(args: DecodeArgs, device: torch.device, stream_handle: int) -> torch.Tensor:
-    lib = load()
-    need = lib.pa_decode_ex_workspace_bytes(ctypes.byref(args))
+    need = load().pa_decode_ex_workspace_bytes(ctypes.byref(args))
     if need == 0:
         raise PAError(PA_ERR_INVALID_ARG, "pa_decode_ex_workspace_bytes")
     return _workspace(need, device, stream_handle)
@@ -292,15 +328,18 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     split plan for batches of mixed lengths. Asynchronous on the current (or given)
     stream.
     """
-    lib = load()
+    lib = _lib or load()
     if out is None:
         out = torch.empty_like(q)
-    args = make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale, max_seq_len, splits,
-                     window, k_scale, v_scale, deterministic, total_tokens)
-    _ensure_device(lib, q.device.index)
-    sh = _stream_handle(q.device, stream)
-    ws = workspace if workspace is not None else workspace_for(args, q.device, sh)
-    rc = lib.pa_decode_ex(ctypes.byref(args), ws.data_ptr(), ws.numel(), sh)
+    dev, args = _decode_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale, max_seq_len,
+                             splits, window, k_scale, v_scale, deterministic, total_tokens)
+    _ensure_device(lib, dev)
+    sh = _stream_of(dev, stream)
+    ws = workspace if workspace is not None else _workspaces.get((dev, sh))
+    rc = PA_ERR_WORKSPACE if ws is None else lib.pa_decode_ex(args, ws.data_ptr(), ws.numel(), sh)
+    if rc == PA_ERR_WORKSPACE and workspace is None:  # none yet, or too small: nothing was launched
+        ws = workspace_for(DecodeArgs.from_buffer_copy(args), q.device, sh)
+        rc = lib.pa_decode_ex(args, ws.data_ptr(), ws.numel(), sh)
     if rc != PA_OK:
         raise PAError(rc, "pa_decode_ex")
     return out
@@ -377,44 +416,30 @@ def rope(rot_dim: int, base: float = 10000.0, interleaved: bool = False,
     return Rope(turns.to(device), bool(interleaved), amp.value)
 
 
-def _rows_shape(name, t, B, starts):
-    """(rows argument, row stride in elements) of a [B, H, D], [B, R, H, D] or, with starts,
-    [rows, H, D] tensor whose heads are dense and whose rows are evenly spaced."""
-    H, D = t.shape[-2:]
-    if t.dim() not in ((3,) if starts is not None else (3, 4)) or \
-            (starts is None and t.shape[0] != B):
-        raise ValueError(f"{name} must be [B, H, D] or [B, R, H, D], or [rows, H, D] with starts")
-    if t.numel() and (t.stride(-1) != 1 or (H > 1 and t.stride(-2) != D)):
+def _row_stride(name, t, shape) -> int:
+    """Elements between the rows of a [B, H, D], [B, R, H, D] or packed [rows, H, D] tensor,
+    whose heads are dense and whose rows are evenly spaced."""
+    st = t.stride()
+    H, D = shape[-2:]
+    if (st[-1] != 1 or (H > 1 and st[-2] != D)) and t.numel():
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    if t.dim() == 3:
-        return (t.shape[0] if starts is not None else 1), (t.stride(0) if t.shape[0] > 1 else H * D)
-    R = t.shape[1]
-    if R == 1:
-        return 1, (t.stride(0) if t.shape[0] > 1 else H * D)
-    if t.shape[0] > 1 and t.stride(0) != R * t.stride(1):
+    if len(shape) == 3 or shape[1] == 1:
+        return st[0] if shape[0] > 1 else H * D
+    if shape[0] > 1 and st[0] != shape[1] * st[1]:
         raise ValueError(f"the rows of {name} must be evenly spaced")
-    return R, t.stride(1)
+    return st[1]
 
 
-def _check_rows_call(device, block_tables, seq_lens, starts, tensors):
+def _tables(block_tables, seq_lens, starts):
+    """(B, table width) of a call's index tensors."""
     if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32 or \
             (starts is not None and starts.dtype != torch.int32):
         raise TypeError("block_tables, seq_lens and starts must be int32")
-    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
-    if B < 0 or block_tables.dim() != 2 or block_tables.shape[0] != B or \
-            (starts is not None and tuple(starts.shape) != (B + 1,)):
+    bts, sls = block_tables.shape, seq_lens.shape
+    if len(sls) != 1 or len(bts) != 2 or bts[0] != sls[0] or \
+            (starts is not None and starts.shape != (sls[0] + 1,)):
         raise ValueError("block_tables must be [B, max_blocks], seq_lens [B] and starts [B + 1]")
-    dense = [("block_tables", block_tables), ("seq_lens", seq_lens), ("starts", starts)]
-    for name, t, contiguous in [(n, t, True) for n, t in dense] + tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the caches on {device}")
-        if contiguous and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    return B
+    return bts
 
 
 def append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -435,49 +460,60 @@ def append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     (v_scale). q_out must be contiguous and may be q itself when that is contiguous.
     Asynchronous on the current (or given) stream.
     """
-    lib = load()
-    if k.dtype not in _DT or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+    lib = _lib or load()
+    dtype, shape = _DT.get(k.dtype), k.shape
+    if dtype is None or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
         raise TypeError("q, k and v must be float16 or bfloat16, all the same")
     kv, nb, bs, Hkv, D = _cache_shape(k_cache, v_cache, k.dtype)
-    if q is None and q_out is not None:
-        raise ValueError("q_out needs q")
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    turns = rope.turns if rope is not None else None
-    B = _check_rows_call(k_cache.device, block_tables, seq_lens, starts, [
-        ("k", k, False), ("v", v, False), ("k_cache", k_cache, True), ("v_cache", v_cache, True),
-        ("q", q, False), ("q_out", q_out, True), ("rope.turns", turns, True)])
-    if k.dim() < 3 or tuple(v.shape) != tuple(k.shape) or tuple(k.shape[-2:]) != (Hkv, D):
+    B, width = _tables(block_tables, seq_lens, starts)
+    packed = starts is not None
+    if len(shape) != 3 and (packed or len(shape) != 4) or (not packed and shape[0] != B):
+        raise ValueError("k must be [B, Hkv, D] or [B, R, Hkv, D], or [rows, Hkv, D] with starts")
+    if v.shape != shape or shape[-2] != Hkv or shape[-1] != D:
         raise ValueError("k and v must have one shape ending in the caches' [Hkv, D]")
-    if turns is not None and (turns.dtype != torch.int64 or turns.dim() != 1):
-        raise TypeError("rope.turns must be int64 [rot_dim / 2]")
-    a = AppendArgs()
-    a.rows, a.k_stride = _rows_shape("k", k, B, starts)
-    _, a.v_stride = _rows_shape("v", v, B, starts)
-    a.k, a.v, a.k_cache, a.v_cache = (t.data_ptr() for t in (k, v, k_cache, v_cache))
-    a.Hkv, a.D = Hkv, D
+    dev = k.get_device()
+    dense = [("k_cache", k_cache), ("v_cache", v_cache), ("block_tables", block_tables),
+             ("seq_lens", seq_lens)]
+    if k.get_device() != v.get_device() or (q is not None and q.get_device() != dev):
+        raise ValueError("q, k and v must be CUDA tensors on one device (no CPU path)")
+    qp = qop = Hq = q_stride = 0
     if q is not None:
-        if q.dim() != k.dim() or tuple(q.shape[:-2]) != tuple(k.shape[:-2]) or q.shape[-1] != D:
+        qs = q.shape
+        if len(qs) != len(shape) or qs[:-2] != shape[:-2] or qs[-1] != D:
             raise ValueError("q must have k's rows and head_dim")
-        if tuple(q_out.shape) != tuple(q.shape) or q_out.dtype != q.dtype:
+        if q_out is None:
+            q_out = torch.empty(qs, dtype=q.dtype, device=q.device)
+        elif q_out.shape != qs or q_out.dtype != q.dtype:
             raise ValueError("q_out must have q's shape and dtype")
-        _, a.q_stride = _rows_shape("q", q, B, starts)
-        a.q, a.q_out, a.Hq = q.data_ptr(), q_out.data_ptr(), q.shape[-2]
-    a.block_tables, a.seq_lens = block_tables.data_ptr(), seq_lens.data_ptr()
-    a.starts = starts.data_ptr() if starts is not None else None
-    a.B, a.block_size, a.num_blocks = B, bs, nb
-    a.max_blocks_per_seq = block_tables.shape[1]
-    a.dtype, a.kv_dtype = _DT[k.dtype], kv
-    a.k_scale, a.v_scale = float(k_scale), float(v_scale)
+        q_stride, Hq = _row_stride("q", q, qs), qs[-2]
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+        dense.append(("q_out", q_out))
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    tp = rot = interleaved = 0
+    amplitude = 1.0
     if rope is not None:
-        a.rope_turns, a.rot_dim = turns.data_ptr(), 2 * turns.shape[0]
-        a.rope_layout = PA_ROPE_INTERLEAVED if rope.interleaved else PA_ROPE_HALF
-        a.rope_amplitude = float(rope.amplitude)
-    device = k_cache.device
-    _ensure_device(lib, device.index)
-    sh = _stream_handle(device, stream)
-    ws = workspace if workspace is not None else _workspace(PA_WORKSPACE_HEADER_BYTES, device, sh)
-    rc = lib.pa_append(ctypes.byref(a), ws.data_ptr(), ws.numel(), sh)
+        turns, interleaved, amplitude = rope
+        if turns.dtype != torch.int64 or turns.dim() != 1:
+            raise TypeError("rope.turns must be int64 [rot_dim / 2]")
+        tp, rot = turns.data_ptr(), 2 * turns.shape[0]
+        dense.append(("rope.turns", turns))
+    if packed:
+        dense.append(("starts", starts))
+    _where(k, dense)
+    args = _pack(
+        _APPEND, qp, qop, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        block_tables.data_ptr(), seq_lens.data_ptr(), starts.data_ptr() if packed else 0, tp,
+        q_stride, _row_stride("k", k, shape), _row_stride("v", v, shape), B,
+        shape[0] if packed else (1 if len(shape) == 3 else shape[1]), Hq, Hkv, D, bs, nb, width,
+        dtype, kv, float(k_scale), float(v_scale), rot,
+        PA_ROPE_INTERLEAVED if interleaved else PA_ROPE_HALF, float(amplitude))
+    _ensure_device(lib, dev)
+    sh = _stream_of(dev, stream)
+    ws = workspace if workspace is not None else _workspaces.get((dev, sh))
+    if ws is None:
+        ws = _workspace(PA_WORKSPACE_HEADER_BYTES, k_cache.device, sh)
+    rc = lib.pa_append(args, ws.data_ptr(), ws.numel(), sh)
     if rc != PA_OK:
         raise PAError(rc, "pa_append")
     return q_out
@@ -492,43 +528,46 @@ def gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Ten
     """Read the last tokens of each sequence back from a paged cache, contiguous and in 16
     bits: (k, v) [B, rows, Hkv, D], the last `rows` tokens of every sequence, or with starts
     [B + 1] int32 packed [rows, Hkv, D], of which rows starts[b] to starts[b + 1] - 1 are the
-    last tokens of sequence b and others are left alone (zero in tensors made here). Keys
-    stay rotated. dtype is that of the rows (float16 or bfloat16; needed for fp8 and 4-bit
+    last tokens of sequence b and others are left alone (uninitialised in tensors made here).
+    Keys stay rotated. dtype is that of the rows (float16 or bfloat16; needed for fp8 and 4-bit
     caches, whose values are multiplied by k_scale, v_scale). A row without a token is zero.
     """
-    lib = load()
+    lib = _lib or load()
     if dtype is None:
         dtype = k_out.dtype if k_out is not None else k_cache.dtype
-    if dtype not in _DT:
+    code = _DT.get(dtype)
+    if code is None:
         raise TypeError("dtype must be float16 or bfloat16")
     kv, nb, bs, Hkv, D = _cache_shape(k_cache, v_cache, dtype)
-    device = k_cache.device
+    B, width = _tables(block_tables, seq_lens, starts)
     if rows < 0:
         raise ValueError("rows must not be negative")
-    shape = (rows, Hkv, D) if starts is not None else (seq_lens.shape[0], rows, Hkv, D)
-    make = torch.zeros if starts is not None else torch.empty
-    outs = [make(shape, dtype=dtype, device=device) if t is None else t for t in (k_out, v_out)]
-    B = _check_rows_call(device, block_tables, seq_lens, starts, [
-        ("k_cache", k_cache, True), ("v_cache", v_cache, True), ("k_out", outs[0], True),
-        ("v_out", outs[1], True)])
-    for t in outs:
-        if tuple(t.shape) != shape or t.dtype != dtype:
-            raise ValueError(f"k_out and v_out must be {dtype} {list(shape)}")
-    a = GatherArgs()
-    a.k_cache, a.v_cache, a.k_out, a.v_out = (t.data_ptr() for t in (k_cache, v_cache, *outs))
-    a.block_tables, a.seq_lens = block_tables.data_ptr(), seq_lens.data_ptr()
-    a.starts = starts.data_ptr() if starts is not None else None
-    a.B, a.rows, a.Hkv, a.D = B, rows, Hkv, D
-    a.block_size, a.num_blocks, a.max_blocks_per_seq = bs, nb, block_tables.shape[1]
-    a.dtype, a.kv_dtype = _DT[dtype], kv
-    a.k_scale, a.v_scale = float(k_scale), float(v_scale)
-    _ensure_device(lib, device.index)
-    sh = _stream_handle(device, stream)
-    ws = workspace if workspace is not None else _workspace(PA_WORKSPACE_HEADER_BYTES, device, sh)
-    rc = lib.pa_gather(ctypes.byref(a), ws.data_ptr(), ws.numel(), sh)
+    shape = (B, rows, Hkv, D) if starts is None else (rows, Hkv, D)
+    dense = [("k_cache", k_cache), ("v_cache", v_cache), ("block_tables", block_tables),
+             ("seq_lens", seq_lens)]
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+    if k_out.shape != shape or v_out.shape != shape or k_out.dtype != dtype or v_out.dtype != dtype:
+        raise ValueError(f"k_out and v_out must be {dtype} {list(shape)}")
+    dense += [("k_out", k_out), ("v_out", v_out)]
+    if starts is not None:
+        dense.append(("starts", starts))
+    dev = _where(k_cache, dense)
+    args = _pack(
+        _GATHER, k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), starts.data_ptr() if starts is not None else 0, k_out.data_ptr(),
+        v_out.data_ptr(), B, rows, Hkv, D, bs, nb, width, code, kv, float(k_scale), float(v_scale))
+    _ensure_device(lib, dev)
+    sh = _stream_of(dev, stream)
+    ws = workspace if workspace is not None else _workspaces.get((dev, sh))
+    if ws is None:
+        ws = _workspace(PA_WORKSPACE_HEADER_BYTES, k_cache.device, sh)
+    rc = lib.pa_gather(args, ws.data_ptr(), ws.numel(), sh)
     if rc != PA_OK:
         raise PAError(rc, "pa_gather")
-    return outs[0], outs[1]
+    return k_out, v_out
 
 
 def plan(B: int, Hq: int, Hkv: int, D: int, block_size: int, max_seq_len: int,
