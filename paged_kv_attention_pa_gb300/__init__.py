@@ -1,8 +1,8 @@
 """Python binding of libpa.so: single-query paged-attention decode on GB300, and the
 rows of its paged cache (append with rotary positions, gather).
 
-Argument marshalling only: every step of the computation runs in the CUDA
-kernels behind the C ABI declared in include/pa.h. PyTorch provides device
+Argument marshalling only (the hot calls' in csrc/binding.cpp): every step of the
+computation runs in the CUDA kernels behind the C ABI declared in include/pa.h. PyTorch provides device
 memory and the current stream. There is no CPU path: if the shared library is
 missing, every call raises.
 
@@ -20,7 +20,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 import threading
 from typing import NamedTuple, Optional, Tuple
 
@@ -122,13 +121,15 @@ class PAError(RuntimeError):
 
 
 _lib = None
+_native = None  # the module of csrc/binding.cpp
 _lib_lock = threading.Lock()
 _tls = threading.local()
 
 
 def load(path: str = LIB_PATH):
-    """Load libpa.so (built in-tree). Raises if it is missing: there is no fallback."""
-    global _lib
+    """Load libpa.so and the binding's module (built in-tree). Raises if one is missing: there
+    is no fallback."""
+    global _lib, _native
     with _lib_lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -140,6 +141,8 @@ def load(path: str = LIB_PATH):
                 fn = getattr(lib, name)
                 fn.restype = res
                 fn.argtypes = args
+            from . import _binding
+            _native = _binding
             _lib = lib
     return _lib
 
@@ -205,80 +208,54 @@ def _cache_shape(k_cache, v_cache, dtype):
     return PA_KV_INT4, nb, bs, hkv, row // 5 * 8
 
 
-# The argument structures are packed in one go: setting their fields one by one costs a
-# call several microseconds.
-_DECODE = struct.Struct("<6Q8if4i2fiI4xq")
-_APPEND = struct.Struct("<10Q3q10i2f2if4x")
-_GATHER = struct.Struct("<7Q9i2f4x")
-assert _DECODE.size == ctypes.sizeof(DecodeArgs) and _APPEND.size == ctypes.sizeof(AppendArgs) \
-    and _GATHER.size == ctypes.sizeof(GatherArgs)
-
-
-def _pack(layout, *values) -> bytes:
-    try:
-        return layout.pack(*values)
-    except (struct.error, OverflowError) as e:
-        raise ValueError(f"an argument is out of range: {e}") from None
-
-
-def _where(first, tensors) -> int:
-    """The device index all (name, tensor) pairs share with `first`; contiguous tensors only."""
-    dev = first.get_device()
-    for name, t in tensors:
-        d = t.get_device()
-        if d != dev or d < 0:
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
-            raise ValueError(f"{name} is on {t.device}, another tensor of the call on {first.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    return dev
-
-
-def _decode_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale, max_seq_len, splits,
-                 window, k_scale, v_scale, deterministic, total_tokens):
-    """Check shapes / dtypes / devices; the packed pa_decode_args and the device index."""
-    shape = q.shape
-    if len(shape) == 3:
-        (B, Hq, D), R = shape, 1
-    elif len(shape) == 4:
-        B, R, Hq, D = shape
-    else:
-        raise ValueError("q must be [B, Hq, D] or [B, R, Hq, D]")
-    dtype = _DT.get(q.dtype)
-    if dtype is None or out.dtype != q.dtype:
-        raise TypeError("q and out must be float16 or bfloat16")
-    kv, nb, bs, Hkv, Dk = _cache_shape(k_cache, v_cache, q.dtype)
-    if Dk != D:
-        raise ValueError("k_cache / v_cache / q shapes disagree")
-    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
-        raise TypeError("block_tables and seq_lens must be int32")
-    bts = block_tables.shape
-    if len(bts) != 2 or bts[0] != B or seq_lens.shape != (B,):
-        raise ValueError("block_tables must be [B, max_blocks] and seq_lens [B]")
-    if out.shape != shape:
-        raise ValueError("out must have q's shape")
-    dev = _where(q, (("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
-                     ("block_tables", block_tables), ("seq_lens", seq_lens), ("out", out)))
-    if kv == PA_KV_AS_DTYPE:
-        k_scale = v_scale = 1.0
-    return dev, _pack(
-        _DECODE, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-        seq_lens.data_ptr(), out.data_ptr(), B, Hq, Hkv, D, bs, nb, bts[1],
-        0 if max_seq_len is None else int(max_seq_len), float(scale), dtype, int(splits),
-        int(window), kv, float(k_scale), float(v_scale), R,
-        PA_FLAG_DETERMINISTIC if deterministic else 0, int(total_tokens))
-
-
 def make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale: float,
               max_seq_len: Optional[int] = None, splits: int = 0, window: int = 0,
               k_scale: float = 1.0, v_scale: float = 1.0,
               deterministic: bool = False, total_tokens: int = 0) -> DecodeArgs:
     """Check shapes / dtypes / devices and fill a pa_decode_args. q is [B, Hq, D], or
     [B, R, Hq, D] for R causal query rows per sequence."""
-    return DecodeArgs.from_buffer_copy(_decode_args(
-        q, k_cache, v_cache, block_tables, seq_lens, out, scale, max_seq_len, splits, window,
-        k_scale, v_scale, deterministic, total_tokens)[1])
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [B, Hq, D] or [B, R, Hq, D]")
+    if q.dim() == 4:
+        B, R, Hq, D = q.shape
+    else:
+        (B, Hq, D), R = q.shape, 1
+    if q.dtype not in _DT or out.dtype != q.dtype:
+        raise TypeError("q and out must be float16 or bfloat16")
+    kv, nb, bs, Hkv, Dk = _cache_shape(k_cache, v_cache, q.dtype)
+    if Dk != D:
+        raise ValueError("k_cache / v_cache / q shapes disagree")
+    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        raise TypeError("block_tables and seq_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(seq_lens.shape) != (B,):
+        raise ValueError("block_tables must be [B, max_blocks] and seq_lens [B]")
+    if tuple(out.shape) != tuple(q.shape):
+        raise ValueError("out must have q's shape")
+    for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
+                    ("block_tables", block_tables), ("seq_lens", seq_lens), ("out", out)):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+        if t.device != q.device:
+            raise ValueError(f"{name} is on {t.device}, q on {q.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    a = DecodeArgs()
+    a.q, a.k_cache, a.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
+    a.block_tables, a.seq_lens, a.out = block_tables.data_ptr(), seq_lens.data_ptr(), out.data_ptr()
+    a.B, a.Hq, a.Hkv, a.D = B, Hq, Hkv, D
+    a.block_size, a.num_blocks = bs, nb
+    a.max_blocks_per_seq = block_tables.shape[1]
+    a.max_seq_len = 0 if max_seq_len is None else int(max_seq_len)
+    a.scale = float(scale)
+    a.dtype = _DT[q.dtype]
+    a.splits = int(splits)
+    a.window = int(window)
+    a.q_len = R
+    a.kv_dtype = kv
+    a.k_scale, a.v_scale = (1.0, 1.0) if kv == PA_KV_AS_DTYPE else (float(k_scale), float(v_scale))
+    a.flags = PA_FLAG_DETERMINISTIC if deterministic else 0
+    a.total_tokens = int(total_tokens)
+    return a
 
 
 # One workspace per (device, stream); grown on demand, zero-filled when made. Workspaces that
@@ -307,6 +284,25 @@ def workspace_for(args: DecodeArgs, device: torch.device, stream_handle: int) ->
     return _workspace(need, device, stream_handle)
 
 
+def _call_on(t: torch.Tensor, stream) -> Tuple[int, int]:
+    """(device index, stream handle) of a call on t's device, made current to the library; -1
+    and 0 for a CPU tensor, which the call then refuses."""
+    lib = _lib or load()
+    dev = t.get_device()
+    if dev < 0:
+        return dev, 0
+    _ensure_device(lib, dev)
+    return dev, _stream_of(dev, stream)
+
+
+def _rows_workspace(t: torch.Tensor, dev: int, sh: int) -> Optional[torch.Tensor]:
+    """The workspace whose error word append and gather use: any of the stream's."""
+    ws = _workspaces.get((dev, sh))
+    if ws is None and dev >= 0:
+        ws = _workspace(PA_WORKSPACE_HEADER_BYTES, t.device, sh)
+    return ws
+
+
 def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
            block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
            out: Optional[torch.Tensor] = None, max_seq_len: Optional[int] = None,
@@ -328,18 +324,16 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     split plan for batches of mixed lengths. Asynchronous on the current (or given)
     stream.
     """
-    lib = _lib or load()
-    if out is None:
-        out = torch.empty_like(q)
-    dev, args = _decode_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale, max_seq_len,
-                             splits, window, k_scale, v_scale, deterministic, total_tokens)
-    _ensure_device(lib, dev)
-    sh = _stream_of(dev, stream)
+    dev, sh = _call_on(q, stream)
     ws = workspace if workspace is not None else _workspaces.get((dev, sh))
-    rc = PA_ERR_WORKSPACE if ws is None else lib.pa_decode_ex(args, ws.data_ptr(), ws.numel(), sh)
+    rc, out = _native.decode(q, k_cache, v_cache, block_tables, seq_lens, scale, out, max_seq_len,
+                             splits, window, k_scale, v_scale, deterministic, total_tokens, ws, sh)
     if rc == PA_ERR_WORKSPACE and workspace is None:  # none yet, or too small: nothing was launched
-        ws = workspace_for(DecodeArgs.from_buffer_copy(args), q.device, sh)
-        rc = lib.pa_decode_ex(args, ws.data_ptr(), ws.numel(), sh)
+        ws = workspace_for(make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale,
+                                     max_seq_len, splits, window, k_scale, v_scale, deterministic,
+                                     total_tokens), q.device, sh)
+        rc, out = _native.decode(q, k_cache, v_cache, block_tables, seq_lens, scale, out, max_seq_len,
+                                 splits, window, k_scale, v_scale, deterministic, total_tokens, ws, sh)
     if rc != PA_OK:
         raise PAError(rc, "pa_decode_ex")
     return out
@@ -392,6 +386,7 @@ class Rope(NamedTuple):
     amplitude: float = 1.0
 
 
+_NO_ROPE = (None, False, 1.0)
 _ROPE_KINDS = {"linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
 
 
@@ -416,32 +411,6 @@ def rope(rot_dim: int, base: float = 10000.0, interleaved: bool = False,
     return Rope(turns.to(device), bool(interleaved), amp.value)
 
 
-def _row_stride(name, t, shape) -> int:
-    """Elements between the rows of a [B, H, D], [B, R, H, D] or packed [rows, H, D] tensor,
-    whose heads are dense and whose rows are evenly spaced."""
-    st = t.stride()
-    H, D = shape[-2:]
-    if (st[-1] != 1 or (H > 1 and st[-2] != D)) and t.numel():
-        raise ValueError(f"the heads of a row of {name} must be contiguous")
-    if len(shape) == 3 or shape[1] == 1:
-        return st[0] if shape[0] > 1 else H * D
-    if shape[0] > 1 and st[0] != shape[1] * st[1]:
-        raise ValueError(f"the rows of {name} must be evenly spaced")
-    return st[1]
-
-
-def _tables(block_tables, seq_lens, starts):
-    """(B, table width) of a call's index tensors."""
-    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32 or \
-            (starts is not None and starts.dtype != torch.int32):
-        raise TypeError("block_tables, seq_lens and starts must be int32")
-    bts, sls = block_tables.shape, seq_lens.shape
-    if len(sls) != 1 or len(bts) != 2 or bts[0] != sls[0] or \
-            (starts is not None and starts.shape != (sls[0] + 1,)):
-        raise ValueError("block_tables must be [B, max_blocks], seq_lens [B] and starts [B + 1]")
-    return bts
-
-
 def append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
            block_tables: torch.Tensor, seq_lens: torch.Tensor,
            q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
@@ -460,60 +429,11 @@ def append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     (v_scale). q_out must be contiguous and may be q itself when that is contiguous.
     Asynchronous on the current (or given) stream.
     """
-    lib = _lib or load()
-    dtype, shape = _DT.get(k.dtype), k.shape
-    if dtype is None or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
-        raise TypeError("q, k and v must be float16 or bfloat16, all the same")
-    kv, nb, bs, Hkv, D = _cache_shape(k_cache, v_cache, k.dtype)
-    B, width = _tables(block_tables, seq_lens, starts)
-    packed = starts is not None
-    if len(shape) != 3 and (packed or len(shape) != 4) or (not packed and shape[0] != B):
-        raise ValueError("k must be [B, Hkv, D] or [B, R, Hkv, D], or [rows, Hkv, D] with starts")
-    if v.shape != shape or shape[-2] != Hkv or shape[-1] != D:
-        raise ValueError("k and v must have one shape ending in the caches' [Hkv, D]")
-    dev = k.get_device()
-    dense = [("k_cache", k_cache), ("v_cache", v_cache), ("block_tables", block_tables),
-             ("seq_lens", seq_lens)]
-    if k.get_device() != v.get_device() or (q is not None and q.get_device() != dev):
-        raise ValueError("q, k and v must be CUDA tensors on one device (no CPU path)")
-    qp = qop = Hq = q_stride = 0
-    if q is not None:
-        qs = q.shape
-        if len(qs) != len(shape) or qs[:-2] != shape[:-2] or qs[-1] != D:
-            raise ValueError("q must have k's rows and head_dim")
-        if q_out is None:
-            q_out = torch.empty(qs, dtype=q.dtype, device=q.device)
-        elif q_out.shape != qs or q_out.dtype != q.dtype:
-            raise ValueError("q_out must have q's shape and dtype")
-        q_stride, Hq = _row_stride("q", q, qs), qs[-2]
-        qp, qop = q.data_ptr(), q_out.data_ptr()
-        dense.append(("q_out", q_out))
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    tp = rot = interleaved = 0
-    amplitude = 1.0
-    if rope is not None:
-        turns, interleaved, amplitude = rope
-        if turns.dtype != torch.int64 or turns.dim() != 1:
-            raise TypeError("rope.turns must be int64 [rot_dim / 2]")
-        tp, rot = turns.data_ptr(), 2 * turns.shape[0]
-        dense.append(("rope.turns", turns))
-    if packed:
-        dense.append(("starts", starts))
-    _where(k, dense)
-    args = _pack(
-        _APPEND, qp, qop, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        block_tables.data_ptr(), seq_lens.data_ptr(), starts.data_ptr() if packed else 0, tp,
-        q_stride, _row_stride("k", k, shape), _row_stride("v", v, shape), B,
-        shape[0] if packed else (1 if len(shape) == 3 else shape[1]), Hq, Hkv, D, bs, nb, width,
-        dtype, kv, float(k_scale), float(v_scale), rot,
-        PA_ROPE_INTERLEAVED if interleaved else PA_ROPE_HALF, float(amplitude))
-    _ensure_device(lib, dev)
-    sh = _stream_of(dev, stream)
-    ws = workspace if workspace is not None else _workspaces.get((dev, sh))
-    if ws is None:
-        ws = _workspace(PA_WORKSPACE_HEADER_BYTES, k_cache.device, sh)
-    rc = lib.pa_append(args, ws.data_ptr(), ws.numel(), sh)
+    dev, sh = _call_on(k_cache, stream)
+    turns, interleaved, amplitude = _NO_ROPE if rope is None else rope
+    ws = workspace if workspace is not None else _rows_workspace(k_cache, dev, sh)
+    rc, q_out = _native.append(k, v, k_cache, v_cache, block_tables, seq_lens, q, q_out, starts,
+                               turns, interleaved, amplitude, k_scale, v_scale, ws, sh)
     if rc != PA_OK:
         raise PAError(rc, "pa_append")
     return q_out
@@ -532,39 +452,15 @@ def gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Ten
     Keys stay rotated. dtype is that of the rows (float16 or bfloat16; needed for fp8 and 4-bit
     caches, whose values are multiplied by k_scale, v_scale). A row without a token is zero.
     """
-    lib = _lib or load()
+    dev, sh = _call_on(k_cache, stream)
     if dtype is None:
         dtype = k_out.dtype if k_out is not None else k_cache.dtype
     code = _DT.get(dtype)
     if code is None:
         raise TypeError("dtype must be float16 or bfloat16")
-    kv, nb, bs, Hkv, D = _cache_shape(k_cache, v_cache, dtype)
-    B, width = _tables(block_tables, seq_lens, starts)
-    if rows < 0:
-        raise ValueError("rows must not be negative")
-    shape = (B, rows, Hkv, D) if starts is None else (rows, Hkv, D)
-    dense = [("k_cache", k_cache), ("v_cache", v_cache), ("block_tables", block_tables),
-             ("seq_lens", seq_lens)]
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
-    if k_out.shape != shape or v_out.shape != shape or k_out.dtype != dtype or v_out.dtype != dtype:
-        raise ValueError(f"k_out and v_out must be {dtype} {list(shape)}")
-    dense += [("k_out", k_out), ("v_out", v_out)]
-    if starts is not None:
-        dense.append(("starts", starts))
-    dev = _where(k_cache, dense)
-    args = _pack(
-        _GATHER, k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-        seq_lens.data_ptr(), starts.data_ptr() if starts is not None else 0, k_out.data_ptr(),
-        v_out.data_ptr(), B, rows, Hkv, D, bs, nb, width, code, kv, float(k_scale), float(v_scale))
-    _ensure_device(lib, dev)
-    sh = _stream_of(dev, stream)
-    ws = workspace if workspace is not None else _workspaces.get((dev, sh))
-    if ws is None:
-        ws = _workspace(PA_WORKSPACE_HEADER_BYTES, k_cache.device, sh)
-    rc = lib.pa_gather(args, ws.data_ptr(), ws.numel(), sh)
+    ws = workspace if workspace is not None else _rows_workspace(k_cache, dev, sh)
+    rc, k_out, v_out = _native.gather(k_cache, v_cache, block_tables, seq_lens, rows, starts, code,
+                                      k_out, v_out, k_scale, v_scale, ws, sh)
     if rc != PA_OK:
         raise PAError(rc, "pa_gather")
     return k_out, v_out

@@ -1,9 +1,11 @@
-"""Build libpa.so in-tree with nvcc for sm_103a (GB300).
+"""Build libpa.so and the Python binding's module in-tree, with nvcc for sm_103a (GB300).
 
 Each .cu under csrc/ compiles to an object in parallel, then nvcc links them into
 paged_kv_attention_pa_gb300/libpa.so with the CUDA runtime linked statically, so
 the library loads without a GPU driver present (the entry points that need a GPU
-return PA_ERR_CUDA there).
+return PA_ERR_CUDA there). csrc/binding.cpp, the CPython module that fills the library's
+arguments from torch tensors, compiles beside them into _binding.so, linked to libpa.so
+next to it and to the torch it is built with.
 
     python -m paged_kv_attention_pa_gb300.build [--force] [--verbose]
 """
@@ -21,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpa.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -46,7 +50,8 @@ def _headers():
 
 
 def _arch_tag() -> str:
-    return os.uname().machine
+    import torch
+    return f"{os.uname().machine} {sys.version_info[0]}.{sys.version_info[1]} torch {torch.__version__}"
 
 
 def _stamp_path() -> str:
@@ -54,13 +59,13 @@ def _stamp_path() -> str:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(_stamp_path()):
+    if not all(os.path.exists(f) for f in (LIB, BINDING, _stamp_path())):
         return False
     with open(_stamp_path()) as f:
         if f.read().strip() != _arch_tag():
             return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(s) <= t for s in _sources() + _headers() + [__file__])
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    return all(os.path.getmtime(s) <= t for s in _sources() + _headers() + [BINDING_SRC, __file__])
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -74,6 +79,40 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_binding(verbose: bool) -> str:
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD_DIR, "binding.o")
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
+           "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-c", BINDING_SRC, "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str, verbose: bool) -> None:
+    import torch
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-shared", "-o", tmp, obj,
+           "-L" + PKG, "-l:libpa.so", "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link libpa.so if needed; returns its path."""
     if not force and up_to_date():
@@ -82,16 +121,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
     srcs = _sources()
     workers = max(1, min(len(srcs), os.cpu_count() or 1))
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:
+        binding = ex.submit(_compile_binding, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        binding_obj = binding.result()
     tmp = LIB + ".tmp"
-    cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs + \
-        ["-lpthread", "-ldl", "-lrt"]
+    cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-Xlinker", "-soname=libpa.so",
+                             "-o", tmp] + objs + ["-lpthread", "-ldl", "-lrt"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj, verbose)
     with open(_stamp_path(), "w") as f:
         f.write(_arch_tag())
     return LIB
