@@ -44,10 +44,10 @@ constexpr int64_t kSplitOverheadBytes = PA_SPLIT_OVERHEAD_BYTES;
 #define PA_PLAN_BALANCED 1
 #endif
 
-bool plan_for(int64_t S_req, int64_t max_len, int64_t p_max, bool floor_p, int64_t quantum,
+bool plan_for(int64_t S_req, int64_t max_len, int64_t p_max, int64_t p_min, int64_t quantum,
               Plan* out) {
   int64_t P = round_up(ceil_div(max_len, std::max<int64_t>(S_req, 1)), quantum);
-  if (floor_p) P = std::max<int64_t>(P, pa::kPartitionMin);
+  P = std::max<int64_t>(P, p_min);
   P = std::min(P, p_max);
   int64_t S = ceil_div(max_len, P);
   if (S > pa::kMaxSplits) {
@@ -69,11 +69,21 @@ bool make_plan(int sm_count, int64_t B, int64_t Hkv, int D, pa::KvKind kv, int64
   const int64_t units = B * Hkv;
   const int64_t sm = sm_count > 0 ? sm_count : 1;
   const int64_t p_max = round_up(max_len, quantum);
-  if (requested > 0) return plan_for(requested, max_len, p_max, false, quantum, out);
+  if (requested > 0) return plan_for(requested, max_len, p_max, 0, quantum, out);
   bool found = false;
   int64_t best_cost = 0;
-  const int64_t cands[9] = {1, sm / units, 2 * sm / units, 3 * sm / units, 4 * sm / units,
-                            ceil_div(sm, units), 2, 3, 4};
+  // 4-bit splits are short (a token is a third of a 16-bit one's bytes), and one-wave grids
+  // that leave an SM in six free end sooner where their length hardly matters: the merge grid
+  // and the next call's CTAs find room (GB300, us per call: one sequence, 8 KV heads, 8K tokens
+  // 7.4 for 128 CTAs against 8.7 for 152; hybrid layer, 8K 8.6 for 128 against 9.4 for 148, 32K
+  // 14.0 against 14.3). So that grid is tried too, and a split one-wave grid beyond it is
+  // charged the difference. Splits below 128 tokens lose (hybrid layer, 2K tokens: 7.6 for 64
+  // tokens a split, 6.6 for 128; 8 heads, 512 tokens: 5.0 and 4.8).
+  const bool int4 = kv == pa::kKvInt4;
+  const int64_t roomy = sm * 27 / 32;
+  const int64_t p_min = int4 ? 2 * pa::kPartitionMin : pa::kPartitionMin;
+  const int64_t cands[10] = {1, sm / units, 2 * sm / units, 3 * sm / units, 4 * sm / units,
+                             ceil_div(sm, units), 2, 3, 4, int4 ? roomy / units : 0};
   // CTAs with tokens to stream: every split of every pair when the lengths are
   // unknown (all taken as max_len); given the batch's total context tokens, the
   // splits past each sequence's end are estimated away (a sequence's last split
@@ -94,7 +104,8 @@ bool make_plan(int sm_count, int64_t B, int64_t Hkv, int D, pa::KvKind kv, int64
     const int64_t waves = ceil_div(live_ctas(pl), sm);
     // the fixed cost in tokens of this cache: K + V bytes per token per KV head
     const int64_t overhead_tokens = kSplitOverheadBytes / (2 * pa::kv_row_bytes(D, kv));
-    const int64_t cost = waves * (round_up(pl.P, round_tokens) + overhead_tokens);
+    int64_t cost = waves * (round_up(pl.P, round_tokens) + overhead_tokens);
+    if (int4 && pl.S > 1 && waves == 1 && live_ctas(pl) > roomy) cost += 100 * 1024 / (2 * pa::kv_row_bytes(D, kv));
     if (!found || cost < best_cost || (cost == best_cost && pl.S < out->S)) {
       *out = pl;
       best_cost = cost;
@@ -104,7 +115,7 @@ bool make_plan(int sm_count, int64_t B, int64_t Hkv, int D, pa::KvKind kv, int64
   for (int64_t c : cands) {
     if (c < 1) continue;
     Plan pl{};
-    if (!plan_for(c, max_len, p_max, true, quantum, &pl)) continue;
+    if (!plan_for(c, max_len, p_max, p_min, quantum, &pl)) continue;
     consider(pl);
     const int64_t pr = std::min(round_up(pl.P, round_tokens), p_max);
     if (pr != pl.P) consider(Plan{(int)ceil_div(max_len, pr), (int)pr});
