@@ -38,14 +38,16 @@ struct Int4Cfg {
   static constexpr int TILE_BYTES = TW * ROWB;
   static constexpr int SLOT_BYTES = 2 * TILE_BYTES;  // K, then V
   static constexpr bool BULK = D == 256 ? PA_I4_BULK_D256 : PA_I4_BULK_D128;
-  static constexpr int FIXED = 1024;  // the slots' mbarriers (bulk copies)
+  static constexpr bool QSHARED = NT >= PA_I4_QSHARED;  // query fragments in shared memory
+  static constexpr int QBYTES = QSHARED ? NT * KS * 256 : 0;
+  static constexpr int FIXED = 1024 + QBYTES;  // the slots' mbarriers (bulk copies), the query
   static constexpr int DEPTH_FIT = (kSmemBudget - FIXED) / (NW * SLOT_BYTES);
   static constexpr int DEPTH = DEPTH_FIT > 5 ? 5 : DEPTH_FIT;  // slots per warp
   static constexpr int WARP_RING = DEPTH * SLOT_BYTES;
   static constexpr int RING = NW * WARP_RING;
   static constexpr int SMEM = RING + FIXED;
   static_assert(TW == 32 && (TW * CPR) % 32 == 0, "tile shape");
-  static_assert(DEPTH >= 2 && NW * DEPTH * 8 <= FIXED, "two slots at least, an mbarrier each");
+  static_assert(DEPTH >= 2 && NW * DEPTH * 8 <= 1024, "two slots at least, an mbarrier each");
 };
 
 template <typename T, int D, int NT, bool WIN>
@@ -276,6 +278,27 @@ __global__ void __launch_bounds__(Int4Cfg<D, NT>::THREADS, 1) decode_int4_kernel
 #pragma unroll
     for (int h = 0; h < 2; ++h) lim[nt][h] = L - R + (nt * 8 + 2 * tig + h) / G + 1;
 
+  Int4Query<D, NT, C::QSHARED> query;
+  if constexpr (C::QSHARED) {  // every warp holds the same fragments: the first one's are kept
+    query.at = smem_addr(smem) + C::RING + 1024 + 8 * lane;
+    if (warp == 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int kk = 0; kk < C::KS; ++kk)
+          sts64(query.at + (nt * C::KS + kk) * 256, qf[nt][kk][0], qf[nt][kk][1]);
+    }
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int kk = 0; kk < C::KS; ++kk) {
+        query.r[nt][kk][0] = qf[nt][kk][0];
+        query.r[nt][kk][1] = qf[nt][kk][1];
+      }
+  }
+
   // running state: this thread's columns are nt*8 + 2*tig + {0, 1}
   float m[NT][2], l[NT][2];
   float ref[NT][2];  // m, or 0 before the first token
@@ -330,9 +353,7 @@ __global__ void __launch_bounds__(Int4Cfg<D, NT>::THREADS, 1) decode_int4_kernel
 
       // ---- scores S^T[token][column], in two parts
       float s[MT][NT][4], sm[MT][NT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-        int4_scores<D, NT>(s[mt], sm[mt], kt + 16 * mt * C::ROWB, qf, qs, gid, tig);
+      int4_scores<D, NT, MT, C::QSHARED>(s, sm, kt, query, qs, gid, tig);
       // ---- online softmax over the tile; -inf by select past each column's limit
       float x[NT][MT][4];
       float mx[NT][2];

@@ -165,49 +165,72 @@ __device__ __forceinline__ float int4_query(uint32_t (&qf)[D / 16][2], uint32_t 
   return down;
 }
 
-// Scores of the 16 tokens at `rows` (their first row in shared memory) with NT column
-// tiles: s[nt] = sum_g step_g (q . n) * 2^-24 and sm[nt] = sum_g minimum_g (sum of q).
-template <int D, int NT>
-__device__ __forceinline__ void int4_scores(float (&s)[NT][4], float (&sm)[NT][4], uint32_t rows,
-                                            const uint32_t (&qf)[NT][D / 16][2],
+// The query fragments of a CTA's columns: in registers, or (SHARED) in shared memory as eight
+// bytes per column tile, k-step and lane, where the registers serve more warps better.
+template <int D, int NT, bool SHARED>
+struct Int4Query {
+  uint32_t r[SHARED ? 1 : NT][SHARED ? 1 : D / 16][2];
+  uint32_t at;  // SHARED: this lane's words of the first fragment
+  __device__ __forceinline__ uint2 operator()(int nt, int ks) const {
+    if constexpr (SHARED) return lds64(at + (nt * (D / 16) + ks) * 256);
+    return make_uint2(r[nt][ks][0], r[nt][ks][1]);
+  }
+};
+
+// Scores of 16 MT tokens from `rows` (their first row in shared memory) with NT column tiles:
+// s[mt][nt] = sum_g step_g (q . n) * 2^-24 and sm[mt][nt] = sum_g minimum_g (sum of q).
+template <int D, int NT, int MT, bool SHARED>
+__device__ __forceinline__ void int4_scores(float (&s)[MT][NT][4], float (&sm)[MT][NT][4], uint32_t rows,
+                                            const Int4Query<D, NT, SHARED>& q,
                                             const uint32_t (&qs)[NT][2], int gid, int tig) {
   using R = Int4Row<D>;
-  const uint32_t r0 = rows + int4_row_of(gid) * R::BYTES, r1 = r0 + 8 * R::BYTES;
-  uint4 k0[R::W], k1[R::W];
+  uint4 k0[MT][R::W], k1[MT][R::W];
+  uint32_t st0[MT][R::G / 2], st1[MT][R::G / 2];
 #pragma unroll
-  for (int i = 0; i < R::W; ++i) {
-    k0[i] = lds128(r0 + 16 * R::W * tig + 16 * i);
-    k1[i] = lds128(r1 + 16 * R::W * tig + 16 * i);
-  }
-  uint32_t st0[R::G / 2], st1[R::G / 2];
-  int4_meta<D>(st0, r0, R::CODES);
-  int4_meta<D>(st1, r1, R::CODES);
-  {
+  for (int mt = 0; mt < MT; ++mt) {
+    const uint32_t r0 = rows + (16 * mt + int4_row_of(gid)) * R::BYTES, r1 = r0 + 8 * R::BYTES;
+#pragma unroll
+    for (int i = 0; i < R::W; ++i) {
+      k0[mt][i] = lds128(r0 + 16 * R::W * tig + 16 * i);
+      k1[mt][i] = lds128(r1 + 16 * R::W * tig + 16 * i);
+    }
+    int4_meta<D>(st0[mt], r0, R::CODES);
+    int4_meta<D>(st1[mt], r1, R::CODES);
     uint32_t a[4];
     a[0] = lds32(r0 + R::MINS + 4 * (tig & (R::G / 2 - 1)));
     a[1] = lds32(r1 + R::MINS + 4 * (tig & (R::G / 2 - 1)));
     a[2] = a[0];
     a[3] = a[1];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) mma16816_zero(sm[nt], a, qs[nt][0], qs[nt][1]);
+    for (int nt = 0; nt < NT; ++nt) mma16816_zero(sm[mt][nt], a, qs[nt][0], qs[nt][1]);
   }
 #pragma unroll
   for (int g = 0; g < R::G; ++g) {
-    const uint32_t w0 = word_of(k0[g / 4], g % 4), w1 = word_of(k1[g / 4], g % 4);
-    const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
-    const uint32_t a0[4] = {w0 & R::LO, w1 & R::LO, h0 & R::LO, h1 & R::LO};
-    const uint32_t a1[4] = {w0 & R::HI, w1 & R::HI, h0 & R::HI, h1 & R::HI};
-    const float2 u0 = unpack2<__half>(st0[g / 2]), u1 = unpack2<__half>(st1[g / 2]);
-    const float f0 = (g & 1) ? u0.y : u0.x, f1 = (g & 1) ? u1.y : u1.x;
+    uint2 b0[NT], b1[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float acc[4];
-      mma16816_zero(acc, a0, qf[nt][2 * g][0], qf[nt][2 * g][1]);
-      mma16816<__half>(acc, a1, qf[nt][2 * g + 1][0], qf[nt][2 * g + 1][1]);
-      s[nt][0] = g == 0 ? f0 * acc[0] : fmaf(f0, acc[0], s[nt][0]);
-      s[nt][1] = g == 0 ? f0 * acc[1] : fmaf(f0, acc[1], s[nt][1]);
-      s[nt][2] = g == 0 ? f1 * acc[2] : fmaf(f1, acc[2], s[nt][2]);
-      s[nt][3] = g == 0 ? f1 * acc[3] : fmaf(f1, acc[3], s[nt][3]);
+      b0[nt] = q(nt, 2 * g);
+      b1[nt] = q(nt, 2 * g + 1);
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const uint32_t w0 = word_of(k0[mt][g / 4], g % 4), w1 = word_of(k1[mt][g / 4], g % 4);
+      const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
+      const uint32_t a0[4] = {w0 & R::LO, w1 & R::LO, h0 & R::LO, h1 & R::LO};
+      const uint32_t a1[4] = {w0 & R::HI, w1 & R::HI, h0 & R::HI, h1 & R::HI};
+      const float2 u0 = unpack2<__half>(st0[mt][g / 2]), u1 = unpack2<__half>(st1[mt][g / 2]);
+      const float f0 = (g & 1) ? u0.y : u0.x, f1 = (g & 1) ? u1.y : u1.x;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float acc[4];
+        mma16816_zero(acc, a0, b0[nt].x, b0[nt].y);
+        mma16816<__half>(acc, a1, b1[nt].x, b1[nt].y);
+        float(&d)[4] = s[mt][nt];
+        d[0] = g == 0 ? f0 * acc[0] : fmaf(f0, acc[0], d[0]);
+        d[1] = g == 0 ? f0 * acc[1] : fmaf(f0, acc[1], d[1]);
+        d[2] = g == 0 ? f1 * acc[2] : fmaf(f1, acc[2], d[2]);
+        d[3] = g == 0 ? f1 * acc[3] : fmaf(f1, acc[3], d[3]);
+      }
     }
   }
 }

@@ -64,17 +64,23 @@ __host__ __device__ constexpr int tile_tokens(int D, KvKind kind) {
 #ifndef PA_WARPS_I4_D128
 #define PA_WARPS_I4_D128 12
 #endif
-#ifndef PA_WARPS_I4_WIDE
+#ifndef PA_WARPS_I4_WIDE  // more than 8 columns
 #define PA_WARPS_I4_WIDE 8
 #endif
 #ifndef PA_WARPS_I4_D256
 #define PA_WARPS_I4_D256 8
 #endif
 __host__ __device__ constexpr int warps_per_cta(int D, KvKind kind, int column_tiles = 1) {
-  return kind == kKvInt4  ? (column_tiles > 2 || (column_tiles > 1 && D > 128) ? 8 : column_tiles > 1 ? PA_WARPS_I4_WIDE : D == 128 ? PA_WARPS_I4_D128 : PA_WARPS_I4_D256)
+  return kind == kKvInt4  ? (column_tiles > 1 ? PA_WARPS_I4_WIDE : D == 128 ? PA_WARPS_I4_D128 : PA_WARPS_I4_D256)
          : kind == kKvFp8 ? (D == 128 ? PA_WARPS_F8_D128 : PA_WARPS_F8_D256)
                           : (D == 128 ? PA_WARPS_D128 : PA_WARPS_D256);
 }
+// 4-bit caches: from this many column tiles on, the query fragments live in shared memory
+// (GB300, 8 sequences of 16K tokens, 32/8 heads, us per call in registers / shared: 8 query
+// rows, four column tiles, 191 / 132; 4 rows, two tiles, 55.3 / 56.0; one row 36.3 / 36.6).
+#ifndef PA_I4_QSHARED
+#define PA_I4_QSHARED 4
+#endif
 // 4-bit caches: bulk copies (one per block and tile) or 16-byte cp.async.
 #ifndef PA_I4_BULK_D128
 #define PA_I4_BULK_D128 0
