@@ -260,28 +260,34 @@ def make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale: float,
 
 # One workspace per (device, stream); grown on demand, zero-filled when made. Workspaces that
 # were outgrown stay allocated: a captured graph may still write to them when it is replayed.
-# Graphs that may be replayed at the same time need workspaces of their own.
+# One made while its stream is captured belongs to that graph alone.
 _workspaces = {}
 _outgrown = []
 
 
-def _workspace(need: int, device: torch.device, stream_handle: int) -> torch.Tensor:
+def _workspace(need: int, device: torch.device, stream_handle: int, stream=None) -> torch.Tensor:
     key = (device.index, stream_handle)
     ws = _workspaces.get(key)
-    if ws is None or ws.numel() < need:
-        if ws is not None:
-            _outgrown.append(ws)
-            need = max(need, 2 * ws.numel())
-        ws = torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
-        _workspaces[key] = ws
-    return ws
+    if ws is not None and ws.numel() >= need:
+        return ws
+    if ws is not None:
+        need = max(need, 2 * ws.numel())
+    with torch.cuda.stream(stream):  # zeroed in the order of the call's stream
+        new = torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
+        if torch.cuda.is_current_stream_capturing():
+            return new  # the graph's own, zeroed at every replay: of no use to calls outside it
+    if ws is not None:
+        _outgrown.append(ws)
+    _workspaces[key] = new
+    return new
 
 
-def workspace_for(args: DecodeArgs, device: torch.device, stream_handle: int) -> torch.Tensor:
+def workspace_for(args: DecodeArgs, device: torch.device, stream_handle: int,
+                  stream=None) -> torch.Tensor:
     need = load().pa_decode_ex_workspace_bytes(ctypes.byref(args))
     if need == 0:
         raise PAError(PA_ERR_INVALID_ARG, "pa_decode_ex_workspace_bytes")
-    return _workspace(need, device, stream_handle)
+    return _workspace(need, device, stream_handle, stream)
 
 
 def _call_on(t: torch.Tensor, stream) -> Tuple[int, int]:
@@ -295,12 +301,20 @@ def _call_on(t: torch.Tensor, stream) -> Tuple[int, int]:
     return dev, _stream_of(dev, stream)
 
 
-def _rows_workspace(t: torch.Tensor, dev: int, sh: int) -> Optional[torch.Tensor]:
+def _rows_workspace(t: torch.Tensor, dev: int, sh: int, stream) -> Optional[torch.Tensor]:
     """The workspace whose error word append and gather use: any of the stream's."""
     ws = _workspaces.get((dev, sh))
     if ws is None and dev >= 0:
-        ws = _workspace(PA_WORKSPACE_HEADER_BYTES, t.device, sh)
+        ws = _workspace(PA_WORKSPACE_HEADER_BYTES, t.device, sh, stream)
     return ws
+
+
+def _made_here(out: torch.Tensor, given, stream) -> torch.Tensor:
+    """An output; one that this call allocated is not reused before a stream of the caller's
+    is done with it."""
+    if stream is not None and given is None and out is not None:
+        out.record_stream(stream)
+    return out
 
 
 def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -322,8 +336,10 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     share out its tail as they finish, and the last bit may vary from call to call).
     total_tokens, the sum of seq_lens when the caller knows it on the host, helps the
     split plan for batches of mixed lengths. Asynchronous on the current (or given)
-    stream.
+    stream. Without `workspace` the call uses the one kept for its device and stream: graphs
+    captured on one stream that may be replayed at the same time need workspaces of their own.
     """
+    given = out
     dev, sh = _call_on(q, stream)
     ws = workspace if workspace is not None else _workspaces.get((dev, sh))
     rc, out = _native.decode(q, k_cache, v_cache, block_tables, seq_lens, scale, out, max_seq_len,
@@ -331,12 +347,12 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     if rc == PA_ERR_WORKSPACE and workspace is None:  # none yet, or too small: nothing was launched
         ws = workspace_for(make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale,
                                      max_seq_len, splits, window, k_scale, v_scale, deterministic,
-                                     total_tokens), q.device, sh)
+                                     total_tokens), q.device, sh, stream)
         rc, out = _native.decode(q, k_cache, v_cache, block_tables, seq_lens, scale, out, max_seq_len,
                                  splits, window, k_scale, v_scale, deterministic, total_tokens, ws, sh)
     if rc != PA_OK:
         raise PAError(rc, "pa_decode_ex")
-    return out
+    return _made_here(out, given, stream)
 
 
 def decode_plain(q, k_cache, v_cache, block_tables, seq_lens, scale, out=None,
@@ -348,7 +364,7 @@ def decode_plain(q, k_cache, v_cache, block_tables, seq_lens, scale, out=None,
     args = make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale, max_seq_len, 0)
     _ensure_device(lib, q.device.index)
     sh = _stream_handle(q.device, stream)
-    ws = workspace if workspace is not None else workspace_for(args, q.device, sh)
+    ws = workspace if workspace is not None else workspace_for(args, q.device, sh, stream)
     rc = lib.pa_decode(args.q, args.k_cache, args.v_cache, args.block_tables, args.seq_lens,
                        args.out, args.B, args.Hq, args.Hkv, args.D, args.block_size,
                        args.num_blocks, args.max_blocks_per_seq, args.max_seq_len,
@@ -431,12 +447,12 @@ def append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     """
     dev, sh = _call_on(k_cache, stream)
     turns, interleaved, amplitude = _NO_ROPE if rope is None else rope
-    ws = workspace if workspace is not None else _rows_workspace(k_cache, dev, sh)
-    rc, q_out = _native.append(k, v, k_cache, v_cache, block_tables, seq_lens, q, q_out, starts,
-                               turns, interleaved, amplitude, k_scale, v_scale, ws, sh)
+    ws = workspace if workspace is not None else _rows_workspace(k_cache, dev, sh, stream)
+    rc, rotated = _native.append(k, v, k_cache, v_cache, block_tables, seq_lens, q, q_out, starts,
+                                 turns, interleaved, amplitude, k_scale, v_scale, ws, sh)
     if rc != PA_OK:
         raise PAError(rc, "pa_append")
-    return q_out
+    return _made_here(rotated, q_out, stream)
 
 
 def gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -458,12 +474,12 @@ def gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Ten
     code = _DT.get(dtype)
     if code is None:
         raise TypeError("dtype must be float16 or bfloat16")
-    ws = workspace if workspace is not None else _rows_workspace(k_cache, dev, sh)
-    rc, k_out, v_out = _native.gather(k_cache, v_cache, block_tables, seq_lens, rows, starts, code,
-                                      k_out, v_out, k_scale, v_scale, ws, sh)
+    ws = workspace if workspace is not None else _rows_workspace(k_cache, dev, sh, stream)
+    rc, k, v = _native.gather(k_cache, v_cache, block_tables, seq_lens, rows, starts, code, k_out,
+                              v_out, k_scale, v_scale, ws, sh)
     if rc != PA_OK:
         raise PAError(rc, "pa_gather")
-    return k_out, v_out
+    return _made_here(k, k_out, stream), _made_here(v, v_out, stream)
 
 
 def plan(B: int, Hq: int, Hkv: int, D: int, block_size: int, max_seq_len: int,

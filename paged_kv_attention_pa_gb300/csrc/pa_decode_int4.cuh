@@ -38,7 +38,8 @@ struct Int4Cfg {
   static constexpr int TILE_BYTES = TW * ROWB;
   static constexpr int SLOT_BYTES = 2 * TILE_BYTES;  // K, then V
   static constexpr bool BULK = D == 256 ? PA_I4_BULK_D256 : PA_I4_BULK_D128;
-  static constexpr bool QSHARED = NT >= PA_I4_QSHARED;  // query fragments in shared memory
+  static constexpr bool QSHARED = NT >= PA_I4_QSHARED || (NT == 1 && D == 128);  // query fragments
+                                                                                 // in shared memory
   static constexpr int QBYTES = QSHARED ? NT * KS * 256 : 0;
   static constexpr int FIXED = 1024 + QBYTES;  // the slots' mbarriers (bulk copies), the query
   static constexpr int DEPTH_FIT = (kSmemBudget - FIXED) / (NW * SLOT_BYTES);

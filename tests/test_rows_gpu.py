@@ -443,3 +443,44 @@ def test_python_refusals(cuda_lib):
         cuda_lib.gather(kc, vc, bt, lens, -1)
     with pytest.raises(ValueError):
         cuda_lib.gather(kc, vc, bt, lens, 2, k_out=torch.empty(2, 3, 2, 128, device="cuda").bfloat16())
+
+
+def test_first_call_in_a_capture_and_given_streams(cuda_lib):
+    # a stream whose first call is captured: the workspace made there stays the graph's, and a
+    # later call outside it starts from one of its own; and calls on a given stream
+    x = make([33, 50], None, 2, 4, 2, 128, 16, "bf16", "int4", seed=30)
+    rope, f, amp = rope_of(cuda_lib, 128)
+    ks, vs = SCALES["int4"]
+    s = torch.cuda.Stream()
+    qkv, kc, vc, bt, lens = x["qkv"].cuda(), x["kc"].cuda(), x["vc"].cuda(), x["bt"].cuda(), i32(x["lens"])
+    q, k, v = views(x, qkv)
+    dq = torch.randn((2, 4, 128), device="cuda").bfloat16()
+    long_bt = bt.repeat(1, 40)     # 2560 tokens of repeated blocks: several splits
+    long_lens = torch.tensor([2500, 1900], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        qo = cuda_lib.append(k, v, kc, vc, bt, lens, q=q, rope=rope, k_scale=ks, v_scale=vs)
+        out = cuda_lib.decode(dq, kc, vc, long_bt, long_lens, 0.088, max_seq_len=2560, deterministic=True,
+                              k_scale=ks, v_scale=vs)
+    assert cuda_lib.default_workspace(stream=s) is None
+    want_cache = append(cuda_lib, x, rope)
+    want = cuda_lib.decode(dq, want_cache[1], want_cache[2], long_bt, long_lens, 0.088, max_seq_len=2560,
+                           deterministic=True, k_scale=ks, v_scale=vs)
+    for _ in range(2):
+        out.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        check_append(x, f, amp, False, qo, kc, vc)
+        assert torch.equal(rh.bits(out), rh.bits(want))
+    # on the given stream, from another current one
+    got = cuda_lib.decode(dq, kc, vc, long_bt, long_lens, 0.088, max_seq_len=2560, deterministic=True,
+                          k_scale=ks, v_scale=vs, stream=s)
+    gk, gv = cuda_lib.gather(kc, vc, bt, lens, 2, dtype=torch.bfloat16, k_scale=ks, v_scale=vs, stream=s)
+    s.synchronize()
+    assert torch.equal(rh.bits(got), rh.bits(want)) and torch.isfinite(gk).all() and torch.isfinite(gv).all()
+    # (the repeated table holds -1 entries of the shorter sequence: the decode calls report them)
+    assert cuda_lib.read_device_errors(cuda_lib.default_workspace(stream=s), stream=s) == \
+        cuda_lib.PA_DEVERR_BLOCK_INDEX
+    assert cuda_lib.read_device_errors(cuda_lib.default_workspace()) == cuda_lib.PA_DEVERR_BLOCK_INDEX
