@@ -87,15 +87,17 @@ typedef enum pa_kv_dtype {
  * The pages hold head after head: k_cache and v_cache are
  * [num_blocks, Hkv, block_size, PA_INT4_ROW_BYTES(D)], so that a KV head's tokens of a
  * block are contiguous. pa_append writes such rows: the minimum rounded down and the step
- * (a fifteenth of the range above it) rounded up to fp16, and the nearest code. A group
- * that holds a NaN or an infinity reads back as NaN.
+ * (a fifteenth of the range above it) rounded up to fp16, and the nearest code. Values
+ * beyond +-65280 saturate there. A group that holds a NaN or an infinity reads back as NaN.
+ * Rows written otherwise: pa_decode needs steps <= 8734 and minimum + 15 * step below 65520
+ * (what fp16 holds) in the V cache.
  */
 #define PA_INT4_ROW_BYTES(D) ((D) / 8 * 5)
 
 /* Bits of the device error word (workspace header). */
 #define PA_DEVERR_BLOCK_INDEX 1u /* a live token's block table entry was outside [0, num_blocks) */
-#define PA_DEVERR_COPY 4u /* a copy into shared memory did not complete in two seconds: no meaningful output */
 #define PA_DEVERR_SEQ_LEN 2u     /* a seq_len < 0, > max_seq_len or > max_blocks_per_seq*block_size */
+#define PA_DEVERR_COPY 4u        /* a copy into shared memory took over two seconds: no meaningful output */
 
 typedef void* pa_stream_t; /* cudaStream_t */
 
@@ -354,8 +356,7 @@ pa_status pa_rope_turns(int rot_dim, double base, const pa_rope_scaling* scaling
  *   k_cache, v_cache, block_tables, block_size, num_blocks, max_blocks_per_seq, kv_dtype
  *             as for pa_decode; the table entries of the new positions must be filled
  *   k_scale, v_scale  for fp8 and 4-bit caches: the cache holds value / scale (E4M3
- *             saturates at +-448, nearest even; 4 bits: see PA_INT4_ROW_BYTES, whose steps
- *             and minima lie within +-65504)
+ *             saturates at +-448, nearest even; 4 bits: see PA_INT4_ROW_BYTES)
  *   rot_dim   elements of a head that turn: 0 (none) or a multiple of 16 up to D
  * Rotation and quantisation are in fp32, with one rounding to what is stored. A row with
  * an invalid length or table entry is not written to the cache and raises a PA_DEVERR_*

@@ -5,7 +5,8 @@ and a minimum in fp16, per element a code n in 0..15, value = minimum + step * n
 tensor's scale). Bytes: D/2 of codes (32-bit little-endian words of eight; the word of
 elements 32 g + 8 t .. + 7 is word t * (D/32) + g, element j of the eight in bits 4 j), then
 the steps, then the minima. Writing a row rounds the minimum down and the step, a fifteenth
-of the range above the minimum, up, and takes the nearest code (ties to even). A group that
+of the range above the minimum, up, and takes the nearest code (ties to even). Values saturate
+at +-65280, so that every value a row holds rounds to a finite fp16. A group that
 holds a NaN or an infinity has NaN (0x7fff) for both.
 """
 from __future__ import annotations
@@ -52,8 +53,7 @@ def dequant(rows: np.ndarray, scale: float = 1.0) -> np.ndarray:
 
 
 def _half(x: np.ndarray, up: bool) -> np.ndarray:
-    """x rounded up (down) to fp16, within fp16's finite range."""
-    x = np.clip(x, -65504.0, 65504.0)
+    """x rounded up (down) to fp16; |x| <= 65280."""
     h = x.astype(np.float16)
     w = h.astype(np.float64)
     return np.where((w < x) if up else (w > x),
@@ -64,7 +64,7 @@ def quantise(x: np.ndarray) -> np.ndarray:
     """uint8 rows that hold x [..., D] (float64, already divided by the scale)."""
     g = np.asarray(x, dtype=np.float64).reshape(*x.shape[:-1], -1, 32)
     bad = ~np.isfinite(g).all(-1)           # such a group reads back as NaN
-    g = np.where(bad[..., None], 0.0, g)
+    g = np.clip(np.where(bad[..., None], 0.0, g), -65280.0, 65280.0)
     minima = _half(g.min(-1), up=False)
     low = minima.astype(np.float64)
     steps = _half((g.max(-1) - low) / 15.0, up=True)

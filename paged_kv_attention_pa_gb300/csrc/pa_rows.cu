@@ -54,25 +54,23 @@ struct RowsParams {
 
 constexpr int kRowThreads = 128, kRowWarps = kRowThreads / 32;
 
-// Where row r lives: sequence b, position pos (negative: a context shorter than its rows) and
-// the row `end` at which the next sequence's rows begin.
+// Where row r lives: sequence b, position pos (negative: a context shorter than its rows).
 struct Place {
   bool row;  // a row of some sequence (padding rows are left alone)
   bool len;  // whose length is valid
-  int b, pos, end;
+  int b, pos;
   __device__ bool live() const { return row && len && pos >= 0; }
 };
 
 // All lanes of the warp together; r is the same in all of them.
 __device__ __forceinline__ Place find_row(const RowsParams& p, int r, bool report) {
-  Place at{false, false, 0, 0, 0};
+  Place at{false, false, 0, 0};
   long long n, i;
   int L;
   if (p.starts == nullptr) {
     at.b = r / p.rows;
     n = p.rows;
     i = r - at.b * p.rows;
-    at.end = (int)min((long long)INT_MAX, r - i + n);
     L = __ldg(p.seq_lens + at.b);
   } else {
     const int lane = threadIdx.x & 31;
@@ -108,7 +106,6 @@ __device__ __forceinline__ Place find_row(const RowsParams& p, int r, bool repor
     n = (long long)s1 - s0;
     i = (long long)r - s0;
     if (i >= n) return at;  // starts that do not ascend
-    at.end = s1;
   }
   at.row = true;
   at.len = L >= 0 && L <= p.cap;
@@ -177,6 +174,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // A quarter of a group (8 consecutive elements; the others in the lanes that differ in the low
 // two bits) to its word of codes, and the group's step and minimum. The minimum is rounded
 // down and the step up, so every element lies between the first and the sixteenth value.
+// Elements saturate at +-65280: with the step's rounding (less than 8) the sixteenth value is
+// then below 65280 + 15 * 8 and rounds to a finite fp16, which decode's sums from the upper end
+// of the codes need, and the step is at most 130560 / 15 = 8704.
 //
 // The code is the nearest integer to (x - minimum) / step, exact ties (frequent for 16-bit
 // inputs) to even, so the quotient has to be the correctly rounded one. With y the correctly
@@ -199,14 +199,17 @@ __device__ __forceinline__ uint32_t int4_octet(float (&x)[8], uint16_t* step16, 
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, s));
   }
   const bool bad = !(lo > -INFINITY && hi < INFINITY);  // a NaN or an infinity in the group
-  const __half mn = __float2half_rd(fminf(fmaxf(lo, -65504.f), 65504.f));
-  const float low = __half2float(mn);
-  const __half st = __float2half_ru(fminf(__fdiv_rn(__fsub_rn(hi, low), 15.f), 65504.f));
-  const float step = __half2float(st);
-  if (lo < -65504.f || hi > 65504.f) {  // beyond what the format holds: saturate
+  constexpr float kMost = 65280.f;
+  if (lo < -kMost || hi > kMost) {
+    lo = fminf(fmaxf(lo, -kMost), kMost);
+    hi = fminf(fmaxf(hi, -kMost), kMost);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], low), low + 15.f * step);
+    for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -kMost), kMost);
   }
+  const __half mn = __float2half_rd(lo);
+  const float low = __half2float(mn);
+  const __half st = __float2half_ru(__fdiv_rn(__fsub_rn(hi, low), 15.f));
+  const float step = __half2float(st);
   const float y = step > 0.f ? __frcp_rn(step) : 0.f;
   constexpr uint32_t kMagic = 0x4b400000u;         // 1.5 * 2^23
   constexpr uint32_t kSum = kMagic * 0x11111111u;  // its bits over eight nibbles, modulo 2^32

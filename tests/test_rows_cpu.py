@@ -57,6 +57,20 @@ def test_int4_quantise_is_within_half_a_step():
     assert np.array_equal(o4.dequant(o4.quantise(x)), x)
 
 
+def test_int4_quantise_saturates_within_fp16():
+    # beyond +-65280 values saturate, and every value of a row, the sixteenth of each group
+    # among them, rounds to a finite fp16
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal((400, 128)) * np.exp(rng.uniform(5, 88, (400, 1)))
+    x[:100] = np.sign(x[:100]) * 65280.0 * (1 - rng.uniform(0, 1e-2, (100, 128)))
+    codes, steps, minima = o4.unpack(o4.quantise(x))
+    assert steps.max() <= 8704 and np.abs(minima).max() <= 65280 + 32
+    assert np.isfinite((minima + 15 * steps).astype(np.float16)).all()
+    want = np.clip(x, -65280, 65280).reshape(400, 4, 32)
+    got = minima[..., None] + steps[..., None] * codes
+    assert np.all(np.abs(got - want) <= steps[..., None] / 2 * (1 + 1e-12))
+
+
 def test_rotation_preserves_relative_positions():
     rng = np.random.default_rng(2)
     q, k = rng.standard_normal((2, 1, 1, 64))
