@@ -53,6 +53,12 @@ float number(PyObject* o) {
   return (float)v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused{};
+  return v != 0;
+}
+
 int dtype_of(ScalarType t) {
   return t == ScalarType::Half ? PA_F16 : t == ScalarType::BFloat16 ? PA_BF16 : -1;
 }
@@ -137,8 +143,9 @@ T* data(const Tensor& t) {
 struct Workspace {
   void* at = nullptr;
   size_t bytes = 0;
-  explicit Workspace(PyObject* o) {
+  Workspace(PyObject* o, int64_t device) {
     if (const Tensor* t = optional_tensor(o)) {
+      on_device(*t, device, true, "workspace");
       at = t->data_ptr();
       bytes = t->nbytes();
     }
@@ -199,9 +206,9 @@ PyObject* do_decode(PyObject* const* v) {
   a.kv_dtype = c.kv;
   a.k_scale = c.kv == PA_KV_AS_DTYPE ? 1.f : number(v[10]);
   a.v_scale = c.kv == PA_KV_AS_DTYPE ? 1.f : number(v[11]);
-  a.flags = PyObject_IsTrue(v[12]) ? PA_FLAG_DETERMINISTIC : 0u;
+  a.flags = truth(v[12]) ? PA_FLAG_DETERMINISTIC : 0u;
   a.total_tokens = integer(v[13]);
-  const Workspace ws(v[14]);
+  const Workspace ws(v[14], dev);
   const Tensor out = given ? *given : new_like(q);
   a.q = data<void>(q);
   a.k_cache = data<void>(kc);
@@ -262,7 +269,7 @@ PyObject* do_append(PyObject* const* v) {
   a.kv_dtype = c.kv;
   a.k_scale = number(v[12]);
   a.v_scale = number(v[13]);
-  a.rope_layout = PyObject_IsTrue(v[10]) ? PA_ROPE_INTERLEAVED : PA_ROPE_HALF;
+  a.rope_layout = truth(v[10]) ? PA_ROPE_INTERLEAVED : PA_ROPE_HALF;
   a.rope_amplitude = number(v[11]);
   Tensor out;
   if (q) {
@@ -272,7 +279,7 @@ PyObject* do_append(PyObject* const* v) {
     a.q = data<void>(*q);
     a.q_out = data<void>(out);
   }
-  const Workspace ws(v[14]);
+  const Workspace ws(v[14], dev);
   a.k = data<void>(k);
   a.v = data<void>(val);
   a.k_cache = data<void>(kc);
@@ -322,7 +329,7 @@ PyObject* do_gather(PyObject* const* v) {
   a.kv_dtype = c.kv;
   a.k_scale = number(v[9]);
   a.v_scale = number(v[10]);
-  const Workspace ws(v[11]);
+  const Workspace ws(v[11], dev);
   const auto options = kc.options().dtype(type).requires_grad(false);
   const Tensor ko = kg ? *kg : at::empty(shape, options), vo = vg ? *vg : at::empty(shape, options);
   a.k_cache = data<void>(kc);

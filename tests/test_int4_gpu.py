@@ -7,6 +7,7 @@ import torch
 
 import rows_harness as rh
 from oracle import decode_ref, decode_ref_rows
+from oracle import int4 as o4
 
 pytestmark = pytest.mark.gpu
 
@@ -220,3 +221,68 @@ def test_outgrown_workspaces_stay_allocated(cuda_lib):
     a = cuda_lib._workspace(1 << 16, dev, s.cuda_stream)
     b = cuda_lib._workspace(a.numel() + 1, dev, s.cuda_stream)
     assert b.numel() >= 2 * a.numel() and any(t is a for t in cuda_lib._outgrown)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_saturated_rows_decode_to_finite_outputs(cuda_lib, D):
+    # values past what a row holds: the bytes are the oracle's, and decode (whose sums run from
+    # both ends of the codes) agrees with the values they stand for
+    Hkv, L, bs = 2, 70, 16
+    g = torch.Generator().manual_seed(13)
+    v = torch.randn((1, L, Hkv, D), generator=g) * torch.exp(torch.rand((1, L, Hkv, 1), generator=g) * 70 + 8)
+    v[0, :20] = torch.sign(v[0, :20]) * 65280.0
+    v = v.bfloat16()
+    k = torch.randn((1, L, Hkv, D), generator=g).bfloat16()
+    nb = -(-L // bs)
+    kc, vc = (torch.zeros((nb, Hkv, bs, D // 8 * 5), dtype=torch.uint8, device="cuda") for _ in range(2))
+    bt, lens = torch.arange(nb, dtype=torch.int32, device="cuda")[None], torch.tensor([L], dtype=torch.int32, device="cuda")
+    cuda_lib.append(k.cuda(), v.cuda(), kc, vc, bt, lens)
+    K, V = (c.cpu().transpose(1, 2).reshape(-1, Hkv, D // 8 * 5)[:L].numpy() for c in (kc, vc))
+    assert np.array_equal(V, o4.quantise(rh.f64(v[0])))
+    q = torch.randn((1, 4, D), generator=g).bfloat16()
+    scale = float(np.float32(0.088))
+    out = cuda_lib.decode(q.cuda(), kc, vc, bt, lens, scale, max_seq_len=L)
+    K, V = [o4.dequant(K)], [o4.dequant(V)]
+    ref = decode_ref(rh.f64(q), K, V, scale)
+    got = rh.f64(out)
+    # (the sixteenth value of a group, rounded to fp16 where the sums start from it: 2^-11)
+    tol = tolerance("bf16", K, V, 8704.0, ref, L) + 2.0 ** -11 * 65520
+    assert np.all(np.isfinite(got)) and np.all(np.abs(got - ref) <= tol)
+
+
+def test_workspaces_and_flags_are_checked(cuda_lib):
+    c = torch.zeros((4, 2, 16, 80), dtype=torch.uint8, device="cuda")
+    bt = torch.zeros((1, 4), dtype=torch.int32, device="cuda")
+    sl = torch.ones(1, dtype=torch.int32, device="cuda")
+    q = torch.zeros((1, 2, 128), dtype=torch.bfloat16, device="cuda")
+    for ws in (torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            cuda_lib.decode(q, c, c, bt, sl, 0.1, workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            cuda_lib.append(q, q, c, c, bt, sl, workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            cuda_lib.gather(c, c, bt, sl, 1, dtype=torch.bfloat16, workspace=ws)
+    with pytest.raises(RuntimeError):   # no truth value
+        cuda_lib.decode(q, c, c, bt, sl, 0.1, deterministic=torch.zeros(2))
+    cuda_lib.decode(q, c, c, bt, sl, 0.1)
+
+
+def test_outputs_of_a_given_stream_are_allocated_in_its_order(cuda_lib):
+    # not from memory that the current stream's pending kernels may still use
+    nb, s = 64, torch.cuda.Stream()
+    c = torch.zeros((nb, 2, 16, 80), dtype=torch.uint8, device="cuda")
+    bt = torch.arange(nb, dtype=torch.int32, device="cuda")[None]
+    sl = torch.tensor([1024], dtype=torch.int32, device="cuda")
+    rows = torch.zeros((1, 1024, 2, 128), dtype=torch.bfloat16, device="cuda")
+    one = rows[:, 0].contiguous()
+    torch.cuda.synchronize()
+    for call in (lambda: cuda_lib.gather(c, c, bt, sl, 1024, dtype=torch.bfloat16, stream=s),
+                 lambda: [cuda_lib.append(rows, rows, c, c, bt, sl, q=rows, stream=s)],
+                 lambda: [cuda_lib.decode(one, c, c, bt, sl, 0.1, stream=s)]):
+        torch.cuda.empty_cache()
+        freed = [torch.empty_like(rows) for _ in range(4)] + [torch.empty(512, device="cuda", dtype=torch.bfloat16) for _ in range(4)]
+        at = {t.data_ptr() for t in freed}
+        del freed
+        outs = call()
+        assert not at & {t.data_ptr() for t in outs}
+        s.synchronize()
