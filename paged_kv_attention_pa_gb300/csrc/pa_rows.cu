@@ -185,7 +185,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // 1990). Adding 1.5 * 2^23 rounds it to an integer in the low bits, and eight of them become
 // a word by multiplications with 16, less what the constant's bits add up to. Six
 // instructions an element: with an IEEE division each, appending 4095 rows of 24/4 heads of
-// 256 took 35.7 us against 29.1.
+// 256 took 6.6 us more (of 35.7; 27.0 now).
 __device__ __forceinline__ uint32_t int4_octet(float (&x)[8], uint16_t* step16, uint16_t* min16) {
   float lo = x[0], hi = x[0];
 #pragma unroll
@@ -232,7 +232,7 @@ template <typename T, KvKind KIND, int D>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(const RowsParams p) {
   constexpr int LPI = D / 16, IPW = 32 / LPI;  // lanes per row item, items per warp
   constexpr int ROWB = kv_row_bytes(D, KIND);
-  __shared__ float2 turn[D / 2];
+  __shared__ __align__(16) float2 turn[D / 2];
   __shared__ __align__(16) float stage[KIND == kKvInt4 ? kRowWarps : 1][KIND == kKvInt4 ? IPW * D : 4];
   __shared__ __align__(16) uint8_t line[KIND == kKvInt4 ? kRowWarps : 1]
                                        [KIND == kKvInt4 ? IPW * PA_INT4_ROW_BYTES(D) : 16];
@@ -244,33 +244,32 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const RowsParams p)
   const bool half = !p.interleaved && p.rot > 0;
   const int h = p.rot / 16;  // chunks of eight elements in half of the rotated part
 
-  // which = 0 query, 1 key, 2 value; the lane's two 8-element chunks of the head: for each of
-  // the two, the lanes' chunks lie side by side, and the second holds the other halves of the
-  // first's pairs where pairs lie apart
+  // A lane holds two chunks of eight elements of a head, one 16-byte load each, so that the
+  // lanes' words lie side by side; where pairs lie apart the second chunk of a query or key
+  // holds the other halves of the first's pairs.
+  const bool on0 = half ? li < h : li < 2 * h, on1 = half ? li < h : li + LPI < 2 * h;  // they turn
+  const int q0 = half && li >= h ? li + h : li, q1 = half && li < h ? li + h : li + LPI;
+  const T* const qrow = static_cast<const T*>(p.q) + (long long)r * p.q_stride;
+  const T* const krow = static_cast<const T*>(p.k) + (long long)r * p.k_stride;
+  const T* const vrow = static_cast<const T*>(p.v) + (long long)r * p.v_stride;
+
   struct Task {
-    int which, head;
+    int which, head;  // which = 0 query, 1 key, 2 value
     bool live;
-    int c0, c1;
   };
   auto task_of = [&](int t) -> Task {
     Task k;
     k.which = t < ntq ? 0 : t < ntq + ntk ? 1 : 2;
     k.head = (t - (k.which == 0 ? 0 : k.which == 1 ? ntq : ntq + ntk)) * IPW + item;
     k.live = t < tasks && k.head < (k.which == 0 ? p.Hq : p.Hkv);
-    const bool apart = half && k.which < 2;
-    k.c0 = apart && li >= h ? li + h : li;
-    k.c1 = apart && li < h ? li + h : li + LPI;
     return k;
   };
   auto load = [&](const Task& k, uint4* a, uint4* b) {
     *a = *b = make_uint4(0u, 0u, 0u, 0u);
     if (!k.live) return;
-    const T* src = k.which == 0   ? static_cast<const T*>(p.q) + (long long)r * p.q_stride
-                   : k.which == 1 ? static_cast<const T*>(p.k) + (long long)r * p.k_stride
-                                  : static_cast<const T*>(p.v) + (long long)r * p.v_stride;
-    const uint4* row = reinterpret_cast<const uint4*>(src + (size_t)k.head * D);
-    *a = __ldcs(row + k.c0);  // read once (and q may be written in place)
-    *b = __ldcs(row + k.c1);
+    const uint4* row = reinterpret_cast<const uint4*>((k.which == 0 ? qrow : k.which == 1 ? krow : vrow) + k.head * D);
+    *a = __ldcs(row + (k.which == 2 ? li : q0));  // read once (and q may be written in place)
+    *b = __ldcs(row + (k.which == 2 ? li + LPI : q1));
   };
 
   pdl_wait();
@@ -283,44 +282,64 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const RowsParams p)
   const bool report = threadIdx.x == 0 && blockIdx.y == 0;
   const Place at = find_row(p, r, report);
   if (!at.row) return;
-  int slot = 0, phys = -1;
+  int phys = -1;
+  size_t row0 = 0;  // the cache row of head 0
   if (at.live()) {
     const int blk = block_index(p, at.pos);
-    slot = at.pos - blk * p.block_size;
     phys = checked_block(p, __ldg(p.block_tables + (size_t)at.b * p.max_blocks + blk), report);
+    row0 = cache_row<KIND>(p, phys, at.pos - blk * p.block_size, 0);
   }
+  const int head_rows = KIND == kKvInt4 ? p.block_size : 1;  // cache rows between heads
   for (int j = threadIdx.x; j < p.rot / 2; j += kRowThreads) {
     const uint64_t f = __ldg(p.turns + j) * (uint64_t)(uint32_t)at.pos;
     float s, c;
     sincospif((float)(int32_t)(f >> 32) * 4.656612873077393e-10f, &s, &c);  // half turns: * 2^-31
-    turn[j] = make_float2(c * p.amplitude, s * p.amplitude);
+    const int chunk = half ? j / 8 : j / 4, e = half ? j % 8 : j % 4;
+    turn[2 * chunk + e / 2 * (half ? 2 : 4) * LPI + e % 2] = make_float2(c * p.amplitude, s * p.amplitude);
   }
   __syncthreads();
+  // Turns 2 i and 2 i + 1 of a chunk lie side by side, those of the lanes' chunks behind one
+  // another: no bank conflicts (a chunk's turns in a row: 4-bit rows as below 29.1 us, not 27.0).
+  // Kept in registers over the heads they cost more in resident warps than the loads: 32.9 us
+  // against 25.9 for 16-bit rows.
+  const float4* const turns = reinterpret_cast<const float4*>(turn);
 
   while (t < tasks) {
     const int tn = t + stride;
     const Task next = task_of(tn);
     uint4 an, bn;
     load(next, &an, &bn);
-    float x0[8], x1[8];  // chunk c0, chunk c1
+    float x0[8], x1[8];  // the first and the second chunk
     unpack8<T>(x0, a);
     unpack8<T>(x1, b);
     // (16-bit chunks that do not turn pass through as they are)
-    const bool turn0 = cur.which < 2 && (half ? li < h : cur.c0 < 2 * h);
-    const bool turn1 = cur.which < 2 && (half ? li < h : cur.c1 < 2 * h);
+    const bool turn0 = cur.which < 2 && on0, turn1 = cur.which < 2 && on1;
+    const int c0 = cur.which == 2 ? li : q0, c1 = cur.which == 2 ? li + LPI : q1;
     if (half) {
       if (turn0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) rotate_pair(x0[e], x1[e], turn[8 * li + e]);
+        for (int e = 0; e < 8; e += 2) {
+          const float4 w = turns[li + e / 2 * LPI];
+          rotate_pair(x0[e], x1[e], make_float2(w.x, w.y));
+          rotate_pair(x0[e + 1], x1[e + 1], make_float2(w.z, w.w));
+        }
       }
     } else {
       if (turn0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) rotate_pair(x0[2 * e], x0[2 * e + 1], turn[4 * cur.c0 + e]);
+        for (int e = 0; e < 2; ++e) {
+          const float4 w = turns[li + e * 2 * LPI];
+          rotate_pair(x0[4 * e], x0[4 * e + 1], make_float2(w.x, w.y));
+          rotate_pair(x0[4 * e + 2], x0[4 * e + 3], make_float2(w.z, w.w));
+        }
       }
       if (turn1) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) rotate_pair(x1[2 * e], x1[2 * e + 1], turn[4 * cur.c1 + e]);
+        for (int e = 0; e < 2; ++e) {
+          const float4 w = turns[li + LPI + e * 2 * LPI];
+          rotate_pair(x1[4 * e], x1[4 * e + 1], make_float2(w.x, w.y));
+          rotate_pair(x1[4 * e + 2], x1[4 * e + 3], make_float2(w.z, w.w));
+        }
       }
     }
     if (cur.which == 0) {
@@ -328,17 +347,17 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const RowsParams p)
         uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) + ((size_t)r * p.Hq + cur.head) * D);
         const bool zero = !at.live();
         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-        dst[cur.c0] = zero ? z : turn0 ? pack8<T>(x0) : a;
-        dst[cur.c1] = zero ? z : turn1 ? pack8<T>(x1) : b;
+        dst[c0] = zero ? z : turn0 ? pack8<T>(x0) : a;
+        dst[c1] = zero ? z : turn1 ? pack8<T>(x1) : b;
       }
     } else if (phys >= 0) {
       uint8_t* cache = static_cast<uint8_t*>(cur.which == 1 ? p.k_cache : p.v_cache);
       const float inv = cur.which == 1 ? p.k_scale : p.v_scale;
-      uint8_t* dst = cache + cache_row<KIND>(p, phys, slot, cur.head) * ROWB;
+      uint8_t* dst = cache + (row0 + (size_t)cur.head * head_rows) * ROWB;
       if constexpr (KIND == kKv16) {
         if (cur.live) {
-          reinterpret_cast<uint4*>(dst)[cur.c0] = turn0 ? pack8<T>(x0) : a;
-          reinterpret_cast<uint4*>(dst)[cur.c1] = turn1 ? pack8<T>(x1) : b;
+          reinterpret_cast<uint4*>(dst)[c0] = turn0 ? pack8<T>(x0) : a;
+          reinterpret_cast<uint4*>(dst)[c1] = turn1 ? pack8<T>(x1) : b;
         }
       } else {
 #pragma unroll
@@ -348,12 +367,12 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const RowsParams p)
         }
         if constexpr (KIND == kKvFp8) {
           if (cur.live) {
-            reinterpret_cast<uint2*>(dst)[cur.c0] = make_uint2(e4m3x4(x0), e4m3x4(x0 + 4));
-            reinterpret_cast<uint2*>(dst)[cur.c1] = make_uint2(e4m3x4(x1), e4m3x4(x1 + 4));
+            reinterpret_cast<uint2*>(dst)[c0] = make_uint2(e4m3x4(x0), e4m3x4(x0 + 4));
+            reinterpret_cast<uint2*>(dst)[c1] = make_uint2(e4m3x4(x1), e4m3x4(x1 + 4));
           }
         } else {
           using R = Int4Row<D>;
-          int c0 = cur.c0, c1 = cur.c1;
+          int g0 = c0, g1 = c1;  // the chunks that x0 and x1 hold
           if (half && cur.which == 1 && h % 4 != 0) {
             // a group's four chunks are not in the four lanes of a quad: exchange them
             // through shared memory
@@ -363,11 +382,11 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const RowsParams p)
             st[2 * c1] = make_float4(x1[0], x1[1], x1[2], x1[3]);
             st[2 * c1 + 1] = make_float4(x1[4], x1[5], x1[6], x1[7]);
             __syncwarp();
-            c0 = li;
-            c1 = li + LPI;
+            g0 = li;
+            g1 = li + LPI;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float4 u = st[2 * c0 + i], w = st[2 * c1 + i];
+              const float4 u = st[2 * g0 + i], w = st[2 * g1 + i];
               x0[4 * i] = u.x;
               x0[4 * i + 1] = u.y;
               x0[4 * i + 2] = u.z;
@@ -382,7 +401,7 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const RowsParams p)
           uint8_t* l = line[warp] + item * R::BYTES;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int c = i ? c1 : c0, g = c >> 2;
+            const int c = i ? g1 : g0, g = c >> 2;
             uint16_t step16, min16;
             reinterpret_cast<uint32_t*>(l)[(c & 3) * R::G + g] = int4_octet(i ? x1 : x0, &step16, &min16);
             if ((c & 3) == 0) {
