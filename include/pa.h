@@ -35,7 +35,8 @@
  *  - Layouts are dense, row-major, with no padding:
  *        q, out        [B, Hq, D]                       (dtype)
  *        k_cache,
- *        v_cache       [num_blocks, block_size, Hkv, D] (dtype)
+ *        v_cache       [num_blocks, block_size, Hkv, D] (dtype, or one byte per element;
+ *                      4-bit caches: head after head, see PA_INT4_ROW_BYTES)
  *        block_tables  [B, max_blocks_per_seq]          int32
  *        seq_lens      [B]                              int32
  *    q, k_cache, v_cache and out must be 16-byte aligned.
@@ -133,7 +134,9 @@ typedef void* pa_stream_t; /* cudaStream_t */
  *           attends causally to the tokens t < L - R + i + 1; a row that sees no
  *           token gets zeros. Every K/V tile is read once for all rows and heads of
  *           its KV head. Limits: G * R <= 32 at head_dim 128, <= 16 at 256; not
- *           combined with a window (PA_ERR_UNSUPPORTED).
+ *           combined with a window (PA_ERR_UNSUPPORTED). Cached values must be finite:
+ *           a NaN or an infinity in V at one of the sequence's tokens reaches the rows
+ *           that do not see it too.
  *   flags   0 or PA_FLAG_DETERMINISTIC. By default, when a long context is split
  *           across CTAs, the splits share out its last eighth tile by tile as
  *           they finish their own shares, so the order of the fp32 sums depends
