@@ -30,6 +30,7 @@ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 struct Plan {
   int S;
   int P;
+  int ordered = 0;  // 4-bit caches: the longest sequences' CTAs first
 };
 
 // A CTA's fixed cost (launch, first round trip, epilogue) expressed as the KV bytes
@@ -69,7 +70,6 @@ bool make_plan(int sm_count, int64_t B, int64_t Hkv, int D, pa::KvKind kv, int64
   const int64_t units = B * Hkv;
   const int64_t sm = sm_count > 0 ? sm_count : 1;
   const int64_t p_max = round_up(max_len, quantum);
-  if (requested > 0) return plan_for(requested, max_len, p_max, 0, quantum, out);
   bool found = false;
   int64_t best_cost = 0;
   // 4-bit splits are short (a token is a third of a 16-bit one's bytes), and one-wave grids
@@ -100,18 +100,42 @@ bool make_plan(int sm_count, int64_t B, int64_t Hkv, int D, pa::KvKind kv, int64
   // tiles: no rounding there (rounded, the fp8 grid and hybrid steps lost 0.5-1%).
   const int64_t round_tokens =
       quantum * (PA_PLAN_BALANCED && kv == pa::kKv16 ? pa::warps_per_cta(D, kv) : 1);
-  auto consider = [&](const Plan& pl) {
+  // the fixed cost in tokens of this cache: K + V bytes per token per KV head
+  const int64_t overhead_tokens = kSplitOverheadBytes / (2 * pa::kv_row_bytes(D, kv));
+  // Unsplit 4-bit batches of mixed lengths with more (sequence, KV head) pairs than SMs start
+  // the longest sequences' CTAs first, so that the SMs finish together; a CTA then reads the
+  // lengths before its table, about a sixth of its fixed cost. GB300, us per call by length /
+  // in the batch's order / the best split count: 32/8 heads of 128, 32 sequences of 1K-32K
+  // 134 / 191 / 158, 64 of 1K-32K 246 / 303 / 281, 64 of 512-4K 48.5 / 50.6 / 77; 24/16 heads
+  // 24 of 1K-16K 88 / 105 / 108; hybrid layer, 64 of 512-8K 57.5 / 83 / 88. 200 sequences of
+  // 128-2K, ten CTAs an SM, lose by it (98 / 86): not where it costs more than a quarter of
+  // the longest context.
+  const bool mixed =
+      int4 && total_tokens > 0 && B <= pa::kOrderedBatch && total_tokens < 7 * B * max_len / 8;
+  auto ordered = [&](const Plan& pl) {
+    return mixed && pl.S == 1 && units > sm && pl.P / 4 * sm > overhead_tokens / 6 * units;
+  };
+  auto consider = [&](Plan pl) {
     const int64_t waves = ceil_div(live_ctas(pl), sm);
-    // the fixed cost in tokens of this cache: K + V bytes per token per KV head
-    const int64_t overhead_tokens = kSplitOverheadBytes / (2 * pa::kv_row_bytes(D, kv));
     int64_t cost = waves * (round_up(pl.P, round_tokens) + overhead_tokens);
-    if (int4 && pl.S > 1 && waves == 1 && live_ctas(pl) > roomy) cost += 100 * 1024 / (2 * pa::kv_row_bytes(D, kv));
+    pl.ordered = ordered(pl);
+    if (pl.ordered)  // an even share or the longest context (which runs faster beside ending
+                     // CTAs), the CTAs' fixed costs, and with under two CTAs an SM their unevenness
+      cost = std::max<int64_t>(3 * pl.P / 4, ceil_div(total_tokens * Hkv, sm)) + overhead_tokens * units / sm +
+             std::max<int64_t>(0, pl.P - pl.P * units / (2 * sm));
+    if (int4 && pl.S > 1 && waves == 1 && live_ctas(pl) > roomy)
+      cost += 100 * 1024 / (2 * pa::kv_row_bytes(D, kv));
     if (!found || cost < best_cost || (cost == best_cost && pl.S < out->S)) {
       *out = pl;
       best_cost = cost;
       found = true;
     }
   };
+  if (requested > 0) {
+    if (!plan_for(requested, max_len, p_max, 0, quantum, out)) return false;
+    out->ordered = ordered(*out);
+    return true;
+  }
   for (int64_t c : cands) {
     if (c < 1) continue;
     Plan pl{};
@@ -399,6 +423,7 @@ static pa_status decode_ex(const pa_decode_args* a, void* workspace, size_t work
   p.steal = reinterpret_cast<int*>(ws + 256);
   p.window = a->window;
   p.q_len = rows;
+  p.ordered = plan.ordered;
   p.kv = kv;
   p.v_scale = kv == pa::kKv16 ? 1.f : a->v_scale;
   // scores live in the exp2 domain; the scale of an fp8 or 4-bit K multiplies every score

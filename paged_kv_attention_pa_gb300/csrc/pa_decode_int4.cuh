@@ -48,10 +48,46 @@ struct Int4Cfg {
   static constexpr int RING = NW * WARP_RING;
   static constexpr int SMEM = RING + FIXED;
   static_assert(TW == 32 && (TW * CPR) % 32 == 0, "tile shape");
-  static_assert(DEPTH >= 2 && NW * DEPTH * 8 <= 1024, "two slots at least, an mbarrier each");
+  static_assert(DEPTH >= 2 && NW * DEPTH * 8 <= 1020, "two slots at least, an mbarrier each");
 };
 
-template <typename T, int D, int NT, bool WIN>
+// The sequence whose CTAs run r-th when the longest come first (see make_plan), up to a sixteenth of
+// max_seq_len (W words of 32 sequences). All lanes together; every CTA finds the same order.
+template <int W>
+__device__ __forceinline__ int by_length(const DecodeParams& p, int r) {
+  const int lane = threadIdx.x & 31;
+  const float per = 16.f / (p.max_seq_len + 1.f);
+  int bucket[W];  // 0: the longest
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    const int b = 32 * j + lane;
+    bucket[j] = b < p.B ? 15 - min(15, max(0, (int)(__ldg(p.seq_lens + b) * per))) : 16;
+  }
+  // the last bucket with at most r sequences before it, by halves
+  int k = 0, before = 0;
+#pragma unroll
+  for (int half = 8; half >= 1; half >>= 1) {
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < W; ++j) n += __popc(__ballot_sync(0xffffffffu, bucket[j] < k + half));
+    if (n <= r) {
+      k += half;
+      before = n;
+    }
+  }
+  r -= before;
+  int b = 0;
+#pragma unroll
+  for (int j = 0; j < W; ++j) {  // the sequences of bucket k in their order
+    const uint32_t in = __ballot_sync(0xffffffffu, bucket[j] == k);
+    const uint32_t at = __ballot_sync(0xffffffffu, bucket[j] == k && __popc(in & ((1u << lane) - 1u)) == r);
+    if (at) b = 32 * j + __ffs(at) - 1;
+    r -= __popc(in);
+  }
+  return b;
+}
+
+template <typename T, int D, int NT, bool WIN, bool ORDERED>
 __global__ void __launch_bounds__(Int4Cfg<D, NT>::THREADS, 1) decode_int4_kernel(const DecodeParams p) {
   using C = Int4Cfg<D, NT>;
   using Row = Int4Row<D>;
@@ -61,7 +97,7 @@ __global__ void __launch_bounds__(Int4Cfg<D, NT>::THREADS, 1) decode_int4_kernel
 
   const int split = blockIdx.x;
   const int kvh = blockIdx.y;
-  const int b = blockIdx.z;
+  int b = blockIdx.z;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int gid = lane >> 2;
@@ -85,6 +121,11 @@ __global__ void __launch_bounds__(Int4Cfg<D, NT>::THREADS, 1) decode_int4_kernel
   // grid get scheduled at once
   pdl_wait();
   if (p.S > 1 && !p.cmerge) pdl_launch_dependents();
+  const uint32_t sequence = smem_addr(smem) + C::RING + 1020;  // b, kept for the epilogue
+  if constexpr (ORDERED) {
+    b = p.B <= 32 ? by_length<1>(p, b) : p.B <= 64 ? by_length<2>(p, b) : by_length<kOrderedBatch / 32>(p, b);
+    if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sequence), "r"(b) : "memory");
+  }
 
   // ---- prologue: length, table entries of the first static tiles and query fragments
   // requested at once
@@ -447,13 +488,14 @@ __global__ void __launch_bounds__(Int4Cfg<D, NT>::THREADS, 1) decode_int4_kernel
 
   if (p.S == 1 || p.cmerge) pdl_launch_dependents();
   int4_finish<D, NT>(o, om, tig);
-  finish_cta<T, kKvInt4, D, NT, C>(p, smem, n_splits, m, l, o);
+  if constexpr (ORDERED) b = lds32(sequence);
+  finish_cta<T, kKvInt4, D, NT, C>(p, smem, b, n_splits, m, l, o);
 }
 
-template <typename T, int D, int NT, bool WIN>
-struct DecodeKernel<T, int4g32, D, NT, WIN> {
+template <typename T, int D, int NT, bool WIN, bool ORDERED>
+struct DecodeKernel<T, int4g32, D, NT, WIN, ORDERED> {
   using C = Int4Cfg<D, NT>;
-  static constexpr auto kernel = decode_int4_kernel<T, D, NT, WIN>;
+  static constexpr auto kernel = decode_int4_kernel<T, D, NT, WIN, ORDERED>;
 };
 
 }  // namespace pa

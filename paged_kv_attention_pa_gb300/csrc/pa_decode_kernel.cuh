@@ -113,11 +113,11 @@ __device__ __forceinline__ void cp_async_wait() {
 // score and PV products) merge, and become the output, a split's partial, or the cluster's
 // output (see the head of this file).
 template <typename T, KvKind KIND, int D, int NT, typename C>
-__device__ __forceinline__ void finish_cta(const DecodeParams& p, uint8_t* ring, int n_splits,
+__device__ __forceinline__ void finish_cta(const DecodeParams& p, uint8_t* ring, int b, int n_splits,
                                            float (&m)[NT][2], float (&l)[NT][2],
                                            float (&o)[NT][D / 16][4]) {
   constexpr int GT = 8 * NT, kWarps = C::NW, kThreads = C::THREADS;
-  const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+  const int split = blockIdx.x, kvh = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int G = p.G, R = p.q_len, cols = G * R;
@@ -795,7 +795,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
 
   if (p.S == 1 || p.cmerge) pdl_launch_dependents();
 
-  finish_cta<T, KIND, D, NT, C>(p, ring, n_splits, m, l, o);
+  finish_cta<T, KIND, D, NT, C>(p, ring, b, n_splits, m, l, o);
 }
 
 // Combine the split partials of one (sequence, query head, 64-wide slice of D):
@@ -922,16 +922,17 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// The kernel of a cache type and its configuration (4-bit caches: pa_decode_int4.cuh).
-template <typename T, typename KV, int D, int NT, bool WIN>
+// The kernel of a cache type and its configuration (4-bit caches: pa_decode_int4.cuh, which has
+// an ORDERED one).
+template <typename T, typename KV, int D, int NT, bool WIN, bool ORDERED>
 struct DecodeKernel {
   using C = Cfg<D, NT, kv_kind_of<KV>>;
   static constexpr auto kernel = decode_kernel<T, KV, D, NT, WIN>;
 };
 
-template <typename T, typename KV, int D, int NT, bool WIN>
+template <typename T, typename KV, int D, int NT, bool WIN, bool ORDERED = false>
 cudaError_t launch_decode_nt(const DecodeParams& p, cudaStream_t st, int* kernels) {
-  using Kernel = DecodeKernel<T, KV, D, NT, WIN>;
+  using Kernel = DecodeKernel<T, KV, D, NT, WIN, ORDERED>;
   using C = typename Kernel::C;
   auto kern = Kernel::kernel;
   // The dynamic shared memory opt-in is per device; remember which devices have it.
@@ -998,6 +999,13 @@ cudaError_t launch_decode_nt(const DecodeParams& p, cudaStream_t st, int* kernel
 template <typename T, typename KV, int D>
 cudaError_t launch_decode_dispatch(const DecodeParams& p, cudaStream_t st, int* kernels) {
   const int cols = p.G * p.q_len;
+  if constexpr (std::is_same<KV, int4g32>::value) {
+    if (p.ordered) {
+      if (cols <= 8) return launch_decode_nt<T, KV, D, 1, false, true>(p, st, kernels);
+      if (cols <= 16 || D != 128) return launch_decode_nt<T, KV, D, 2, false, true>(p, st, kernels);
+      if constexpr (D == 128) return launch_decode_nt<T, KV, D, 4, false, true>(p, st, kernels);
+    }
+  }
   if (p.window > 0)
     return cols <= 8 ? launch_decode_nt<T, KV, D, 1, true>(p, st, kernels)
                      : launch_decode_nt<T, KV, D, 2, true>(p, st, kernels);

@@ -82,6 +82,35 @@ def test_decode_int4_query_rows(cuda_lib, rows, Hq, Hkv, D):
         run_case(cuda_lib, [600, rows, 1, 0, 33], Hq, Hkv, D, 16, rows=rows, seed=3, splits=S)
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,D,bs,rows", [
+    (32, 16, 8, 128, 16, 1), (50, 8, 4, 128, 16, 2), (200, 4, 2, 128, 16, 1), (256, 6, 2, 256, 48, 1),
+    (41, 16, 4, 256, 784, 1), (24, 64, 8, 128, 16, 4), (20, 8, 8, 128, 16, 1),
+])
+def test_decode_int4_mixed_batches_run_by_length(cuda_lib, B, Hq, Hkv, D, bs, rows):
+    # more (sequence, KV head) pairs than SMs (152; the last case has about as many) and the
+    # total given: CTAs start by length, in an order of their own, with the same results as in
+    # the batch's order
+    r = np.random.default_rng(B)
+    lens = [int(x) for x in r.integers(0, 200, B)]
+    lens[B // 3], lens[B // 2], lens[-1] = 4000, 0, 4000
+    run_case(cuda_lib, lens, Hq, Hkv, D, bs, rows=rows, seed=14, total_tokens=sum(lens))
+    kc, vc, bt, _, _ = rh.random_int4_pool(lens, bs, Hkv, D, 15)
+    q = torch.randn((B, Hq, D) if rows == 1 else (B, rows, Hq, D)).bfloat16().cuda()
+    for bad in (False, True):   # lengths that the call reports are clamped in either order
+        if bad:
+            lens[1], lens[2] = -5, 2 ** 31 - 1
+            bt = torch.where(bt < 0, torch.zeros_like(bt), bt)
+        sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        outs, flags = [], []
+        for total in (0, 4000 + 100 * B):
+            ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+            outs.append(cuda_lib.decode(q, kc.cuda(), vc.cuda(), bt.cuda(), sl, 0.088, max_seq_len=4000,
+                                        splits=1, total_tokens=total, workspace=ws))
+            flags.append(cuda_lib.read_device_errors(ws))
+        assert flags == [cuda_lib.PA_DEVERR_SEQ_LEN if bad else 0] * 2
+        assert torch.equal(rh.bits(outs[0].cpu()), rh.bits(outs[1].cpu()))
+
+
 @pytest.mark.parametrize("W", [1, 17, 1000])
 def test_decode_int4_window(cuda_lib, W):
     run_case(cuda_lib, [1500, 999, 16, 1], 8, 4, 128, 16, seed=4, window=W)
