@@ -13,10 +13,9 @@
 // PA_DEVERR_COPY.
 //
 // Math. 160 bytes per token and KV head at head_dim 128 pass through an SM in 3.6 ns at the
-// memory's rate, and the arithmetic of its tiles takes as
-// long. Twelve warps at head_dim 128 with up to 8 columns: 5.7 TB/s
-// with every SM busy (152 pairs of 8K tokens, 34.9 us; eight warps 40.3), against 6.2 TB/s
-// for the copies alone. Tiles whose length is known at compile time and the refill ahead of
+// memory's rate, and the arithmetic of its tiles takes as long. Twelve warps at head_dim 128
+// with up to 8 columns: 5.7 TB/s with every SM busy (152 pairs of 8K tokens, 34.9 us; eight
+// warps 40.3), against 6.2 TB/s for the copies alone. Two CTAs of six warps an SM: 37.6 us. Tiles whose length is known at compile time and the refill ahead of
 // the wait matter: runtime tiles of 64 tokens with the refill behind the arithmetic ran
 // 38.3-40.1 us with fewer instructions.
 #pragma once
@@ -38,7 +37,7 @@ struct Int4Cfg {
   static constexpr int TILE_BYTES = TW * ROWB;
   static constexpr int SLOT_BYTES = 2 * TILE_BYTES;  // K, then V
   static constexpr bool BULK = D == 256 ? PA_I4_BULK_D256 : PA_I4_BULK_D128;
-  static constexpr bool QSHARED = NT >= PA_I4_QSHARED || (NT == 1 && D == 128);  // query fragments
+  static constexpr bool QSHARED = NT * KS >= PA_I4_QSHARED || (NT == 1 && D == 128);  // query fragments
                                                                                  // in shared memory
   static constexpr int QBYTES = QSHARED ? NT * KS * 256 : 0;
   static constexpr int FIXED = 1024 + QBYTES;  // the slots' mbarriers (bulk copies), the query

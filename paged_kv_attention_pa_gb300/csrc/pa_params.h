@@ -75,13 +75,14 @@ __host__ __device__ constexpr int warps_per_cta(int D, KvKind kind, int column_t
          : kind == kKvFp8 ? (D == 128 ? PA_WARPS_F8_D128 : PA_WARPS_F8_D256)
                           : (D == 128 ? PA_WARPS_D128 : PA_WARPS_D256);
 }
-// 4-bit caches: from this many column tiles on the query fragments live in shared memory, and
-// with one tile at head_dim 128, whose twelve warps have fewer registers each (GB300, 32/8
-// heads of 128, us per call in registers / shared: 8 query rows of 8 sequences of 16K tokens,
-// four column tiles, 191 / 132; 4 rows, two tiles, 55.3 / 56.0; 32 sequences of 16K, one tile,
-// 126.9 / 125.0; hybrid layer, head_dim 256, 32K, one tile, 13.9 / 14.1).
+// 4-bit caches: from this many query fragments a warp on (column tiles times head_dim / 16)
+// they live in shared memory, and with one tile at head_dim 128, whose twelve warps have fewer
+// registers each (GB300, us per call in registers / shared: 32/8 heads of 128, 8 query rows of
+// 8 sequences of 16K tokens, 32 fragments, 191 / 132; 4 rows, 16 fragments, 55.3 / 56.0; 32
+// sequences of 16K, one tile, 126.9 / 125.0; 24/4 heads of 256, 2 rows of 8 sequences of 8K,
+// 32 fragments, 36.1 / 35.7; hybrid layer, 32K, one tile, 16 fragments, 13.9 / 14.1).
 #ifndef PA_I4_QSHARED
-#define PA_I4_QSHARED 4
+#define PA_I4_QSHARED 32
 #endif
 // 4-bit caches: bulk copies (one per block and tile) or 16-byte cp.async.
 #ifndef PA_I4_BULK_D128
