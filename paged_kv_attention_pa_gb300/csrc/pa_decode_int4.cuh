@@ -40,7 +40,7 @@ struct Int4Cfg {
   static constexpr bool QSHARED = NT * KS >= PA_I4_QSHARED || (NT == 1 && D == 128);  // query fragments
                                                                                  // in shared memory
   static constexpr int QBYTES = QSHARED ? NT * KS * 256 : 0;
-  static constexpr int FIXED = 1024 + QBYTES;  // the slots' mbarriers (bulk copies), the query
+  static constexpr int FIXED = 1024 + QBYTES;  // the slots' mbarriers, by_length's answer; the query
   static constexpr int DEPTH_FIT = (kSmemBudget - FIXED) / (NW * SLOT_BYTES);
   static constexpr int DEPTH = DEPTH_FIT > 5 ? 5 : DEPTH_FIT;  // slots per warp
   static constexpr int WARP_RING = DEPTH * SLOT_BYTES;
@@ -488,7 +488,23 @@ __global__ void __launch_bounds__(Int4Cfg<D, NT>::THREADS, 1) decode_int4_kernel
   if (p.S == 1 || p.cmerge) pdl_launch_dependents();
   int4_finish<D, NT>(o, om, tig);
   if constexpr (ORDERED) b = lds32(sequence);
-  finish_cta<T, kKvInt4, D, NT, C>(p, smem, b, n_splits, m, l, o);
+  // Where registers are scarce the epilogue's indexes are made anew there rather than kept
+  // through the main loop (GB300, us per call, kept / anew: 32/8 heads of 128, 32 sequences of
+  // 16K 126.4 / 125.0, 8 query rows of 8 of 16K 141.9 / 132.5, 4 rows 54.2 / 55.3 (by length,
+  // 32 of 1K-16K, 101.4 / 97.2); 24/4 heads
+  // of 256, 2 rows of 8 of 8K 35.0 / 35.6).
+  if constexpr (D == 128 && (NT != 2 || ORDERED)) {
+    const int warp2 = threadIdx.x >> 5, gid2 = (threadIdx.x & 31) >> 2, tig2 = threadIdx.x & 3;
+    const int G2 = p.G, R2 = p.q_len, kvh2 = blockIdx.y;
+    auto qrow2 = [&](int c) -> size_t {
+      return ((size_t)b * R2 + c / G2) * p.Hq + (size_t)kvh2 * G2 + c % G2;
+    };
+    finish_cta<T, kKvInt4, D, NT, C>(p, smem, blockIdx.x, kvh2, b, warp2, gid2, tig2, G2 * R2,
+                                     reinterpret_cast<T*>(p.out), qrow2, n_splits, m, l, o);
+  } else {
+    finish_cta<T, kKvInt4, D, NT, C>(p, smem, split, kvh, b, warp, gid, tig, cols, out, qrow,
+                                     n_splits, m, l, o);
+  }
 }
 
 template <typename T, int D, int NT, bool WIN, bool ORDERED>

@@ -112,19 +112,13 @@ __device__ __forceinline__ void cp_async_wait() {
 // What follows a CTA's last tile: its warps' states (m, l, o in the fragment layout of the
 // score and PV products) merge, and become the output, a split's partial, or the cluster's
 // output (see the head of this file).
-template <typename T, KvKind KIND, int D, int NT, typename C>
-__device__ __forceinline__ void finish_cta(const DecodeParams& p, uint8_t* ring, int b, int n_splits,
-                                           float (&m)[NT][2], float (&l)[NT][2],
+// qrow(c): the row of q and out that holds column c.
+template <typename T, KvKind KIND, int D, int NT, typename C, typename Row>
+__device__ __forceinline__ void finish_cta(const DecodeParams& p, uint8_t* ring, int split, int kvh, int b,
+                                           int warp, int gid, int tig, int cols, T* out, const Row& qrow,
+                                           int n_splits, float (&m)[NT][2], float (&l)[NT][2],
                                            float (&o)[NT][D / 16][4]) {
   constexpr int GT = 8 * NT, kWarps = C::NW, kThreads = C::THREADS;
-  const int split = blockIdx.x, kvh = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gid = lane >> 2, tig = lane & 3;
-  const int G = p.G, R = p.q_len, cols = G * R;
-  T* out = reinterpret_cast<T*>(p.out);
-  auto qrow = [&](int c) -> size_t {  // row of q / out holding column c
-    return ((size_t)b * R + c / G) * p.Hq + (size_t)kvh * G + c % G;
-  };
 
   // ---- denominators: sum over the 8 lanes that share tig (different tokens)
 #pragma unroll
@@ -795,7 +789,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, kv_kind_of<KV>>::THREADS, 1)
 
   if (p.S == 1 || p.cmerge) pdl_launch_dependents();
 
-  finish_cta<T, KIND, D, NT, C>(p, ring, b, n_splits, m, l, o);
+  finish_cta<T, KIND, D, NT, C>(p, ring, split, kvh, b, warp, gid, tig, cols, out, qrow, n_splits, m, l, o);
 }
 
 // Combine the split partials of one (sequence, query head, 64-wide slice of D):
