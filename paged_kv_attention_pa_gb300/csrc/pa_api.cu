@@ -30,7 +30,7 @@ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 struct Plan {
   int S;
   int P;
-  int ordered = 0;  // 4-bit caches: the longest sequences' CTAs first
+  pa::Int4Mode mode = pa::kPlain;  // 4-bit caches
 };
 
 // A CTA's fixed cost (launch, first round trip, epilogue) expressed as the KV bytes
@@ -61,7 +61,7 @@ bool plan_for(int64_t S_req, int64_t max_len, int64_t p_max, int64_t p_min, int6
 }
 
 bool make_plan(int sm_count, int64_t B, int64_t Hkv, int D, pa::KvKind kv, int64_t max_len,
-               int requested, int64_t total_tokens, Plan* out) {
+               int requested, int64_t total_tokens, bool short_ctas, Plan* out) {
   const int64_t quantum = pa::tile_tokens(D, kv);
   if (max_len <= 0) {
     *out = {1, (int)quantum};
@@ -112,17 +112,32 @@ bool make_plan(int sm_count, int64_t B, int64_t Hkv, int D, pa::KvKind kv, int64
   // the longest context.
   const bool mixed =
       int4 && total_tokens > 0 && B <= pa::kOrderedBatch && total_tokens < 7 * B * max_len / 8;
-  auto ordered = [&](const Plan& pl) {
-    return mixed && pl.S == 1 && units > sm && pl.P / 4 * sm > overhead_tokens / 6 * units;
+  //
+  // Other unsplit batches of short contexts run CTAs of four warps, three an SM (head_dim 256:
+  // two), so that the start of one and the end of another pass behind the third. A few long
+  // ones leave an SM's end to one such CTA: so up to 1024 tokens for every CTA that an SM has
+  // at once. Short / plain, 8 KV heads of 128: 64 sequences of 300 11.6 / 18.8, of 1K 23.0 /
+  // 29.2, of 4K 72.7 / 74.6, of 8K 138 / 132; 32 of 512 8.6 / 11.6, of 2K 23.6 / 23.6, of 4K
+  // 42.3 / 38.8; 200 of 128-2K 62 / 86; hybrid layer, 64 of 1K 18.8 / 21.7. Mixed lengths as
+  // above: 64 of 512-4K 51.9, by length 48.2.
+  const int64_t an_sm = ceil_div(units, sm);
+  auto mode_of = [&](const Plan& pl) {
+    if (pl.S > 1 || units <= sm) return pa::kPlain;
+    if (mixed && pl.P / 4 * sm > overhead_tokens / 6 * units) return pa::kOrdered;
+    return int4 && short_ctas && pl.P <= 1024 * std::min<int64_t>(an_sm, D == 128 ? 3 : 2) ? pa::kShort
+                                                                                       : pa::kPlain;
   };
   auto consider = [&](Plan pl) {
     const int64_t waves = ceil_div(live_ctas(pl), sm);
     int64_t cost = waves * (round_up(pl.P, round_tokens) + overhead_tokens);
-    pl.ordered = ordered(pl);
-    if (pl.ordered)  // an even share or the longest context (which runs faster beside ending
+    pl.mode = mode_of(pl);
+    if (pl.mode == pa::kOrdered)  // an even share or the longest context (which runs faster beside ending
                      // CTAs), the CTAs' fixed costs, and with under two CTAs an SM their unevenness
       cost = std::max<int64_t>(3 * pl.P / 4, ceil_div(total_tokens * Hkv, sm)) + overhead_tokens * units / sm +
              std::max<int64_t>(0, pl.P - pl.P * units / (2 * sm));
+    if (pl.mode == pa::kShort)
+      cost = std::max<int64_t>(pl.P, total_tokens > 0 ? ceil_div(total_tokens * Hkv, sm) : an_sm * pl.P) +
+             overhead_tokens * an_sm / 2;
     if (int4 && pl.S > 1 && waves == 1 && live_ctas(pl) > roomy)
       cost += 100 * 1024 / (2 * pa::kv_row_bytes(D, kv));
     if (!found || cost < best_cost || (cost == best_cost && pl.S < out->S)) {
@@ -133,7 +148,7 @@ bool make_plan(int sm_count, int64_t B, int64_t Hkv, int D, pa::KvKind kv, int64
   };
   if (requested > 0) {
     if (!plan_for(requested, max_len, p_max, 0, quantum, out)) return false;
-    out->ordered = ordered(*out);
+    out->mode = mode_of(*out);
     return true;
   }
   for (int64_t c : cands) {
@@ -224,6 +239,11 @@ int64_t plan_len(const pa_decode_args* a, int64_t max_len) {
   return (a->window > 0 && a->window < max_len) ? a->window : max_len;
 }
 
+// One MMA column tile and no window: the calls that short CTAs may serve.
+bool one_tile(const pa_decode_args* a) {
+  return a->window == 0 && a->Hq / a->Hkv * (a->q_len > 0 ? a->q_len : 1) <= 8;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
@@ -303,7 +323,7 @@ pa_status pa_decode_plan(const pa_decode_args* a, int sm_count, int* splits,
   if (sm_count <= 0) return PA_ERR_CUDA;
   Plan plan{};
   if (!make_plan(sm_count, a->B, a->Hkv, a->D, kv_kind(a), plan_len(a, max_len), a->splits,
-                 plan_tokens(a), &plan))
+                 plan_tokens(a), one_tile(a), &plan))
     return PA_ERR_UNSUPPORTED;
   *splits = plan.S;
   *partition_tokens = plan.P;
@@ -381,7 +401,8 @@ static pa_status decode_ex(const pa_decode_args* a, void* workspace, size_t work
   if (sm <= 0) return PA_ERR_CUDA;
   Plan plan{};
   const pa::KvKind kv = kv_kind(a);
-  if (!make_plan(sm, a->B, a->Hkv, a->D, kv, plan_len(a, max_len), a->splits, plan_tokens(a), &plan))
+  if (!make_plan(sm, a->B, a->Hkv, a->D, kv, plan_len(a, max_len), a->splits, plan_tokens(a),
+                 one_tile(a), &plan))
     return PA_ERR_UNSUPPORTED;
   const int G = a->Hq / a->Hkv;
   const int rows = a->q_len > 0 ? a->q_len : 1;
@@ -423,7 +444,7 @@ static pa_status decode_ex(const pa_decode_args* a, void* workspace, size_t work
   p.steal = reinterpret_cast<int*>(ws + 256);
   p.window = a->window;
   p.q_len = rows;
-  p.ordered = plan.ordered;
+  p.mode = plan.mode;
   p.kv = kv;
   p.v_scale = kv == pa::kKv16 ? 1.f : a->v_scale;
   // scores live in the exp2 domain; the scale of an fp8 or 4-bit K multiplies every score

@@ -25,9 +25,11 @@
 
 namespace pa {
 
-template <int D, int NT>
+template <int D, int NT, Int4Mode MODE>
 struct Int4Cfg {
-  static constexpr int NW = warps_per_cta(D, kKvInt4, NT);
+  static constexpr bool SHORT = MODE == kShort;
+  static constexpr int NW = SHORT ? 4 : warps_per_cta(D, kKvInt4, NT);
+  static constexpr int CTAS = SHORT ? (D == 128 ? 3 : 2) : 1;  // resident per SM
   static constexpr int THREADS = NW * 32;
   static constexpr int TW = tile_tokens(D, kKvInt4);  // tokens per tile, at most one per lane
   static constexpr int GT = 8 * NT;
@@ -41,7 +43,7 @@ struct Int4Cfg {
                                                                                  // in shared memory
   static constexpr int QBYTES = QSHARED ? NT * KS * 256 : 0;
   static constexpr int FIXED = 1024 + QBYTES;  // the slots' mbarriers, by_length's answer; the query
-  static constexpr int DEPTH_FIT = (kSmemBudget - FIXED) / (NW * SLOT_BYTES);
+  static constexpr int DEPTH_FIT = (kSmemBudget / CTAS - FIXED) / (NW * SLOT_BYTES);
   static constexpr int DEPTH = DEPTH_FIT > 5 ? 5 : DEPTH_FIT;  // slots per warp
   static constexpr int WARP_RING = DEPTH * SLOT_BYTES;
   static constexpr int RING = NW * WARP_RING;
@@ -86,9 +88,11 @@ __device__ __forceinline__ int by_length(const DecodeParams& p, int r) {
   return b;
 }
 
-template <typename T, int D, int NT, bool WIN, bool ORDERED>
-__global__ void __launch_bounds__(Int4Cfg<D, NT>::THREADS, 1) decode_int4_kernel(const DecodeParams p) {
-  using C = Int4Cfg<D, NT>;
+template <typename T, int D, int NT, bool WIN, Int4Mode MODE>
+__global__ void __launch_bounds__(Int4Cfg<D, NT, MODE>::THREADS, Int4Cfg<D, NT, MODE>::CTAS)
+    decode_int4_kernel(const DecodeParams p) {
+  using C = Int4Cfg<D, NT, MODE>;
+  constexpr bool ORDERED = MODE == kOrdered;
   using Row = Int4Row<D>;
   constexpr int kWarps = C::NW, kThreads = C::THREADS;
   constexpr int MT = C::TW / 16;  // MMA row blocks of a tile
@@ -507,10 +511,10 @@ __global__ void __launch_bounds__(Int4Cfg<D, NT>::THREADS, 1) decode_int4_kernel
   }
 }
 
-template <typename T, int D, int NT, bool WIN, bool ORDERED>
-struct DecodeKernel<T, int4g32, D, NT, WIN, ORDERED> {
-  using C = Int4Cfg<D, NT>;
-  static constexpr auto kernel = decode_int4_kernel<T, D, NT, WIN, ORDERED>;
+template <typename T, int D, int NT, bool WIN, Int4Mode MODE>
+struct DecodeKernel<T, int4g32, D, NT, WIN, MODE> {
+  using C = Int4Cfg<D, NT, MODE>;
+  static constexpr auto kernel = decode_int4_kernel<T, D, NT, WIN, MODE>;
 };
 
 }  // namespace pa

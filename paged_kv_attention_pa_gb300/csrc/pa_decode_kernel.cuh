@@ -918,15 +918,15 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream
 
 // The kernel of a cache type and its configuration (4-bit caches: pa_decode_int4.cuh, which has
 // an ORDERED one).
-template <typename T, typename KV, int D, int NT, bool WIN, bool ORDERED>
+template <typename T, typename KV, int D, int NT, bool WIN, Int4Mode MODE>
 struct DecodeKernel {
   using C = Cfg<D, NT, kv_kind_of<KV>>;
   static constexpr auto kernel = decode_kernel<T, KV, D, NT, WIN>;
 };
 
-template <typename T, typename KV, int D, int NT, bool WIN, bool ORDERED = false>
+template <typename T, typename KV, int D, int NT, bool WIN, Int4Mode MODE = kPlain>
 cudaError_t launch_decode_nt(const DecodeParams& p, cudaStream_t st, int* kernels) {
-  using Kernel = DecodeKernel<T, KV, D, NT, WIN, ORDERED>;
+  using Kernel = DecodeKernel<T, KV, D, NT, WIN, MODE>;
   using C = typename Kernel::C;
   auto kern = Kernel::kernel;
   // The dynamic shared memory opt-in is per device; remember which devices have it.
@@ -994,10 +994,11 @@ template <typename T, typename KV, int D>
 cudaError_t launch_decode_dispatch(const DecodeParams& p, cudaStream_t st, int* kernels) {
   const int cols = p.G * p.q_len;
   if constexpr (std::is_same<KV, int4g32>::value) {
-    if (p.ordered) {
-      if (cols <= 8) return launch_decode_nt<T, KV, D, 1, false, true>(p, st, kernels);
-      if (cols <= 16 || D != 128) return launch_decode_nt<T, KV, D, 2, false, true>(p, st, kernels);
-      if constexpr (D == 128) return launch_decode_nt<T, KV, D, 4, false, true>(p, st, kernels);
+    if (p.mode == kShort) return launch_decode_nt<T, KV, D, 1, false, kShort>(p, st, kernels);
+    if (p.mode == kOrdered) {
+      if (cols <= 8) return launch_decode_nt<T, KV, D, 1, false, kOrdered>(p, st, kernels);
+      if (cols <= 16 || D != 128) return launch_decode_nt<T, KV, D, 2, false, kOrdered>(p, st, kernels);
+      if constexpr (D == 128) return launch_decode_nt<T, KV, D, 4, false, kOrdered>(p, st, kernels);
     }
   }
   if (p.window > 0)

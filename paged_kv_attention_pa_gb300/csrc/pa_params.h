@@ -113,7 +113,10 @@ constexpr int kHeaderBytes = 256 + kStealUnits * 4;  // error word, then the cou
 static_assert(kHeaderBytes % 256 == 0, "header keeps 256-byte alignment");
 static_assert(kHeaderBytes == PA_WORKSPACE_HEADER_BYTES, "header size is part of the ABI");
 
-constexpr int kOrderedBatch = 256;  // sequences of a batch whose CTAs may start by length
+// How a 4-bit decode call runs (see make_plan): as the others do, unsplit with the longest
+// sequences' CTAs first (batches of up to kOrderedBatch), or unsplit with short CTAs.
+enum Int4Mode { kPlain, kOrdered, kShort };
+constexpr int kOrderedBatch = 256;
 
 struct DecodeParams {
   const void* q;
@@ -137,7 +140,7 @@ struct DecodeParams {
   int Ps;             // static tokens per split (== P: no shared tiles)
   int window;         // > 0: attend to the last `window` tokens only
   int q_len;          // query rows per sequence (causal among themselves)
-  int ordered;        // 4-bit caches: the longest sequences' CTAs first (see by_length)
+  Int4Mode mode;      // 4-bit caches
   KvKind kv;          // what the caches hold (fp8, 4-bit: k_scale is folded into scale_log2)
   int cmerge;         // 0, or C = S: the S splits of each (sequence, KV head) run as one
                       // thread-block cluster and merge in distributed shared memory (set

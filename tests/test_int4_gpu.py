@@ -111,6 +111,28 @@ def test_decode_int4_mixed_batches_run_by_length(cuda_lib, B, Hq, Hkv, D, bs, ro
         assert torch.equal(rh.bits(outs[0].cpu()), rh.bits(outs[1].cpu()))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("B,Hq,Hkv,D,bs,longest", [
+    (40, 8, 4, 128, 16, 300), (160, 1, 1, 128, 7, 2000), (30, 24, 6, 256, 33, 500),
+    (300, 8, 8, 128, 16, 70), (20, 64, 8, 128, 16, 1000), (90, 4, 2, 256, 784, 1900),
+])
+def test_decode_int4_many_short_contexts(cuda_lib, dtype, B, Hq, Hkv, D, bs, longest):
+    # more (sequence, KV head) pairs than SMs, unsplit: CTAs of four warps
+    r = np.random.default_rng(B)
+    lens = [int(x) for x in r.integers(0, longest + 1, B)]
+    lens[0], lens[1], lens[2], lens[-1] = longest, 0, 1, longest
+    run_case(cuda_lib, lens, Hq, Hkv, D, bs, dtype, seed=16)
+    run_case(cuda_lib, lens, Hq, Hkv, D, bs, dtype, seed=17, total_tokens=sum(lens), deterministic=True)
+    kc, vc, bt, _, _ = rh.random_int4_pool(lens, bs, Hkv, D, 18)
+    lens[3], lens[4] = -1, longest + 1
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    out = cuda_lib.decode(torch.randn((B, Hq, D)).to(rh.DT[dtype]).cuda(), kc.cuda(), vc.cuda(),
+                          bt.clamp(min=0).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), 0.088,
+                          max_seq_len=longest, workspace=ws)
+    assert cuda_lib.read_device_errors(ws) == cuda_lib.PA_DEVERR_SEQ_LEN
+    assert torch.isfinite(out[5:]).all() and not out[3].any()
+
+
 @pytest.mark.parametrize("W", [1, 17, 1000])
 def test_decode_int4_window(cuda_lib, W):
     run_case(cuda_lib, [1500, 999, 16, 1], 8, 4, 128, 16, seed=4, window=W)
