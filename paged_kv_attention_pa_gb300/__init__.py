@@ -309,9 +309,9 @@ def _rows_workspace(t: torch.Tensor, dev: int, sh: int, stream) -> Optional[torc
     return ws
 
 
-def _on(stream, call, *args):
-    """call(*args), what it allocates allocated in the order of the caller's stream."""
-    if stream is None:
+def _on(stream, allocates: bool, call, *args):
+    """call(*args), what it allocates (if anything) allocated in the order of the caller's stream."""
+    if stream is None or not allocates:
         return call(*args)
     with torch.cuda.stream(stream):
         return call(*args)
@@ -350,16 +350,16 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     given = out
     dev, sh = _call_on(q, stream)
     ws = workspace if workspace is not None else _workspaces.get((dev, sh))
-    rc, out = _on(stream, _native.decode, q, k_cache, v_cache, block_tables, seq_lens, scale, out,
-                  max_seq_len, splits, window, k_scale, v_scale, deterministic, total_tokens, ws,
-                  sh)
+    rc, out = _on(stream, out is None, _native.decode, q, k_cache, v_cache, block_tables, seq_lens,
+                  scale, out, max_seq_len, splits, window, k_scale, v_scale, deterministic,
+                  total_tokens, ws, sh)
     if rc == PA_ERR_WORKSPACE and workspace is None:  # none yet, or too small: nothing was launched
         ws = workspace_for(make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale,
                                      max_seq_len, splits, window, k_scale, v_scale, deterministic,
                                      total_tokens), q.device, sh, stream)
-        rc, out = _on(stream, _native.decode, q, k_cache, v_cache, block_tables, seq_lens, scale, out,
-                      max_seq_len, splits, window, k_scale, v_scale, deterministic, total_tokens,
-                      ws, sh)
+        rc, out = _on(stream, out is None, _native.decode, q, k_cache, v_cache, block_tables,
+                      seq_lens, scale, out, max_seq_len, splits, window, k_scale, v_scale,
+                      deterministic, total_tokens, ws, sh)
     if rc != PA_OK:
         raise PAError(rc, "pa_decode_ex")
     return _made_here(out, given, stream)
@@ -458,8 +458,9 @@ def append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     dev, sh = _call_on(k_cache, stream)
     turns, interleaved, amplitude = _NO_ROPE if rope is None else rope
     ws = workspace if workspace is not None else _rows_workspace(k_cache, dev, sh, stream)
-    rc, rotated = _on(stream, _native.append, k, v, k_cache, v_cache, block_tables, seq_lens, q,
-                      q_out, starts, turns, interleaved, amplitude, k_scale, v_scale, ws, sh)
+    rc, rotated = _on(stream, q is not None and q_out is None, _native.append, k, v, k_cache,
+                      v_cache, block_tables, seq_lens, q, q_out, starts, turns, interleaved,
+                      amplitude, k_scale, v_scale, ws, sh)
     if rc != PA_OK:
         raise PAError(rc, "pa_append")
     return _made_here(rotated, q_out, stream)
@@ -485,8 +486,8 @@ def gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Ten
     if code is None:
         raise TypeError("dtype must be float16 or bfloat16")
     ws = workspace if workspace is not None else _rows_workspace(k_cache, dev, sh, stream)
-    rc, k, v = _on(stream, _native.gather, k_cache, v_cache, block_tables, seq_lens, rows, starts,
-                   code, k_out, v_out, k_scale, v_scale, ws, sh)
+    rc, k, v = _on(stream, k_out is None or v_out is None, _native.gather, k_cache, v_cache,
+                   block_tables, seq_lens, rows, starts, code, k_out, v_out, k_scale, v_scale, ws, sh)
     if rc != PA_OK:
         raise PAError(rc, "pa_gather")
     return _made_here(k, k_out, stream), _made_here(v, v_out, stream)
