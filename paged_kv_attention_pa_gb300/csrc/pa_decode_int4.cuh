@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(Int4Cfg<D, NT, MODE>::THREADS, Int4Cfg<D, NT, 
   if constexpr (ORDERED) {
     b = p.B <= 32 ? by_length<1>(p, b) : p.B <= 64 ? by_length<2>(p, b) : by_length<kOrderedBatch / 32>(p, b);
     if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sequence), "r"(b) : "memory");
+    __syncwarp();
   }
 
   // ---- prologue: length, table entries of the first static tiles and query fragments
