@@ -365,10 +365,21 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     return _made_here(out, given, stream)
 
 
+def _only_plain(q, k_cache, v_cache):
+    """Refuse what pa_decode and pa_decode_noalloc have no argument for: other caches than of
+    q's dtype, and several query rows."""
+    if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
+        raise TypeError("the caches must have q's dtype here: fp8 and 4-bit caches are for decode()")
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, D] here: several query rows are for decode()")
+
+
 def decode_plain(q, k_cache, v_cache, block_tables, seq_lens, scale, out=None,
                  max_seq_len: Optional[int] = None, workspace=None, stream=None):
-    """The same operation through pa_decode, the plain positional entry point."""
+    """The same operation through pa_decode, the plain positional entry point: caches of q's
+    dtype and one query row per sequence."""
     lib = load()
+    _only_plain(q, k_cache, v_cache)
     if out is None:
         out = torch.empty_like(q)
     args = make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale, max_seq_len, 0)
@@ -388,8 +399,10 @@ def decode_noalloc(q, k_cache, v_cache, block_tables, seq_lens, scale, out=None,
                    max_seq_len: Optional[int] = None, stream=None):
     """The same operation through pa_decode_noalloc: no workspace, no allocation by
     the library (the split partials live in a fixed device array of the library,
-    shared by all such calls on a device; see include/pa.h for the limit)."""
+    shared by all such calls on a device; see include/pa.h for the limit). Caches of q's
+    dtype and one query row per sequence."""
     lib = load()
+    _only_plain(q, k_cache, v_cache)
     if out is None:
         out = torch.empty_like(q)
     args = make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale, max_seq_len, 0)

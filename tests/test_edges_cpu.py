@@ -1,0 +1,29 @@
+"""Calls at the edges of what the Python functions and the C entry points take, without a GPU."""
+import pytest
+import torch
+
+import paged_kv_attention_pa_gb300 as pa
+from paged_kv_attention_pa_gb300 import build as pa_build
+
+
+@pytest.fixture(scope="module")
+def lib():
+    pa_build.build()
+    return pa.load()
+
+
+@pytest.mark.parametrize("fn", [pa.decode_plain, pa.decode_noalloc])
+def test_plain_calls_refuse_what_their_entry_points_cannot_tell(lib, fn):
+    # pa_decode and pa_decode_noalloc take no cache type and no query rows: an fp8 or 4-bit cache
+    # would be read as 16-bit rows, past its end
+    q = torch.zeros(2, 8, 128, dtype=torch.bfloat16)
+    kc = torch.zeros(4, 16, 8, 128, dtype=torch.bfloat16)
+    bt, sl = torch.zeros(2, 1, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    c4 = torch.zeros(4, 8, 16, pa.int4_row_bytes(128), dtype=torch.uint8)
+    for k, v in ((c4, c4), (kc.to(torch.float8_e4m3fn),) * 2, (kc, c4), (kc.half(),) * 2):
+        with pytest.raises(TypeError, match="dtype"):
+            fn(q, k, v, bt, sl, 0.1)
+    with pytest.raises(ValueError, match="B, Hq, D"):
+        fn(q[:, None].expand(2, 3, 8, 128).contiguous(), kc, kc, bt, sl, 0.1)
+    with pytest.raises(ValueError, match="CUDA"):
+        fn(q, kc, kc, bt, sl, 0.1)
