@@ -63,11 +63,11 @@ bool plan_for(int64_t S_req, int64_t max_len, int64_t p_max, int64_t p_min, int6
 bool make_plan(int sm_count, int64_t B, int64_t Hkv, int D, pa::KvKind kv, int64_t max_len,
                int requested, int64_t total_tokens, bool short_ctas, Plan* out) {
   const int64_t quantum = pa::tile_tokens(D, kv);
-  if (max_len <= 0) {
+  const int64_t units = B * Hkv;
+  if (max_len <= 0 || units <= 0) {  // an empty batch: nothing to split
     *out = {1, (int)quantum};
     return true;
   }
-  const int64_t units = B * Hkv;
   const int64_t sm = sm_count > 0 ? sm_count : 1;
   const int64_t p_max = round_up(max_len, quantum);
   bool found = false;

@@ -27,3 +27,10 @@ def test_plain_calls_refuse_what_their_entry_points_cannot_tell(lib, fn):
         fn(q[:, None].expand(2, 3, 8, 128).contiguous(), kc, kc, bt, sl, 0.1)
     with pytest.raises(ValueError, match="CUDA"):
         fn(q, kc, kc, bt, sl, 0.1)
+
+
+@pytest.mark.parametrize("kw", [{}, dict(kv_fp8=True), dict(kv_int4=True), dict(splits=3), dict(window=64)])
+def test_plan_of_an_empty_batch(lib, kw):
+    # nothing to split, and no division by the number of (sequence, KV head) pairs
+    S, P = pa.plan(0, 8, 8, 128, 16, 512, sm_count=152, **kw)
+    assert S == 1 and P >= 16
