@@ -123,7 +123,8 @@ int32_t tables_of(const Tensor& bt, const Tensor& sl, const Tensor* starts) {
 int64_t row_stride(const Tensor& t, const char* name) {
   const auto s = t.sizes(), st = t.strides();
   const int d = (int)s.size();
-  if (t.numel() && (st[d - 1] != 1 || (s[d - 2] > 1 && st[d - 2] != s[d - 1]))) {
+  if (t.numel() == 0) return 0;  // no rows: their spacing says nothing
+  if (st[d - 1] != 1 || (s[d - 2] > 1 && st[d - 2] != s[d - 1])) {
     PyErr_Format(PyExc_ValueError, "the heads of a row of %s must be contiguous", name);
     throw Refused{};
   }
@@ -247,6 +248,9 @@ PyObject* do_append(PyObject* const* v) {
     refuse_value("q_out must have q's shape and dtype");
   if (turns && (turns->scalar_type() != ScalarType::Long || turns->dim() != 1))
     refuse_type("rope.turns must be int64 [rot_dim / 2]");
+  a.k_stride = row_stride(k, "k");
+  a.v_stride = row_stride(val, "v");
+  if (q) a.q_stride = row_stride(*q, "q");
   const int64_t dev = kc.get_device();
   on_device(kc, dev, true, "k_cache");
   on_device(vc, dev, true, "v_cache");
@@ -259,8 +263,6 @@ PyObject* do_append(PyObject* const* v) {
   if (starts) on_device(*starts, dev, true, "starts");
   if (turns) on_device(*turns, dev, true, "rope.turns");
   a.rows = starts || d == 4 ? to32(k.size(starts ? 0 : 1)) : 1;
-  a.k_stride = row_stride(k, "k");
-  a.v_stride = row_stride(val, "v");
   a.Hkv = c.Hkv;
   a.D = c.D;
   a.block_size = c.block_size;
@@ -274,7 +276,6 @@ PyObject* do_append(PyObject* const* v) {
   Tensor out;
   if (q) {
     a.Hq = to32(q->size(d - 2));
-    a.q_stride = row_stride(*q, "q");
     out = given ? *given : new_like(*q);
     a.q = data<void>(*q);
     a.q_out = data<void>(out);

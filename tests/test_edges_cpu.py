@@ -34,3 +34,21 @@ def test_plan_of_an_empty_batch(lib, kw):
     # nothing to split, and no division by the number of (sequence, KV head) pairs
     S, P = pa.plan(0, 8, 8, 128, 16, 512, sm_count=152, **kw)
     assert S == 1 and P >= 16
+
+
+@pytest.mark.parametrize("B", [0, 1, 3])
+def test_append_of_no_tokens_is_not_refused_for_its_strides(lib, B):
+    # [B, 0, H, D]: the next check is the device's
+    k, q = torch.zeros(B, 0, 2, 128).half(), torch.zeros(B, 0, 4, 128).half()
+    kc = torch.zeros(4, 16, 2, 128).half()
+    bt, sl = torch.zeros(B, 1, dtype=torch.int32), torch.ones(B, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        pa.append(k, k, kc, kc, bt, sl, q=q)
+
+
+def test_append_refuses_rows_that_are_not_evenly_spaced(lib):
+    k = torch.zeros(3, 4, 2, 128).half()[:, :3]
+    kc = torch.zeros(4, 16, 2, 128).half()
+    bt, sl = torch.zeros(3, 1, dtype=torch.int32), torch.ones(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="evenly spaced"):
+        pa.append(k, k, kc, kc, bt, sl)

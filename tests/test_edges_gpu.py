@@ -1,0 +1,24 @@
+"""Calls at the edges of what append, gather and decode take (GB300 only)."""
+import numpy as np
+import pytest
+import torch
+
+import rows_harness as rh
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("B", [1, 3])
+def test_a_step_without_new_tokens(cuda_lib, B):
+    # [B, 0, heads, D]: nothing written, nothing rotated, nothing read
+    kc = torch.full((4, 16, 2, 128), 3.0, dtype=torch.float16, device="cuda")
+    k, q = (torch.zeros(B, 0, h, 128, dtype=torch.float16, device="cuda") for h in (2, 4))
+    bt, sl = i32([[b] for b in range(B)]), i32([5] * B)
+    out = cuda_lib.append(k, k, kc, kc, bt, sl, q=q)
+    assert out.shape == q.shape and torch.all(kc == 3.0)
+    ko, vo = cuda_lib.gather(kc, kc, bt, sl, 0)
+    assert ko.shape == vo.shape == k.shape
