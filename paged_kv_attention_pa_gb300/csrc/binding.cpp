@@ -33,8 +33,11 @@ const Tensor& tensor(PyObject* o) {
 }
 const Tensor* optional_tensor(PyObject* o) { return o == Py_None ? nullptr : &tensor(o); }
 
-int64_t integer(PyObject* o) {
-  const long long v = PyLong_AsLongLong(o);
+int64_t integer(PyObject* o) {  // int(o)
+  PyObject* n = PyLong_Check(o) ? Py_NewRef(o) : PyNumber_Long(o);
+  if (!n) throw Refused{};
+  const long long v = PyLong_AsLongLong(n);
+  Py_DECREF(n);
   if (v == -1 && PyErr_Occurred()) throw Refused{};
   return v;
 }
@@ -47,7 +50,7 @@ int32_t to32(int64_t v) {
   if (v > INT32_MAX) refuse_value("a tensor is too large");
   return (int32_t)v;
 }
-float number(PyObject* o) {
+float number(PyObject* o) {  // float(o)
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw Refused{};
   return (float)v;
@@ -184,6 +187,14 @@ PyObject* do_decode(PyObject* const* v) {
   if (bt.dim() != 2 || bt.size(0) != q.size(0) || sl.dim() != 1 || sl.size(0) != q.size(0))
     refuse_value("block_tables must be [B, max_blocks] and seq_lens [B]");
   if (given && given->sizes() != q.sizes()) refuse_value("out must have q's shape");
+  a.max_seq_len = v[7] == Py_None ? 0 : integer32(v[7]);
+  a.scale = number(v[5]);
+  a.splits = integer32(v[8]);
+  a.window = integer32(v[9]);
+  a.k_scale = c.kv == PA_KV_AS_DTYPE ? 1.f : number(v[10]);
+  a.v_scale = c.kv == PA_KV_AS_DTYPE ? 1.f : number(v[11]);
+  a.flags = truth(v[12]) ? PA_FLAG_DETERMINISTIC : 0u;
+  a.total_tokens = integer(v[13]);
   const int64_t dev = q.get_device();
   on_device(q, dev, true, "q");
   on_device(kc, dev, true, "k_cache");
@@ -199,16 +210,8 @@ PyObject* do_decode(PyObject* const* v) {
   a.block_size = c.block_size;
   a.num_blocks = c.num_blocks;
   a.max_blocks_per_seq = to32(bt.size(1));
-  a.max_seq_len = v[7] == Py_None ? 0 : integer32(v[7]);
-  a.scale = number(v[5]);
   a.dtype = dt;
-  a.splits = integer32(v[8]);
-  a.window = integer32(v[9]);
   a.kv_dtype = c.kv;
-  a.k_scale = c.kv == PA_KV_AS_DTYPE ? 1.f : number(v[10]);
-  a.v_scale = c.kv == PA_KV_AS_DTYPE ? 1.f : number(v[11]);
-  a.flags = truth(v[12]) ? PA_FLAG_DETERMINISTIC : 0u;
-  a.total_tokens = integer(v[13]);
   const Workspace ws(v[14], dev);
   const Tensor out = given ? *given : new_like(q);
   a.q = data<void>(q);

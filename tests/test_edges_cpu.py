@@ -1,4 +1,5 @@
 """Calls at the edges of what the Python functions and the C entry points take, without a GPU."""
+import numpy as np
 import pytest
 import torch
 
@@ -52,3 +53,19 @@ def test_append_refuses_rows_that_are_not_evenly_spaced(lib):
     bt, sl = torch.zeros(3, 1, dtype=torch.int32), torch.ones(3, dtype=torch.int32)
     with pytest.raises(ValueError, match="evenly spaced"):
         pa.append(k, k, kc, kc, bt, sl)
+
+
+def test_numbers_are_taken_as_int_and_float_take_them(lib):
+    # whole numbers held as floats, arrays or tensors of one element; the next check is the device's
+    q = torch.zeros(2, 8, 128).half()
+    kc = torch.zeros(4, 16, 8, 128).half()
+    bt, sl = torch.zeros(2, 1, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    for n in (16, 16.0, np.float64(16), np.int32(16), torch.tensor(16), torch.tensor(16.0)):
+        with pytest.raises(ValueError, match="CUDA"):
+            pa.decode(q, kc, kc, bt, sl, np.float32(0.1), max_seq_len=n, splits=n, window=n, total_tokens=n)
+        with pytest.raises(ValueError, match="CUDA"):
+            pa.decode(q, kc, kc, bt, sl, torch.tensor(0.1), max_seq_len=n)
+    for bad in ("sixteen", [16], torch.zeros(2), float("nan"), float("inf"), 2.0 ** 40):
+        with pytest.raises((TypeError, ValueError, RuntimeError, OverflowError)) as e:
+            pa.decode(q, kc, kc, bt, sl, 0.1, max_seq_len=bad)
+        assert "CUDA" not in str(e.value)
