@@ -8,6 +8,7 @@
 #include <exception>
 
 #include <ATen/ops/empty.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "pa.h"
@@ -359,8 +360,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return F(args);
   } catch (const Refused&) {
     return nullptr;
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {  // torch's own (a failed allocation is torch.OutOfMemoryError)
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }

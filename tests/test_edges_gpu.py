@@ -22,3 +22,11 @@ def test_a_step_without_new_tokens(cuda_lib, B):
     assert out.shape == q.shape and torch.all(kc == 3.0)
     ko, vo = cuda_lib.gather(kc, kc, bt, sl, 0)
     assert ko.shape == vo.shape == k.shape
+
+
+def test_an_allocation_that_fails_is_out_of_memory(cuda_lib):
+    # 2^30 rows of two heads of 128 in 16 bits, 550 GB: the output cannot be made, nothing is launched
+    kc = torch.zeros((4, 16, 2, 128), dtype=torch.float16, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        cuda_lib.gather(kc, kc, i32([[0]]), i32([5]), 1 << 30)
+    assert cuda_lib.gather(kc, kc, i32([[0]]), i32([5]), 5)[0].shape == (1, 5, 2, 128)
