@@ -1,4 +1,9 @@
 """Calls at the edges of what the Python functions and the C entry points take, without a GPU."""
+import os
+import shutil
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -69,3 +74,20 @@ def test_numbers_are_taken_as_int_and_float_take_them(lib):
         with pytest.raises((TypeError, ValueError, RuntimeError, OverflowError)) as e:
             pa.decode(q, kc, kc, bt, sl, 0.1, max_seq_len=bad)
         assert "CUDA" not in str(e.value)
+
+
+def test_a_library_loaded_from_elsewhere_serves_every_call(lib, tmp_path):
+    # one library is mapped, the one at the path given to load()
+    other = str(tmp_path / "libpa_copy.so")
+    shutil.copy(pa.LIB_PATH, other)
+    code = ("import sys, torch, paged_kv_attention_pa_gb300 as pa\n"
+            f"pa.load({other!r})\n"
+            "maps = open('/proc/self/maps').read()\n"
+            "assert 'libpa_copy.so' in maps and '/libpa.so' not in maps\n"
+            "q, c = torch.zeros(2, 8, 128).half(), torch.zeros(4, 16, 8, 128).half()\n"
+            "bt, sl = torch.zeros(2, 1, dtype=torch.int32), torch.ones(2, dtype=torch.int32)\n"
+            "try:\n    pa.decode(q, c, c, bt, sl, 0.1)\n"
+            "except ValueError as e:\n    assert 'CUDA' in str(e)\n"
+            "else:\n    sys.exit(3)\n")
+    root = os.path.dirname(os.path.dirname(pa.LIB_PATH))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root)
