@@ -278,6 +278,7 @@ def _workspace(need: int, device: torch.device, stream_handle: int, stream=None)
             return new  # the graph's own, zeroed at every replay: of no use to calls outside it
     if ws is not None:
         _outgrown.append(ws)
+        new.outgrown = ws  # its error word is read with the new one's
     _workspaces[key] = new
     return new
 
@@ -548,15 +549,20 @@ def kernel_count(q, k_cache, v_cache, block_tables, seq_lens, scale, max_seq_len
 
 
 def read_device_errors(workspace: torch.Tensor, stream=None) -> int:
-    """Wait for the stream, return and clear the PA_DEVERR_* bits of a workspace."""
+    """Wait for the stream, return and clear the PA_DEVERR_* bits of a workspace (and, of a
+    default one, those of the smaller ones that it took the place of)."""
     lib = load()
     _ensure_device(lib, workspace.device.index)
-    flags = ctypes.c_uint32(0)
-    rc = lib.pa_read_device_errors(workspace.data_ptr(),
-                                   _stream_handle(workspace.device, stream), ctypes.byref(flags))
-    if rc != PA_OK:
-        raise PAError(rc, "pa_read_device_errors")
-    return flags.value
+    sh = _stream_handle(workspace.device, stream)
+    found = 0
+    while workspace is not None:
+        flags = ctypes.c_uint32(0)
+        rc = lib.pa_read_device_errors(workspace.data_ptr(), sh, ctypes.byref(flags))
+        if rc != PA_OK:
+            raise PAError(rc, "pa_read_device_errors")
+        found |= flags.value
+        workspace = getattr(workspace, "outgrown", None)
+    return found
 
 
 def default_workspace(device=None, stream=None) -> Optional[torch.Tensor]:

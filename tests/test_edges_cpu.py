@@ -1,4 +1,5 @@
 """Calls at the edges of what the Python functions and the C entry points take, without a GPU."""
+import ctypes
 import os
 import shutil
 import subprocess
@@ -91,3 +92,42 @@ def test_a_library_loaded_from_elsewhere_serves_every_call(lib, tmp_path):
             "else:\n    sys.exit(3)\n")
     root = os.path.dirname(os.path.dirname(pa.LIB_PATH))
     subprocess.run([sys.executable, "-c", code], check=True, cwd=root)
+
+
+class FakeLib:
+    """pa_read_device_errors on host memory."""
+
+    def pa_set_device(self, index):
+        return pa.PA_OK
+
+    def pa_read_device_errors(self, ws, stream, flags):
+        word = ctypes.c_uint32.from_address(ws)
+        flags._obj.value, word.value = word.value, 0
+        return pa.PA_OK
+
+
+class FakeStream:
+    cuda_stream = 77
+
+
+@pytest.fixture
+def host_workspaces(monkeypatch):
+    monkeypatch.setattr(pa, "load", FakeLib)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(pa, "_workspaces", {})
+    monkeypatch.setattr(pa, "_outgrown", [])
+    return lambda need: pa._workspace(need, torch.device("cpu"), FakeStream.cuda_stream)
+
+
+def test_error_bits_survive_the_growth_of_a_workspace(host_workspaces):
+    # append's kernel reports into the stream's workspace, decode replaces it by a larger one
+    ws = host_workspaces(pa.PA_WORKSPACE_HEADER_BYTES)
+    ws[0] = pa.PA_DEVERR_BLOCK_INDEX
+    more = host_workspaces(ws.numel() + 1)
+    more[0] = pa.PA_DEVERR_COPY
+    most = host_workspaces(more.numel() + 1)
+    most[0] = pa.PA_DEVERR_SEQ_LEN
+    assert len({w.data_ptr() for w in (ws, more, most)}) == 3
+    assert pa.read_device_errors(most, FakeStream) == 7
+    assert pa.read_device_errors(most, FakeStream) == 0
+    assert pa.read_device_errors(torch.zeros(64, dtype=torch.uint8), FakeStream) == 0
