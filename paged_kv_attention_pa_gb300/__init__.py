@@ -258,27 +258,49 @@ def make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale: float,
     return a
 
 
-# One workspace per (device, stream); grown on demand, zero-filled when made. Workspaces that
-# were outgrown stay allocated: a captured graph may still write to them when it is replayed.
-# One made while its stream is captured belongs to that graph alone.
+# One workspace per (device, stream), and per capture one of each stream that takes part in it;
+# grown on demand, zero-filled when made. A captured call never uses the workspace of calls
+# outside its graph: graphs, and calls beside them, may run at the same time. Made during a
+# capture it lies in the graph's own memory and is zeroed once in every replay. Workspaces that
+# were outgrown stay allocated: calls before may have left error bits in them.
 _workspaces = {}
+_captured = {}  # (device, stream) -> (id of its last capture, that capture's workspace)
 _outgrown = []
 
 
+def _capture_of(stream_handle: int) -> int:
+    """The id of the capture that a stream takes part in, 0 outside one."""
+    return _native.capture_id(stream_handle)
+
+
+def _kept(key, capture: int) -> Optional[torch.Tensor]:
+    """The workspace that a (device, stream) has, in a capture that capture's."""
+    if not capture:
+        return _workspaces.get(key)
+    held = _captured.get(key)
+    return held[1] if held is not None and held[0] == capture else None
+
+
+def _default_workspace(dev: int, stream_handle: int) -> Optional[torch.Tensor]:
+    return _kept((dev, stream_handle), _capture_of(stream_handle)) if dev >= 0 else None
+
+
 def _workspace(need: int, device: torch.device, stream_handle: int, stream=None) -> torch.Tensor:
-    key = (device.index, stream_handle)
-    ws = _workspaces.get(key)
+    key, capture = (device.index, stream_handle), _capture_of(stream_handle)
+    ws = _kept(key, capture)
     if ws is not None and ws.numel() >= need:
         return ws
     if ws is not None:
         need = max(need, 2 * ws.numel())
     with torch.cuda.stream(stream):  # zeroed in the order of the call's stream
         new = torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
-        if torch.cuda.is_current_stream_capturing():
-            return new  # the graph's own, zeroed at every replay: of no use to calls outside it
+    if ws is not None:
+        new.outgrown = ws  # its error word is read with the new one's
+    if capture:
+        _captured[key] = (capture, new)
+        return new
     if ws is not None:
         _outgrown.append(ws)
-        new.outgrown = ws  # its error word is read with the new one's
     _workspaces[key] = new
     return new
 
@@ -304,7 +326,7 @@ def _call_on(t: torch.Tensor, stream) -> Tuple[int, int]:
 
 def _rows_workspace(t: torch.Tensor, dev: int, sh: int, stream) -> Optional[torch.Tensor]:
     """The workspace whose error word append and gather use: any of the stream's."""
-    ws = _workspaces.get((dev, sh))
+    ws = _default_workspace(dev, sh)
     if ws is None and dev >= 0:
         ws = _workspace(PA_WORKSPACE_HEADER_BYTES, t.device, sh, stream)
     return ws
@@ -345,12 +367,12 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     share out its tail as they finish, and the last bit may vary from call to call).
     total_tokens, the sum of seq_lens when the caller knows it on the host, helps the
     split plan for batches of mixed lengths. Asynchronous on the current (or given)
-    stream. Without `workspace` the call uses the one kept for its device and stream: graphs
-    captured on one stream that may be replayed at the same time need workspaces of their own.
+    stream. Without `workspace` the call uses the one kept for its device and stream; captured
+    calls use one that belongs to their graph (see default_workspace).
     """
     given = out
     dev, sh = _call_on(q, stream)
-    ws = workspace if workspace is not None else _workspaces.get((dev, sh))
+    ws = workspace if workspace is not None else _default_workspace(dev, sh)
     rc, out = _on(stream, out is None, _native.decode, q, k_cache, v_cache, block_tables, seq_lens,
                   scale, out, max_seq_len, splits, window, k_scale, v_scale, deterministic,
                   total_tokens, ws, sh)
@@ -566,6 +588,9 @@ def read_device_errors(workspace: torch.Tensor, stream=None) -> int:
 
 
 def default_workspace(device=None, stream=None) -> Optional[torch.Tensor]:
-    """The workspace decode() used last on this device and stream, if any."""
+    """The workspace that calls without one use on this device and stream, if they had any. In
+    a capture it is the graph's: taken there, it holds the error bits of the graph's last
+    replay."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    return _workspaces.get((dev.index, _stream_handle(dev, stream)))
+    load()
+    return _default_workspace(dev.index, _stream_handle(dev, stream))

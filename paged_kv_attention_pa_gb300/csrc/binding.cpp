@@ -12,6 +12,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "pa.h"
+#include "pa_internal.h"
 
 namespace {
 
@@ -349,6 +350,12 @@ PyObject* do_gather(PyObject* const* v) {
                        vg ? Py_NewRef(v[8]) : THPVariable_Wrap(vo));
 }
 
+// capture_id(stream) -> id of the capture that the stream takes part in, 0 outside one
+PyObject* do_capture_id(PyObject* const* v) {
+  return PyLong_FromUnsignedLongLong(
+      pa_stream_capture_id(reinterpret_cast<pa_stream_t>(static_cast<uintptr_t>(integer(v[0])))));
+}
+
 // A call with its exceptions turned into Python's.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -372,7 +379,8 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef kMethods[] = {method<do_decode, 16>("decode"), method<do_append, 16>("append"),
-                          method<do_gather, 13>("gather"), {nullptr, nullptr, 0, nullptr}};
+                          method<do_gather, 13>("gather"),
+                          method<do_capture_id, 1>("capture_id"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include "pa.h"
+#include "pa_internal.h"
 #include "pa_params.h"
 
 namespace {
@@ -311,6 +312,16 @@ pa_status pa_set_device(int device) {
     return PA_ERR_CUDA;
   }
   return PA_OK;
+}
+
+unsigned long long pa_stream_capture_id(pa_stream_t stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo((cudaStream_t)stream, &status, &id) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return status == cudaStreamCaptureStatusActive ? id : 0;
 }
 
 pa_status pa_decode_plan(const pa_decode_args* a, int sm_count, int* splits,

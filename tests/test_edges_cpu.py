@@ -110,11 +110,17 @@ class FakeStream:
     cuda_stream = 77
 
 
+capture = [0]  # the id of the capture under way
+
+
 @pytest.fixture
 def host_workspaces(monkeypatch):
+    capture[0] = 0
     monkeypatch.setattr(pa, "load", FakeLib)
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(pa, "_capture_of", lambda stream_handle: capture[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: bool(capture[0]))
     monkeypatch.setattr(pa, "_workspaces", {})
+    monkeypatch.setattr(pa, "_captured", {}, raising=False)
     monkeypatch.setattr(pa, "_outgrown", [])
     return lambda need: pa._workspace(need, torch.device("cpu"), FakeStream.cuda_stream)
 
@@ -131,3 +137,22 @@ def test_error_bits_survive_the_growth_of_a_workspace(host_workspaces):
     assert pa.read_device_errors(most, FakeStream) == 7
     assert pa.read_device_errors(most, FakeStream) == 0
     assert pa.read_device_errors(torch.zeros(64, dtype=torch.uint8), FakeStream) == 0
+
+
+def test_a_capture_has_one_workspace_of_its_own(host_workspaces):
+    eager = host_workspaces(1 << 16)
+    capture[0] = 5
+    mine = host_workspaces(1 << 16)
+    assert mine is not eager                       # calls outside may run beside the graph's
+    assert all(host_workspaces(n) is mine for n in (1, pa.PA_WORKSPACE_HEADER_BYTES, 1 << 16))
+    grown = host_workspaces((1 << 16) + 1)
+    assert grown.outgrown is mine and host_workspaces(1 << 16) is grown
+    capture[0] = 6
+    other = host_workspaces(1 << 16)
+    assert other is not grown and other is not eager and not hasattr(other, "outgrown")
+    capture[0] = 0
+    assert host_workspaces(1 << 16) is eager and pa._outgrown == []
+
+
+def test_no_capture_without_a_device(lib):
+    assert pa._capture_of(0) == 0

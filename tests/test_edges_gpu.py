@@ -46,3 +46,58 @@ def test_errors_of_append_survive_a_decode_that_grows_the_workspace(cuda_lib):
         assert cuda_lib.default_workspace(stream=s) is not first
         assert cuda_lib.read_device_errors(cuda_lib.default_workspace(stream=s)) == cuda_lib.PA_DEVERR_BLOCK_INDEX
         assert cuda_lib.read_device_errors(cuda_lib.default_workspace(stream=s)) == 0
+
+
+def test_captured_calls_share_one_workspace_of_their_graph(cuda_lib, monkeypatch):
+    # two graphs captured on one stream that has a workspace of its own: each makes one, once;
+    # replayed beside each other and beside eager calls of that stream, whose splits share
+    # tails through counters in the workspace, all agree
+    B, Hkv, L, nb = 2, 2, 8192, 1024
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    kc, vc = (torch.randn((nb, 16, Hkv, 128), generator=gen, device="cuda").half() for _ in range(2))
+    bt = torch.randperm(nb, generator=gen, device="cuda").to(torch.int32).view(B, -1)
+    sl = i32([L, L - 777])
+    q = torch.randn((B, 8, 128), generator=gen, device="cuda").half()
+    S, P = cuda_lib.plan(B, 8, Hkv, 128, 16, L, splits=6)
+    assert S > 1 and P * 512 >= 512 << 10     # a shared tail
+    call = lambda **kw: cuda_lib.decode(q, kc, vc, bt, sl, 0.088, max_seq_len=L, splits=6, **kw)
+    want = call(deterministic=True).float()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        call()
+        eager = cuda_lib.default_workspace()
+    torch.cuda.synchronize()
+    made = []
+    zeros = torch.zeros
+    monkeypatch.setattr(torch, "zeros", lambda *a, **kw: made.append(1) or zeros(*a, **kw))
+    graphs = []
+    for _ in range(2):
+        g, before = torch.cuda.CUDAGraph(), len(made)
+        with torch.cuda.graph(g, stream=s):
+            assert cuda_lib.default_workspace() is None
+            outs = [call() for _ in range(16)]
+            rows = cuda_lib.gather(kc, vc, bt, sl, 3)
+            ws = cuda_lib.default_workspace()
+        assert len(made) == before + 1 and ws is not eager
+        graphs.append((g, outs, rows, ws, torch.cuda.Stream()))
+    assert graphs[0][3] is not graphs[1][3]
+    with torch.cuda.stream(s):
+        assert cuda_lib.default_workspace() is eager
+    tol = 2.0 ** -10 * want.abs() + 2.0 ** -14      # a rounding of the output, the order of fp32 sums
+    for _ in range(3):
+        for g, _, _, _, t in graphs:
+            with torch.cuda.stream(t):
+                g.replay()
+        with torch.cuda.stream(s):
+            beside = [call() for _ in range(16)]
+        torch.cuda.synchronize()
+        for out in graphs[0][1] + graphs[1][1] + beside:
+            assert torch.all((out.float() - want).abs() <= tol)
+    for _, _, rows, ws, _ in graphs:
+        assert torch.equal(rows[0][0], kc[bt[0, -1].long(), 13:16]) and cuda_lib.read_device_errors(ws) == 0
+    sl[0] = L + 1                                    # the error of a replay, in its graph's workspace
+    graphs[1][0].replay()
+    torch.cuda.synchronize()
+    assert cuda_lib.read_device_errors(graphs[0][3]) == 0
+    assert cuda_lib.read_device_errors(graphs[1][3]) == cuda_lib.PA_DEVERR_SEQ_LEN
