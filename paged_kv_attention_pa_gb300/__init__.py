@@ -313,15 +313,18 @@ def workspace_for(args: DecodeArgs, device: torch.device, stream_handle: int,
     return _workspace(need, device, stream_handle, stream)
 
 
-def _call_on(t: torch.Tensor, stream) -> Tuple[int, int]:
-    """(device index, stream handle) of a call on t's device, made current to the library; -1
-    and 0 for a CPU tensor, which the call then refuses."""
+def _call_on(t: torch.Tensor, stream):
+    """(device index, stream handle, stream) of a call on t's device, made current to the
+    library; -1, 0 and None for a CPU tensor, which the call then refuses."""
     lib = _lib or load()
     dev = t.get_device()
     if dev < 0:
-        return dev, 0
+        return dev, 0, None
     _ensure_device(lib, dev)
-    return dev, _stream_of(dev, stream)
+    sh = _stream_of(dev, stream)
+    if stream is not None and not isinstance(stream, torch.Stream):  # another library's
+        stream = torch.cuda.ExternalStream(sh, device=dev)
+    return dev, sh, stream
 
 
 def _rows_workspace(t: torch.Tensor, dev: int, sh: int, stream) -> Optional[torch.Tensor]:
@@ -330,22 +333,6 @@ def _rows_workspace(t: torch.Tensor, dev: int, sh: int, stream) -> Optional[torc
     if ws is None and dev >= 0:
         ws = _workspace(PA_WORKSPACE_HEADER_BYTES, t.device, sh, stream)
     return ws
-
-
-def _on(stream, allocates: bool, call, *args):
-    """call(*args), what it allocates (if anything) allocated in the order of the caller's stream."""
-    if stream is None or not allocates:
-        return call(*args)
-    with torch.cuda.stream(stream):
-        return call(*args)
-
-
-def _made_here(out: torch.Tensor, given, stream) -> torch.Tensor:
-    """An output; one that a call on a given stream allocated there is not reused before the
-    current stream, where it is used next, is done with it."""
-    if stream is not None and given is None and out is not None:
-        out.record_stream(torch.cuda.current_stream(out.device))
-    return out
 
 
 def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -370,22 +357,21 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     stream. Without `workspace` the call uses the one kept for its device and stream; captured
     calls use one that belongs to their graph (see default_workspace).
     """
-    given = out
-    dev, sh = _call_on(q, stream)
+    dev, sh, stream = _call_on(q, stream)
     ws = workspace if workspace is not None else _default_workspace(dev, sh)
-    rc, out = _on(stream, out is None, _native.decode, q, k_cache, v_cache, block_tables, seq_lens,
-                  scale, out, max_seq_len, splits, window, k_scale, v_scale, deterministic,
-                  total_tokens, ws, sh)
+    rc, out = _native.decode(q, k_cache, v_cache, block_tables, seq_lens, scale, out, max_seq_len,
+                             splits, window, k_scale, v_scale, deterministic, total_tokens, ws, sh,
+                             stream)
     if rc == PA_ERR_WORKSPACE and workspace is None:  # none yet, or too small: nothing was launched
         ws = workspace_for(make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale,
                                      max_seq_len, splits, window, k_scale, v_scale, deterministic,
                                      total_tokens), q.device, sh, stream)
-        rc, out = _on(stream, out is None, _native.decode, q, k_cache, v_cache, block_tables,
-                      seq_lens, scale, out, max_seq_len, splits, window, k_scale, v_scale,
-                      deterministic, total_tokens, ws, sh)
+        rc, out = _native.decode(q, k_cache, v_cache, block_tables, seq_lens, scale, out,
+                                 max_seq_len, splits, window, k_scale, v_scale, deterministic,
+                                 total_tokens, ws, sh, stream)
     if rc != PA_OK:
         raise PAError(rc, "pa_decode_ex")
-    return _made_here(out, given, stream)
+    return out
 
 
 def _only_plain(q, k_cache, v_cache):
@@ -491,15 +477,14 @@ def append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     (v_scale). q_out must be contiguous and may be q itself when that is contiguous.
     Asynchronous on the current (or given) stream.
     """
-    dev, sh = _call_on(k_cache, stream)
+    dev, sh, stream = _call_on(k_cache, stream)
     turns, interleaved, amplitude = _NO_ROPE if rope is None else rope
     ws = workspace if workspace is not None else _rows_workspace(k_cache, dev, sh, stream)
-    rc, rotated = _on(stream, q is not None and q_out is None, _native.append, k, v, k_cache,
-                      v_cache, block_tables, seq_lens, q, q_out, starts, turns, interleaved,
-                      amplitude, k_scale, v_scale, ws, sh)
+    rc, rotated = _native.append(k, v, k_cache, v_cache, block_tables, seq_lens, q, q_out, starts,
+                                 turns, interleaved, amplitude, k_scale, v_scale, ws, sh, stream)
     if rc != PA_OK:
         raise PAError(rc, "pa_append")
-    return _made_here(rotated, q_out, stream)
+    return rotated
 
 
 def gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -515,18 +500,18 @@ def gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Ten
     Keys stay rotated. dtype is that of the rows (float16 or bfloat16; needed for fp8 and 4-bit
     caches, whose values are multiplied by k_scale, v_scale). A row without a token is zero.
     """
-    dev, sh = _call_on(k_cache, stream)
+    dev, sh, stream = _call_on(k_cache, stream)
     if dtype is None:
         dtype = k_out.dtype if k_out is not None else k_cache.dtype
     code = _DT.get(dtype)
     if code is None:
         raise TypeError("dtype must be float16 or bfloat16")
     ws = workspace if workspace is not None else _rows_workspace(k_cache, dev, sh, stream)
-    rc, k, v = _on(stream, k_out is None or v_out is None, _native.gather, k_cache, v_cache,
-                   block_tables, seq_lens, rows, starts, code, k_out, v_out, k_scale, v_scale, ws, sh)
+    rc, k, v = _native.gather(k_cache, v_cache, block_tables, seq_lens, rows, starts, code, k_out,
+                              v_out, k_scale, v_scale, ws, sh, stream)
     if rc != PA_OK:
         raise PAError(rc, "pa_gather")
-    return _made_here(k, k_out, stream), _made_here(v, v_out, stream)
+    return k, v
 
 
 def plan(B: int, Hq: int, Hkv: int, D: int, block_size: int, max_seq_len: int,

@@ -6,8 +6,11 @@
 #include <Python.h>
 
 #include <exception>
+#include <optional>
 
 #include <ATen/ops/empty.h>
+#include <c10/core/StreamGuard.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -169,10 +172,44 @@ pa_status launch(Fn fn, const Args& a, const Workspace& ws, PyObject* stream) {
   return rc;
 }
 
-Tensor new_like(const Tensor& t) { return at::empty(t.sizes(), t.options().requires_grad(false)); }
+// Outputs that a call makes. With a stream given (a torch.Stream, else None) they are allocated
+// in its order, and not reused before the current stream, where they are used next, is done
+// with them.
+class Outputs {
+ public:
+  Outputs(PyObject* given, int64_t device) : device_(at::kCUDA, (c10::DeviceIndex)device) {
+    if (given == Py_None) return;
+    if (number_of(given, "device_index") != device) refuse_value("stream is of another device than the call's tensors");
+    stream_.emplace(c10::Stream::UNSAFE, device_, number_of(given, "stream_id"));
+  }
+  Tensor make(at::IntArrayRef shape, const at::TensorOptions& options) const {
+    if (!stream_) return at::empty(shape, options);
+    const c10::Stream current = c10::impl::VirtualGuardImpl(at::kCUDA).getStream(device_);
+    Tensor t;
+    {
+      const c10::StreamGuard guard(*stream_);
+      t = at::empty(shape, options);
+    }
+    if (current != *stream_ && t.numel()) t.record_stream(current);
+    return t;
+  }
+  Tensor like(const Tensor& t) const { return make(t.sizes(), t.options().requires_grad(false)); }
+
+ private:
+  static int64_t number_of(PyObject* o, const char* name) {
+    PyObject* n = PyObject_GetAttrString(o, name);
+    if (!n) throw Refused{};
+    const long long v = PyLong_AsLongLong(n);
+    Py_DECREF(n);
+    if (v == -1 && PyErr_Occurred()) throw Refused{};
+    return v;
+  }
+  c10::Device device_;
+  std::optional<c10::Stream> stream_;
+};
 
 // decode(q, k_cache, v_cache, block_tables, seq_lens, scale, out, max_seq_len, splits, window,
-//        k_scale, v_scale, deterministic, total_tokens, workspace, stream) -> (status, out)
+//        k_scale, v_scale, deterministic, total_tokens, workspace, stream handle, stream or None) -> (status, out)
 PyObject* do_decode(PyObject* const* v) {
   const Tensor &q = tensor(v[0]), &kc = tensor(v[1]), &vc = tensor(v[2]), &bt = tensor(v[3]), &sl = tensor(v[4]);
   const int64_t d = q.dim();
@@ -215,7 +252,8 @@ PyObject* do_decode(PyObject* const* v) {
   a.dtype = dt;
   a.kv_dtype = c.kv;
   const Workspace ws(v[14], dev);
-  const Tensor out = given ? *given : new_like(q);
+  const Outputs outputs(v[16], dev);
+  const Tensor out = given ? *given : outputs.like(q);
   a.q = data<void>(q);
   a.k_cache = data<void>(kc);
   a.v_cache = data<void>(vc);
@@ -227,7 +265,7 @@ PyObject* do_decode(PyObject* const* v) {
 }
 
 // append(k, v, k_cache, v_cache, block_tables, seq_lens, q, q_out, starts, turns, interleaved,
-//        amplitude, k_scale, v_scale, workspace, stream) -> (status, q_out or None)
+//        amplitude, k_scale, v_scale, workspace, stream handle, stream or None) -> (status, q_out or None)
 PyObject* do_append(PyObject* const* v) {
   const Tensor &k = tensor(v[0]), &val = tensor(v[1]), &kc = tensor(v[2]), &vc = tensor(v[3]), &bt = tensor(v[4]),
                &sl = tensor(v[5]);
@@ -278,10 +316,11 @@ PyObject* do_append(PyObject* const* v) {
   a.v_scale = number(v[13]);
   a.rope_layout = truth(v[10]) ? PA_ROPE_INTERLEAVED : PA_ROPE_HALF;
   a.rope_amplitude = number(v[11]);
+  const Outputs outputs(v[16], dev);
   Tensor out;
   if (q) {
     a.Hq = to32(q->size(d - 2));
-    out = given ? *given : new_like(*q);
+    out = given ? *given : outputs.like(*q);
     a.q = data<void>(*q);
     a.q_out = data<void>(out);
   }
@@ -303,7 +342,7 @@ PyObject* do_append(PyObject* const* v) {
 }
 
 // gather(k_cache, v_cache, block_tables, seq_lens, rows, starts, like, k_out, v_out, k_scale,
-//        v_scale, workspace, stream) -> (status, k_out, v_out); like: 0 float16, 1 bfloat16
+//        v_scale, workspace, stream handle, stream or None) -> (status, k_out, v_out); like: 0 float16, 1 bfloat16
 PyObject* do_gather(PyObject* const* v) {
   const Tensor &kc = tensor(v[0]), &vc = tensor(v[1]), &bt = tensor(v[2]), &sl = tensor(v[3]);
   const Tensor *starts = optional_tensor(v[5]), *kg = optional_tensor(v[7]), *vg = optional_tensor(v[8]);
@@ -336,8 +375,9 @@ PyObject* do_gather(PyObject* const* v) {
   a.k_scale = number(v[9]);
   a.v_scale = number(v[10]);
   const Workspace ws(v[11], dev);
+  const Outputs outputs(v[13], dev);
   const auto options = kc.options().dtype(type).requires_grad(false);
-  const Tensor ko = kg ? *kg : at::empty(shape, options), vo = vg ? *vg : at::empty(shape, options);
+  const Tensor ko = kg ? *kg : outputs.make(shape, options), vo = vg ? *vg : outputs.make(shape, options);
   a.k_cache = data<void>(kc);
   a.v_cache = data<void>(vc);
   a.block_tables = data<int32_t>(bt);
@@ -378,8 +418,8 @@ PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<F, N>)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef kMethods[] = {method<do_decode, 16>("decode"), method<do_append, 16>("append"),
-                          method<do_gather, 13>("gather"),
+PyMethodDef kMethods[] = {method<do_decode, 17>("decode"), method<do_append, 17>("append"),
+                          method<do_gather, 14>("gather"),
                           method<do_capture_id, 1>("capture_id"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,5 +1,4 @@
 """Calls at the edges of what append, gather and decode take (GB300 only)."""
-import numpy as np
 import pytest
 import torch
 
@@ -101,3 +100,29 @@ def test_captured_calls_share_one_workspace_of_their_graph(cuda_lib, monkeypatch
     torch.cuda.synchronize()
     assert cuda_lib.read_device_errors(graphs[0][3]) == 0
     assert cuda_lib.read_device_errors(graphs[1][3]) == cuda_lib.PA_DEVERR_SEQ_LEN
+
+
+class Handle:
+    """Another library's stream: a handle and nothing else."""
+
+    def __init__(self, stream):
+        self.cuda_stream = stream.cuda_stream
+
+
+@pytest.mark.parametrize("given", [lambda s: s, lambda s: torch.cuda.ExternalStream(s.cuda_stream), Handle])
+def test_calls_on_a_given_stream_leave_the_current_one(cuda_lib, given):
+    s = torch.cuda.Stream()
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    kc, vc = (torch.randn((64, 16, 2, 128), generator=gen, device="cuda").half() for _ in range(2))
+    k, q = (torch.randn((1, h, 128), generator=gen, device="cuda").half() for h in (2, 4))
+    bt, sl = torch.arange(64, dtype=torch.int32, device="cuda")[None], i32([1000])
+    want = [cuda_lib.append(k, k, kc, vc, bt, sl, q=q), *cuda_lib.gather(kc, vc, bt, sl, 5),
+            cuda_lib.decode(q, kc, vc, bt, sl, 0.088, max_seq_len=1000, deterministic=True)]
+    torch.cuda.synchronize()
+    here = torch.cuda.current_stream()
+    got = [cuda_lib.append(k, k, kc, vc, bt, sl, q=q, stream=given(s)),
+           *cuda_lib.gather(kc, vc, bt, sl, 5, stream=given(s)),
+           cuda_lib.decode(q, kc, vc, bt, sl, 0.088, max_seq_len=1000, deterministic=True, stream=given(s))]
+    assert torch.cuda.current_stream() == here
+    s.synchronize()
+    assert all(torch.equal(rh.bits(a), rh.bits(b)) for a, b in zip(got, want))
