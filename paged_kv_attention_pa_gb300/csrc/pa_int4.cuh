@@ -54,11 +54,6 @@ __device__ __forceinline__ uint32_t mul2_half(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-__device__ __forceinline__ uint32_t fma2_half(uint32_t a, uint32_t b, uint32_t c) {
-  const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b),
-                            *reinterpret_cast<__half2*>(&c));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 // c = a b with a zero accumulator (fp16 in, fp32 out).
 __device__ __forceinline__ void mma16816_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                               uint32_t b1) {
@@ -280,14 +275,20 @@ __device__ __forceinline__ void int4_pv(float (&o)[NT][D / 16][4], float (&om)[N
     }
   }
   {
-    const uint32_t a[4] = {DOWN ? fma2_half(st[0], 0x4b804b80u, mn[0]) : mn[0], 0u,  // 15 step + minimum
-                           DOWN ? fma2_half(st[1], 0x4b804b80u, mn[1]) : mn[1], 0u};
+    const uint32_t a[4] = {mn[0], 0u, mn[1], 0u};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) mma16816<__half>(om[nt], a, pb[nt][0], pb[nt][1]);
   }
-  if (DOWN) {
+  if (DOWN) {  // the maximum is the minimum and 16 - 1 steps, all exact products
+    const uint32_t a[4] = {st[0], 0u, st[1], 0u};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      mma16816<__half>(om[nt], a, mul2_half(pb[nt][0], 0x4c004c00u), mul2_half(pb[nt][1], 0x4c004c00u));
     st[0] ^= 0x80008000u;
     st[1] ^= 0x80008000u;
+    const uint32_t minus[4] = {st[0], 0u, st[1], 0u};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mma16816<__half>(om[nt], minus, pb[nt][0], pb[nt][1]);
   }
   const uint32_t sel = (gid & 1) ? 0x7632u : 0x5410u;  // the half of the octet's word
 #pragma unroll
