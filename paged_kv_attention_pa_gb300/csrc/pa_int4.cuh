@@ -245,7 +245,13 @@ __device__ __forceinline__ void int4_scores(float (&s)[MT][NT][4], float (&sm)[M
 // The steps of two tokens, for the multiplication of the weights, come from a transposing
 // load of the tokens' steps and minima: lane 4 g + tig then holds those of group g and
 // tokens 2 tig, 2 tig + 1 (of the MMA's order), and a shuffle hands them to the others.
-// om[nt][0..1], row gid: the sum of the minima (maxima) of group gid.
+// om[nt][0..1], row gid: the sum of the minima (maxima) of group gid. A maximum is the minimum,
+// plus 16 steps, minus one: rounded to fp16 it cost 4.4e-4 of the output's norm, as three
+// exact products nothing. The MMAs of the three lie apart, since they add to one accumulator
+// (GB300, us per call, one rounded product / three in a row / three apart: 32/8 heads of 128,
+// 32 sequences of 16K 125.1 / 129.1 / 127.0, 4 query rows of 8 of 16K 55.4 / 55.3 / 55.1, 8 rows
+// 133.9 / 140.9 / 138.2; 24/4 of 256, 2 rows of 8 of 8K 35.4 / 35.9 / 35.6). The minus one in the
+// idle rows of the first MMA, with accumulators of its own: 127.1, 56.4, 139.1 and 36.5.
 template <int D, int NT, bool DOWN>
 __device__ __forceinline__ void int4_pv(float (&o)[NT][D / 16][4], float (&om)[NT][4], uint32_t rows,
                                         const uint32_t (&pb)[NT][2], int lane) {
@@ -279,16 +285,9 @@ __device__ __forceinline__ void int4_pv(float (&o)[NT][D / 16][4], float (&om)[N
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) mma16816<__half>(om[nt], a, pb[nt][0], pb[nt][1]);
   }
-  if (DOWN) {  // the maximum is the minimum and 16 - 1 steps, all exact products
-    const uint32_t a[4] = {st[0], 0u, st[1], 0u};
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      mma16816<__half>(om[nt], a, mul2_half(pb[nt][0], 0x4c004c00u), mul2_half(pb[nt][1], 0x4c004c00u));
+  if (DOWN) {
     st[0] ^= 0x80008000u;
     st[1] ^= 0x80008000u;
-    const uint32_t minus[4] = {st[0], 0u, st[1], 0u};
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) mma16816<__half>(om[nt], minus, pb[nt][0], pb[nt][1]);
   }
   const uint32_t sel = (gid & 1) ? 0x7632u : 0x5410u;  // the half of the octet's word
 #pragma unroll
@@ -310,6 +309,17 @@ __device__ __forceinline__ void int4_pv(float (&o)[NT][D / 16][4], float (&om)[N
       mma16816<__half>(o[nt][2 * g], a0, b0, b1);
       mma16816<__half>(o[nt][2 * g + 1], a1, b0, b1);
     }
+    if (DOWN && g == R::G / 2) {  // st is negative here: plus 16 steps ..
+      const uint32_t a[4] = {st[0], 0u, st[1], 0u};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        mma16816<__half>(om[nt], a, mul2_half(pb[nt][0], 0xcc00cc00u), mul2_half(pb[nt][1], 0xcc00cc00u));
+    }
+  }
+  if (DOWN) {  // .. minus one
+    const uint32_t a[4] = {st[0], 0u, st[1], 0u};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mma16816<__half>(om[nt], a, pb[nt][0], pb[nt][1]);
   }
 }
 
