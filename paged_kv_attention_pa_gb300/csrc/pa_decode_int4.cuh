@@ -9,8 +9,8 @@
 // both ways on GB300: head_dim 256, one sequence of 4K / 32K tokens 7.65 / 14.1 us against
 // 8.06 / 14.4 us with cp.async; head_dim 128, 32 sequences of 16K 134 us against 125 us (a
 // warp's bulk copies issue lane after lane in the path of its arithmetic, and 16-token
-// blocks make four a tile). A wait for a bulk copy gives up after two seconds with
-// PA_DEVERR_COPY.
+// blocks make four a tile). A warp whose copy does not arrive within two seconds reports
+// PA_DEVERR_COPY, issues nothing more, waits as long again for each copy in flight and ends.
 //
 // Math. 160 bytes per token and KV head at head_dim 128 pass through an SM in 3.6 ns at the
 // memory's rate, and the arithmetic of its tiles takes as long. Twelve warps at head_dim 128
@@ -51,6 +51,16 @@ struct Int4Cfg {
   static_assert(TW == 32 && (TW * CPR) % 32 == 0, "tile shape");
   static_assert(DEPTH >= 2 && NW * DEPTH * 8 <= 1020, "two slots at least, an mbarrier each");
 };
+
+// All lanes wait for the bulk copies of the warp's k-th tile; its slots' mbarriers lie at `bars`.
+// Where they are late (two seconds) the error is reported and false returned, once the copies
+// in flight behind them have landed or are late themselves: this memory is used again.
+static __device__ __noinline__ bool wait_for_tile(uint32_t bars, int k, int depth, uint32_t* err) {
+  if (__all_sync(0xffffffffu, mbar_wait_long(bars + 8 * (k % depth), (k / depth) & 1))) return true;
+  atomicOr(err, PA_DEVERR_COPY);
+  for (int i = k; i < k + depth; ++i) mbar_wait_long(bars + 8 * (i % depth), (i / depth) & 1);
+  return false;
+}
 
 // The sequence whose CTAs run r-th when the longest come first (see make_plan), up to a sixteenth of
 // max_seq_len (W words of 32 sequences). All lanes together; every CTA finds the same order.
@@ -365,7 +375,6 @@ __global__ void __launch_bounds__(Int4Cfg<D, NT, MODE>::THREADS, Int4Cfg<D, NT, 
   // step skips the rescaling. The weights are also multiplied by the values' steps in fp16:
   // at most 2^2 * 8734, the largest step of a finite fp16 range.
   constexpr float kSlack = 2.f;  // log2 units
-  uint32_t late_bar = 0, late_parity = 0;  // bulk copies: one did not arrive in time
 
   for (int k = 0; tq[0] >= 0; ++k) {  // tile k of the stream: tokens tq[0] ..
     const int entry = next_entry;
@@ -380,11 +389,8 @@ __global__ void __launch_bounds__(Int4Cfg<D, NT, MODE>::THREADS, Int4Cfg<D, NT, 
     const uint32_t kt = ring + (k % C::DEPTH) * C::SLOT_BYTES, vt = kt + C::TILE_BYTES;
     if constexpr (C::BULK) {  // tile k has landed
       const uint32_t bar = bars + 8 * (k % C::DEPTH), parity = (k / C::DEPTH) & 1;
-      if (!mbar_try(bar, parity) && (late_bar || !mbar_wait_long(bar, parity))) {
-        atomicOr(p.err, PA_DEVERR_COPY);  // later tiles are not waited for; the outputs mean nothing
-        late_bar = bar;
-        late_parity = parity;
-      }
+      if (!__all_sync(0xffffffffu, mbar_try(bar, parity)) && !wait_for_tile(bars, k, C::DEPTH, p.err))
+        break;  // the outputs mean nothing
     } else {
       cp_async_wait<C::DEPTH - 1>();
     }
@@ -393,9 +399,12 @@ __global__ void __launch_bounds__(Int4Cfg<D, NT, MODE>::THREADS, Int4Cfg<D, NT, 
       // are finite whatever they are), so that p = 0 meets 0
       for (int i = lane; i < (C::TW - n) * Row::W; i += 32)
         sts128_zero(vt + (n + i / Row::W) * C::ROWB + Row::CODES + 16 * (i % Row::W));
-      if constexpr (C::BULK) async_proxy_fence();
+      if constexpr (C::BULK) {
+        async_proxy_fence();
+        __syncwarp();
+      }
     }
-    __syncwarp();  // every lane's copies (and the zeros) are visible
+    if constexpr (!C::BULK) __syncwarp();  // every lane's copies (and the zeros) are visible
 
       // ---- scores S^T[token][column], in two parts
       float s[MT][NT][4], sm[MT][NT][4];
@@ -484,11 +493,7 @@ __global__ void __launch_bounds__(Int4Cfg<D, NT, MODE>::THREADS, Int4Cfg<D, NT, 
       }
     __syncwarp();  // every lane is done with this slot before it is refilled
   }
-  if constexpr (C::BULK) {
-    if (late_bar) mbar_wait_long(late_bar, late_parity);  // its copy may still land
-  } else {
-    cp_async_wait<0>();
-  }
+  if constexpr (!C::BULK) cp_async_wait<0>();
 
   if (p.S == 1 || p.cmerge) pdl_launch_dependents();
   int4_finish<D, NT>(o, om, tig);

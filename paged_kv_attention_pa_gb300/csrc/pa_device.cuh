@@ -113,13 +113,16 @@ __device__ __forceinline__ uint64_t global_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// Wait for a phase to complete, at most two seconds; false when it did not.
+// Wait for a phase to complete, at most two seconds; false when it did not. The time is read
+// before the last look at the phase, so that a program held up for seconds is not one whose
+// copy is late.
 static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = global_ns();
-  do {
+  for (;;) {
+    const bool over = global_ns() - t0 >= 2000000000ull;
     if (mbar_try(bar, parity)) return true;
-  } while (global_ns() - t0 < 2000000000ull);
-  return false;
+    if (over) return false;
+  }
 }
 
 // ---------------------------------------------------------------- dependent launch
