@@ -8,7 +8,7 @@
 // Rotation. Pair j of a head at position t turns by the angle t * f_j. The angle is kept
 // as a 64-bit fraction of a turn, turns[j] = f_j / 2 pi * 2^64, so that t * turns[j] modulo
 // 2^64 is the fraction at any position, with an error of t * 2^-64 turns; fp32 enters only
-// at the sine of the remaining half turn.
+// at the sine of the eighth of a turn that is left beside the nearest quarter.
 //
 // Both kernels move bytes: a lane handles 16 elements of a row (two 16-byte words of 16-bit
 // elements), D / 16 lanes a row, all loads of a warp's rows in flight together. What bounds
@@ -143,6 +143,17 @@ template <typename T>
 __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]),
                     pack2<T>(x[6], x[7]));
+}
+
+// Cosine and sine of the angle turn / 2^32 turns. The nearest quarter turn comes off in integers,
+// so that fp32 rounds only the at most eighth of a turn that is left: taken whole, angles near a
+// half turn were off by 9e-8, however small their sine.
+__device__ __forceinline__ float2 cos_sin(uint32_t turn) {
+  const uint32_t quarters = (turn + 0x20000000u) >> 30;
+  float s, c;
+  sincospif((float)(int32_t)(turn - (quarters << 30)) * 4.656612873077393e-10f, &s, &c);  // half turns: * 2^-31
+  const float x = quarters & 1 ? -s : c, y = quarters & 1 ? c : s;
+  return quarters & 2 ? make_float2(-x, -y) : make_float2(x, y);
 }
 
 // (a, b) turned by the angle with cosine cs.x and sine cs.y; each product rounded on its own.
@@ -291,9 +302,8 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const RowsParams p)
   }
   const int head_rows = KIND == kKvInt4 ? p.block_size : 1;  // cache rows between heads
   for (int j = threadIdx.x; j < p.rot / 2; j += kRowThreads) {
-    const uint64_t f = __ldg(p.turns + j) * (uint64_t)(uint32_t)at.pos;
-    float s, c;
-    sincospif((float)(int32_t)(f >> 32) * 4.656612873077393e-10f, &s, &c);  // half turns: * 2^-31
+    const float2 cs = cos_sin((uint32_t)(__ldg(p.turns + j) * (uint64_t)(uint32_t)at.pos >> 32));
+    const float c = cs.x, s = cs.y;
     const int chunk = half ? j / 8 : j / 4, e = half ? j % 8 : j % 4;
     turn[2 * chunk + e / 2 * (half ? 2 : 4) * LPI + e % 2] = make_float2(c * p.amplitude, s * p.amplitude);
   }

@@ -1,4 +1,5 @@
 """Calls at the edges of what append, gather and decode take (GB300 only)."""
+import numpy as np
 import pytest
 import torch
 
@@ -126,3 +127,37 @@ def test_calls_on_a_given_stream_leave_the_current_one(cuda_lib, given):
     assert torch.cuda.current_stream() == here
     s.synchronize()
     assert all(torch.equal(rh.bits(a), rh.bits(b)) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotation_by_angles_near_the_axes(cuda_lib, interleaved):
+    # (2^14, 0) turned by angles all around and close to the multiples of a quarter turn, where
+    # the sine or cosine is small and its relative error shows. The angle keeps 32 bits of a turn
+    # (2 pi 2^-32 = 1.5e-9) and is rounded to fp32 relative to the nearest quarter (2^-25), sine,
+    # cosine (2 units) and their product round relatively as well: 2^-21 in all; the output once
+    rng = np.random.default_rng(3)
+    T = 4096
+    turns = rng.integers(0, 2 ** 64, (T, 64), dtype=np.uint64)
+    near = np.exp(rng.uniform(np.log(2.0 ** 34), np.log(2.0 ** 61), (T // 2, 64))).astype(np.uint64)
+    sign = rng.integers(0, 2, near.shape).astype(bool)
+    turns[:T // 2] = (turns[:T // 2] >> np.uint64(62) << np.uint64(62)) + np.where(sign, near, ~near + np.uint64(1))
+    a = turns.astype(np.longdouble) / np.longdouble(2.0 ** 64) * 2
+    a = np.where(a >= 1, a - 2, a)                    # half turns in [-1, 1)
+    k = np.rint(a * 2)                                # quarters, taken off before the sine is
+    r = ((a - k / 2) * np.longdouble(np.pi)).astype(np.float64)
+    k = k.astype(np.int64) % 4
+    c, s = np.cos(r), np.sin(r)
+    cos, sin = np.choose(k, [c, -s, -c, s]), np.choose(k, [s, c, -s, -c])
+    q = torch.zeros((1, 1, 128), dtype=torch.float16, device="cuda")
+    at = slice(0, 128, 2) if interleaved else slice(0, 64)
+    other = slice(1, 128, 2) if interleaved else slice(64, 128)
+    q[..., at] = 2.0 ** 14
+    kc = torch.zeros((1, 16, 1, 128), dtype=torch.float16, device="cuda")
+    bt, sl = i32([[0]]), i32([2])                     # one token, at position 1
+    tt = torch.from_numpy(turns.view(np.int64)).cuda()
+    got = torch.cat([cuda_lib.append(q, q, kc, kc, bt, sl, q=q, rope=cuda_lib.Rope(tt[i], interleaved))
+                     for i in range(T)]).cpu().double().numpy()[:, 0]
+    for y, ref in ((got[:, at], cos), (got[:, other], sin)):
+        ref = ref * 2.0 ** 14
+        tol = 2.0 ** -11 * np.abs(ref) + 2.0 ** -21 * np.abs(ref) + 2.0 ** 14 * 1.6e-9 + 2.0 ** -25
+        assert np.all(np.abs(y - ref) <= tol)
