@@ -50,6 +50,7 @@ struct RowsParams {
   int rot, interleaved;    // rotated elements of a head
   float amplitude;
   float k_scale, v_scale;  // append: 1 / scale, gather: scale
+  float k_div, v_div;      // append: scale
 };
 
 constexpr int kRowThreads = 128, kRowWarps = kRowThreads / 32;
@@ -163,6 +164,13 @@ __device__ __forceinline__ void rotate_pair(float& a, float& b, float2 cs) {
   a = x;
 }
 
+// x / s, correctly rounded, where y is 1 / s so rounded: as in int4_octet. Quotients from 2^100 on,
+// which saturate in every cache, are left as x y (their residual overflows).
+__device__ __forceinline__ float quotient(float x, float s, float y) {
+  const float q = __fmul_rn(x, y);
+  return fabsf(q) < 1.267650600228229e30f ? fmaf(fmaf(-q, s, x), y, q) : q;
+}
+
 // Four fp32 values to four E4M3 codes: nearest even, saturating at +-448, NaN kept.
 __device__ __forceinline__ uint32_t e4m3x4(const float* x) {
   uint16_t lo, hi;
@@ -238,8 +246,10 @@ __device__ __forceinline__ uint32_t int4_octet(float (&x)[8], uint16_t* step16, 
 }
 
 // One row per CTA column blockIdx.x; its warps (and the parts blockIdx.y) share the row's
-// warp tasks: IPW query heads, then IPW key heads, then IPW value heads at a time.
-template <typename T, KvKind KIND, int D>
+// warp tasks: IPW query heads, then IPW key heads, then IPW value heads at a time. DIV: a scale is
+// no power of two, so that values are divided by it (4096 rows of 24/4 heads of 256 into 4 bits
+// 27.4 us, with products 26.8).
+template <typename T, KvKind KIND, int D, bool DIV>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(const RowsParams p) {
   constexpr int LPI = D / 16, IPW = 32 / LPI;  // lanes per row item, items per warp
   constexpr int ROWB = kv_row_bytes(D, KIND);
@@ -370,10 +380,11 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const RowsParams p)
           reinterpret_cast<uint4*>(dst)[c1] = turn1 ? pack8<T>(x1) : b;
         }
       } else {
+        const float div = cur.which == 1 ? p.k_div : p.v_div;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          x0[e] *= inv;
-          x1[e] *= inv;
+          x0[e] = DIV ? quotient(x0[e], div, inv) : x0[e] * inv;
+          x1[e] = DIV ? quotient(x1[e], div, inv) : x1[e] * inv;
         }
         if constexpr (KIND == kKvFp8) {
           if (cur.live) {
@@ -541,6 +552,11 @@ cudaError_t launch_rows(Kern kern, dim3 grid, cudaStream_t st, const RowsParams&
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+bool power_of_two(float s) {
+  int e;
+  return std::frexp(s, &e) == 0.5f;
+}
+
 template <bool APPEND, typename T, KvKind KIND, int D>
 cudaError_t launch_kind(const RowsParams& p, int sms, cudaStream_t st) {
   constexpr int IPW = 32 / (D / 16);
@@ -550,7 +566,11 @@ cudaError_t launch_kind(const RowsParams& p, int sms, cudaStream_t st) {
     const int tasks = (p.Hq + IPW - 1) / IPW + 2 * nk;
     const int most = (tasks + kRowWarps - 1) / kRowWarps;
     const int parts = (int)std::min<long long>(most, std::max<long long>(1, 4ll * sms / p.T));
-    return launch_rows(append_kernel<T, KIND, D>, dim3(p.T, std::min(parts, 65535)), st, p);
+    const dim3 grid(p.T, std::min(parts, 65535));
+    if constexpr (KIND != kKv16)
+      if (!power_of_two(p.k_div) || !power_of_two(p.v_div))
+        return launch_rows(append_kernel<T, KIND, D, true>, grid, st, p);
+    return launch_rows(append_kernel<T, KIND, D, false>, grid, st, p);
   } else {
     const unsigned ctas = ((unsigned)p.T * (unsigned)nk + kRowWarps - 1) / kRowWarps;
     return launch_rows(gather_kernel<T, KIND, D>, dim3(ctas), st, p);
@@ -669,6 +689,8 @@ pa_status pa_append(const pa_append_args* a, void* workspace, size_t workspace_b
   const bool scaled = a->kv_dtype != PA_KV_AS_DTYPE;
   p.k_scale = scaled ? 1.f / a->k_scale : 1.f;
   p.v_scale = scaled ? 1.f / a->v_scale : 1.f;
+  p.k_div = a->k_scale;
+  p.v_div = a->v_scale;
   if (launch<true>(p, a->D, a->dtype == PA_BF16, kind_of(a->kv_dtype), sms, (cudaStream_t)stream) !=
       cudaSuccess) {
     cudaGetLastError();

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import rows_harness as rh
+from oracle import int4 as o4
 
 pytestmark = pytest.mark.gpu
 
@@ -161,3 +162,35 @@ def test_rotation_by_angles_near_the_axes(cuda_lib, interleaved):
         ref = ref * 2.0 ** 14
         tol = 2.0 ** -11 * np.abs(ref) + 2.0 ** -21 * np.abs(ref) + 2.0 ** 14 * 1.6e-9 + 2.0 ** -25
         assert np.all(np.abs(y - ref) <= tol)
+
+
+@pytest.mark.parametrize("scale", [7.0, 0.7, 5.0 / 448, 11.0, 3e38, 1e-38, 0.125])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_quantised_rows_hold_the_quotient(cuda_lib, dtype, scale):
+    # value / scale, the correctly rounded fp32 quotient, and then the nearest code: products
+    # with a rounded 1 / scale fall off the ties between codes (1.4375, say, from 10.0625 / 7)
+    s32 = np.float32(scale)
+    rng = np.random.default_rng(7)
+    L, D = 4096, 128
+    ties = (2 * rng.integers(8, 16, (L, 2, D)) + 1) / 16 * 2.0 ** rng.integers(-4, 5, (L, 2, D))
+    x = np.where(rng.random((L, 2, D)) < 0.5, ties * float(s32), rng.standard_normal((L, 2, D)) * float(s32))
+    if scale in (3e38, 1e-38):
+        x = rng.standard_normal((L, 2, D)) * (1e38 if scale > 1 and dtype == "bf16" else 1.0)
+    with np.errstate(over="ignore", under="ignore"):
+        v = torch.from_numpy(x.astype(np.float32)).to(rh.DT[dtype])
+        y = (v.float().numpy() / s32).astype(np.float32)
+    nb = L // 16
+    bt, sl = torch.arange(nb, dtype=torch.int32, device="cuda")[None], i32([L])
+    for kind in ("fp8", "int4"):
+        if kind == "fp8":
+            kc, vc = (torch.zeros((nb, 16, 2, D), device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+        else:
+            kc, vc = (torch.zeros((nb, 2, 16, o4.row_bytes(D)), dtype=torch.uint8, device="cuda") for _ in range(2))
+        cuda_lib.append(v[None].cuda(), v[None].cuda(), kc, vc, bt, sl, k_scale=scale, v_scale=scale)
+        if kind == "fp8":
+            want = torch.from_numpy(np.clip(y, -448, 448)).to(torch.float8_e4m3fn).view(torch.uint8)
+            got = [c.view(torch.uint8).cpu().reshape(L, 2, D) for c in (kc, vc)]
+        else:
+            want = torch.from_numpy(o4.quantise(y.astype(np.float64)))
+            got = [c.cpu().transpose(1, 2).reshape(L, 2, -1) for c in (kc, vc)]
+        assert all(torch.equal(g, want) for g in got), kind
