@@ -516,10 +516,12 @@ def gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Ten
 
 def plan(B: int, Hq: int, Hkv: int, D: int, block_size: int, max_seq_len: int,
          splits: int = 0, sm_count: int = 0, window: int = 0,
-         kv_fp8: bool = False, total_tokens: int = 0, kv_int4: bool = False) -> Tuple[int, int]:
+         kv_fp8: bool = False, total_tokens: int = 0, kv_int4: bool = False,
+         rows: int = 1) -> Tuple[int, int]:
     """(splits, tokens per split) the library would launch with. sm_count <= 0 asks
-    the current device; a positive sm_count needs no GPU. kv_fp8: FP8 E4M3 caches
-    (their warp tile is 32 tokens, so splits are multiples of 32). kv_int4: 4-bit caches."""
+    the current device; a positive sm_count needs no GPU. kv_fp8, kv_int4: FP8 E4M3 and
+    4-bit caches (their warp tile is 32 tokens, so splits are multiples of 32). rows: query rows
+    per sequence (4-bit plans depend on them)."""
     lib = load()
     a = DecodeArgs()
     a.B, a.Hq, a.Hkv, a.D = B, Hq, Hkv, D
@@ -529,6 +531,7 @@ def plan(B: int, Hq: int, Hkv: int, D: int, block_size: int, max_seq_len: int,
     a.dtype = PA_BF16
     a.splits = splits
     a.window = window
+    a.q_len = rows
     if kv_fp8 or kv_int4:
         a.kv_dtype, a.k_scale, a.v_scale = PA_KV_INT4 if kv_int4 else PA_KV_FP8_E4M3, 1.0, 1.0
     a.total_tokens = int(total_tokens)

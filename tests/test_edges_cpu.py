@@ -156,3 +156,13 @@ def test_a_capture_has_one_workspace_of_its_own(host_workspaces):
 
 def test_no_capture_without_a_device(lib):
     assert pa._capture_of(0) == 0
+
+
+def test_plan_knows_the_query_rows(lib):
+    # unsplit short contexts run on short CTAs with at most eight columns: another cost, another plan
+    kw = dict(sm_count=152, kv_int4=True, total_tokens=1600)
+    one = pa.plan(10, 64, 16, 128, 16, 160, **kw)
+    assert one == pa.plan(10, 64, 16, 128, 16, 160, rows=1, **kw) == pa.plan(10, 64, 16, 128, 16, 160, rows=2, **kw)
+    assert one != pa.plan(10, 64, 16, 128, 16, 160, rows=4, **kw)
+    with pytest.raises(pa.PAError):
+        pa.plan(1, 32, 8, 128, 16, 512, sm_count=152, rows=9)
