@@ -406,91 +406,91 @@ __global__ void __launch_bounds__(Int4Cfg<D, NT, MODE>::THREADS, Int4Cfg<D, NT, 
     }
     if constexpr (!C::BULK) __syncwarp();  // every lane's copies (and the zeros) are visible
 
-      // ---- scores S^T[token][column], in two parts
-      float s[MT][NT][4], sm[MT][NT][4];
-      int4_scores<D, NT, MT, C::QSHARED>(s, sm, kt, query, qs, gid, tig);
-      // ---- online softmax over the tile; -inf by select past each column's limit
-      float x[NT][MT][4];
-      float mx[NT][2];
-      bool grow = false;  // some column of this lane sees a score above its running max + slack
+    // ---- scores S^T[token][column], in two parts
+    float s[MT][NT][4], sm[MT][NT][4];
+    int4_scores<D, NT, MT, C::QSHARED>(s, sm, kt, query, qs, gid, tig);
+    // ---- online softmax over the tile; -inf by select past each column's limit
+    float x[NT][MT][4];
+    float mx[NT][2];
+    bool grow = false;  // some column of this lane sees a score above its running max + slack
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[nt][mt][i] = fmaf(s[mt][nt][i], cs[nt][i & 1], sm[mt][nt][i] * cm[nt][i & 1]);
+    if (t0 + C::TW > L - R + 1) {  // some token is at or past some column's limit
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            x[nt][mt][i] = fmaf(s[mt][nt][i], cs[nt][i & 1], sm[mt][nt][i] * cm[nt][i & 1]);
-      if (t0 + C::TW > L - R + 1) {  // some token is at or past some column's limit
+            if (t0 + 16 * mt + trow + 8 * (i >> 1) >= lim[nt][i & 1]) x[nt][mt][i] = -INFINITY;
+    }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (t0 + 16 * mt + trow + 8 * (i >> 1) >= lim[nt][i & 1]) x[nt][mt][i] = -INFINITY;
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        mx[nt][0] = mx[nt][1] = -INFINITY;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mx[nt][0] = fmaxf(mx[nt][0], fmaxf(x[nt][mt][0], x[nt][mt][2]));
-          mx[nt][1] = fmaxf(mx[nt][1], fmaxf(x[nt][mt][1], x[nt][mt][3]));
-        }
-        grow = grow || mx[nt][0] > m[nt][0] + kSlack || mx[nt][1] > m[nt][1] + kSlack;
-      }
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float mx0 = mx[nt][0], mx1 = mx[nt][1];
-#pragma unroll
-          for (int o2 = 4; o2 < 32; o2 <<= 1) {
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o2));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o2));
-          }
-          const float mn0 = fmaxf(m[nt][0], mx0), mn1 = fmaxf(m[nt][1], mx1);
-          ref[nt][0] = mn0 == -INFINITY ? 0.f : mn0;
-          ref[nt][1] = mn1 == -INFINITY ? 0.f : mn1;
-          const float al0 = exp2_approx(m[nt][0] - ref[nt][0]);
-          const float al1 = exp2_approx(m[nt][1] - ref[nt][1]);
-          m[nt][0] = mn0;
-          m[nt][1] = mn1;
-          l[nt][0] *= al0;
-          l[nt][1] *= al1;
-          om[nt][0] *= al0;
-          om[nt][1] *= al1;
-#pragma unroll
-          for (int dd = 0; dd < C::KS; ++dd) {
-            o[nt][dd][0] *= al0;
-            o[nt][dd][1] *= al1;
-            o[nt][dd][2] *= al0;
-            o[nt][dd][3] *= al1;
-          }
-        }
-      }
-      uint32_t pb[MT][NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float r0 = ref[nt][0], r1 = ref[nt][1];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const float p0 = exp2_approx(x[nt][mt][0] - r0), p1 = exp2_approx(x[nt][mt][1] - r1);
-          const float p2 = exp2_approx(x[nt][mt][2] - r0), p3 = exp2_approx(x[nt][mt][3] - r1);
-          l[nt][0] += p0 + p2;
-          l[nt][1] += p1 + p3;
-          pb[mt][nt][0] = movmatrix_trans(pack2<__half>(p0, p1));
-          pb[mt][nt][1] = movmatrix_trans(pack2<__half>(p2, p3));
-        }
-      }
-      // ---- O^T[d][column] += V_step^T . P^T
+    for (int nt = 0; nt < NT; ++nt) {
+      mx[nt][0] = mx[nt][1] = -INFINITY;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const uint32_t rows16 = vt + 16 * mt * C::ROWB;
-        if (mt & 1)
-          int4_pv<D, NT, true>(o, om, rows16, pb[mt], lane);
-        else
-          int4_pv<D, NT, false>(o, om, rows16, pb[mt], lane);
+        mx[nt][0] = fmaxf(mx[nt][0], fmaxf(x[nt][mt][0], x[nt][mt][2]));
+        mx[nt][1] = fmaxf(mx[nt][1], fmaxf(x[nt][mt][1], x[nt][mt][3]));
       }
+      grow = grow || mx[nt][0] > m[nt][0] + kSlack || mx[nt][1] > m[nt][1] + kSlack;
+    }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float mx0 = mx[nt][0], mx1 = mx[nt][1];
+#pragma unroll
+        for (int o2 = 4; o2 < 32; o2 <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o2));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o2));
+        }
+        const float mn0 = fmaxf(m[nt][0], mx0), mn1 = fmaxf(m[nt][1], mx1);
+        ref[nt][0] = mn0 == -INFINITY ? 0.f : mn0;
+        ref[nt][1] = mn1 == -INFINITY ? 0.f : mn1;
+        const float al0 = exp2_approx(m[nt][0] - ref[nt][0]);
+        const float al1 = exp2_approx(m[nt][1] - ref[nt][1]);
+        m[nt][0] = mn0;
+        m[nt][1] = mn1;
+        l[nt][0] *= al0;
+        l[nt][1] *= al1;
+        om[nt][0] *= al0;
+        om[nt][1] *= al1;
+#pragma unroll
+        for (int dd = 0; dd < C::KS; ++dd) {
+          o[nt][dd][0] *= al0;
+          o[nt][dd][1] *= al1;
+          o[nt][dd][2] *= al0;
+          o[nt][dd][3] *= al1;
+        }
+      }
+    }
+    uint32_t pb[MT][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float r0 = ref[nt][0], r1 = ref[nt][1];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const float p0 = exp2_approx(x[nt][mt][0] - r0), p1 = exp2_approx(x[nt][mt][1] - r1);
+        const float p2 = exp2_approx(x[nt][mt][2] - r0), p3 = exp2_approx(x[nt][mt][3] - r1);
+        l[nt][0] += p0 + p2;
+        l[nt][1] += p1 + p3;
+        pb[mt][nt][0] = movmatrix_trans(pack2<__half>(p0, p1));
+        pb[mt][nt][1] = movmatrix_trans(pack2<__half>(p2, p3));
+      }
+    }
+    // ---- O^T[d][column] += V_step^T . P^T
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const uint32_t rows16 = vt + 16 * mt * C::ROWB;
+      if (mt & 1)
+        int4_pv<D, NT, true>(o, om, rows16, pb[mt], lane);
+      else
+        int4_pv<D, NT, false>(o, om, rows16, pb[mt], lane);
+    }
     __syncwarp();  // every lane is done with this slot before it is refilled
   }
   if constexpr (!C::BULK) cp_async_wait<0>();

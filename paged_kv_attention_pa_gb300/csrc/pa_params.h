@@ -28,12 +28,6 @@ constexpr int kPartitionMin = 64;   // tokens: below this a split's fixed cost d
 #ifndef PA_TILE_TOKENS_F8_D256
 #define PA_TILE_TOKENS_F8_D256 32
 #endif
-#ifndef PA_TILE_TOKENS_I4_D128
-#define PA_TILE_TOKENS_I4_D128 32
-#endif
-#ifndef PA_TILE_TOKENS_I4_D256
-#define PA_TILE_TOKENS_I4_D256 32
-#endif
 // What the caches hold: elements of the q/out type, FP8 E4M3, or 4-bit groups.
 enum KvKind { kKv16 = 0, kKvFp8 = 1, kKvInt4 = 2 };
 // Bytes of one cache row (one token of one KV head) of K or V.
@@ -43,7 +37,7 @@ __host__ __device__ constexpr int kv_row_bytes(int D, KvKind kind) {
 // Per head_dim and cache type: a 256-wide 16-bit row pair is already 1 KB a token;
 // fp8 rows carry half the bytes of a 16-bit row for the same arithmetic.
 __host__ __device__ constexpr int tile_tokens(int D, KvKind kind) {
-  return kind == kKvInt4  ? (D == 128 ? PA_TILE_TOKENS_I4_D128 : PA_TILE_TOKENS_I4_D256)
+  return kind == kKvInt4  ? 32
          : kind == kKvFp8 ? (D == 128 ? PA_TILE_TOKENS_F8_D128 : PA_TILE_TOKENS_F8_D256)
                           : (D == 128 ? PA_TILE_TOKENS_D128 : PA_TILE_TOKENS_D256);
 }
