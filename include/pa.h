@@ -90,8 +90,8 @@ typedef enum pa_kv_dtype {
  * block are contiguous. pa_append writes such rows: the minimum rounded down and the step
  * (a fifteenth of the range above it) rounded up to fp16, and the nearest code. Values
  * beyond +-65280 saturate there. A group that holds a NaN or an infinity reads back as NaN.
- * Rows written otherwise: pa_decode needs steps <= 8734 and minimum + 15 * step below 65520
- * (what fp16 holds) in the V cache.
+ * Rows written otherwise: pa_decode needs steps <= 8734 in the V cache (weights times steps
+ * are fp16).
  */
 #define PA_INT4_ROW_BYTES(D) ((D) / 8 * 5)
 
@@ -123,7 +123,8 @@ typedef void* pa_stream_t; /* cudaStream_t */
  *           ROCm paged-attention kernel wins all sixty cells", section 6).
  *           4-bit caches (layout above): the codes enter the tensor-core products exactly
  *           as fp16, the queries rounded to fp16 after scaling by a power of two (any
- *           range), the weights times the steps rounded to fp16, with fp32 accumulation.
+ *           range up to 2^110 / (scale * k_scale)), the weights rounded to fp16 and once more
+ *           after multiplication by the steps, with fp32 accumulation; nothing else is rounded.
  *           v_scale should leave the larger steps above about 2^-10 (values / v_scale
  *           around 1): smaller products with weights lose bits to fp16's 2^-24.
  *   k_scale, v_scale  per-tensor dequantisation scales (finite, > 0) for an fp8 or
@@ -234,9 +235,10 @@ pa_status pa_decode_ex(const pa_decode_args* args, void* workspace, size_t works
 /*
  * The launch plan pa_decode_ex would use on a GPU with `sm_count` SMs: the number
  * of context splits and the tokens per split, a whole number of warp tiles (32
- * tokens at head_dim 128 and for fp8 caches, 16 at head_dim 256). It depends on the
- * sizes, max_seq_len, window, kv_dtype, splits and total_tokens of `args`. Pure
- * host arithmetic; needs no GPU. sm_count <= 0 means the current device's SM count.
+ * tokens at head_dim 128 and for fp8 and 4-bit caches, 16 at head_dim 256). It depends on
+ * the sizes, max_seq_len, window, kv_dtype, splits and total_tokens of `args`, and for
+ * 4-bit caches on q_len. Pure host arithmetic; needs no GPU. sm_count <= 0 means the
+ * current device's SM count.
  */
 pa_status pa_decode_plan(const pa_decode_args* args, int sm_count, int* splits,
                          int* partition_tokens);
@@ -361,7 +363,9 @@ pa_status pa_rope_turns(int rot_dim, double base, const pa_rope_scaling* scaling
  *   k_scale, v_scale  for fp8 and 4-bit caches: the cache holds value / scale (E4M3
  *             saturates at +-448, nearest even; 4 bits: see PA_INT4_ROW_BYTES)
  *   rot_dim   elements of a head that turn: 0 (none) or a multiple of 16 up to D
- * Rotation and quantisation are in fp32, with one rounding to what is stored. A row with
+ * Angles are rounded to fp32 relative to the nearest quarter turn; sines and cosines (times
+ * the amplitude), rotated values and quotients by a scale are fp32 values, each rounded once,
+ * and what is stored is rounded once from them. A row with
  * an invalid length or table entry is not written to the cache and raises a PA_DEVERR_*
  * bit. Two rows of one call that name the same cache slot leave either's values there, or
  * a mixture. `workspace`: >= PA_WORKSPACE_HEADER_BYTES, 256-byte aligned; only its error

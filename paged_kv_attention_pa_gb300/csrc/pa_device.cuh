@@ -42,8 +42,9 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint16_t x) {
 }
 
 // 2^x by the hardware approximation (PTX ex2.approx.ftz.f32, relative error about
-// 2^-22). Every use here has x <= 0 (softmax weights, rescale factors): results lie
-// in [0, 1], subnormal ones flush to zero, and 2^-inf = +0.
+// 2^-22). Rescale factors and the weights of 16-bit caches have x <= 0; the weights of fp8
+// and 4-bit caches, whose reference point lags behind the running maximum, x up to 8 and
+// 2. Subnormal results flush to zero, and 2^-inf = +0.
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

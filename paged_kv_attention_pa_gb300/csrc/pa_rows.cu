@@ -194,8 +194,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // two bits) to its word of codes, and the group's step and minimum. The minimum is rounded
 // down and the step up, so every element lies between the first and the sixteenth value.
 // Elements saturate at +-65280: with the step's rounding (less than 8) the sixteenth value is
-// then below 65280 + 15 * 8 and rounds to a finite fp16, which decode's sums from the upper end
-// of the codes need, and the step is at most 130560 / 15 = 8704.
+// then below 65280 + 15 * 8 and rounds to a finite fp16 (gather's outputs), and the step is at
+// most 130560 / 15 = 8704, whose products with weights are finite in fp16 (decode).
 //
 // The code is the nearest integer to (x - minimum) / step, exact ties (frequent for 16-bit
 // inputs) to even, so the quotient has to be the correctly rounded one. With y the correctly
