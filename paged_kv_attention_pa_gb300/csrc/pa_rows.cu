@@ -649,6 +649,7 @@ pa_status pa_append(const pa_append_args* a, void* workspace, size_t workspace_b
   for (int64_t s : {a->k_stride, a->v_stride, a->q ? a->q_stride : 0})
     if (s < 0 || s % 8 != 0) return PA_ERR_INVALID_ARG;
   if (T == 0) return PA_OK;
+  if (a->q && a->q_out == a->q && T > 1 && a->q_stride != (int64_t)a->Hq * a->D) return PA_ERR_INVALID_ARG;
   if (!a->k || !a->v || !a->k_cache || !a->v_cache || !a->block_tables || !a->seq_lens ||
       (a->rot_dim > 0 && !a->rope_turns))
     return PA_ERR_INVALID_ARG;

@@ -166,3 +166,20 @@ def test_plan_knows_the_query_rows(lib):
     assert one != pa.plan(10, 64, 16, 128, 16, 160, rows=4, **kw)
     with pytest.raises(pa.PAError):
         pa.plan(1, 32, 8, 128, 16, 512, sm_count=152, rows=9)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=32, q_out=32, q_stride=8 * 128), pa.PA_ERR_WORKSPACE),          # in place: the next check
+    (dict(q=32, q_out=32, q_stride=24 * 128), pa.PA_ERR_INVALID_ARG),       # the heads of a projection's rows
+    (dict(q=32, q_out=32, q_stride=24 * 128, B=1), pa.PA_ERR_WORKSPACE),    # one row: dense
+    (dict(q=32, q_out=32, q_stride=24 * 128, rows=0), pa.PA_OK),
+])
+def test_append_in_place_needs_dense_queries(lib, kw, code):
+    # q_out is dense: written over the strided rows of q, it would destroy rows not yet read
+    a = pa.AppendArgs()
+    base = dict(q=16, q_out=32, k=48, v=64, k_cache=80, v_cache=96, block_tables=4, seq_lens=8, q_stride=1024,
+                k_stride=1024, v_stride=1024, B=2, rows=1, Hq=8, Hkv=8, D=128, block_size=16, num_blocks=8,
+                max_blocks_per_seq=4, dtype=pa.PA_BF16, rope_amplitude=1.0)
+    for k, v in dict(base, **kw).items():
+        setattr(a, k, v)
+    assert lib.pa_append(ctypes.byref(a), 0, 0, None) == code
