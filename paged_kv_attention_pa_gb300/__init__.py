@@ -123,7 +123,6 @@ class PAError(RuntimeError):
 _lib = None
 _native = None  # the module of csrc/binding.cpp
 _lib_lock = threading.Lock()
-_tls = threading.local()
 
 
 def load(path: str = LIB_PATH):
@@ -159,11 +158,16 @@ _DT = {torch.float16: PA_F16, torch.bfloat16: PA_BF16}
 
 
 def _ensure_device(lib, index: int):
-    if getattr(_tls, "device", None) != index:
-        rc = lib.pa_set_device(index)
-        if rc != PA_OK:
-            raise PAError(rc, "pa_set_device")
-        _tls.device = index
+    """Make a device current, for the library as for torch. (The calls below change it for
+    their own duration only.)"""
+    rc = lib.pa_set_device(index)
+    if rc != PA_OK:
+        raise PAError(rc, "pa_set_device")
+
+
+def _device_of(t):
+    """Context in which t's device is the current one."""
+    return torch.cuda.device(t.device.index if t.is_cuda else -1)
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -307,20 +311,21 @@ def _workspace(need: int, device: torch.device, stream_handle: int, stream=None)
 
 def workspace_for(args: DecodeArgs, device: torch.device, stream_handle: int,
                   stream=None) -> torch.Tensor:
-    need = load().pa_decode_ex_workspace_bytes(ctypes.byref(args))
+    with torch.cuda.device(device):  # the plan follows its number of SMs
+        need = load().pa_decode_ex_workspace_bytes(ctypes.byref(args))
     if need == 0:
         raise PAError(PA_ERR_INVALID_ARG, "pa_decode_ex_workspace_bytes")
     return _workspace(need, device, stream_handle, stream)
 
 
 def _call_on(t: torch.Tensor, stream):
-    """(device index, stream handle, stream) of a call on t's device, made current to the
-    library; -1, 0 and None for a CPU tensor, which the call then refuses."""
-    lib = _lib or load()
+    """(device index, stream handle, stream) of a call on t's device; -1, 0 and None for a CPU
+    tensor, which the call then refuses."""
+    if _lib is None:
+        load()
     dev = t.get_device()
     if dev < 0:
         return dev, 0, None
-    _ensure_device(lib, dev)
     sh = _stream_of(dev, stream)
     if stream is not None and not isinstance(stream, torch.Stream):  # another library's
         stream = torch.cuda.ExternalStream(sh, device=dev)
@@ -392,13 +397,13 @@ def decode_plain(q, k_cache, v_cache, block_tables, seq_lens, scale, out=None,
     if out is None:
         out = torch.empty_like(q)
     args = make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale, max_seq_len, 0)
-    _ensure_device(lib, q.device.index)
     sh = _stream_handle(q.device, stream)
     ws = workspace if workspace is not None else workspace_for(args, q.device, sh, stream)
-    rc = lib.pa_decode(args.q, args.k_cache, args.v_cache, args.block_tables, args.seq_lens,
-                       args.out, args.B, args.Hq, args.Hkv, args.D, args.block_size,
-                       args.num_blocks, args.max_blocks_per_seq, args.max_seq_len,
-                       args.scale, args.dtype, ws.data_ptr(), ws.numel(), sh)
+    with _device_of(q):
+        rc = lib.pa_decode(args.q, args.k_cache, args.v_cache, args.block_tables, args.seq_lens,
+                           args.out, args.B, args.Hq, args.Hkv, args.D, args.block_size,
+                           args.num_blocks, args.max_blocks_per_seq, args.max_seq_len,
+                           args.scale, args.dtype, ws.data_ptr(), ws.numel(), sh)
     if rc != PA_OK:
         raise PAError(rc, "pa_decode")
     return out
@@ -415,12 +420,12 @@ def decode_noalloc(q, k_cache, v_cache, block_tables, seq_lens, scale, out=None,
     if out is None:
         out = torch.empty_like(q)
     args = make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale, max_seq_len, 0)
-    _ensure_device(lib, q.device.index)
     sh = _stream_handle(q.device, stream)
-    rc = lib.pa_decode_noalloc(args.q, args.k_cache, args.v_cache, args.block_tables,
-                               args.seq_lens, args.out, args.B, args.Hq, args.Hkv, args.D,
-                               args.block_size, args.num_blocks, args.max_blocks_per_seq,
-                               args.max_seq_len, args.scale, args.dtype, sh)
+    with _device_of(q):
+        rc = lib.pa_decode_noalloc(args.q, args.k_cache, args.v_cache, args.block_tables,
+                                   args.seq_lens, args.out, args.B, args.Hq, args.Hkv, args.D,
+                                   args.block_size, args.num_blocks, args.max_blocks_per_seq,
+                                   args.max_seq_len, args.scale, args.dtype, sh)
     if rc != PA_OK:
         raise PAError(rc, "pa_decode_noalloc")
     return out
@@ -550,9 +555,9 @@ def kernel_count(q, k_cache, v_cache, block_tables, seq_lens, scale, max_seq_len
     out = q  # only its shape and dtype are read
     args = make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale, max_seq_len,
                      splits, window, total_tokens=total_tokens)
-    _ensure_device(lib, q.device.index)
     n = ctypes.c_int(-1)
-    rc = lib.pa_decode_kernel_count(ctypes.byref(args), ctypes.byref(n))
+    with _device_of(q):
+        rc = lib.pa_decode_kernel_count(ctypes.byref(args), ctypes.byref(n))
     if rc != PA_OK:
         raise PAError(rc, "pa_decode_kernel_count")
     return n.value
@@ -562,12 +567,12 @@ def read_device_errors(workspace: torch.Tensor, stream=None) -> int:
     """Wait for the stream, return and clear the PA_DEVERR_* bits of a workspace (and, of a
     default one, those of the smaller ones that it took the place of)."""
     lib = load()
-    _ensure_device(lib, workspace.device.index)
     sh = _stream_handle(workspace.device, stream)
     found = 0
     while workspace is not None:
         flags = ctypes.c_uint32(0)
-        rc = lib.pa_read_device_errors(workspace.data_ptr(), sh, ctypes.byref(flags))
+        with _device_of(workspace):
+            rc = lib.pa_read_device_errors(workspace.data_ptr(), sh, ctypes.byref(flags))
         if rc != PA_OK:
             raise PAError(rc, "pa_read_device_errors")
         found |= flags.value

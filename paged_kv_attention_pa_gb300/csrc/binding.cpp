@@ -9,6 +9,7 @@
 #include <optional>
 
 #include <ATen/ops/empty.h>
+#include <c10/core/DeviceGuard.h>
 #include <c10/core/StreamGuard.h>
 #include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/Exceptions.h>
@@ -161,10 +162,11 @@ struct Workspace {
   }
 };
 
-// (status, results...) with the library's own call made without the interpreter's lock.
+// The library's own call, made on the tensors' device and without the interpreter's lock.
 template <typename Args, typename Fn>
-pa_status launch(Fn fn, const Args& a, const Workspace& ws, PyObject* stream) {
+pa_status launch(Fn fn, const Args& a, int64_t device, const Workspace& ws, PyObject* stream) {
   const pa_stream_t s = reinterpret_cast<pa_stream_t>(static_cast<uintptr_t>(integer(stream)));
+  const c10::DeviceGuard guard(c10::Device(at::kCUDA, (c10::DeviceIndex)device));
   pa_status rc;
   Py_BEGIN_ALLOW_THREADS;
   rc = fn(&a, ws.at, ws.bytes, s);
@@ -260,7 +262,7 @@ PyObject* do_decode(PyObject* const* v) {
   a.block_tables = data<int32_t>(bt);
   a.seq_lens = data<int32_t>(sl);
   a.out = data<void>(out);
-  const pa_status rc = launch(pa_decode_ex, a, ws, v[15]);
+  const pa_status rc = launch(pa_decode_ex, a, dev, ws, v[15]);
   return Py_BuildValue("(iN)", (int)rc, given ? Py_NewRef(v[6]) : THPVariable_Wrap(out));
 }
 
@@ -336,7 +338,7 @@ PyObject* do_append(PyObject* const* v) {
     a.rope_turns = reinterpret_cast<const uint64_t*>(data<int64_t>(*turns));
     a.rot_dim = to32(2 * turns->size(0));
   }
-  const pa_status rc = launch(pa_append, a, ws, v[15]);
+  const pa_status rc = launch(pa_append, a, dev, ws, v[15]);
   return Py_BuildValue("(iN)", (int)rc,
                        given ? Py_NewRef(v[7]) : q ? THPVariable_Wrap(out) : Py_NewRef(Py_None));
 }
@@ -385,7 +387,7 @@ PyObject* do_gather(PyObject* const* v) {
   a.starts = starts ? data<int32_t>(*starts) : nullptr;
   a.k_out = data<void>(ko);
   a.v_out = data<void>(vo);
-  const pa_status rc = launch(pa_gather, a, ws, v[12]);
+  const pa_status rc = launch(pa_gather, a, dev, ws, v[12]);
   return Py_BuildValue("(iNN)", (int)rc, kg ? Py_NewRef(v[7]) : THPVariable_Wrap(ko),
                        vg ? Py_NewRef(v[8]) : THPVariable_Wrap(vo));
 }

@@ -183,3 +183,46 @@ def test_append_in_place_needs_dense_queries(lib, kw, code):
     for k, v in dict(base, **kw).items():
         setattr(a, k, v)
     assert lib.pa_append(ctypes.byref(a), 0, 0, None) == code
+
+
+def test_calls_run_on_their_tensors_device_and_leave_the_current_one(monkeypatch):
+    # the current device may have changed since the last call, and belongs to the caller
+    at = [0]
+
+    class device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before = at[0]
+            if self.index >= 0:
+                at[0] = self.index
+
+        def __exit__(self, *_):
+            at[0] = self.before
+
+    class Lib(FakeLib):
+        seen = []
+
+        def pa_set_device(self, index):
+            at[0] = index
+            return pa.PA_OK
+
+        def pa_read_device_errors(self, ws, stream, flags):
+            self.seen.append(at[0])
+            return pa.PA_OK
+
+    class Workspace:
+        def __init__(self, index):
+            self.is_cuda, self.device = True, torch.device("cuda", index)
+
+        def data_ptr(self):
+            return 256
+
+    monkeypatch.setattr(pa, "load", Lib)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    for current in (0, 2):
+        at[0] = current
+        for index in (1, 0, 1):
+            pa.read_device_errors(Workspace(index), FakeStream)
+            assert Lib.seen[-1] == index and at[0] == current
