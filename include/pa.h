@@ -363,9 +363,9 @@ pa_status pa_rope_turns(int rot_dim, double base, const pa_rope_scaling* scaling
  *   k_scale, v_scale  for fp8 and 4-bit caches: the cache holds value / scale (E4M3
  *             saturates at +-448, nearest even; 4 bits: see PA_INT4_ROW_BYTES)
  *   rot_dim   elements of a head that turn: 0 (none) or a multiple of 16 up to D
- * Angles are rounded to fp32 relative to the nearest quarter turn; sines and cosines (times
- * the amplitude), rotated values and quotients by a scale are fp32 values, each rounded once,
- * and what is stored is rounded once from them. A row with
+ * Angles are rounded to fp32 relative to the nearest quarter turn. Sines and cosines, their
+ * products with the amplitude, the rotation and the (correctly rounded) quotients by a scale
+ * are fp32; what is stored is rounded once from that. A row with
  * an invalid length or table entry is not written to the cache and raises a PA_DEVERR_*
  * bit. Two rows of one call that name the same cache slot leave either's values there, or
  * a mixture. `workspace`: >= PA_WORKSPACE_HEADER_BYTES, 256-byte aligned; only its error

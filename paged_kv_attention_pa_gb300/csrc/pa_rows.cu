@@ -157,10 +157,10 @@ __device__ __forceinline__ float2 cos_sin(uint32_t turn) {
   return quarters & 2 ? make_float2(-x, -y) : make_float2(x, y);
 }
 
-// (a, b) turned by the angle with cosine cs.x and sine cs.y; each product rounded on its own.
+// (a, b) turned by the angle with cosine cs.x and sine cs.y; of each sum one product is rounded.
 __device__ __forceinline__ void rotate_pair(float& a, float& b, float2 cs) {
-  const float x = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
-  b = __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
+  const float x = __fmaf_rn(a, cs.x, -__fmul_rn(b, cs.y));
+  b = __fmaf_rn(b, cs.x, __fmul_rn(a, cs.y));
   a = x;
 }
 
