@@ -1,5 +1,6 @@
 """Decode over 4-bit caches against float64 with bounds that see a lost token or tile
 (test_int4_bounds_cpu.py), through every way its tiles reach a warp (GB300 only)."""
+import os
 import random
 
 import pytest
@@ -9,6 +10,8 @@ from int4_bounds import Case
 
 pytestmark = pytest.mark.gpu
 
+# 24 by default; PA_RANDOM_LONG runs more draws of the same seeded generator
+N_LONG = int(os.environ.get("PA_RANDOM_LONG", "24"))
 EDGES = (0, 1, 15, 16, 31, 32, 33, -1, -2, -33)
 
 
@@ -111,7 +114,7 @@ def test_short_ctas(cuda_lib, B, Hq, Hkv, D, bs, longest):
     check(cuda_lib, Case(lens, Hq, Hkv, D, bs, "f16", seed=7, heavy=(0, -1)))
 
 
-@pytest.mark.parametrize("idx", range(24))
+@pytest.mark.parametrize("idx", range(N_LONG))
 def test_random_long_contexts(cuda_lib, idx):
     r = random.Random(9000 + idx)
     D = r.choice([128, 256])
