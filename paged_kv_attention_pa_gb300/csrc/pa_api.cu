@@ -77,8 +77,10 @@ bool make_plan(int sm_count, int64_t B, int64_t Hkv, int D, pa::KvKind kv, int64
   // that leave an SM in six free end sooner where their length hardly matters: the merge grid
   // and the next call's CTAs find room (GB300, us per call: one sequence, 8 KV heads, 8K tokens
   // 7.4 for 128 CTAs against 8.7 for 152; hybrid layer, 8K 8.6 for 128 against 9.4 for 148, 32K
-  // 14.0 against 14.3). So that grid is tried too, and a split one-wave grid beyond it is
-  // charged the difference. Splits below 128 tokens lose (hybrid layer, 2K tokens: 7.6 for 64
+  // 14.0 against 14.3; head_dim 128, 1, 2, 3, 5, 6 and 12 heads, 32K, roomy / all SMs 9.5 / 9.0, 7.7 /
+  // 9.1, 9.1 / 9.0, 11.0 / 11.3, 12.1 / 12.6, 19.3 / 18.0, and at 256 10.4 / 11.4, 9.1 / 11.5, 11.7 /
+  // 12.4, 15.2 / 15.4, 17.0 / 16.9, 29.0 / 26.2, where the plan takes all SMs). So that grid is tried
+  // too, and a split one-wave grid beyond it is charged the difference. Splits below 128 tokens lose (hybrid layer, 2K tokens: 7.6 for 64
   // tokens a split, 6.6 for 128; 8 heads, 512 tokens: 5.0 and 4.8).
   const bool int4 = kv == pa::kKvInt4;
   const int64_t roomy = sm * 27 / 32;
@@ -111,6 +113,8 @@ bool make_plan(int sm_count, int64_t B, int64_t Hkv, int D, pa::KvKind kv, int64
   // 24 of 1K-16K 88 / 105 / 108; hybrid layer, 64 of 512-8K 57.5 / 83 / 88. 200 sequences of
   // 128-2K, ten CTAs an SM, lose by it (98 / 86): not where it costs more than a quarter of
   // the longest context.
+  // (Few long sequences among short ones are planned badly: the cost of splits below charges
+  // every CTA a full one. 2 of 32K and 22 of 200-2K tokens 66.6 us, in four splits 40.)
   const bool mixed =
       int4 && total_tokens > 0 && B <= pa::kOrderedBatch && total_tokens < 7 * B * max_len / 8;
   //

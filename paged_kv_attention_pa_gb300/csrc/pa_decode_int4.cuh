@@ -14,10 +14,12 @@
 //
 // Math. 160 bytes per token and KV head at head_dim 128 pass through an SM in 3.6 ns at the
 // memory's rate, and the arithmetic of its tiles takes as long. Twelve warps at head_dim 128
-// with up to 8 columns: 5.7 TB/s with every SM busy (152 pairs of 8K tokens, 34.9 us; eight
-// warps 40.3), against 6.2 TB/s for the copies alone. Two CTAs of six warps an SM: 37.6 us. Tiles whose length is known at compile time and the refill ahead of
-// the wait matter: runtime tiles of 64 tokens with the refill behind the arithmetic ran
-// 38.3-40.1 us with fewer instructions.
+// with up to 8 columns: 5.5 TB/s with every SM busy (152 pairs of 8K tokens, 36.0 us), against
+// 6.2 TB/s for the copies alone. (An earlier build, 34.9 us: eight warps 40.3; two CTAs of six
+// warps an SM 37.6; tiles of 64 tokens whose length is known at run time only, with the refill
+// behind the arithmetic, 38.3-40.1 with fewer instructions.) More than 16 columns at head_dim 128
+// and more than 8 at 256 spill registers (320 and 178 bytes a thread) and run at 0.18 and 0.34
+// of the copy rate, where 8 and 16 reach 0.78 and 0.46.
 #pragma once
 
 #include "pa_decode_kernel.cuh"
