@@ -99,6 +99,8 @@ typedef enum pa_kv_dtype {
 #define PA_DEVERR_BLOCK_INDEX 1u /* a live token's block table entry was outside [0, num_blocks) */
 #define PA_DEVERR_SEQ_LEN 2u     /* a seq_len < 0, > max_seq_len or > max_blocks_per_seq*block_size */
 #define PA_DEVERR_COPY 4u        /* a copy into shared memory took over two seconds: no meaningful output */
+#define PA_DEVERR_ROWS 8u        /* pa_cross, pa_decode_shared: starts or groups that do not ascend, or
+                                    reach past the call's rows or sequences */
 
 typedef void* pa_stream_t; /* cudaStream_t */
 
@@ -422,6 +424,76 @@ typedef struct pa_gather_args {
 
 pa_status pa_gather(const pa_gather_args* args, void* workspace, size_t workspace_bytes,
                     pa_stream_t stream);
+
+/*
+ * Cross attention: query rows over a context of another length, for example a decoder's tokens
+ * over an encoder's states held in a paged cache. Every row of sequence b sees all seq_lens[b]
+ * tokens of its context:
+ *   out[r,h] = sum_t softmax(scale * q[r,h] . K[b,t,h / G])_t * V[b,t,h / G]    t < seq_lens[b]
+ * Any number of rows: one (a decode step), a few (the beams of a search, which share their
+ * source), or a prompt's thousands.
+ *   q         [rows, Hq, D] (dtype); row r starts at element r * q_stride (a multiple of 8), the
+ *             heads of a row are dense
+ *   starts    as for pa_append: NULL, and sequence b has the `rows` rows b * rows + i; or [B + 1]
+ *             ascending int32 on the device, and `rows` is the number of rows in all. Rows of no
+ *             sequence are padding: neither read nor written in out
+ *   out       dense [rows, Hq, D]; rows over an empty context (seq_lens[b] = 0) are zero
+ *   k_cache, v_cache, block_tables, seq_lens, max_seq_len, kv_dtype, k_scale, v_scale
+ *             as for pa_decode_ex, with 16-bit and fp8 caches (with fp8 the queries are rounded to
+ *             fp16: |x| <= 65504). 4-bit caches: PA_ERR_UNSUPPORTED
+ * G = Hq / Hkv up to PA_MAX_GQA_GROUP; rows * G below 2^28, rows * Hq below 2^31. Scores, softmax
+ * statistics and sums are fp32; the weights are rounded to the type of the products (dtype, fp16
+ * for fp8 caches), the output once. The work is divided among the SMs by the lengths found on the
+ * device: the host needs none of them, and repeated calls give the same bits. `workspace`:
+ * pa_cross_workspace_bytes, 256-byte aligned, its header zero before first use, as for pa_decode;
+ * calls that overlap on the GPU must not share one.
+ */
+typedef struct pa_cross_args {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* starts;
+  void* out;
+  int64_t q_stride;
+  int32_t B, rows, Hq, Hkv, D;
+  int32_t block_size, num_blocks, max_blocks_per_seq, max_seq_len;
+  float scale;
+  int32_t dtype;    /* pa_dtype */
+  int32_t kv_dtype; /* pa_kv_dtype */
+  float k_scale, v_scale;
+} pa_cross_args;
+
+/* Workspace bytes of a pa_cross call on the current device (pointers are not read, but whether
+ * starts is NULL matters); 0 for invalid sizes. */
+size_t pa_cross_workspace_bytes(const pa_cross_args* args);
+
+pa_status pa_cross(const pa_cross_args* args, void* workspace, size_t workspace_bytes,
+                   pa_stream_t stream);
+
+/*
+ * Decode for sequences that share prefixes: pa_decode_ex's result, with the keys and values of a
+ * shared prefix read once for all sequences of its group.
+ *   args         as for pa_decode_ex, with q_len causal query rows per sequence (any number);
+ *                16-bit and fp8 caches (4 bits: PA_ERR_UNSUPPORTED); splits and window must be 0
+ *   groups       [num_groups + 1] ascending int32 on the device: sequences groups[n] to
+ *                groups[n + 1] - 1 are group n. Sequences of no group share nothing
+ *   prefix_lens  [num_groups] int32 on the device: how many leading tokens they share. What is
+ *                shared is the first min(prefix_lens[n], seq_lens[groups[n]]) tokens, any number
+ *                of them, read through the table row of the group's FIRST sequence; the others'
+ *                entries, and slots of their own blocks, before that are not used
+ * A row sees what it sees in pa_decode_ex: tokens t < seq_lens[b] - q_len + i + 1, the shared ones
+ * among them; a row that sees none is zero. Cached values must be finite at the tokens of a group's
+ * prefix and of each sequence: a NaN or an infinity in V reaches rows that do not see its token
+ * too. Repeated calls give the same bits. Rounding and limits as for pa_cross, with B * q_len
+ * rows. `workspace`: pa_decode_shared_workspace_bytes, as for pa_decode.
+ */
+size_t pa_decode_shared_workspace_bytes(const pa_decode_args* args, int num_groups);
+
+pa_status pa_decode_shared(const pa_decode_args* args, const int32_t* groups,
+                           const int32_t* prefix_lens, int num_groups, void* workspace,
+                           size_t workspace_bytes, pa_stream_t stream);
 
 /* Static text for a status code. */
 const char* pa_status_string(pa_status status);

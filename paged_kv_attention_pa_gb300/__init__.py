@@ -36,7 +36,7 @@ PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA, \
 PA_F16, PA_BF16 = 0, 1
 PA_KV_AS_DTYPE, PA_KV_FP8_E4M3, PA_KV_INT4 = 0, 1, 2
 PA_ROPE_HALF, PA_ROPE_INTERLEAVED = 0, 1
-PA_DEVERR_BLOCK_INDEX, PA_DEVERR_SEQ_LEN, PA_DEVERR_COPY = 1, 2, 4
+PA_DEVERR_BLOCK_INDEX, PA_DEVERR_SEQ_LEN, PA_DEVERR_COPY, PA_DEVERR_ROWS = 1, 2, 4, 8
 PA_FLAG_DETERMINISTIC = 1
 PA_WORKSPACE_HEADER_BYTES = 8448
 PA_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -56,6 +56,10 @@ SIGNATURES = {
     "pa_decode_kernel_count": (_c.c_int, [_c.c_void_p, _c.c_void_p]),
     "pa_append": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
     "pa_gather": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "pa_cross": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "pa_cross_workspace_bytes": (_c.c_size_t, [_c.c_void_p]),
+    "pa_decode_shared": (_c.c_int, [_c.c_void_p] * 3 + [_c.c_int, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "pa_decode_shared_workspace_bytes": (_c.c_size_t, [_c.c_void_p, _c.c_int]),
     "pa_rope_turns": (_c.c_int, [_c.c_int, _c.c_double, _c.c_void_p, _c.c_void_p, _c.c_void_p]),
     "pa_workspace_init": (_c.c_int, [_c.c_void_p, _c.c_size_t, _c.c_void_p]),
     "pa_read_device_errors": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p]),
@@ -103,6 +107,19 @@ class GatherArgs(ctypes.Structure):
         ("v_out", _c.c_void_p), ("B", _c.c_int32), ("rows", _c.c_int32), ("Hkv", _c.c_int32),
         ("D", _c.c_int32), ("block_size", _c.c_int32), ("num_blocks", _c.c_int32),
         ("max_blocks_per_seq", _c.c_int32), ("dtype", _c.c_int32), ("kv_dtype", _c.c_int32),
+        ("k_scale", _c.c_float), ("v_scale", _c.c_float),
+    ]
+
+
+class CrossArgs(ctypes.Structure):
+    """Mirror of pa_cross_args (include/pa.h)."""
+    _fields_ = [
+        ("q", _c.c_void_p), ("k_cache", _c.c_void_p), ("v_cache", _c.c_void_p),
+        ("block_tables", _c.c_void_p), ("seq_lens", _c.c_void_p), ("starts", _c.c_void_p),
+        ("out", _c.c_void_p), ("q_stride", _c.c_int64), ("B", _c.c_int32), ("rows", _c.c_int32),
+        ("Hq", _c.c_int32), ("Hkv", _c.c_int32), ("D", _c.c_int32), ("block_size", _c.c_int32),
+        ("num_blocks", _c.c_int32), ("max_blocks_per_seq", _c.c_int32), ("max_seq_len", _c.c_int32),
+        ("scale", _c.c_float), ("dtype", _c.c_int32), ("kv_dtype", _c.c_int32),
         ("k_scale", _c.c_float), ("v_scale", _c.c_float),
     ]
 
@@ -517,6 +534,67 @@ def gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Ten
     if rc != PA_OK:
         raise PAError(rc, "pa_gather")
     return k, v
+
+
+def _with_workspace(call, t: torch.Tensor, dev: int, sh: int, stream, workspace, where: str):
+    """A native call that returns (status, out, workspace bytes it lacks), on the workspace given
+    or the one kept for the device and stream, which grows to what the call needs."""
+    ws = workspace if workspace is not None else _default_workspace(dev, sh)
+    rc, out, need = call(ws, None)
+    if rc == PA_ERR_WORKSPACE and workspace is None:  # none yet, or too small: nothing was launched
+        rc, out, _ = call(_workspace(need, t.device, sh, stream), out)
+    if rc != PA_OK:
+        raise PAError(rc, where)
+    return out
+
+
+def cross(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+          block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+          out: Optional[torch.Tensor] = None, starts: Optional[torch.Tensor] = None,
+          max_seq_len: Optional[int] = None, k_scale: float = 1.0, v_scale: float = 1.0,
+          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Cross attention: query rows over a paged context of another length (an encoder's states,
+    a retrieved text), all of which every row sees:
+    out[r, h] = softmax(scale * q[r, h] . K_b^T) V_b over the seq_lens[b] tokens of its sequence b.
+
+    q is [B, Hq, D] (one row per sequence), [B, R, Hq, D] (R rows, such as beams over one source),
+    or packed [rows, Hq, D] with starts [B + 1] int32 (rows starts[b] to starts[b + 1] - 1 belong to
+    sequence b; others are padding, left alone in out and uninitialised in an out made here). It may
+    be a slice of a projection: the heads of a row contiguous, the rows evenly spaced. The caches,
+    tables and max_seq_len are as in decode(), 16-bit or float8_e4m3fn. An empty context gives
+    zeros. out must be contiguous. Repeated calls are bitwise identical. Asynchronous on the current
+    (or given) stream; workspace as in decode().
+    """
+    dev, sh, stream = _call_on(q, stream)
+    return _with_workspace(
+        lambda ws, made: _native.cross(q, k_cache, v_cache, block_tables, seq_lens, scale,
+                                       out if made is None else made, starts, max_seq_len, k_scale,
+                                       v_scale, ws, sh, stream),
+        q, dev, sh, stream, workspace, "pa_cross")
+
+
+def decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                  block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+                  groups: torch.Tensor, prefix_lens: torch.Tensor,
+                  out: Optional[torch.Tensor] = None, max_seq_len: Optional[int] = None,
+                  k_scale: float = 1.0, v_scale: float = 1.0,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """decode() for sequences that share prefixes (a system prompt, several answers to one
+    question): the keys and values of a shared prefix are read once for all sequences of a group.
+
+    groups [N + 1] int32, ascending: sequences groups[n] to groups[n + 1] - 1 are group n; sequences
+    of no group share nothing. prefix_lens [N] int32: how many of their leading tokens they share
+    (any number; no more than the first sequence of the group has), read through the table row of
+    that first sequence. q [B, Hq, D], or [B, R, Hq, D] for R causal query rows per sequence, any
+    number of them; the rest is as in decode(), with 16-bit or float8_e4m3fn caches. Repeated calls
+    are bitwise identical. Asynchronous on the current (or given) stream.
+    """
+    dev, sh, stream = _call_on(q, stream)
+    return _with_workspace(
+        lambda ws, made: _native.decode_shared(q, k_cache, v_cache, block_tables, seq_lens, scale,
+                                               groups, prefix_lens, out if made is None else made,
+                                               max_seq_len, k_scale, v_scale, ws, sh, stream),
+        q, dev, sh, stream, workspace, "pa_decode_shared")
 
 
 def plan(B: int, Hq: int, Hkv: int, D: int, block_size: int, max_seq_len: int,

@@ -392,6 +392,125 @@ PyObject* do_gather(PyObject* const* v) {
                        vg ? Py_NewRef(v[8]) : THPVariable_Wrap(vo));
 }
 
+// The caches, tables and lengths of a call into its arguments.
+template <typename Args>
+void cache_args(Args& a, const Cache& c, const Tensor& kc, const Tensor& vc, const Tensor& bt, const Tensor& sl) {
+  a.D = c.D;
+  a.Hkv = c.Hkv;
+  a.block_size = c.block_size;
+  a.num_blocks = c.num_blocks;
+  a.max_blocks_per_seq = to32(bt.size(1));
+  a.kv_dtype = c.kv;
+  a.k_cache = data<void>(kc);
+  a.v_cache = data<void>(vc);
+  a.block_tables = data<int32_t>(bt);
+  a.seq_lens = data<int32_t>(sl);
+}
+
+// cross(q, k_cache, v_cache, block_tables, seq_lens, scale, out, starts, max_seq_len, k_scale, v_scale,
+//       workspace, stream handle, stream or None) -> (status, out, workspace bytes needed when it is too small)
+PyObject* do_cross(PyObject* const* v) {
+  const Tensor &q = tensor(v[0]), &kc = tensor(v[1]), &vc = tensor(v[2]), &bt = tensor(v[3]), &sl = tensor(v[4]);
+  const Tensor *given = optional_tensor(v[6]), *starts = optional_tensor(v[7]);
+  pa_cross_args a{};
+  const int64_t d = q.dim();
+  a.dtype = dtype_of(q.scalar_type());
+  if (a.dtype < 0 || (given && given->scalar_type() != q.scalar_type()))
+    refuse_type("q and out must be float16 or bfloat16");
+  const Cache c = cache_of(kc, vc, q.scalar_type());
+  a.B = tables_of(bt, sl, starts);
+  if ((d != 3 && (starts || d != 4)) || (!starts && q.size(0) != a.B))
+    refuse_value("q must be [B, Hq, D] or [B, R, Hq, D], or [rows, Hq, D] with starts");
+  if (c.D != q.size(d - 1)) refuse_value("k_cache / v_cache / q shapes disagree");
+  if (given && given->sizes() != q.sizes()) refuse_value("out must have q's shape");
+  a.q_stride = row_stride(q, "q");
+  const int64_t dev = q.get_device();
+  on_device(q, dev, false, "q");
+  on_device(kc, dev, true, "k_cache");
+  on_device(vc, dev, true, "v_cache");
+  on_device(bt, dev, true, "block_tables");
+  on_device(sl, dev, true, "seq_lens");
+  if (starts) on_device(*starts, dev, true, "starts");
+  if (given) on_device(*given, dev, true, "out");
+  a.rows = starts || d == 4 ? to32(q.size(starts ? 0 : 1)) : 1;
+  a.Hq = to32(q.size(d - 2));
+  a.scale = number(v[5]);
+  a.max_seq_len = v[8] == Py_None ? 0 : integer32(v[8]);
+  a.k_scale = c.kv == PA_KV_AS_DTYPE ? 1.f : number(v[9]);
+  a.v_scale = c.kv == PA_KV_AS_DTYPE ? 1.f : number(v[10]);
+  const Workspace ws(v[11], dev);
+  const Outputs outputs(v[13], dev);
+  const Tensor out = given ? *given : outputs.like(q);
+  cache_args(a, c, kc, vc, bt, sl);
+  a.q = data<void>(q);
+  a.starts = starts ? data<int32_t>(*starts) : nullptr;
+  a.out = data<void>(out);
+  const pa_status rc = launch(pa_cross, a, dev, ws, v[12]);
+  size_t need = 0;
+  if (rc == PA_ERR_WORKSPACE) {
+    const c10::DeviceGuard guard(c10::Device(at::kCUDA, (c10::DeviceIndex)dev));
+    need = pa_cross_workspace_bytes(&a);
+  }
+  return Py_BuildValue("(iNn)", (int)rc, given ? Py_NewRef(v[6]) : THPVariable_Wrap(out), (Py_ssize_t)need);
+}
+
+// decode_shared(q, k_cache, v_cache, block_tables, seq_lens, scale, groups, prefix_lens, out, max_seq_len,
+//               k_scale, v_scale, workspace, stream handle, stream or None) -> as cross
+PyObject* do_decode_shared(PyObject* const* v) {
+  const Tensor &q = tensor(v[0]), &kc = tensor(v[1]), &vc = tensor(v[2]), &bt = tensor(v[3]), &sl = tensor(v[4]),
+               &groups = tensor(v[6]), &prefix = tensor(v[7]);
+  const Tensor* given = optional_tensor(v[8]);
+  pa_decode_args a{};
+  const int64_t d = q.dim();
+  if (d != 3 && d != 4) refuse_value("q must be [B, Hq, D] or [B, R, Hq, D]");
+  a.dtype = dtype_of(q.scalar_type());
+  if (a.dtype < 0 || (given && given->scalar_type() != q.scalar_type()))
+    refuse_type("q and out must be float16 or bfloat16");
+  const Cache c = cache_of(kc, vc, q.scalar_type());
+  a.B = tables_of(bt, sl, nullptr);
+  if (q.size(0) != a.B) refuse_value("block_tables must be [B, max_blocks] and seq_lens [B]");
+  if (c.D != q.size(d - 1)) refuse_value("k_cache / v_cache / q shapes disagree");
+  if (given && given->sizes() != q.sizes()) refuse_value("out must have q's shape");
+  if (groups.scalar_type() != ScalarType::Int || prefix.scalar_type() != ScalarType::Int)
+    refuse_type("groups and prefix_lens must be int32");
+  if (groups.dim() != 1 || prefix.dim() != 1 || groups.size(0) != prefix.size(0) + 1)
+    refuse_value("groups must be [N + 1] and prefix_lens [N]");
+  const int64_t dev = q.get_device();
+  on_device(q, dev, true, "q");
+  on_device(kc, dev, true, "k_cache");
+  on_device(vc, dev, true, "v_cache");
+  on_device(bt, dev, true, "block_tables");
+  on_device(sl, dev, true, "seq_lens");
+  on_device(groups, dev, true, "groups");
+  on_device(prefix, dev, true, "prefix_lens");
+  if (given) on_device(*given, dev, true, "out");
+  a.q_len = d == 4 ? to32(q.size(1)) : 1;
+  a.Hq = to32(q.size(d - 2));
+  a.scale = number(v[5]);
+  a.max_seq_len = v[9] == Py_None ? 0 : integer32(v[9]);
+  a.k_scale = c.kv == PA_KV_AS_DTYPE ? 1.f : number(v[10]);
+  a.v_scale = c.kv == PA_KV_AS_DTYPE ? 1.f : number(v[11]);
+  const Workspace ws(v[12], dev);
+  const Outputs outputs(v[14], dev);
+  const Tensor out = given ? *given : outputs.like(q);
+  if (q.numel() == 0)  // no sequences, rows or heads' elements: nothing to compute
+    return Py_BuildValue("(iNn)", (int)PA_OK, given ? Py_NewRef(v[8]) : THPVariable_Wrap(out), (Py_ssize_t)0);
+  cache_args(a, c, kc, vc, bt, sl);
+  a.q = data<void>(q);
+  a.out = data<void>(out);
+  const int32_t n = to32(prefix.size(0));
+  const auto call = [&](const pa_decode_args* args, void* w, size_t bytes, pa_stream_t s) {
+    return pa_decode_shared(args, data<int32_t>(groups), data<int32_t>(prefix), n, w, bytes, s);
+  };
+  const pa_status rc = launch(call, a, dev, ws, v[13]);
+  size_t need = 0;
+  if (rc == PA_ERR_WORKSPACE) {
+    const c10::DeviceGuard guard(c10::Device(at::kCUDA, (c10::DeviceIndex)dev));
+    need = pa_decode_shared_workspace_bytes(&a, n);
+  }
+  return Py_BuildValue("(iNn)", (int)rc, given ? Py_NewRef(v[8]) : THPVariable_Wrap(out), (Py_ssize_t)need);
+}
+
 // capture_id(stream) -> id of the capture that the stream takes part in, 0 outside one
 PyObject* do_capture_id(PyObject* const* v) {
   return PyLong_FromUnsignedLongLong(
@@ -421,7 +540,8 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef kMethods[] = {method<do_decode, 17>("decode"), method<do_append, 17>("append"),
-                          method<do_gather, 14>("gather"),
+                          method<do_gather, 14>("gather"), method<do_cross, 14>("cross"),
+                          method<do_decode_shared, 15>("decode_shared"),
                           method<do_capture_id, 1>("capture_id"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

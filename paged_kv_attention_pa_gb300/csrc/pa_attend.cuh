@@ -1,0 +1,1115 @@
+// Attention of many query rows over paged contexts: pa_cross and pa_decode_shared.
+//
+// Segments. A call is a list of segments, each a run of query tokens that attend to the same
+// tokens [lo, hi) of one table row: for cross attention a sequence's queries over its states;
+// for shared prefixes first every group's queries over the group's prefix, then every sequence's
+// over the rest of its own context. The rows of a segment and KV head are its (query token, head
+// of the group) pairs, cut into items of up to RT rows (two tensor core tiles of 128 at head_dim
+// 128, one at 256).
+//
+// Division of the work. An item of n token tiles counts n + 1 units (the start and end of an item
+// cost about one tile). Every CTA, one per SM, takes an equal run of the units of all items in
+// order, found from the lengths on the device: runs begin and end inside items, and the pieces of
+// an item that several CTAs hold, as well as the two contexts of a row with a shared prefix, leave
+// (reference, sum, unnormalised output) in the workspace, which merge_rows_kernel joins. The
+// division depends on the sizes alone, so repeated calls give the same bits.
+//
+// Roles of the warps of a CTA:
+//   softmax   one or two groups of four warps, a thread per row
+//   products  one warp, whose lane 0 issues the tensor core products
+//   plan      one warp that writes the items into a ring
+//   queries   one warp that copies the items' queries
+//   load      one warp that issues tensor copies of K and V, or four that stage and widen them
+// S = Q K^T goes to tensor memory, a thread reads its row's scores, writes the weights over them
+// as the A operand of O += P V, and O stays in tensor memory. Step i of an item uses score buffer
+// i % 2, so that the tensor cores work on one while the softmax of the other runs: with two groups
+// of softmax warps (head_dim 128) each has its own buffer and accumulator, and takes either one of
+// the item's two row tiles over the same K and V, or, when all rows fit in one tile, every other
+// token tile (the two states then merge in the epilogue).
+//
+// The reference of a row's weights is its running maximum, raised only when a score exceeds it by
+// more than kSlack: the accumulator in tensor memory is rescaled only then, by its softmax warp.
+// Weights are 2^(s - ref) in fp32, summed in fp32, and rounded once to the type of the products.
+// fp16 weights are kept 2^kLift larger (up to 2^14), so that only those under 2^-20 of the
+// row's largest become subnormal.
+//
+// What bounds it: for few rows HBM (K and V are read once for all rows of an item); for many rows
+// the tensor cores and, per row, the exponentials.
+#pragma once
+
+#include <cstdint>
+#include <type_traits>
+
+#include "pa.h"
+#include "pa_attend.h"
+#include "pa_device.cuh"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+
+template <typename T, int D, AttendLoad LOAD>
+struct AttendCfg {
+  using TM = std::conditional_t<LOAD == kLoadFp8, __half, T>;  // type of the products
+  static constexpr int NWG = D == 128 ? 2 : 1;                 // groups of softmax warps
+  static constexpr int TN = attend_tile(D);
+  static constexpr int RT = attend_rows(D);
+  static_assert(RT == 128 * NWG, "a row tile per group");
+  static constexpr int PANELS = D / 64;
+  static constexpr int QTILE = 128 * D * 2, NQ = D == 128 ? 2 : 1;
+  static constexpr int STAGE = TN * D * 2;
+  static constexpr int NS = LOAD == kLoadTensor ? 5 : 3;
+  static constexpr int KVB = LOAD == kLoadFp8 ? 1 : 2;
+  static constexpr int RAW = LOAD == kLoadTensor ? 0 : TN * D * KVB;  // a staged tile
+  static constexpr int NR = LOAD == kLoadTensor ? 0 : LOAD == kLoadFp8 ? 4 : 2;
+  static constexpr int NSW = 4 * NWG;
+  static constexpr int W_MMA = NSW, W_PLAN = NSW + 1, W_Q = NSW + 2, W_LOAD = NSW + 3;
+  static constexpr int NLOAD = LOAD == kLoadTensor ? 1 : 4;
+  static constexpr int WARPS = NSW + 3 + NLOAD, THREADS = WARPS * 32;
+  static constexpr int READERS = WARPS - 1;  // warps that read the ring of items
+  static constexpr int ITEMS = 4;            // slots of that ring
+  static constexpr int OFF_STAGE = NQ * QTILE;
+  static constexpr int OFF_RAW = OFF_STAGE + NS * STAGE;
+  static constexpr int OFF_SYNC = OFF_RAW + NR * RAW;
+  static constexpr int SYNC_BYTES = 3072;
+  static constexpr int SMEM = OFF_SYNC + SYNC_BYTES;
+  static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
+  // tensor memory: score buffers, then accumulators
+  static constexpr int S_COL = 0, O_COL = 256;
+  static_assert(2 * TN <= 256 && O_COL + NWG * D <= (int)kTmemColumns, "tensor memory");
+  static constexpr float kSlack = 8.f;  // log2 units
+  static constexpr float kLift = std::is_same_v<TM, __half> ? 6.f : 0.f;
+};
+
+// ------------------------------------------------------------------ segments
+struct Segment {
+  int tok0, n;    // its query tokens
+  int lo, hi;     // its context
+  int table;      // row of the block tables
+  int partial;    // 0: the rows' only context; 1, 2: the shared, the own part of two
+};
+
+__device__ __forceinline__ int clamp_len(const AttendParams& p, int b) {
+  const int L = __ldg(p.seq_lens + b);
+  return L < 0 ? 0 : min(L, p.cap);
+}
+// The group that sequence b is in: the last n with groups[n] <= b, -1 for none.
+__device__ __forceinline__ int group_of(const AttendParams& p, int b) {
+  if (p.N == 0) return -1;
+  int lo = 0, hi = p.N + 1;  // the answer + 1 is in [lo, hi]
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.groups + mid) <= b)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  const int n = lo - 1;
+  return n >= 0 && n < p.N && b < __ldg(p.groups + n + 1) ? n : -1;
+}
+// Tokens that group n shares: none in a group of one sequence.
+__device__ __forceinline__ int shared_tokens(const AttendParams& p, int n, int* first, int* end) {
+  const int g0 = min(max(__ldg(p.groups + n), 0), p.B), g1 = min(max(__ldg(p.groups + n + 1), g0), p.B);
+  *first = g0;
+  *end = g1;
+  if (g1 - g0 < 2) return 0;
+  return max(0, min(__ldg(p.prefix + n), clamp_len(p, g0)));
+}
+__device__ __forceinline__ int segment_count(const AttendParams& p) { return p.N + p.B; }
+__device__ __forceinline__ Segment segment_of(const AttendParams& p, int s) {
+  Segment g{};
+  if (s < p.N) {
+    int a, b;
+    g.hi = shared_tokens(p, s, &a, &b);
+    g.tok0 = a * p.R;
+    g.n = g.hi > 0 ? (b - a) * p.R : 0;
+    g.table = a;
+    g.partial = 1;
+    return g;
+  }
+  const int b = s - p.N;
+  g.table = b;
+  g.hi = clamp_len(p, b);
+  if (p.starts) {
+    g.tok0 = min(max(__ldg(p.starts + b), 0), p.T);
+    g.n = min(max(__ldg(p.starts + b + 1), g.tok0), p.T) - g.tok0;
+  } else {
+    g.tok0 = b * p.R;
+    g.n = p.R;
+  }
+  if (p.shared) {
+    const int n = group_of(p, b);
+    int a, e;
+    if (n >= 0) g.lo = shared_tokens(p, n, &a, &e);
+    g.partial = g.lo > 0 ? 2 : 0;
+  }
+  return g;
+}
+// Where its tiles start (tensor copies start at a multiple of the box), how many there are (one,
+// without a token, for an empty context), items and units.
+__device__ __forceinline__ int first_token(const AttendParams& p, const Segment& g) { return g.lo & -p.box; }
+template <int D>
+__device__ __forceinline__ int tiles_of(const AttendParams& p, const Segment& g) {
+  return max(1, (g.hi - first_token(p, g) + attend_tile(D) - 1) / attend_tile(D));
+}
+template <int D>
+__device__ __forceinline__ int row_tiles(const AttendParams& p, const Segment& g) {
+  return (g.n * p.G + attend_rows(D) - 1) / attend_rows(D);
+}
+constexpr int kItemCost = 1;  // units of an item beside its tiles
+template <int D>
+__device__ __forceinline__ long long units_of(const AttendParams& p, const Segment& g) {
+  return (long long)row_tiles<D>(p, g) * p.Hkv * (tiles_of<D>(p, g) + kItemCost);
+}
+__device__ __forceinline__ int div_group(const AttendParams& p, int r) {
+  return p.G == 1 ? r : (int)__umulhi((uint32_t)r, p.g_magic);
+}
+__device__ __forceinline__ int div_block(const AttendParams& p, int t) {
+  return p.bs_magic == 0 ? t >> p.bs_shift : (int)(__umulhi((uint32_t)t, p.bs_magic) >> p.bs_shift);
+}
+
+// A piece of an item: the tiles of it that a CTA computes.
+enum Dest { kDirect = 0, kSlotFirst = 1, kSlotNext = 2, kRowShared = 3, kRowOwn = 4 };
+struct Item {
+  int tiles;      // 0: the end of the CTA's work
+  int t0;         // first token of the first tile
+  int lo, hi;     // the segment's context
+  int table, kvh;
+  int tok0;       // the segment's first query token
+  int row0, rows; // the item's rows in the segment
+  int once;       // no other item reads this context's K and V
+  int dest;
+};
+
+// ------------------------------------------------------------------ waits
+// Wait for a phase of a barrier; false when it took over two seconds or another warp gave up. The
+// whole warp together.
+static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* give_up) {
+  const uint64_t t0 = global_ns();
+  for (;;) {
+    const bool over = global_ns() - t0 >= 2000000000ull || *give_up != 0;
+    const bool done = mbar_try(bar, parity);
+    if (__all_sync(0xffffffffu, done)) return true;
+    if (__any_sync(0xffffffffu, over)) {
+      *give_up = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* give_up) {
+  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+  return wait_long(bar, parity, give_up);
+}
+
+// ------------------------------------------------------------------ shared memory
+template <typename C>
+struct AttendShared {
+  uint64_t kv_full[C::NS], kv_empty[C::NS];
+  uint64_t q_full[C::NQ], q_empty[C::NQ];
+  uint64_t s_full[2], p_full[2];
+  uint64_t pv_done[C::NWG];
+  uint64_t item_full[C::ITEMS], item_empty[C::ITEMS];
+  uint64_t pair, drain;
+  uint32_t tmem;
+  int give_up;
+  int first_segment;
+  long long first_unit, per, total;
+  Item items[C::ITEMS];
+  float2 state[2][128];    // (reference, sum) of the two softmax groups
+  int2 staged[4][4];       // [slot][load warp] rows of a staged tile that hold tokens
+  long long scan[32];
+};
+
+#define PA_WAIT(bar, parity) \
+  if (!wait_for(smem_addr(&(bar)), (parity), &sh.give_up)) return
+
+// ------------------------------------------------------------------ plan
+// Every CTA finds the first unit of its run: a sum over the segments' units. CTA 0 writes what the
+// merge reads and reports lengths and groups that are out of range.
+template <typename C, int D>
+__device__ __forceinline__ void plan_work(const AttendParams& p, AttendShared<C>& sh) {
+  const int n = segment_count(p), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int each = (n + C::THREADS - 1) / C::THREADS;
+  const int s0 = min(n, tid * each), s1 = min(n, s0 + each);
+  long long mine = 0;
+  for (int s = s0; s < s1; ++s) {
+    mine += units_of<D>(p, segment_of(p, s));
+    if (blockIdx.x == 0) {
+      uint32_t bad = 0;
+      if (s < p.N) {
+        const int a = __ldg(p.groups + s), b = __ldg(p.groups + s + 1), x = __ldg(p.prefix + s);
+        if (a < 0 || b < a || b > p.B) bad |= PA_DEVERR_ROWS;
+        if (x < 0 || x > p.cap) bad |= PA_DEVERR_SEQ_LEN;
+      } else {
+        const int b = s - p.N, L = __ldg(p.seq_lens + b);
+        if (L < 0 || L > p.cap) bad |= PA_DEVERR_SEQ_LEN;
+        if (p.starts) {
+          const int x = __ldg(p.starts + b), y = __ldg(p.starts + b + 1);
+          if (x < 0 || y < x || y > p.T) bad |= PA_DEVERR_ROWS;
+        }
+      }
+      if (bad) atomicOr(p.err, bad);
+    }
+  }
+  long long upto = mine;  // inclusive sum over the threads
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) sh.scan[warp] = upto;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < C::WARPS; ++w) {
+    const long long x = sh.scan[w];
+    if (w < warp) upto += x;
+    total += x;
+  }
+  const long long per = (total + p.ctas - 1) / p.ctas;
+  const long long from = per * blockIdx.x;
+  long long at = upto - mine;
+  if (tid == 0) {
+    sh.per = per;
+    sh.total = total;
+    if (from >= total) sh.first_segment = n;
+  }
+  if (from >= at && from < upto) {
+    for (int s = s0; s < s1; ++s) {
+      const long long u = units_of<D>(p, segment_of(p, s));
+      if (from < at + u) {
+        sh.first_segment = s;
+        sh.first_unit = at;
+        break;
+      }
+      at += u;
+    }
+    at = upto - mine;
+  }
+  if (blockIdx.x == 0) {
+    if (tid == 0) {
+      p.plan[0] = per;
+      p.plan[1] = total;
+    }
+    for (int s = s0; s < s1; ++s) {
+      p.plan[2 + s] = at;
+      at += units_of<D>(p, segment_of(p, s));
+    }
+  }
+}
+
+// The plan warp: the pieces of this CTA's run, in order.
+template <typename C, int D>
+__device__ __forceinline__ void plan_role(const AttendParams& p, AttendShared<C>& sh) {
+  const int lane = threadIdx.x & 31;
+  const long long lo = sh.per * blockIdx.x, hi = min(lo + sh.per, sh.total);
+  uint32_t count = 0;
+  int s = sh.first_segment;
+  const int n = segment_count(p);
+  long long at = sh.first_unit;
+  bool first = true;
+  while (s < n && at < hi) {
+    const Segment g = segment_of(p, s);
+    const int tiles = tiles_of<D>(p, g), rt = row_tiles<D>(p, g), cost = tiles + kItemCost;
+    const int items = rt * p.Hkv;
+    int x = first && items > 0 ? (int)((lo - at) / cost) : 0;
+    first = false;
+    for (; x < items; ++x) {
+      const long long u = at + (long long)x * cost + kItemCost;  // the unit of the first tile
+      if (u - kItemCost >= hi) break;
+      const int ta = (int)max(0ll, lo - u), tb = (int)min((long long)tiles, hi - u);
+      if (ta >= tb) continue;
+      const int slot = count % C::ITEMS;
+      PA_WAIT(sh.item_empty[slot], ((count / C::ITEMS) & 1) ^ 1);
+      if (lane == 0) {
+        Item& it = sh.items[slot];
+        const int kvh = x / rt, r = x - kvh * rt;
+        it.tiles = tb - ta;
+        it.t0 = first_token(p, g) + ta * C::TN;
+        it.lo = g.lo;
+        it.hi = g.hi;
+        it.table = g.table;
+        it.kvh = kvh;
+        it.tok0 = g.tok0;
+        it.row0 = r * C::RT;
+        it.rows = min(C::RT, g.n * p.G - r * C::RT);
+        it.once = rt == 1;
+        it.dest = ta > 0 ? kSlotNext
+                  : tb < tiles ? kSlotFirst
+                  : g.partial == 1 ? kRowShared : g.partial == 2 ? kRowOwn : kDirect;
+        mbar_arrive(smem_addr(&sh.item_full[slot]));
+      }
+      __syncwarp();
+      ++count;
+    }
+    at += (long long)items * cost;
+    ++s;
+  }
+  const int slot = count % C::ITEMS;
+  PA_WAIT(sh.item_empty[slot], ((count / C::ITEMS) & 1) ^ 1);
+  if (lane == 0) {
+    sh.items[slot].tiles = 0;
+    mbar_arrive(smem_addr(&sh.item_full[slot]));
+  }
+}
+
+// The next item, read by a whole warp.
+template <typename C>
+__device__ __forceinline__ bool next_item(AttendShared<C>& sh, uint32_t& count, Item& it) {
+  const int slot = count % C::ITEMS;
+  if (!wait_for(smem_addr(&sh.item_full[slot]), (count / C::ITEMS) & 1, &sh.give_up)) return false;
+  it = sh.items[slot];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&sh.item_empty[slot]));
+  ++count;
+  return it.tiles > 0;
+}
+
+// Both softmax groups work on the item's two row tiles, or share the tiles of one.
+template <typename C>
+__device__ __forceinline__ bool two_row_tiles(const Item& it) {
+  return C::NWG == 2 && it.rows > 128;
+}
+
+// ------------------------------------------------------------------ load
+// The order in which the products need K and V: K runs `lead` tiles ahead.
+//   K(0) .. K(lead - 1), V(0), K(lead), V(1), ...
+// so V(t) is tile min(t + lead, tiles) + t of an item's 2 * tiles.
+template <typename C>
+__device__ __forceinline__ int lead_of(const Item& it) {
+  return two_row_tiles<C>(it) ? 1 : 2;
+}
+
+// Tensor copies: lane l copies box l of a tile. Boxes without a token are left out.
+template <typename C, int D>
+__device__ __forceinline__ void tensor_load_role(const AttendParams& p, const AttendMaps& maps, AttendShared<C>& sh,
+                                                 uint8_t* stages) {
+  const int lane = threadIdx.x & 31;
+  const int boxes = C::TN / p.box;
+  const uint32_t base = smem_addr(stages);
+  uint32_t pos = 0, count = 0;
+  Item it;
+  const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
+  while (next_item(sh, count, it)) {
+    const int32_t* row = p.block_tables + (size_t)it.table * p.max_blocks;
+    const uint64_t pol = it.once ? once : again;
+    auto entry = [&](int t) -> int {
+      const int tok = it.t0 + t * C::TN + lane * p.box;
+      if (t >= it.tiles || lane >= boxes || tok >= it.hi || tok + p.box <= it.lo) return -1;
+      return __ldg(row + div_block(p, tok));
+    };
+    auto load = [&](const void* map, int t, int phys) -> bool {
+      const int stage = pos % C::NS;
+      const uint32_t bar = smem_addr(&sh.kv_full[stage]);
+      if (!wait_for(smem_addr(&sh.kv_empty[stage]), ((pos / C::NS) & 1) ^ 1, &sh.give_up)) return false;
+      const int tok = it.t0 + t * C::TN + lane * p.box;
+      const bool live = lane < boxes && tok < it.hi && tok + p.box > it.lo;
+      const int n = __popc(__ballot_sync(0xffffffffu, live));
+      if (lane == 0) mbar_expect(bar, (uint32_t)(n * p.box * 128 * C::PANELS));
+      __syncwarp();
+      if (live) {
+        if ((unsigned)phys >= (unsigned)p.num_blocks) {
+          atomicOr(p.err, PA_DEVERR_BLOCK_INDEX);
+          phys = 0;
+        }
+        const int at = phys * p.block_size + (tok - div_block(p, tok) * p.block_size);
+        const uint32_t dst = base + stage * C::STAGE + lane * p.box * 128;
+#pragma unroll
+        for (int c = 0; c < C::PANELS; ++c) tensor_load3(dst + c * C::TN * 128, map, bar, c * 64, it.kvh, at, pol);
+      }
+      ++pos;
+      return true;
+    };
+    const int lead = lead_of<C>(it);
+    int e = entry(0);  // of the next K
+    for (int t = 0; t < it.tiles + lead; ++t) {
+      // V of a tile whose K went out `lead` tiles ago: its entries are in L1
+      if (t >= lead && !load(&maps.v, t - lead, entry(t - lead))) return;
+      if (t < it.tiles) {
+        const int ahead = entry(t + 1);
+        if (!load(&maps.k, t, e)) return;
+        e = ahead;
+      }
+    }
+  }
+  // nothing more is issued; a CTA that gives up waits for its copies in drain_copies
+}
+
+// Staged copies: each lane copies 16-byte chunks of its warp's rows into a ring of raw tiles with
+// cp.async, and later widens its own chunks into the swizzled tile. Rows without a token are zero.
+template <typename C, int D, bool FP8>
+__device__ __forceinline__ void staged_load_role(const AttendParams& p, AttendShared<C>& sh, uint8_t* stages,
+                                                 uint8_t* raw) {
+  constexpr int CPR = D * C::KVB / 16;  // chunks of a row
+  constexpr int RW = C::TN / 4;         // rows of a warp
+  constexpr int CH = RW * CPR / 32;     // chunks of a lane
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - C::W_LOAD;
+  const uint64_t pol = l2_evict_normal_policy();
+  const uint32_t raw_lane = smem_addr(raw) + warp * (C::RAW / 4) + lane * 16;
+  uint32_t count = 0;
+  Item it;
+  bool more = next_item(sh, count, it);
+  int lead = more ? lead_of<C>(it) : 0, k = 0, v = 0;  // tiles of K and V issued
+  uint32_t issued = 0, done = 0;
+  // issue the next tile, if there is one
+  auto issue = [&]() {
+    if (more) {
+      const bool is_k = k < it.tiles && k < v + lead;
+      const int t = is_k ? k++ : v++;
+      const int t0 = it.t0 + t * C::TN;
+      const uint8_t* cache = static_cast<const uint8_t*>(is_k ? p.k_cache : p.v_cache);
+      const int tok = t0 + warp * RW + lane;
+      const bool live = lane < RW && tok >= it.lo && tok < it.hi;
+      uint32_t ridx = 0;
+      if (live) {
+        const int blk = div_block(p, tok);
+        int phys = __ldg(p.block_tables + (size_t)it.table * p.max_blocks + blk);
+        if ((unsigned)phys >= (unsigned)p.num_blocks) {
+          atomicOr(p.err, PA_DEVERR_BLOCK_INDEX);
+          phys = 0;
+        }
+        ridx = ((uint32_t)phys * (uint32_t)p.block_size + (uint32_t)(tok - blk * p.block_size)) * (uint32_t)p.Hkv +
+               (uint32_t)it.kvh;
+      }
+      const int c0 = max(0, min(C::TN, it.lo - t0)), c1 = max(0, min(C::TN, it.hi - t0));
+      const int slot = issued % C::NR;
+      if (lane == 0) sh.staged[slot][warp] = make_int2(c0, c1);
+      const uint32_t dst = raw_lane + slot * C::RAW;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int f = i * 32 + lane, r = f / CPR, c = f % CPR;
+        const uint32_t rr = __shfl_sync(0xffffffffu, ridx, r);
+        const int row = warp * RW + r;
+        if (row >= c0 && row < c1)
+          asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst + i * 512),
+                       "l"(cache + (size_t)rr * (D * C::KVB) + c * 16), "l"(pol)
+                       : "memory");
+      }
+      ++issued;
+      if (v == it.tiles) {
+        more = next_item(sh, count, it);
+        lead = lead_of<C>(it);
+        k = v = 0;
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < C::NR - 1; ++i) issue();
+  for (;;) {
+    issue();
+    if (done == issued) break;
+    asm volatile("cp.async.wait_group %0;" ::"n"(C::NR - 1) : "memory");
+    __syncwarp();
+    const int slot = done % C::NR, stage = done % C::NS;
+    const int2 rows = sh.staged[slot][warp];
+    if (!wait_for(smem_addr(&sh.kv_empty[stage]), ((done / C::NS) & 1) ^ 1, &sh.give_up)) break;
+    const uint32_t src = raw_lane + slot * C::RAW;
+    const uint32_t tile = smem_addr(stages) + stage * C::STAGE;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int f = i * 32 + lane, r = warp * RW + f / CPR, c = f % CPR;
+      uint4 x = lds128(src + i * 512);
+      if (r < rows.x || r >= rows.y) x = make_uint4(0u, 0u, 0u, 0u);
+      auto put = [&](int chunk, const uint4& y) {  // chunk: 8 elements of the row
+        const uint32_t a = tile + (chunk >> 3) * (C::TN * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                     : "memory");
+      };
+      if constexpr (FP8) {
+        uint4 lo, hi;
+        lo.x = e4m3x2_to_half2(x.x & 0xffff);
+        lo.y = e4m3x2_to_half2(x.x >> 16);
+        lo.z = e4m3x2_to_half2(x.y & 0xffff);
+        lo.w = e4m3x2_to_half2(x.y >> 16);
+        hi.x = e4m3x2_to_half2(x.z & 0xffff);
+        hi.y = e4m3x2_to_half2(x.z >> 16);
+        hi.z = e4m3x2_to_half2(x.w & 0xffff);
+        hi.w = e4m3x2_to_half2(x.w >> 16);
+        put(2 * c, lo);
+        put(2 * c + 1, hi);
+      } else {
+        put(c, x);
+      }
+    }
+    async_proxy_fence();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&sh.kv_full[stage]));
+    ++done;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ queries
+template <typename C, typename T, int D>
+__device__ __forceinline__ void query_role(const AttendParams& p, AttendShared<C>& sh, uint8_t* tiles) {
+  constexpr int CPR = D / 8;  // 16-byte chunks of a row
+  const int lane = threadIdx.x & 31;
+  const uint32_t base = smem_addr(tiles);
+  uint32_t count = 0, used = 0;
+  Item it;
+  while (next_item(sh, count, it)) {
+    for (int first = 0; first < it.rows; first += 128, ++used) {
+      const int slot = used % C::NQ;
+      PA_WAIT(sh.q_empty[slot], ((used / C::NQ) & 1) ^ 1);
+      const int chunks = min(128, it.rows - first) * CPR;
+      const uint32_t tile = base + slot * C::QTILE;
+      auto place = [&](int f) -> uint32_t {
+        const int r = f / CPR, c = f % CPR;
+        return tile + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+      };
+#pragma unroll 4
+      for (int f = lane; f < chunks; f += 32) {
+        const int r = it.row0 + first + f / CPR, tok = div_group(p, r);
+        const T* src = static_cast<const T*>(p.q) + (size_t)(it.tok0 + tok) * p.q_stride +
+                       (size_t)(it.kvh * p.G + r - tok * p.G) * D + (f % CPR) * 8;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(place(f)), "l"(src) : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if constexpr (!std::is_same_v<T, typename C::TM>) {  // this lane's own chunks, to the products' type
+#pragma unroll 4
+        for (int f = lane; f < chunks; f += 32) {
+          const uint32_t a = place(f);
+          uint4 x = lds128(a);
+          uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = unpack2<T>(w[j]);
+            w[j] = pack2<typename C::TM>(y.x, y.y);
+          }
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                       : "memory");
+        }
+      }
+      async_proxy_fence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.q_full[slot]));
+    }
+  }
+}
+
+// ------------------------------------------------------------------ products
+// Steps of an item: one per token tile, or one per token tile and row tile. Products issued by one
+// thread run in order, so that a score buffer is overwritten only after the weights in it are used.
+template <typename C, int D>
+__device__ __forceinline__ void product_role(AttendShared<C>& sh, uint8_t* q_tiles, uint8_t* stages, uint32_t tmem) {
+  using TM = typename C::TM;
+  const bool issuer = (threadIdx.x & 31) == 0;
+  const uint32_t q_base = smem_addr(q_tiles), kv_base = smem_addr(stages);
+  const uint64_t by_k = operand_desc(16), by_n = operand_desc(C::TN * 128);
+  constexpr uint32_t kScores = mma_desc<TM>(C::TN, false), kValues = mma_desc<TM>(D, true);
+  uint32_t count = 0, pos = 0, used = 0;  // items, K and V tiles, query tiles
+  uint32_t weights[2] = {0, 0};           // steps that used each score buffer
+  Item it;
+  while (next_item(sh, count, it)) {
+    const bool two = two_row_tiles<C>(it);
+    const int dup = two ? 1 : 0, steps = it.tiles << dup;
+    const int q_tile[2] = {(int)(used % C::NQ), (int)((used + dup) % C::NQ)};
+    for (int i = 0; i <= dup; ++i) PA_WAIT(sh.q_full[(used + i) % C::NQ], ((used + i) / C::NQ) & 1);
+    used += 1 + dup;
+    int k_stage = 0, v_stage = 0;
+    auto scores = [&](int i) -> bool {  // step i: S = Q K^T
+      if (!(i & dup)) {
+        k_stage = pos % C::NS;
+        if (!wait_for(smem_addr(&sh.kv_full[k_stage]), (pos / C::NS) & 1, &sh.give_up)) return false;
+        ++pos;
+      }
+      tc_fence_after();
+      if (issuer) {
+        const uint32_t a = q_base + q_tile[i & dup] * C::QTILE, b = kv_base + k_stage * C::STAGE;
+        const uint32_t d = tmem + C::S_COL + (i & 1) * C::TN;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(d, desc_at(by_k, a + (kk / 4) * (128 * 128) + (kk % 4) * 32),
+                 desc_at(by_k, b + (kk / 4) * (C::TN * 128) + (kk % 4) * 32), kScores, kk > 0);
+        mma_commit(smem_addr(&sh.s_full[i & 1]));
+        if (dup == 0 || (i & 1)) mma_commit(smem_addr(&sh.kv_empty[k_stage]));
+        if (i >= steps - 1 - dup) {  // the last step of its row tile
+          mma_commit(smem_addr(&sh.q_empty[q_tile[i & dup]]));
+        }
+      }
+      __syncwarp();
+      return true;
+    };
+    for (int i = 0; i < 2 && i < steps; ++i)
+      if (!scores(i)) return;
+    for (int i = 0; i < steps; ++i) {
+      const int buf = i & 1, group = C::NWG == 2 ? buf : 0;
+      if (!(i & dup)) {
+        v_stage = pos % C::NS;
+        PA_WAIT(sh.kv_full[v_stage], (pos / C::NS) & 1);
+        ++pos;
+      }
+      PA_WAIT(sh.p_full[buf], weights[buf] & 1);
+      ++weights[buf];
+      tc_fence_after();
+      if (issuer) {  // O += P V
+        const uint32_t a = tmem + C::S_COL + buf * C::TN, b = kv_base + v_stage * C::STAGE;
+        const uint32_t d = tmem + C::O_COL + group * D;
+#pragma unroll
+        for (int kk = 0; kk < C::TN / 16; ++kk)
+          mma_ts(d, a + kk * 8, desc_at(by_n, b + kk * 2048), kValues, i >= C::NWG || kk > 0);
+        mma_commit(smem_addr(&sh.pv_done[group]));
+        if (dup == 0 || (i & 1)) mma_commit(smem_addr(&sh.kv_empty[v_stage]));
+      }
+      __syncwarp();
+      if (i + 2 < steps && !scores(i + 2)) return;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ softmax
+// One thread per row of a row tile.
+template <typename C, typename T, int D, bool ZERO_V>
+__device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared<C>& sh, uint8_t* stages,
+                                             uint32_t tmem) {
+  using TM = typename C::TM;
+  constexpr int NC = C::TN / 32;
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 7, at = threadIdx.x & 127;
+  const uint32_t lanes = (uint32_t)((threadIdx.x >> 5) & 3) << 21;  // 32 (warp % 4) in the upper half
+  const uint32_t own_o = tmem + C::O_COL + group * D + lanes;
+  const float sl2 = p.scale_log2;
+  uint32_t count = 0, used[2] = {0, 0}, pvs = 0, pairs = 0, tiles_before = 0;
+  Item it;
+  while (next_item(sh, count, it)) {
+    const bool two = two_row_tiles<C>(it);
+    const int dup = two ? 1 : 0, steps = it.tiles << dup;
+    const int r = (two ? group * 128 : 0) + at;  // the item's row of this thread
+    const bool live = r < it.rows;
+    const bool warp_live = r - lane < it.rows;
+    const int seg_row = it.row0 + r, tok = live ? it.tok0 + div_group(p, seg_row) : 0;
+    const int head = it.kvh * p.G + seg_row - div_group(p, seg_row) * p.G;
+    int end = it.hi;  // this row sees tokens in [lo, end)
+    if (p.shared && live) {
+      const int b = tok / p.R;
+      end = min(end, clamp_len(p, b) - p.R + 1 + (tok - b * p.R));
+    }
+    if (!live) end = it.lo;
+    float ref = -INFINITY, sum = 0.f;
+    int mine = 0;  // steps of this group in the item
+    for (int i = C::NWG == 2 ? group : 0; i < steps; i += C::NWG, ++mine) {
+      const int buf = i & 1, t = i >> dup;
+      const uint32_t s_at = tmem + C::S_COL + buf * C::TN + lanes;
+      PA_WAIT(sh.s_full[buf], used[buf] & 1);
+      ++used[buf];
+      const int t0 = it.t0 + t * C::TN;
+      if (warp_live) {
+        tc_fence_after();
+        const int c0 = it.lo - t0, c1 = end - t0;  // columns [c0, c1) are seen
+        const bool whole = __all_sync(0xffffffffu, !live || (c0 <= 0 && c1 >= C::TN));
+        // the largest scaled score
+        uint32_t x[2][32];
+        float top = -INFINITY;
+        tmem_load32(x[0], s_at);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          uint32_t(&y)[32] = x[c & 1];
+          tmem_loaded(y);
+          if (c + 1 < NC) tmem_load32(x[(c + 1) & 1], s_at + 32 * (c + 1));
+          if (whole) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(y[j]) * sl2);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int col = 32 * c + j;
+              if (col >= c0 && col < c1) top = fmaxf(top, __uint_as_float(y[j]) * sl2);
+            }
+          }
+        }
+        top -= C::kLift;
+        tmem_load32(x[0], s_at);
+        const bool raise = top > ref + C::kSlack;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float now = raise ? top : ref;
+          const float f = now == -INFINITY ? 1.f : exp2_approx(ref - now);
+          ref = now;
+          sum *= f;
+          if (mine > 0) {  // the accumulator of the steps before
+            PA_WAIT(sh.pv_done[group], (pvs - 1) & 1);
+            tc_fence_after();
+            tmem_loaded(x[0]);
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_load32(o, own_o + 32 * c);
+              tmem_loaded(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_store32(own_o + 32 * c, o);
+            }
+          }
+        }
+        const float sub = ref == -INFINITY ? 0.f : ref;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          uint32_t(&y)[32] = x[c & 1];
+          tmem_loaded(y);
+          if (c + 1 < NC) tmem_load32(x[(c + 1) & 1], s_at + 32 * (c + 1));
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float a = exp2_approx(fmaf(__uint_as_float(y[j]), sl2, -sub));
+            float b = exp2_approx(fmaf(__uint_as_float(y[j + 1]), sl2, -sub));
+            if (!whole) {
+              const int col = 32 * c + j;
+              a = col >= c0 && col < c1 ? a : 0.f;
+              b = col + 1 >= c0 && col + 1 < c1 ? b : 0.f;
+            }
+            part[(j / 2) & 1] += a;
+            part[2 + ((j / 2) & 1)] += b;
+            w[j / 2] = pack2<TM>(a, b);
+          }
+          // over columns of scores that are in registers already
+          tmem_store16(s_at + 16 * c, w);
+        }
+        sum += (part[0] + part[1]) + (part[2] + part[3]);
+        tmem_stored();
+      }
+      if constexpr (ZERO_V) {
+        // V rows outside the context hold whatever the cache or an earlier tile left: zeros there,
+        // so that weights of 0 meet 0
+        if ((t0 < it.lo || t0 + C::TN > it.hi) && !(dup && group)) {
+          const uint32_t n = tiles_before + min(t + lead_of<C>(it), it.tiles) + t;
+          PA_WAIT(sh.kv_full[n % C::NS], (n / C::NS) & 1);
+          const uint32_t tile = smem_addr(stages) + (n % C::NS) * C::STAGE;
+          for (int row = at; row < C::TN; row += 128)
+            if (t0 + row < it.lo || t0 + row >= it.hi)
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c) sts128_zero(tile + (c >> 3) * (C::TN * 128) + row * 128 + (c & 7) * 16);
+          async_proxy_fence();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[buf]));
+      ++pvs;
+    }
+    tiles_before += 2 * it.tiles;
+
+    // ---- the item's rows: O / sum, or (reference, sum, O) of a piece
+    if (mine > 0) PA_WAIT(sh.pv_done[group], (pvs - 1) & 1);
+    tc_fence_after();
+    const bool joint = C::NWG == 2 && !two;  // two states of the same rows
+    float f_own = 1.f, f_other = 0.f;
+    if constexpr (C::NWG == 2) {
+      if (joint) {
+        sh.state[group][at] = make_float2(ref, sum);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.pair));
+        PA_WAIT(sh.pair, pairs & 1);
+        ++pairs;
+        tc_fence_after();
+        const float2 other = sh.state[group ^ 1][at];
+        const float m = fmaxf(ref, other.x);
+        f_own = ref == -INFINITY ? 0.f : exp2_approx(ref - m);
+        f_other = other.x == -INFINITY ? 0.f : exp2_approx(other.x - m);
+        sum = sum * f_own + other.y * f_other;
+        ref = m;
+      }
+    }
+    if (warp_live) {
+      const bool whole = it.dest == kDirect;
+      const float mul = whole ? (sum > 0.f ? p.v_scale / sum : 0.f) : p.v_scale;
+      const size_t row = (size_t)tok * p.Hq + head;
+      size_t part = 0;  // row of the partials
+      float* acc = nullptr;
+      float2* ml = nullptr;
+      if (!whole) {
+        if (it.dest == kRowShared || it.dest == kRowOwn) {
+          part = (it.dest == kRowOwn ? (size_t)p.T * p.Hq : 0) + row;
+          acc = p.row_acc;
+          ml = p.row_ml;
+        } else {
+          part = ((size_t)blockIdx.x * 2 + (it.dest == kSlotFirst ? 1 : 0)) * p.slot_rows + r;
+          acc = p.slot_acc;
+          ml = p.slot_ml;
+        }
+        if (live && !(joint && group)) ml[part] = make_float2(ref, sum);
+      }
+      // joint groups take half of the columns each
+      const int from = joint ? group * (D / 2) : 0, to = joint ? from + D / 2 : D;
+      const uint32_t other_o = tmem + C::O_COL + (group ^ 1) * D + lanes;
+#pragma unroll 1
+      for (int c = from; c < to; c += 32) {
+        uint32_t o[32];
+        tmem_load32(o, own_o + c);
+        tmem_loaded(o);
+        if (joint) {
+          uint32_t o2[32];
+          tmem_load32(o2, other_o + c);
+          tmem_loaded(o2);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {  // an accumulator that saw no token may hold anything
+            const float a = f_own > 0.f ? __uint_as_float(o[j]) * f_own : 0.f;
+            const float b = f_other > 0.f ? __uint_as_float(o2[j]) * f_other : 0.f;
+            o[j] = __float_as_uint(a + b);
+          }
+        }
+        if (live) {
+          if (whole) {
+            T* dst = static_cast<T*>(p.out) + row * D + c;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              uint4 y;
+              uint32_t* w = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float a = __uint_as_float(o[j + 2 * i]), b = __uint_as_float(o[j + 2 * i + 1]);
+                w[i] = pack2<T>(sum > 0.f ? a * mul : 0.f, sum > 0.f ? b * mul : 0.f);
+              }
+              *reinterpret_cast<uint4*>(dst + j) = y;
+            }
+          } else {
+            float* dst = acc + part * D + c;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4*>(dst + j) =
+                  make_float4(__uint_as_float(o[j]) * mul, __uint_as_float(o[j + 1]) * mul,
+                              __uint_as_float(o[j + 2]) * mul, __uint_as_float(o[j + 3]) * mul);
+          }
+        }
+      }
+    }
+    if constexpr (C::NWG == 2) {
+      if (joint) {  // both accumulators are read before either group's next weights
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.pair));
+        PA_WAIT(sh.pair, pairs & 1);
+        ++pairs;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+template <typename T, int D, AttendLoad LOAD>
+__global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
+    attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps maps) {
+  using C = AttendCfg<T, D, LOAD>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_addr(smem) & 1023) {  // the swizzle counts on it
+    if (threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_COPY);
+    return;
+  }
+  uint8_t *q_tiles = smem, *stages = smem + C::OFF_STAGE, *raw = smem + C::OFF_RAW;
+  AttendShared<C>& sh = *reinterpret_cast<AttendShared<C>*>(smem + C::OFF_SYNC);
+  static_assert(sizeof(AttendShared<C>) <= C::SYNC_BYTES, "barriers and items");
+  const int warp = threadIdx.x >> 5;
+
+  if (threadIdx.x == 0) {
+    auto init = [](uint64_t* bars, int n, int count) {
+      for (int i = 0; i < n; ++i) mbar_init_count(smem_addr(bars + i), count);
+    };
+    init(sh.kv_full, C::NS, C::NLOAD);
+    init(sh.kv_empty, C::NS, 1);
+    init(sh.q_full, C::NQ, 1);
+    init(sh.q_empty, C::NQ, 1);
+    init(sh.s_full, 2, 1);
+    init(sh.p_full, 2, 4);
+    init(sh.pv_done, C::NWG, 1);
+    init(sh.item_full, C::ITEMS, 1);
+    init(sh.item_empty, C::ITEMS, C::READERS);
+    init(&sh.pair, 1, C::NSW);
+    init(&sh.drain, 1, 1);
+    sh.give_up = 0;
+    mbar_init_fence();
+    if constexpr (LOAD == kLoadTensor) {
+      tensor_prefetch(&maps.k);
+      tensor_prefetch(&maps.v);
+    }
+  }
+  if (warp == C::W_MMA) tmem_alloc(smem_addr(&sh.tmem));
+  tc_fence_before();
+  // inputs may come from the kernel before in the stream
+  pdl_wait();
+  plan_work<C, D>(p, sh);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp < C::NSW)
+    softmax_role<C, T, D, LOAD == kLoadTensor>(p, sh, stages, tmem);
+  else if (warp == C::W_MMA)
+    product_role<C, D>(sh, q_tiles, stages, tmem);
+  else if (warp == C::W_PLAN)
+    plan_role<C, D>(p, sh);
+  else if (warp == C::W_Q)
+    query_role<C, T, D>(p, sh, q_tiles);
+  else if constexpr (LOAD == kLoadTensor)
+    tensor_load_role<C, D>(p, maps, sh, stages);
+  else
+    staged_load_role<C, D, LOAD == kLoadFp8>(p, sh, stages, raw);
+
+  __syncwarp();
+  pdl_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  if (sh.give_up) {
+    // some wait took over two seconds: copies and products in flight are waited for, with a limit,
+    // before the CTA gives its memory back
+    if (threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_COPY);
+    if (warp == C::W_MMA) {
+      if ((threadIdx.x & 31) == 0) mma_commit(smem_addr(&sh.drain));
+      __syncwarp();
+    }
+    const uint64_t t0 = global_ns();
+    while (global_ns() - t0 < 100000000ull && !(warp == C::W_MMA && mbar_try(smem_addr(&sh.drain), 0)))
+      ;
+    __syncthreads();
+  }
+  tc_fence_after();
+  if (warp == C::W_MMA) tmem_free(tmem);
+}
+
+// ------------------------------------------------------------------ merge
+// One warp per output row and head: its pieces weighed by 2^(reference - largest), their sums and
+// outputs added in order.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) merge_rows_kernel(const AttendParams p) {
+  constexpr int V = D / 32;  // elements of a lane
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (row >= (long long)p.T * p.Hq) return;
+  const int tok = (int)(row / p.Hq), head = (int)(row - (long long)tok * p.Hq);
+  const int kvh = head / p.G;
+  int b;
+  if (p.starts) {
+    int lo = 0, hi = p.B + 1;  // the last start at or below tok
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(p.starts + mid) <= tok)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    b = lo - 1;
+    if (b < 0 || b >= p.B || tok >= __ldg(p.starts + b + 1)) return;  // padding
+  } else {
+    b = tok / p.R;
+  }
+  const long long per = __ldcg(p.plan);
+  // the pieces of this row in segment s: CTAs from .. to, its first one's slot differing
+  struct Pieces {
+    int from, to, r, whole;  // r: the row in the item
+  };
+  auto pieces_of = [&](int s, const Segment& g) -> Pieces {
+    const int tiles = tiles_of<D>(p, g), rt = row_tiles<D>(p, g);
+    const int r = (tok - g.tok0) * p.G + head - kvh * p.G;
+    const int x = kvh * rt + r / attend_rows(D);
+    const long long u = __ldcg(p.plan + 2 + s) + (long long)x * (tiles + kItemCost) + kItemCost;
+    Pieces z;
+    z.from = (int)(u / per);
+    z.to = (int)((u + tiles - 1) / per);
+    z.r = r % attend_rows(D);
+    z.whole = z.from == z.to;
+    return z;
+  };
+  const Segment own = segment_of(p, p.N + b);
+  const Pieces po = pieces_of(p.N + b, own);
+  if (own.partial == 0 && po.whole) return;  // written by the attention grid
+  Pieces ps{0, -1, 0, 0};
+  if (own.partial) {
+    const int n = group_of(p, b);
+    ps = pieces_of(n, segment_of(p, n));
+  }
+  const int n_shared = ps.to - ps.from + 1, n = n_shared + po.to - po.from + 1;
+  auto at = [&](int i, const float2** ml, const float** acc) {
+    const bool mine = i >= n_shared;
+    const Pieces& z = mine ? po : ps;
+    size_t k;
+    if (z.whole) {
+      k = (mine ? (size_t)p.T * p.Hq : 0) + row;
+      *ml = p.row_ml + k;
+      *acc = p.row_acc + k * D;
+      return;
+    }
+    const int c = z.from + (mine ? i - n_shared : i);
+    k = ((size_t)c * 2 + (c == z.from ? 1 : 0)) * p.slot_rows + z.r;
+    *ml = p.slot_ml + k;
+    *acc = p.slot_acc + k * D;
+  };
+  float top = -INFINITY;
+  for (int i = lane; i < n; i += 32) {
+    const float2* ml;
+    const float* acc;
+    at(i, &ml, &acc);
+    top = fmaxf(top, __ldcg(ml).x);
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float sum = 0.f, v[V] = {};
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float2* ml;
+    const float* acc;
+    at(i, &ml, &acc);
+    const float2 x = __ldcg(ml);
+    const float w = x.x == -INFINITY ? 0.f : exp2_approx(x.x - top);
+    sum += w * x.y;
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(acc + 32 * j + 4 * lane));
+      if (w > 0.f) {  // a piece that saw no token of the row may hold anything
+        v[j] += w * y.x;
+        v[j + 1] += w * y.y;
+        v[j + 2] += w * y.z;
+        v[j + 3] += w * y.w;
+      }
+    }
+  }
+  const float f = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int j = 0; j < V; j += 4) {
+    uint2 y;
+    y.x = pack2<T>(v[j] * f, v[j + 1] * f);
+    y.y = pack2<T>(v[j + 2] * f, v[j + 3] * f);
+    *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * D + 32 * j + 4 * lane) = y;
+  }
+}
+
+// ------------------------------------------------------------------ launch
+template <typename T, int D, AttendLoad LOAD>
+cudaError_t launch_attend_load(const AttendParams& p, const AttendMaps& maps, cudaStream_t st) {
+  using C = AttendCfg<T, D, LOAD>;
+  auto kern = attend_kernel<T, D, LOAD>;
+  // the opt-in to this much shared memory is per device
+  static unsigned long long done_mask = 0ull;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    __atomic_fetch_or(&done_mask, bit, __ATOMIC_ACQ_REL);
+  }
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.stream = st;
+  cfg.gridDim = dim3(p.ctas);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  e = cudaLaunchKernelEx(&cfg, kern, p, maps);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)(((long long)p.T * p.Hq + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, merge_rows_kernel<T, D>, p);
+}
+template <typename T, int D>
+cudaError_t launch_attend(const AttendParams& p, const AttendMaps& maps, AttendLoad load, cudaStream_t st) {
+  return load == kLoadTensor ? launch_attend_load<T, D, kLoadTensor>(p, maps, st)
+         : load == kLoad16   ? launch_attend_load<T, D, kLoad16>(p, maps, st)
+                             : launch_attend_load<T, D, kLoadFp8>(p, maps, st);
+}
+
+}  // namespace pa

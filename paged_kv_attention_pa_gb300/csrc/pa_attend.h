@@ -1,0 +1,60 @@
+// Launch parameters of the kernels behind pa_cross and pa_decode_shared.
+#pragma once
+
+#include <cuda.h>  // CUtensorMap (a type only: the library does not link the driver)
+
+#include "pa_params.h"
+
+namespace pa {
+
+// How K and V reach shared memory: 16-bit caches whose blocks are whole groups of eight tokens by
+// tensor copies, other 16-bit caches and fp8 ones through a staging ring.
+enum AttendLoad { kLoadTensor = 0, kLoad16 = 1, kLoadFp8 = 2 };
+
+struct AttendParams {
+  const void* q;
+  void* out;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* starts;     // cross: [B + 1], or null
+  const int32_t* groups;     // shared prefixes: [N + 1]
+  const int32_t* prefix;     // [N]
+  uint32_t* err;             // device error word
+  // workspace (see attend_workspace)
+  long long* plan;           // units per CTA, units in all, then the first unit of every segment
+  float2* slot_ml;           // [CTAs][2][slot_rows] reference and sum of the pieces of items that
+                             // CTAs share: 0 the end of one, 1 the start of the next
+  float* slot_acc;           // [CTAs][2][slot_rows][D] their unnormalised outputs
+  float2* row_ml;            // [2][T * Hq] the same of whole items whose rows have two contexts
+  float* row_acc;            // [2][T * Hq][D]
+  long long q_stride;        // elements between query rows
+  int B, N, T, R;            // sequences, groups (cross: 0), query rows, rows per sequence
+  int shared;                // pa_decode_shared
+  int Hq, Hkv, G;
+  uint32_t g_magic;          // r / G = umulhi(r, g_magic) for r < 2^28, G > 1
+  int block_size, num_blocks, max_blocks, cap;
+  uint32_t bs_magic;         // t / block_size as in DecodeParams
+  int bs_shift;
+  int box;                   // tokens of a tensor copy, a power of two that divides the block size
+  int ctas;                  // CTAs that share out the work
+  int slot_rows;             // bound on an item's rows
+  float scale_log2, v_scale;
+};
+
+// Query rows (token and head of a KV head's group) of an item, tokens of a tile.
+__host__ __device__ constexpr int attend_rows(int D) { return D == 128 ? 256 : 128; }
+__host__ __device__ constexpr int attend_tile(int D) { return D == 128 ? 128 : 64; }
+
+struct AttendMaps {
+  CUtensorMap k, v;
+};
+
+// One launcher per type and head_dim: the attention grid and the grid that merges its pieces.
+cudaError_t launch_attend_bf16_d128(const AttendParams& p, const AttendMaps& maps, AttendLoad load, cudaStream_t st);
+cudaError_t launch_attend_bf16_d256(const AttendParams& p, const AttendMaps& maps, AttendLoad load, cudaStream_t st);
+cudaError_t launch_attend_f16_d128(const AttendParams& p, const AttendMaps& maps, AttendLoad load, cudaStream_t st);
+cudaError_t launch_attend_f16_d256(const AttendParams& p, const AttendMaps& maps, AttendLoad load, cudaStream_t st);
+
+}  // namespace pa
