@@ -1,6 +1,8 @@
 // Host side of pa_cross and pa_decode_shared: checks, the workspace, tensor maps and the launch.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
+#include <cmath>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -143,7 +145,12 @@ pa_status run(const Call& c, AttendParams& p, int cap, void* workspace, size_t b
   p.ctas = sms;
   const bool fp8 = c.kv_dtype == PA_KV_FP8_E4M3;
   p.v_scale = fp8 ? c.v_scale : 1.f;
-  p.scale_log2 = (float)((double)c.scale * 1.4426950408889634 * (fp8 ? (double)c.k_scale : 1.0));
+  // The kernel masks scores before it scales them, so its scale is positive: a negative one negates
+  // the queries in the product, and with one that is (or rounds to) zero the smallest normal number
+  // gives the same equal weights.
+  const double scale = (double)c.scale * 1.4426950408889634 * (fp8 ? (double)c.k_scale : 1.0);
+  p.scale_log2 = std::max((float)std::fabs(scale), FLT_MIN);
+  p.negate = scale < 0.0;
   // The largest power of two that divides the block size, up to a tile; the swizzle's pattern
   // repeats every eight rows, so smaller ones are staged.
   p.box = std::min(c.block_size & -c.block_size, attend_tile(c.D));

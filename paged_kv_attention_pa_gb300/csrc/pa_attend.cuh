@@ -19,10 +19,11 @@
 //   products  one warp, whose lane 0 issues the tensor core products
 //   plan      one warp that writes the items into a ring
 //   queries   one warp that copies the items' queries
-//   load      one warp that issues tensor copies of K and V, or four that stage and widen them
+//   load      four warps that issue tensor copies of K and V, or stage and widen them
 // S = Q K^T goes to tensor memory, a thread reads its row's scores, writes the weights over them
 // as the A operand of O += P V, and O stays in tensor memory. Step i of an item uses score buffer
-// i % 2, so that the tensor cores work on one while the softmax of the other runs: with two groups
+// i % 2, so that the tensor cores work on one while the softmax of the other runs (barriers are kept
+// by score buffer: a group never falls two phases of one behind, which parities could not tell): with two groups
 // of softmax warps (head_dim 128) each has its own buffer and accumulator, and takes either one of
 // the item's two row tiles over the same K and V, or, when all rows fit in one tile, every other
 // token tile (the two states then merge in the epilogue).
@@ -63,7 +64,7 @@ struct AttendCfg {
   static constexpr int NR = LOAD == kLoadTensor ? 0 : LOAD == kLoadFp8 ? 4 : 2;
   static constexpr int NSW = 4 * NWG;
   static constexpr int W_MMA = NSW, W_PLAN = NSW + 1, W_Q = NSW + 2, W_LOAD = NSW + 3;
-  static constexpr int NLOAD = LOAD == kLoadTensor ? 1 : 4;
+  static constexpr int NLOAD = 4;
   static constexpr int WARPS = NSW + 3 + NLOAD, THREADS = WARPS * 32;
   static constexpr int READERS = WARPS - 1;  // warps that read the ring of items
   static constexpr int ITEMS = 4;            // slots of that ring
@@ -176,7 +177,6 @@ struct Item {
   int table, kvh;
   int tok0;       // the segment's first query token
   int row0, rows; // the item's rows in the segment
-  int once;       // no other item reads this context's K and V
   int dest;
 };
 
@@ -199,6 +199,21 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
   if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
   return wait_long(bar, parity, give_up);
 }
+// The same for one thread.
+static __device__ __noinline__ bool wait_long_alone(uint32_t bar, uint32_t parity, volatile int* give_up) {
+  const uint64_t t0 = global_ns();
+  for (;;) {
+    const bool over = global_ns() - t0 >= 2000000000ull || *give_up != 0;
+    if (mbar_try(bar, parity)) return true;
+    if (over) {
+      *give_up = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_alone(uint32_t bar, uint32_t parity, volatile int* give_up) {
+  return mbar_try(bar, parity) || wait_long_alone(bar, parity, give_up);
+}
 
 // ------------------------------------------------------------------ shared memory
 template <typename C>
@@ -206,7 +221,7 @@ struct AttendShared {
   uint64_t kv_full[C::NS], kv_empty[C::NS];
   uint64_t q_full[C::NQ], q_empty[C::NQ];
   uint64_t s_full[2], p_full[2];
-  uint64_t pv_done[C::NWG];
+  uint64_t pv_done[2];  // by the step's score buffer
   uint64_t item_full[C::ITEMS], item_empty[C::ITEMS];
   uint64_t pair, drain;
   uint32_t tmem;
@@ -221,6 +236,8 @@ struct AttendShared {
 
 #define PA_WAIT(bar, parity) \
   if (!wait_for(smem_addr(&(bar)), (parity), &sh.give_up)) return
+#define PA_WAIT_ALONE(bar, parity) \
+  if (!wait_alone(smem_addr(&(bar)), (parity), &sh.give_up)) return
 
 // ------------------------------------------------------------------ plan
 // Every CTA finds the first unit of its run: a sum over the segments' units. CTA 0 writes what the
@@ -332,7 +349,6 @@ __device__ __forceinline__ void plan_role(const AttendParams& p, AttendShared<C>
         it.tok0 = g.tok0;
         it.row0 = r * C::RT;
         it.rows = min(C::RT, g.n * p.G - r * C::RT);
-        it.once = rt == 1;
         it.dest = ta > 0 ? kSlotNext
                   : tb < tiles ? kSlotFirst
                   : g.partial == 1 ? kRowShared : g.partial == 2 ? kRowOwn : kDirect;
@@ -373,65 +389,62 @@ __device__ __forceinline__ bool two_row_tiles(const Item& it) {
 // ------------------------------------------------------------------ load
 // The order in which the products need K and V: K runs `lead` tiles ahead.
 //   K(0) .. K(lead - 1), V(0), K(lead), V(1), ...
-// so V(t) is tile min(t + lead, tiles) + t of an item's 2 * tiles.
+// Tiles are staged in this order; place_k and place_v are a tile's place among an item's
+// 2 * tiles.
 template <typename C>
 __device__ __forceinline__ int lead_of(const Item& it) {
   return two_row_tiles<C>(it) ? 1 : 2;
 }
+__device__ __forceinline__ int place_k(int t, int lead) { return t < lead ? t : 2 * t - lead + 1; }
+__device__ __forceinline__ int place_v(int t, int lead, int tiles) { return min(t + lead, tiles) + t; }
 
-// Tensor copies: lane l copies box l of a tile. Boxes without a token are left out.
+// Tensor copies, two warps for K and two for V, which take half of the panels each: a warp is held
+// for about 75 cycles and 4.4 for every 128-byte row of a copy, so that of blocks of 16 tokens one
+// warp brings 15 bytes a cycle and four bring 59 (with an L2 policy fewer once they are many: 66
+// bytes a cycle at most, without one 84). The tensor cores need 32 at head_dim 128, HBM gives 24.
+// Lane l copies box l of a tile; boxes without a token are left out.
 template <typename C, int D>
-__device__ __forceinline__ void tensor_load_role(const AttendParams& p, const AttendMaps& maps, AttendShared<C>& sh,
-                                                 uint8_t* stages) {
+__device__ __forceinline__ void tensor_load_role(const AttendParams& p, const CUtensorMap* map, bool is_k, int half,
+                                                 AttendShared<C>& sh, uint8_t* stages) {
+  constexpr int P0 = C::PANELS / 2;  // panels of a warp
   const int lane = threadIdx.x & 31;
   const int boxes = C::TN / p.box;
-  const uint32_t base = smem_addr(stages);
-  uint32_t pos = 0, count = 0;
+  const uint32_t base = smem_addr(stages) + half * P0 * C::TN * 128, box_bytes = p.box * 128;
+  uint32_t before = 0, count = 0;  // tiles of K and V of the items before
   Item it;
-  const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
   while (next_item(sh, count, it)) {
     const int32_t* row = p.block_tables + (size_t)it.table * p.max_blocks;
-    const uint64_t pol = it.once ? once : again;
-    auto entry = [&](int t) -> int {
-      const int tok = it.t0 + t * C::TN + lane * p.box;
-      if (t >= it.tiles || lane >= boxes || tok >= it.hi || tok + p.box <= it.lo) return -1;
-      return __ldg(row + div_block(p, tok));
-    };
-    auto load = [&](const void* map, int t, int phys) -> bool {
-      const int stage = pos % C::NS;
-      const uint32_t bar = smem_addr(&sh.kv_full[stage]);
-      if (!wait_for(smem_addr(&sh.kv_empty[stage]), ((pos / C::NS) & 1) ^ 1, &sh.give_up)) return false;
-      const int tok = it.t0 + t * C::TN + lane * p.box;
-      const bool live = lane < boxes && tok < it.hi && tok + p.box > it.lo;
-      const int n = __popc(__ballot_sync(0xffffffffu, live));
-      if (lane == 0) mbar_expect(bar, (uint32_t)(n * p.box * 128 * C::PANELS));
-      __syncwarp();
-      if (live) {
-        if ((unsigned)phys >= (unsigned)p.num_blocks) {
-          atomicOr(p.err, PA_DEVERR_BLOCK_INDEX);
-          phys = 0;
-        }
-        const int at = phys * p.block_size + (tok - div_block(p, tok) * p.block_size);
-        const uint32_t dst = base + stage * C::STAGE + lane * p.box * 128;
-#pragma unroll
-        for (int c = 0; c < C::PANELS; ++c) tensor_load3(dst + c * C::TN * 128, map, bar, c * 64, it.kvh, at, pol);
-      }
-      ++pos;
-      return true;
-    };
     const int lead = lead_of<C>(it);
-    int e = entry(0);  // of the next K
-    for (int t = 0; t < it.tiles + lead; ++t) {
-      // V of a tile whose K went out `lead` tiles ago: its entries are in L1
-      if (t >= lead && !load(&maps.v, t - lead, entry(t - lead))) return;
-      if (t < it.tiles) {
-        const int ahead = entry(t + 1);
-        if (!load(&maps.k, t, e)) return;
-        e = ahead;
+    int tok = it.t0 + lane * p.box;  // the box's first token
+    auto holds = [&](int tk) { return lane < boxes && tk < it.hi && tk + p.box > it.lo; };
+    auto entry = [&](int t, int tk) -> int { return t < it.tiles && holds(tk) ? __ldg(row + div_block(p, tk)) : 0; };
+    int phys = entry(0, tok);
+    for (int t = 0; t < it.tiles; ++t, tok += C::TN) {
+      const uint32_t n = before + (is_k ? place_k(t, lead) : place_v(t, lead, it.tiles));
+      const int stage = n % C::NS;
+      const int ahead = entry(t + 1, tok + C::TN);
+      const bool here = holds(tok);
+      if ((unsigned)phys >= (unsigned)p.num_blocks) {
+        atomicOr(p.err, PA_DEVERR_BLOCK_INDEX);
+        phys = 0;
       }
+      const int at = phys * p.block_size + (tok - div_block(p, tok) * p.block_size);
+      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, here)) * box_bytes * P0;
+      const uint32_t bar = smem_addr(&sh.kv_full[stage]);
+      PA_WAIT(sh.kv_empty[stage], ((n / C::NS) & 1) ^ 1);
+      if (lane == 0) mbar_expect(bar, bytes);
+      __syncwarp();
+      if (here) {
+        const uint32_t dst = base + stage * C::STAGE + lane * box_bytes;
+#pragma unroll
+        for (int c = 0; c < P0; ++c)
+          tensor_load3(dst + c * C::TN * 128, map, bar, (half * P0 + c) * 64, it.kvh, at);
+      }
+      __syncwarp();
+      phys = ahead;
     }
+    before += 2 * it.tiles;
   }
-  // nothing more is issued; a CTA that gives up waits for its copies in drain_copies
 }
 
 // Staged copies: each lane copies 16-byte chunks of its warp's rows into a ring of raw tiles with
@@ -443,7 +456,6 @@ __device__ __forceinline__ void staged_load_role(const AttendParams& p, AttendSh
   constexpr int RW = C::TN / 4;         // rows of a warp
   constexpr int CH = RW * CPR / 32;     // chunks of a lane
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - C::W_LOAD;
-  const uint64_t pol = l2_evict_normal_policy();
   const uint32_t raw_lane = smem_addr(raw) + warp * (C::RAW / 4) + lane * 16;
   uint32_t count = 0;
   Item it;
@@ -480,8 +492,8 @@ __device__ __forceinline__ void staged_load_role(const AttendParams& p, AttendSh
         const uint32_t rr = __shfl_sync(0xffffffffu, ridx, r);
         const int row = warp * RW + r;
         if (row >= c0 && row < c1)
-          asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst + i * 512),
-                       "l"(cache + (size_t)rr * (D * C::KVB) + c * 16), "l"(pol)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 512),
+                       "l"(cache + (size_t)rr * (D * C::KVB) + c * 16)
                        : "memory");
       }
       ++issued;
@@ -590,44 +602,49 @@ __device__ __forceinline__ void query_role(const AttendParams& p, AttendShared<C
 // ------------------------------------------------------------------ products
 // Steps of an item: one per token tile, or one per token tile and row tile. Products issued by one
 // thread run in order, so that a score buffer is overwritten only after the weights in it are used.
+// One thread does it all: it has about 1000 cycles for a step's 16 products, so operands are
+// addressed by adding constants to the lower words of their descriptors.
 template <typename C, int D>
-__device__ __forceinline__ void product_role(AttendShared<C>& sh, uint8_t* q_tiles, uint8_t* stages, uint32_t tmem) {
+__device__ __forceinline__ void product_role(const AttendParams& p, AttendShared<C>& sh, uint8_t* q_tiles,
+                                             uint8_t* stages, uint32_t tmem) {
   using TM = typename C::TM;
-  const bool issuer = (threadIdx.x & 31) == 0;
-  const uint32_t q_base = smem_addr(q_tiles), kv_base = smem_addr(stages);
   const uint64_t by_k = operand_desc(16), by_n = operand_desc(C::TN * 128);
-  constexpr uint32_t kScores = mma_desc<TM>(C::TN, false), kValues = mma_desc<TM>(D, true);
+  const uint32_t q_lo = (uint32_t)by_k + (smem_addr(q_tiles) >> 4), k_lo = (uint32_t)by_k + (smem_addr(stages) >> 4),
+                 v_lo = (uint32_t)by_n + (smem_addr(stages) >> 4);
+  const uint32_t k_hi = (uint32_t)(by_k >> 32), v_hi = (uint32_t)(by_n >> 32);
+  // a negative scale: the scores of -Q
+  const uint32_t for_scores = mma_desc<TM>(C::TN, false) | (p.negate ? kNegateA : 0u);
+  constexpr uint32_t kForValues = mma_desc<TM>(D, true);
   uint32_t count = 0, pos = 0, used = 0;  // items, K and V tiles, query tiles
   uint32_t weights[2] = {0, 0};           // steps that used each score buffer
-  Item it;
-  while (next_item(sh, count, it)) {
-    const bool two = two_row_tiles<C>(it);
-    const int dup = two ? 1 : 0, steps = it.tiles << dup;
-    const int q_tile[2] = {(int)(used % C::NQ), (int)((used + dup) % C::NQ)};
-    for (int i = 0; i <= dup; ++i) PA_WAIT(sh.q_full[(used + i) % C::NQ], ((used + i) / C::NQ) & 1);
+  for (;;) {
+    const int at = count % C::ITEMS;
+    PA_WAIT_ALONE(sh.item_full[at], (count / C::ITEMS) & 1);
+    ++count;
+    const int tiles = sh.items[at].tiles, dup = C::NWG == 2 && sh.items[at].rows > 128 ? 1 : 0;
+    mbar_arrive(smem_addr(&sh.item_empty[at]));
+    if (tiles == 0) return;
+    const int steps = tiles << dup;
+    const uint32_t q_tile[2] = {used % C::NQ, (used + dup) % C::NQ};
+    for (int i = 0; i <= dup; ++i) PA_WAIT_ALONE(sh.q_full[(used + i) % C::NQ], ((used + i) / C::NQ) & 1);
     used += 1 + dup;
-    int k_stage = 0, v_stage = 0;
+    uint32_t k_stage = 0, v_stage = 0;
     auto scores = [&](int i) -> bool {  // step i: S = Q K^T
       if (!(i & dup)) {
         k_stage = pos % C::NS;
-        if (!wait_for(smem_addr(&sh.kv_full[k_stage]), (pos / C::NS) & 1, &sh.give_up)) return false;
+        if (!wait_alone(smem_addr(&sh.kv_full[k_stage]), (pos / C::NS) & 1, &sh.give_up)) return false;
         ++pos;
       }
       tc_fence_after();
-      if (issuer) {
-        const uint32_t a = q_base + q_tile[i & dup] * C::QTILE, b = kv_base + k_stage * C::STAGE;
-        const uint32_t d = tmem + C::S_COL + (i & 1) * C::TN;
+      const uint32_t a = q_lo + q_tile[i & dup] * (C::QTILE >> 4), b = k_lo + k_stage * (C::STAGE >> 4);
+      const uint32_t d = tmem + C::S_COL + (i & 1) * C::TN;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(d, desc_at(by_k, a + (kk / 4) * (128 * 128) + (kk % 4) * 32),
-                 desc_at(by_k, b + (kk / 4) * (C::TN * 128) + (kk % 4) * 32), kScores, kk > 0);
-        mma_commit(smem_addr(&sh.s_full[i & 1]));
-        if (dup == 0 || (i & 1)) mma_commit(smem_addr(&sh.kv_empty[k_stage]));
-        if (i >= steps - 1 - dup) {  // the last step of its row tile
-          mma_commit(smem_addr(&sh.q_empty[q_tile[i & dup]]));
-        }
-      }
-      __syncwarp();
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_ss(d, a + (((kk / 4) * (128 * 128) + (kk % 4) * 32) >> 4), k_hi,
+               b + (((kk / 4) * (C::TN * 128) + (kk % 4) * 32) >> 4), k_hi, for_scores, kk > 0);
+      mma_commit(smem_addr(&sh.s_full[i & 1]));
+      if (dup == 0 || (i & 1)) mma_commit(smem_addr(&sh.kv_empty[k_stage]));
+      if (i >= steps - 1 - dup) mma_commit(smem_addr(&sh.q_empty[q_tile[i & dup]]));  // its row tile's last
       return true;
     };
     for (int i = 0; i < 2 && i < steps; ++i)
@@ -636,22 +653,20 @@ __device__ __forceinline__ void product_role(AttendShared<C>& sh, uint8_t* q_til
       const int buf = i & 1, group = C::NWG == 2 ? buf : 0;
       if (!(i & dup)) {
         v_stage = pos % C::NS;
-        PA_WAIT(sh.kv_full[v_stage], (pos / C::NS) & 1);
+        PA_WAIT_ALONE(sh.kv_full[v_stage], (pos / C::NS) & 1);
         ++pos;
       }
-      PA_WAIT(sh.p_full[buf], weights[buf] & 1);
+      PA_WAIT_ALONE(sh.p_full[buf], weights[buf] & 1);
       ++weights[buf];
       tc_fence_after();
-      if (issuer) {  // O += P V
-        const uint32_t a = tmem + C::S_COL + buf * C::TN, b = kv_base + v_stage * C::STAGE;
-        const uint32_t d = tmem + C::O_COL + group * D;
+      // O += P V
+      const uint32_t a = tmem + C::S_COL + buf * C::TN, b = v_lo + v_stage * (C::STAGE >> 4);
+      const uint32_t d = tmem + C::O_COL + group * D;
+      mma_ts(d, a, b, v_hi, kForValues, i >= C::NWG);
 #pragma unroll
-        for (int kk = 0; kk < C::TN / 16; ++kk)
-          mma_ts(d, a + kk * 8, desc_at(by_n, b + kk * 2048), kValues, i >= C::NWG || kk > 0);
-        mma_commit(smem_addr(&sh.pv_done[group]));
-        if (dup == 0 || (i & 1)) mma_commit(smem_addr(&sh.kv_empty[v_stage]));
-      }
-      __syncwarp();
+      for (int kk = 1; kk < C::TN / 16; ++kk) mma_ts(d, a + kk * 8, b + kk * (2048 >> 4), v_hi, kForValues, true);
+      mma_commit(smem_addr(&sh.pv_done[buf]));
+      if (dup == 0 || (i & 1)) mma_commit(smem_addr(&sh.kv_empty[v_stage]));
       if (i + 2 < steps && !scores(i + 2)) return;
     }
   }
@@ -668,7 +683,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
   const uint32_t lanes = (uint32_t)((threadIdx.x >> 5) & 3) << 21;  // 32 (warp % 4) in the upper half
   const uint32_t own_o = tmem + C::O_COL + group * D + lanes;
   const float sl2 = p.scale_log2;
-  uint32_t count = 0, used[2] = {0, 0}, pvs = 0, pairs = 0, tiles_before = 0;
+  uint32_t count = 0, used[2] = {0, 0}, pairs = 0, tiles_before = 0;
   Item it;
   while (next_item(sh, count, it)) {
     const bool two = two_row_tiles<C>(it);
@@ -695,29 +710,35 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
       if (warp_live) {
         tc_fence_after();
         const int c0 = it.lo - t0, c1 = end - t0;  // columns [c0, c1) are seen
-        const bool whole = __all_sync(0xffffffffu, !live || (c0 <= 0 && c1 >= C::TN));
-        // the largest scaled score
         uint32_t x[2][32];
-        float top = -INFINITY;
+        if (!__all_sync(0xffffffffu, !live || (c0 <= 0 && c1 >= C::TN))) {
+          // scores of tokens that the row does not see become -inf, whatever they are
+#pragma unroll 1
+          for (int c = 0; c < C::TN; c += 32) {
+            tmem_load32(x[0], s_at + c);
+            tmem_loaded(x[0]);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j < c0 || c + j >= c1) x[0][j] = 0xff800000u;
+            tmem_store32(s_at + c, x[0]);
+          }
+          tmem_stored();
+        }
+        // the largest score, scaled
+        float most[2] = {-INFINITY, -INFINITY};
         tmem_load32(x[0], s_at);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           uint32_t(&y)[32] = x[c & 1];
           tmem_loaded(y);
-          if (c + 1 < NC) tmem_load32(x[(c + 1) & 1], s_at + 32 * (c + 1));
-          if (whole) {
+          tmem_load32(x[(c + 1) & 1], s_at + 32 * ((c + 1) % NC));  // the last one: the first columns again
 #pragma unroll
-            for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(y[j]) * sl2);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int col = 32 * c + j;
-              if (col >= c0 && col < c1) top = fmaxf(top, __uint_as_float(y[j]) * sl2);
-            }
+          for (int j = 0; j < 32; j += 4) {
+            most[0] = fmaxf(fmaxf(most[0], __uint_as_float(y[j])), __uint_as_float(y[j + 1]));
+            most[1] = fmaxf(fmaxf(most[1], __uint_as_float(y[j + 2])), __uint_as_float(y[j + 3]));
           }
         }
-        top -= C::kLift;
-        tmem_load32(x[0], s_at);
+        const float top = fmaxf(most[0], most[1]) * sl2 - C::kLift;
         const bool raise = top > ref + C::kSlack;
         if (__any_sync(0xffffffffu, raise)) {
           const float now = raise ? top : ref;
@@ -725,9 +746,10 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
           ref = now;
           sum *= f;
           if (mine > 0) {  // the accumulator of the steps before
-            PA_WAIT(sh.pv_done[group], (pvs - 1) & 1);
+            const int last = C::NWG == 2 ? buf : buf ^ 1;
+            PA_WAIT(sh.pv_done[last], (used[last] - (C::NWG == 2 ? 2 : 1)) & 1);
             tc_fence_after();
-            tmem_loaded(x[0]);
+            tmem_loaded(x[NC & 1]);
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -739,38 +761,35 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
             }
           }
         }
-        const float sub = ref == -INFINITY ? 0.f : ref;
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
+        const float sub = ref == -INFINITY ? 0.f : -ref;
+        const float2 by = make_float2(sl2, sl2), plus = make_float2(sub, sub);
+        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          uint32_t(&y)[32] = x[c & 1];
+          uint32_t(&y)[32] = x[(NC + c) & 1];
           tmem_loaded(y);
-          if (c + 1 < NC) tmem_load32(x[(c + 1) & 1], s_at + 32 * (c + 1));
+          if (c + 1 < NC) tmem_load32(x[(NC + c + 1) & 1], s_at + 32 * (c + 1));
           uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            float a = exp2_approx(fmaf(__uint_as_float(y[j]), sl2, -sub));
-            float b = exp2_approx(fmaf(__uint_as_float(y[j + 1]), sl2, -sub));
-            if (!whole) {
-              const int col = 32 * c + j;
-              a = col >= c0 && col < c1 ? a : 0.f;
-              b = col + 1 >= c0 && col + 1 < c1 ? b : 0.f;
-            }
-            part[(j / 2) & 1] += a;
-            part[2 + ((j / 2) & 1)] += b;
-            w[j / 2] = pack2<TM>(a, b);
+            float2 e = fma2(make_float2(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), by, plus);
+            e.x = exp2_approx(e.x);
+            e.y = exp2_approx(e.y);
+            part[(j / 2) & 1] = add2(part[(j / 2) & 1], e);
+            w[j / 2] = pack2<TM>(e.x, e.y);
           }
           // over columns of scores that are in registers already
           tmem_store16(s_at + 16 * c, w);
         }
-        sum += (part[0] + part[1]) + (part[2] + part[3]);
+        const float2 both = add2(part[0], part[1]);
+        sum += both.x + both.y;
         tmem_stored();
       }
       if constexpr (ZERO_V) {
         // V rows outside the context hold whatever the cache or an earlier tile left: zeros there,
         // so that weights of 0 meet 0
         if ((t0 < it.lo || t0 + C::TN > it.hi) && !(dup && group)) {
-          const uint32_t n = tiles_before + min(t + lead_of<C>(it), it.tiles) + t;
+          const uint32_t n = tiles_before + place_v(t, lead_of<C>(it), it.tiles);
           PA_WAIT(sh.kv_full[n % C::NS], (n / C::NS) & 1);
           const uint32_t tile = smem_addr(stages) + (n % C::NS) * C::STAGE;
           for (int row = at; row < C::TN; row += 128)
@@ -783,12 +802,14 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[buf]));
-      ++pvs;
     }
     tiles_before += 2 * it.tiles;
 
     // ---- the item's rows: O / sum, or (reference, sum, O) of a piece
-    if (mine > 0) PA_WAIT(sh.pv_done[group], (pvs - 1) & 1);
+    if (mine > 0) {
+      const int last = C::NWG == 2 ? group : (steps - 1) & 1;
+      PA_WAIT(sh.pv_done[last], (used[last] - 1) & 1);
+    }
     tc_fence_after();
     const bool joint = C::NWG == 2 && !two;  // two states of the same rows
     float f_own = 1.f, f_other = 0.f;
@@ -903,13 +924,13 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
     auto init = [](uint64_t* bars, int n, int count) {
       for (int i = 0; i < n; ++i) mbar_init_count(smem_addr(bars + i), count);
     };
-    init(sh.kv_full, C::NS, C::NLOAD);
+    init(sh.kv_full, C::NS, LOAD == kLoadTensor ? 2 : C::NLOAD);
     init(sh.kv_empty, C::NS, 1);
     init(sh.q_full, C::NQ, 1);
     init(sh.q_empty, C::NQ, 1);
     init(sh.s_full, 2, 1);
     init(sh.p_full, 2, 4);
-    init(sh.pv_done, C::NWG, 1);
+    init(sh.pv_done, 2, 1);
     init(sh.item_full, C::ITEMS, 1);
     init(sh.item_empty, C::ITEMS, C::READERS);
     init(&sh.pair, 1, C::NSW);
@@ -932,14 +953,16 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
 
   if (warp < C::NSW)
     softmax_role<C, T, D, LOAD == kLoadTensor>(p, sh, stages, tmem);
-  else if (warp == C::W_MMA)
-    product_role<C, D>(sh, q_tiles, stages, tmem);
+  else if (warp == C::W_MMA) {
+    if ((threadIdx.x & 31) == 0) product_role<C, D>(p, sh, q_tiles, stages, tmem);
+  }
   else if (warp == C::W_PLAN)
     plan_role<C, D>(p, sh);
   else if (warp == C::W_Q)
     query_role<C, T, D>(p, sh, q_tiles);
   else if constexpr (LOAD == kLoadTensor)
-    tensor_load_role<C, D>(p, maps, sh, stages);
+    tensor_load_role<C, D>(p, warp < C::W_LOAD + 2 ? &maps.k : &maps.v, warp < C::W_LOAD + 2,
+                           (warp - C::W_LOAD) & 1, sh, stages);
   else
     staged_load_role<C, D, LOAD == kLoadFp8>(p, sh, stages, raw);
 

@@ -40,7 +40,8 @@ struct AttendParams {
   int box;                   // tokens of a tensor copy, a power of two that divides the block size
   int ctas;                  // CTAs that share out the work
   int slot_rows;             // bound on an item's rows
-  float scale_log2, v_scale;
+  float scale_log2, v_scale; // |scale| log2(e) (and the scale of K), not zero
+  int negate;                // the scale is negative
 };
 
 // Query rows (token and head of a KV head's group) of an item, tokens of a tile.
