@@ -199,21 +199,6 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
   if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
   return wait_long(bar, parity, give_up);
 }
-// The same for one thread.
-static __device__ __noinline__ bool wait_long_alone(uint32_t bar, uint32_t parity, volatile int* give_up) {
-  const uint64_t t0 = global_ns();
-  for (;;) {
-    const bool over = global_ns() - t0 >= 2000000000ull || *give_up != 0;
-    if (mbar_try(bar, parity)) return true;
-    if (over) {
-      *give_up = 1;
-      return false;
-    }
-  }
-}
-__device__ __forceinline__ bool wait_alone(uint32_t bar, uint32_t parity, volatile int* give_up) {
-  return mbar_try(bar, parity) || wait_long_alone(bar, parity, give_up);
-}
 
 // ------------------------------------------------------------------ shared memory
 template <typename C>
@@ -236,8 +221,6 @@ struct AttendShared {
 
 #define PA_WAIT(bar, parity) \
   if (!wait_for(smem_addr(&(bar)), (parity), &sh.give_up)) return
-#define PA_WAIT_ALONE(bar, parity) \
-  if (!wait_alone(smem_addr(&(bar)), (parity), &sh.give_up)) return
 
 // ------------------------------------------------------------------ plan
 // Every CTA finds the first unit of its run: a sum over the segments' units. CTA 0 writes what the
@@ -601,13 +584,12 @@ __device__ __forceinline__ void query_role(const AttendParams& p, AttendShared<C
 
 // ------------------------------------------------------------------ products
 // Steps of an item: one per token tile, or one per token tile and row tile. Products issued by one
-// thread run in order, so that a score buffer is overwritten only after the weights in it are used.
-// One thread does it all: it has about 1000 cycles for a step's 16 products, so operands are
-// addressed by adding constants to the lower words of their descriptors.
+// lane run in order, so that a score buffer is overwritten only after the weights in it are used.
 template <typename C, int D>
 __device__ __forceinline__ void product_role(const AttendParams& p, AttendShared<C>& sh, uint8_t* q_tiles,
-                                             uint8_t* stages, uint32_t tmem) {
+                                             uint8_t* stages, uint32_t tmem_lane) {
   using TM = typename C::TM;
+  const uint32_t tmem = __reduce_or_sync(0xffffffffu, tmem_lane);  // uniform, as the compiler sees it
   const uint64_t by_k = operand_desc(16), by_n = operand_desc(C::TN * 128);
   const uint32_t q_lo = (uint32_t)by_k + (smem_addr(q_tiles) >> 4), k_lo = (uint32_t)by_k + (smem_addr(stages) >> 4),
                  v_lo = (uint32_t)by_n + (smem_addr(stages) >> 4);
@@ -615,58 +597,62 @@ __device__ __forceinline__ void product_role(const AttendParams& p, AttendShared
   // a negative scale: the scores of -Q
   const uint32_t for_scores = mma_desc<TM>(C::TN, false) | (p.negate ? kNegateA : 0u);
   constexpr uint32_t kForValues = mma_desc<TM>(D, true);
-  uint32_t count = 0, pos = 0, used = 0;  // items, K and V tiles, query tiles
-  uint32_t weights[2] = {0, 0};           // steps that used each score buffer
-  for (;;) {
-    const int at = count % C::ITEMS;
-    PA_WAIT_ALONE(sh.item_full[at], (count / C::ITEMS) & 1);
-    ++count;
-    const int tiles = sh.items[at].tiles, dup = C::NWG == 2 && sh.items[at].rows > 128 ? 1 : 0;
-    mbar_arrive(smem_addr(&sh.item_empty[at]));
-    if (tiles == 0) return;
+  const uint32_t on = elected();
+  uint32_t count = 0, used = 0;  // items, query tiles
+  uint32_t stage = 0, lap = 0;   // of the next K or V tile
+  uint32_t weights[2] = {0, 0};  // steps that used each score buffer
+  Item it;
+  auto next_tile = [&](uint32_t& which) -> bool {
+    which = stage;
+    if (!wait_for(smem_addr(&sh.kv_full[stage]), lap, &sh.give_up)) return false;
+    if (++stage == C::NS) {
+      stage = 0;
+      lap ^= 1;
+    }
+    return true;
+  };
+  while (next_item(sh, count, it)) {
+    const int tiles = __reduce_max_sync(0xffffffffu, it.tiles);
+    const int dup = __any_sync(0xffffffffu, two_row_tiles<C>(it)) ? 1 : 0;
     const int steps = tiles << dup;
-    const uint32_t q_tile[2] = {used % C::NQ, (used + dup) % C::NQ};
-    for (int i = 0; i <= dup; ++i) PA_WAIT_ALONE(sh.q_full[(used + i) % C::NQ], ((used + i) / C::NQ) & 1);
+    const uint32_t q0 = used % C::NQ, q1 = (used + dup) % C::NQ;
+    for (int i = 0; i <= dup; ++i) PA_WAIT(sh.q_full[(used + i) % C::NQ], ((used + i) / C::NQ) & 1);
     used += 1 + dup;
     uint32_t k_stage = 0, v_stage = 0;
     auto scores = [&](int i) -> bool {  // step i: S = Q K^T
-      if (!(i & dup)) {
-        k_stage = pos % C::NS;
-        if (!wait_alone(smem_addr(&sh.kv_full[k_stage]), (pos / C::NS) & 1, &sh.give_up)) return false;
-        ++pos;
-      }
+      if (!(i & dup) && !next_tile(k_stage)) return false;
       tc_fence_after();
-      const uint32_t a = q_lo + q_tile[i & dup] * (C::QTILE >> 4), b = k_lo + k_stage * (C::STAGE >> 4);
+      const uint32_t q_tile = i & dup ? q1 : q0;
+      const uint32_t a = q_lo + q_tile * (C::QTILE >> 4), b = k_lo + k_stage * (C::STAGE >> 4);
       const uint32_t d = tmem + C::S_COL + (i & 1) * C::TN;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss(d, a + (((kk / 4) * (128 * 128) + (kk % 4) * 32) >> 4), k_hi,
+        mma_ss(on, d, a + (((kk / 4) * (128 * 128) + (kk % 4) * 32) >> 4), k_hi,
                b + (((kk / 4) * (C::TN * 128) + (kk % 4) * 32) >> 4), k_hi, for_scores, kk > 0);
-      mma_commit(smem_addr(&sh.s_full[i & 1]));
-      if (dup == 0 || (i & 1)) mma_commit(smem_addr(&sh.kv_empty[k_stage]));
-      if (i >= steps - 1 - dup) mma_commit(smem_addr(&sh.q_empty[q_tile[i & dup]]));  // its row tile's last
+      mma_commit(on, smem_addr(&sh.s_full[i & 1]));
+      if (dup == 0 || (i & 1)) mma_commit(on, smem_addr(&sh.kv_empty[k_stage]));
+      if (i >= steps - 1 - dup) mma_commit(on, smem_addr(&sh.q_empty[q_tile]));  // its row tile's last
       return true;
     };
     for (int i = 0; i < 2 && i < steps; ++i)
       if (!scores(i)) return;
     for (int i = 0; i < steps; ++i) {
       const int buf = i & 1, group = C::NWG == 2 ? buf : 0;
-      if (!(i & dup)) {
-        v_stage = pos % C::NS;
-        PA_WAIT_ALONE(sh.kv_full[v_stage], (pos / C::NS) & 1);
-        ++pos;
-      }
-      PA_WAIT_ALONE(sh.p_full[buf], weights[buf] & 1);
-      ++weights[buf];
+      if (!(i & dup) && !next_tile(v_stage)) return;
+      PA_WAIT(sh.p_full[buf], (buf ? weights[1] : weights[0]) & 1);
+      if (buf)
+        ++weights[1];
+      else
+        ++weights[0];
       tc_fence_after();
       // O += P V
       const uint32_t a = tmem + C::S_COL + buf * C::TN, b = v_lo + v_stage * (C::STAGE >> 4);
       const uint32_t d = tmem + C::O_COL + group * D;
-      mma_ts(d, a, b, v_hi, kForValues, i >= C::NWG);
+      mma_ts(on, d, a, b, v_hi, kForValues, i >= C::NWG);
 #pragma unroll
-      for (int kk = 1; kk < C::TN / 16; ++kk) mma_ts(d, a + kk * 8, b + kk * (2048 >> 4), v_hi, kForValues, true);
-      mma_commit(smem_addr(&sh.pv_done[buf]));
-      if (dup == 0 || (i & 1)) mma_commit(smem_addr(&sh.kv_empty[v_stage]));
+      for (int kk = 1; kk < C::TN / 16; ++kk) mma_ts(on, d, a + kk * 8, b + kk * (2048 >> 4), v_hi, kForValues, true);
+      mma_commit(on, smem_addr(&sh.pv_done[buf]));
+      if (dup == 0 || (i & 1)) mma_commit(on, smem_addr(&sh.kv_empty[v_stage]));
       if (i + 2 < steps && !scores(i + 2)) return;
     }
   }
@@ -953,9 +939,8 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
 
   if (warp < C::NSW)
     softmax_role<C, T, D, LOAD == kLoadTensor>(p, sh, stages, tmem);
-  else if (warp == C::W_MMA) {
-    if ((threadIdx.x & 31) == 0) product_role<C, D>(p, sh, q_tiles, stages, tmem);
-  }
+  else if (warp == C::W_MMA)
+    product_role<C, D>(p, sh, q_tiles, stages, tmem);
   else if (warp == C::W_PLAN)
     plan_role<C, D>(p, sh);
   else if (warp == C::W_Q)
@@ -975,7 +960,7 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
     // before the CTA gives its memory back
     if (threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_COPY);
     if (warp == C::W_MMA) {
-      if ((threadIdx.x & 31) == 0) mma_commit(smem_addr(&sh.drain));
+      mma_commit(elected(), smem_addr(&sh.drain));
       __syncwarp();
     }
     const uint64_t t0 = global_ns();

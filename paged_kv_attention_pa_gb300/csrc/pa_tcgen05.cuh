@@ -95,29 +95,41 @@ __host__ __device__ constexpr uint32_t mma_desc(uint32_t n, bool b_by_n) {
   return (1u << 4) | (type << 7) | (type << 10) | ((b_by_n ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 constexpr uint32_t kNegateA = 1u << 13;
-// D[tmem] (+)= A[shared] B[shared], K = 16; descriptors as (lower, upper) words. One thread.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
+// The products are issued by one lane of a warp that runs converged, so that the compiler keeps
+// descriptors in uniform registers, where the instructions take them from: issued inside a branch
+// of one lane, each took about 100 cycles instead of the 64 that it runs.
+__device__ __forceinline__ uint32_t elected() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+// D[tmem] (+)= A[shared] B[shared], K = 16; descriptors as (lower, upper) words. Issued where `on`.
+__device__ __forceinline__ void mma_ss(uint32_t on, uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
                                        uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 e, %7, 0;\n\t"
       "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"((uint32_t)accumulate)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"((uint32_t)accumulate), "r"(on)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[shared], K = 16: A's lanes are its rows, a column holds two elements.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc,
+__device__ __forceinline__ void mma_ts(uint32_t on, uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc,
                                        bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
       "mov.b64 y, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"((uint32_t)accumulate)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"((uint32_t)accumulate), "r"(on)
       : "memory");
 }
-// The barrier gets an arrival when every product that this thread issued before is done.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// The barrier gets an arrival when every product that this lane issued before is done.
+__device__ __forceinline__ void mma_commit(uint32_t on, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(on)
+      : "memory");
 }
 
 // ---------------------------------------------------------------- pairs of fp32
