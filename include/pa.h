@@ -432,8 +432,8 @@ pa_status pa_gather(const pa_gather_args* args, void* workspace, size_t workspac
  *   out[r,h] = sum_t softmax(scale * q[r,h] . K[b,t,h / G])_t * V[b,t,h / G]    t < seq_lens[b]
  * Any number of rows: one (a decode step), a few (the beams of a search, which share their
  * source), or a prompt's thousands.
- *   q         [rows, Hq, D] (dtype); row r starts at element r * q_stride (a multiple of 8), the
- *             heads of a row are dense
+ *   q         [rows, Hq, D] (dtype); row r starts at element r * q_stride (a multiple of 8, at
+ *             least Hq * D), the heads of a row are dense
  *   starts    as for pa_append: NULL, and sequence b has the `rows` rows b * rows + i; or [B + 1]
  *             ascending int32 on the device, and `rows` is the number of rows in all. Rows of no
  *             sequence are padding: neither read nor written in out
@@ -441,7 +441,7 @@ pa_status pa_gather(const pa_gather_args* args, void* workspace, size_t workspac
  *   k_cache, v_cache, block_tables, seq_lens, max_seq_len, kv_dtype, k_scale, v_scale
  *             as for pa_decode_ex, with 16-bit and fp8 caches (with fp8 the queries are rounded to
  *             fp16: |x| <= 65504). 4-bit caches: PA_ERR_UNSUPPORTED
- * G = Hq / Hkv up to PA_MAX_GQA_GROUP; rows * G below 2^28, rows * Hq below 2^31. Scores, softmax
+ * G = Hq / Hkv up to PA_MAX_GQA_GROUP; rows * Hq below 2^31. Scores, softmax
  * statistics and sums are fp32; the weights are rounded to the type of the products (dtype, fp16
  * for fp8 caches), the output once. The work is divided among the SMs by the lengths found on the
  * device: the host needs none of them, and repeated calls give the same bits. `workspace`:

@@ -42,8 +42,7 @@ pa_status check_sizes(const Call& c, int* cap) {
       !(c.k_scale > 0.f && c.v_scale > 0.f && c.k_scale < INFINITY && c.v_scale < INFINITY))
     return PA_ERR_INVALID_ARG;
   if ((int64_t)c.num_blocks * c.block_size * c.Hkv > (int64_t)UINT32_MAX) return PA_ERR_UNSUPPORTED;
-  // rows of a segment are numbered in 28 bits, rows and heads of the output in 31
-  if (c.T * (c.Hq / c.Hkv) >= 1 << 28 || c.T * c.Hq > INT_MAX) return PA_ERR_UNSUPPORTED;
+  if (c.T * c.Hq > INT_MAX) return PA_ERR_UNSUPPORTED;  // rows of the output
   const int64_t all = (int64_t)c.max_blocks * c.block_size;
   const int64_t len = c.max_seq_len <= 0 ? all : c.max_seq_len;
   if (len > all || len > INT_MAX - 1024) return PA_ERR_OUT_OF_RANGE;  // 1024: tiles past the end
@@ -52,13 +51,14 @@ pa_status check_sizes(const Call& c, int* cap) {
 }
 
 struct Layout {
-  size_t plan, slot_ml, slot_acc, row_ml, row_acc, total;
+  size_t plan, split, slot_ml, slot_acc, row_ml, row_acc, total;
   int slot_rows;
 };
 // both: rows may have two contexts
 Layout layout_of(const Call& c, int ctas, int segments, bool both) {
   Layout w{};
-  w.slot_rows = (int)std::min<int64_t>(attend_rows(c.D), std::max<int64_t>(c.item_rows * (c.Hq / c.Hkv), 1));
+  const int G = c.Hq / c.Hkv;
+  w.slot_rows = (int)std::min<int64_t>(attend_row_tiles(c.D) * (128 / G), std::max<int64_t>(c.item_rows, 1)) * G;
   const size_t slots = (size_t)ctas * 2 * w.slot_rows, rows = both ? (size_t)(2 * c.T * c.Hq) : 0;
   size_t off = kHeaderBytes;
   auto take = [&](size_t bytes) {
@@ -67,6 +67,7 @@ Layout layout_of(const Call& c, int ctas, int segments, bool both) {
     return at;
   };
   w.plan = take((size_t)(2 + (int64_t)segments) * 8);
+  w.split = take((size_t)ctas * sizeof(SplitItem));
   w.slot_ml = take(slots * 8);
   w.slot_acc = take(slots * c.D * 4);
   w.row_ml = take(rows * 8);
@@ -94,16 +95,17 @@ EncodeTiled encode_tiled() {
   return f;
 }
 
-// A cache as [tokens of the pool, Hkv, D]; a copy takes `box` tokens of one head, 64 elements wide
-// (128 bytes, the swizzle's row).
-bool make_map(CUtensorMap* map, const Call& c, const void* cache, int box) {
+// [rows, heads, D] with `stride` elements between rows; a copy takes `box` rows of `box_heads` heads,
+// 64 elements wide (128 bytes, the swizzle's row).
+bool make_map(CUtensorMap* map, const Call& c, const void* at, int64_t rows, int64_t stride, int heads, int box,
+              int box_heads) {
   const EncodeTiled encode = encode_tiled();
   if (!encode) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)c.D, (cuuint64_t)c.Hkv, (cuuint64_t)c.num_blocks * c.block_size};
-  const cuuint64_t strides[2] = {(cuuint64_t)c.D * 2, (cuuint64_t)c.Hkv * c.D * 2};
-  const cuuint32_t tile[3] = {64, 1, (cuuint32_t)box}, step[3] = {1, 1, 1};
+  const cuuint64_t dims[3] = {(cuuint64_t)c.D, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)c.D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t tile[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box}, step[3] = {1, 1, 1};
   return encode(map, c.dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-                const_cast<void*>(cache), dims, strides, tile, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                const_cast<void*>(at), dims, strides, tile, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -125,18 +127,20 @@ pa_status run(const Call& c, AttendParams& p, int cap, void* workspace, size_t b
   p.seq_lens = c.seq_lens;
   p.err = reinterpret_cast<uint32_t*>(ws);
   p.plan = reinterpret_cast<long long*>(ws + w.plan);
+  p.split = reinterpret_cast<SplitItem*>(ws + w.split);
   p.slot_ml = reinterpret_cast<float2*>(ws + w.slot_ml);
   p.slot_acc = reinterpret_cast<float*>(ws + w.slot_acc);
   p.row_ml = reinterpret_cast<float2*>(ws + w.row_ml);
   p.row_acc = reinterpret_cast<float*>(ws + w.row_acc);
   p.slot_rows = w.slot_rows;
-  p.q_stride = c.q_stride;
   p.T = (int)c.T;
   p.Hq = c.Hq;
   p.Hkv = c.Hkv;
   p.G = c.Hq / c.Hkv;
-  // r (m G - 2^32) < 2^28 * 16 <= 2^32 with m = ceil(2^32 / G): floor(r m / 2^32) = floor(r / G)
+  // r (m G - 2^32) < 2^16 * 16 < 2^32 with m = ceil(2^32 / G): floor(r m / 2^32) = floor(r / G)
   p.g_magic = p.G == 1 ? 0u : (uint32_t)(((1ull << 32) + p.G - 1) / p.G);
+  p.tile_tokens = 128 / p.G;
+  p.out_wide = (reinterpret_cast<uintptr_t>(c.out) & 31u) == 0;
   p.block_size = c.block_size;
   p.num_blocks = c.num_blocks;
   p.max_blocks = c.max_blocks;
@@ -157,8 +161,13 @@ pa_status run(const Call& c, AttendParams& p, int cap, void* workspace, size_t b
   const AttendLoad load =
       fp8 ? kLoadFp8 : p.box >= 8 && (int64_t)c.num_blocks * c.block_size <= INT_MAX ? kLoadTensor : kLoad16;
   AttendMaps maps{};
+  if (!make_map(&maps.q, c, c.q, c.T, c.T > 1 ? c.q_stride : (int64_t)c.Hq * c.D, c.Hq, p.tile_tokens, p.G))
+    return PA_ERR_CUDA;
   if (load == kLoadTensor) {
-    if (!make_map(&maps.k, c, c.k_cache, p.box) || !make_map(&maps.v, c, c.v_cache, p.box)) return PA_ERR_CUDA;
+    const int64_t tokens = (int64_t)c.num_blocks * c.block_size, stride = (int64_t)c.Hkv * c.D;
+    if (!make_map(&maps.k, c, c.k_cache, tokens, stride, c.Hkv, p.box, 1) ||
+        !make_map(&maps.v, c, c.v_cache, tokens, stride, c.Hkv, p.box, 1))
+      return PA_ERR_CUDA;
   } else {
     p.box = 1;
   }
@@ -180,7 +189,7 @@ pa_status cross_call(const pa_cross_args* a, Call* c, int* cap) {
   *c = Call{a->q, a->k_cache, a->v_cache, a->block_tables, a->seq_lens, a->out, a->q_stride, a->B, a->Hq, a->Hkv, a->D,
             a->block_size, a->num_blocks, a->max_blocks_per_seq, a->max_seq_len, a->scale, a->dtype, a->kv_dtype,
             a->k_scale, a->v_scale, T, (int64_t)a->rows};
-  if (a->q_stride < 0 || a->q_stride % 8 != 0) return PA_ERR_INVALID_ARG;
+  if (a->q_stride % 8 != 0 || (T > 1 && a->q_stride < (int64_t)a->Hq * a->D)) return PA_ERR_INVALID_ARG;
   return check_sizes(*c, cap);
 }
 

@@ -4,14 +4,14 @@
 // tokens [lo, hi) of one table row: for cross attention a sequence's queries over its states;
 // for shared prefixes first every group's queries over the group's prefix, then every sequence's
 // over the rest of its own context. The rows of a segment and KV head are its (query token, head
-// of the group) pairs, cut into items of up to RT rows (two tensor core tiles of 128 at head_dim
-// 128, one at 256).
+// of the group) pairs, whole tokens to a row tile of at most 128, cut into items of two row tiles at
+// head_dim 128 and of one at 256.
 //
 // Division of the work. An item of n token tiles counts n + 1 units (the start and end of an item
 // cost about one tile). Every CTA, one per SM, takes an equal run of the units of all items in
 // order, found from the lengths on the device: runs begin and end inside items, and the pieces of
 // an item that several CTAs hold, as well as the two contexts of a row with a shared prefix, leave
-// (reference, sum, unnormalised output) in the workspace, which merge_rows_kernel joins. The
+// (reference, sum, unnormalised output) in the workspace, which a second grid joins. The
 // division depends on the sizes alone, so repeated calls give the same bits.
 //
 // Roles of the warps of a CTA:
@@ -51,10 +51,8 @@ namespace pa {
 template <typename T, int D, AttendLoad LOAD>
 struct AttendCfg {
   using TM = std::conditional_t<LOAD == kLoadFp8, __half, T>;  // type of the products
-  static constexpr int NWG = D == 128 ? 2 : 1;                 // groups of softmax warps
+  static constexpr int NWG = attend_row_tiles(D);              // groups of softmax warps
   static constexpr int TN = attend_tile(D);
-  static constexpr int RT = attend_rows(D);
-  static_assert(RT == 128 * NWG, "a row tile per group");
   static constexpr int PANELS = D / 64;
   static constexpr int QTILE = 128 * D * 2, NQ = D == 128 ? 2 : 1;
   static constexpr int STAGE = TN * D * 2;
@@ -153,13 +151,14 @@ __device__ __forceinline__ int tiles_of(const AttendParams& p, const Segment& g)
   return max(1, (g.hi - first_token(p, g) + attend_tile(D) - 1) / attend_tile(D));
 }
 template <int D>
-__device__ __forceinline__ int row_tiles(const AttendParams& p, const Segment& g) {
-  return (g.n * p.G + attend_rows(D) - 1) / attend_rows(D);
+__device__ __forceinline__ int items_of(const AttendParams& p, const Segment& g) {  // of a KV head
+  const int tokens = p.tile_tokens * attend_row_tiles(D);
+  return (int)(((unsigned)g.n + tokens - 1) / tokens);
 }
 constexpr int kItemCost = 1;  // units of an item beside its tiles
 template <int D>
 __device__ __forceinline__ long long units_of(const AttendParams& p, const Segment& g) {
-  return (long long)row_tiles<D>(p, g) * p.Hkv * (tiles_of<D>(p, g) + kItemCost);
+  return (long long)items_of<D>(p, g) * p.Hkv * (tiles_of<D>(p, g) + kItemCost);
 }
 __device__ __forceinline__ int div_group(const AttendParams& p, int r) {
   return p.G == 1 ? r : (int)__umulhi((uint32_t)r, p.g_magic);
@@ -175,8 +174,7 @@ struct Item {
   int t0;         // first token of the first tile
   int lo, hi;     // the segment's context
   int table, kvh;
-  int tok0;       // the segment's first query token
-  int row0, rows; // the item's rows in the segment
+  int tok, rows;  // its first query token, its rows
   int dest;
 };
 
@@ -204,7 +202,7 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
 template <typename C>
 struct AttendShared {
   uint64_t kv_full[C::NS], kv_empty[C::NS];
-  uint64_t q_full[C::NQ], q_empty[C::NQ];
+  uint64_t q_raw[C::NQ], q_full[C::NQ], q_empty[C::NQ];
   uint64_t s_full[2], p_full[2];
   uint64_t pv_done[2];  // by the step's score buffer
   uint64_t item_full[C::ITEMS], item_empty[C::ITEMS];
@@ -306,10 +304,10 @@ __device__ __forceinline__ void plan_role(const AttendParams& p, AttendShared<C>
   int s = sh.first_segment;
   const int n = segment_count(p);
   long long at = sh.first_unit;
-  bool first = true;
+  bool first = true, split = false;
   while (s < n && at < hi) {
     const Segment g = segment_of(p, s);
-    const int tiles = tiles_of<D>(p, g), rt = row_tiles<D>(p, g), cost = tiles + kItemCost;
+    const int tiles = tiles_of<D>(p, g), rt = items_of<D>(p, g), cost = tiles + kItemCost;
     const int items = rt * p.Hkv;
     int x = first && items > 0 ? (int)((lo - at) / cost) : 0;
     first = false;
@@ -329,13 +327,17 @@ __device__ __forceinline__ void plan_role(const AttendParams& p, AttendShared<C>
         it.hi = g.hi;
         it.table = g.table;
         it.kvh = kvh;
-        it.tok0 = g.tok0;
-        it.row0 = r * C::RT;
-        it.rows = min(C::RT, g.n * p.G - r * C::RT);
+        const int t0 = r * C::NWG * p.tile_tokens;
+        it.tok = g.tok0 + t0;
+        it.rows = min(C::NWG * p.tile_tokens, g.n - t0) * p.G;
         it.dest = ta > 0 ? kSlotNext
                   : tb < tiles ? kSlotFirst
                   : g.partial == 1 ? kRowShared : g.partial == 2 ? kRowOwn : kDirect;
         mbar_arrive(smem_addr(&sh.item_full[slot]));
+        if (it.dest == kSlotFirst) {
+          p.split[blockIdx.x] = SplitItem{it.tok, it.rows, kvh, (int)((u + tiles - 1) / sh.per) - (int)blockIdx.x + 1};
+          split = true;
+        }
       }
       __syncwarp();
       ++count;
@@ -346,6 +348,7 @@ __device__ __forceinline__ void plan_role(const AttendParams& p, AttendShared<C>
   const int slot = count % C::ITEMS;
   PA_WAIT(sh.item_empty[slot], ((count / C::ITEMS) & 1) ^ 1);
   if (lane == 0) {
+    if (!split) p.split[blockIdx.x].pieces = 0;
     sh.items[slot].tiles = 0;
     mbar_arrive(smem_addr(&sh.item_full[slot]));
   }
@@ -365,8 +368,8 @@ __device__ __forceinline__ bool next_item(AttendShared<C>& sh, uint32_t& count, 
 
 // Both softmax groups work on the item's two row tiles, or share the tiles of one.
 template <typename C>
-__device__ __forceinline__ bool two_row_tiles(const Item& it) {
-  return C::NWG == 2 && it.rows > 128;
+__device__ __forceinline__ bool two_row_tiles(const AttendParams& p, const Item& it) {
+  return C::NWG == 2 && it.rows > p.tile_tokens * p.G;
 }
 
 // ------------------------------------------------------------------ load
@@ -375,8 +378,8 @@ __device__ __forceinline__ bool two_row_tiles(const Item& it) {
 // Tiles are staged in this order; place_k and place_v are a tile's place among an item's
 // 2 * tiles.
 template <typename C>
-__device__ __forceinline__ int lead_of(const Item& it) {
-  return two_row_tiles<C>(it) ? 1 : 2;
+__device__ __forceinline__ int lead_of(const AttendParams& p, const Item& it) {
+  return two_row_tiles<C>(p, it) ? 1 : 2;
 }
 __device__ __forceinline__ int place_k(int t, int lead) { return t < lead ? t : 2 * t - lead + 1; }
 __device__ __forceinline__ int place_v(int t, int lead, int tiles) { return min(t + lead, tiles) + t; }
@@ -397,7 +400,7 @@ __device__ __forceinline__ void tensor_load_role(const AttendParams& p, const CU
   Item it;
   while (next_item(sh, count, it)) {
     const int32_t* row = p.block_tables + (size_t)it.table * p.max_blocks;
-    const int lead = lead_of<C>(it);
+    const int lead = lead_of<C>(p, it);
     int tok = it.t0 + lane * p.box;  // the box's first token
     auto holds = [&](int tk) { return lane < boxes && tk < it.hi && tk + p.box > it.lo; };
     auto entry = [&](int t, int tk) -> int { return t < it.tiles && holds(tk) ? __ldg(row + div_block(p, tk)) : 0; };
@@ -443,7 +446,7 @@ __device__ __forceinline__ void staged_load_role(const AttendParams& p, AttendSh
   uint32_t count = 0;
   Item it;
   bool more = next_item(sh, count, it);
-  int lead = more ? lead_of<C>(it) : 0, k = 0, v = 0;  // tiles of K and V issued
+  int lead = more ? lead_of<C>(p, it) : 0, k = 0, v = 0;  // tiles of K and V issued
   uint32_t issued = 0, done = 0;
   // issue the next tile, if there is one
   auto issue = [&]() {
@@ -482,7 +485,7 @@ __device__ __forceinline__ void staged_load_role(const AttendParams& p, AttendSh
       ++issued;
       if (v == it.tiles) {
         more = next_item(sh, count, it);
-        lead = lead_of<C>(it);
+        lead = lead_of<C>(p, it);
         k = v = 0;
       }
     }
@@ -535,35 +538,36 @@ __device__ __forceinline__ void staged_load_role(const AttendParams& p, AttendSh
 }
 
 // ------------------------------------------------------------------ queries
+// A tensor copy per panel brings 128 / G tokens with the G heads of the KV head, token after token
+// (those past the item's rows are other sequences', or zeros behind the last one: rows nobody reads).
+// bf16 queries of an fp8 cache are then rounded to fp16 in place.
 template <typename C, typename T, int D>
-__device__ __forceinline__ void query_role(const AttendParams& p, AttendShared<C>& sh, uint8_t* tiles) {
-  constexpr int CPR = D / 8;  // 16-byte chunks of a row
+__device__ __forceinline__ void query_role(const AttendParams& p, const CUtensorMap* map, AttendShared<C>& sh,
+                                           uint8_t* tiles) {
+  constexpr bool kConvert = !std::is_same_v<T, typename C::TM>;
   const int lane = threadIdx.x & 31;
-  const uint32_t base = smem_addr(tiles);
+  const uint32_t bytes = p.tile_tokens * p.G * D * 2;
   uint32_t count = 0, used = 0;
   Item it;
   while (next_item(sh, count, it)) {
-    for (int first = 0; first < it.rows; first += 128, ++used) {
+    const int n = two_row_tiles<C>(p, it) ? 2 : 1;
+    for (int i = 0; i < n; ++i, ++used) {
       const int slot = used % C::NQ;
-      PA_WAIT(sh.q_empty[slot], ((used / C::NQ) & 1) ^ 1);
-      const int chunks = min(128, it.rows - first) * CPR;
-      const uint32_t tile = base + slot * C::QTILE;
-      auto place = [&](int f) -> uint32_t {
-        const int r = f / CPR, c = f % CPR;
-        return tile + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-      };
+      const uint32_t lap = (used / C::NQ) & 1;
+      PA_WAIT(sh.q_empty[slot], lap ^ 1);
+      uint64_t* const bar = kConvert ? &sh.q_raw[slot] : &sh.q_full[slot];
+      const uint32_t tile = smem_addr(tiles) + slot * C::QTILE;
+      if (lane == 0) mbar_expect(smem_addr(bar), bytes);
+      __syncwarp();
+      if (lane < C::PANELS)
+        tensor_load3(tile + lane * (128 * 128), map, smem_addr(bar), lane * 64, it.kvh * p.G,
+                     it.tok + i * p.tile_tokens);
+      if constexpr (kConvert) {
+        PA_WAIT(*bar, lap);
+        const int rows = p.tile_tokens * p.G;
 #pragma unroll 4
-      for (int f = lane; f < chunks; f += 32) {
-        const int r = it.row0 + first + f / CPR, tok = div_group(p, r);
-        const T* src = static_cast<const T*>(p.q) + (size_t)(it.tok0 + tok) * p.q_stride +
-                       (size_t)(it.kvh * p.G + r - tok * p.G) * D + (f % CPR) * 8;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(place(f)), "l"(src) : "memory");
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if constexpr (!std::is_same_v<T, typename C::TM>) {  // this lane's own chunks, to the products' type
-#pragma unroll 4
-        for (int f = lane; f < chunks; f += 32) {
-          const uint32_t a = place(f);
+        for (int f = lane; f < rows * (D / 8); f += 32) {
+          const uint32_t a = tile + (f / (rows * 8)) * (128 * 128) + (f % (rows * 8)) * 16;
           uint4 x = lds128(a);
           uint32_t* w = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
@@ -574,10 +578,10 @@ __device__ __forceinline__ void query_role(const AttendParams& p, AttendShared<C
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
                        : "memory");
         }
+        async_proxy_fence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.q_full[slot]));
       }
-      async_proxy_fence();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sh.q_full[slot]));
     }
   }
 }
@@ -613,7 +617,7 @@ __device__ __forceinline__ void product_role(const AttendParams& p, AttendShared
   };
   while (next_item(sh, count, it)) {
     const int tiles = __reduce_max_sync(0xffffffffu, it.tiles);
-    const int dup = __any_sync(0xffffffffu, two_row_tiles<C>(it)) ? 1 : 0;
+    const int dup = __any_sync(0xffffffffu, two_row_tiles<C>(p, it)) ? 1 : 0;
     const int steps = tiles << dup;
     const uint32_t q0 = used % C::NQ, q1 = (used + dup) % C::NQ;
     for (int i = 0; i <= dup; ++i) PA_WAIT(sh.q_full[(used + i) % C::NQ], ((used + i) / C::NQ) & 1);
@@ -672,13 +676,14 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
   uint32_t count = 0, used[2] = {0, 0}, pairs = 0, tiles_before = 0;
   Item it;
   while (next_item(sh, count, it)) {
-    const bool two = two_row_tiles<C>(it);
+    const bool two = two_row_tiles<C>(p, it);
     const int dup = two ? 1 : 0, steps = it.tiles << dup;
-    const int r = (two ? group * 128 : 0) + at;  // the item's row of this thread
-    const bool live = r < it.rows;
-    const bool warp_live = r - lane < it.rows;
-    const int seg_row = it.row0 + r, tok = live ? it.tok0 + div_group(p, seg_row) : 0;
-    const int head = it.kvh * p.G + seg_row - div_group(p, seg_row) * p.G;
+    const int tile_rows = p.tile_tokens * p.G;
+    const int r = (two ? group * tile_rows : 0) + at;  // the item's row of this thread
+    const bool live = at < tile_rows && r < it.rows;
+    const bool warp_live = at - lane < tile_rows && r - lane < it.rows;
+    const int tok = live ? it.tok + div_group(p, r) : 0;
+    const int head = it.kvh * p.G + r - div_group(p, r) * p.G;
     int end = it.hi;  // this row sees tokens in [lo, end)
     if (p.shared && live) {
       const int b = tok / p.R;
@@ -775,7 +780,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
         // V rows outside the context hold whatever the cache or an earlier tile left: zeros there,
         // so that weights of 0 meet 0
         if ((t0 < it.lo || t0 + C::TN > it.hi) && !(dup && group)) {
-          const uint32_t n = tiles_before + place_v(t, lead_of<C>(it), it.tiles);
+          const uint32_t n = tiles_before + place_v(t, lead_of<C>(p, it), it.tiles);
           PA_WAIT(sh.kv_full[n % C::NS], (n / C::NS) & 1);
           const uint32_t tile = smem_addr(stages) + (n % C::NS) * C::STAGE;
           for (int row = at; row < C::TN; row += 128)
@@ -858,23 +863,29 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
           if (whole) {
             T* dst = static_cast<T*>(p.out) + row * D + c;
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              uint4 y;
-              uint32_t* w = reinterpret_cast<uint32_t*>(&y);
+            for (int j = 0; j < 32; j += 16) {
+              uint32_t w[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
+              for (int i = 0; i < 8; ++i) {
                 const float a = __uint_as_float(o[j + 2 * i]), b = __uint_as_float(o[j + 2 * i + 1]);
                 w[i] = pack2<T>(sum > 0.f ? a * mul : 0.f, sum > 0.f ? b * mul : 0.f);
               }
-              *reinterpret_cast<uint4*>(dst + j) = y;
+              if (p.out_wide) {
+                store32(dst + j, w);
+              } else {
+                *reinterpret_cast<uint4*>(dst + j) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4*>(dst + j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+              }
             }
           } else {
             float* dst = acc + part * D + c;
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<float4*>(dst + j) =
-                  make_float4(__uint_as_float(o[j]) * mul, __uint_as_float(o[j + 1]) * mul,
-                              __uint_as_float(o[j + 2]) * mul, __uint_as_float(o[j + 3]) * mul);
+            for (int j = 0; j < 32; j += 8) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__uint_as_float(o[j + i]) * mul);
+              store32(dst + j, w);
+            }
           }
         }
       }
@@ -912,6 +923,7 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
     };
     init(sh.kv_full, C::NS, LOAD == kLoadTensor ? 2 : C::NLOAD);
     init(sh.kv_empty, C::NS, 1);
+    init(sh.q_raw, C::NQ, 1);
     init(sh.q_full, C::NQ, 1);
     init(sh.q_empty, C::NQ, 1);
     init(sh.s_full, 2, 1);
@@ -923,6 +935,7 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
     init(&sh.drain, 1, 1);
     sh.give_up = 0;
     mbar_init_fence();
+    tensor_prefetch(&maps.q);
     if constexpr (LOAD == kLoadTensor) {
       tensor_prefetch(&maps.k);
       tensor_prefetch(&maps.v);
@@ -944,7 +957,7 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
   else if (warp == C::W_PLAN)
     plan_role<C, D>(p, sh);
   else if (warp == C::W_Q)
-    query_role<C, T, D>(p, sh, q_tiles);
+    query_role<C, T, D>(p, &maps.q, sh, q_tiles);
   else if constexpr (LOAD == kLoadTensor)
     tensor_load_role<C, D>(p, warp < C::W_LOAD + 2 ? &maps.k : &maps.v, warp < C::W_LOAD + 2,
                            (warp - C::W_LOAD) & 1, sh, stages);
@@ -973,47 +986,93 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
 }
 
 // ------------------------------------------------------------------ merge
-// One warp per output row and head: its pieces weighed by 2^(reference - largest), their sums and
-// outputs added in order.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) merge_rows_kernel(const AttendParams p) {
+// The pieces of a row, weighed by 2^(reference - largest), their sums and outputs added in order; a
+// warp per row. at(i) gives the addresses of piece i's (reference, sum) and output.
+template <typename T, int D, typename At>
+__device__ __forceinline__ void merge_pieces(int n, const At& at, T* out) {
   constexpr int V = D / 32;  // elements of a lane
   const int lane = threadIdx.x & 31;
+  const float2* ml;
+  const float* acc;
+  float top = -INFINITY;
+  for (int i = lane; i < n; i += 32) {
+    at(i, &ml, &acc);
+    top = fmaxf(top, __ldcg(ml).x);
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float sum = 0.f, v[V] = {};
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    at(i, &ml, &acc);
+    const float2 x = __ldcg(ml);
+    const float w = x.x == -INFINITY ? 0.f : exp2_approx(x.x - top);
+    sum += w * x.y;
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(acc + 32 * j + 4 * lane));
+      if (w > 0.f) {  // a piece that saw no token of the row may hold anything
+        v[j] += w * y.x;
+        v[j + 1] += w * y.y;
+        v[j + 2] += w * y.z;
+        v[j + 3] += w * y.w;
+      }
+    }
+  }
+  const float f = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int j = 0; j < V; j += 4) {
+    uint2 y;
+    y.x = pack2<T>(v[j] * f, v[j + 1] * f);
+    y.y = pack2<T>(v[j + 2] * f, v[j + 3] * f);
+    *reinterpret_cast<uint2*>(out + 32 * j + 4 * lane) = y;
+  }
+}
+
+// Rows with one context: grid (CTAs, rows of an item / 8), the item that CTA blockIdx.x begins and
+// others end.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) merge_items_kernel(const AttendParams p) {
+  const int c = blockIdx.x, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  pdl_wait();
+  pdl_launch_dependents();
+  const int4 x = __ldcg(reinterpret_cast<const int4*>(p.split + c));
+  const SplitItem it{x.x, x.y, x.z, x.w};
+  if (it.pieces == 0 || r >= it.rows) return;
+  const int tok = div_group(p, r);
+  merge_pieces<T, D>(
+      it.pieces,
+      [&](int i, const float2** ml, const float** acc) {
+        const size_t k = ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * p.slot_rows + r;
+        *ml = p.slot_ml + k;
+        *acc = p.slot_acc + k * D;
+      },
+      static_cast<T*>(p.out) + ((size_t)(it.tok + tok) * p.Hq + it.kvh * p.G + r - tok * p.G) * D);
+}
+
+// Rows with two contexts, and others: every row finds its pieces.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) merge_rows_kernel(const AttendParams p) {
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   pdl_wait();
   pdl_launch_dependents();
   if (row >= (long long)p.T * p.Hq) return;
   const int tok = (int)(row / p.Hq), head = (int)(row - (long long)tok * p.Hq);
   const int kvh = head / p.G;
-  int b;
-  if (p.starts) {
-    int lo = 0, hi = p.B + 1;  // the last start at or below tok
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(p.starts + mid) <= tok)
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    b = lo - 1;
-    if (b < 0 || b >= p.B || tok >= __ldg(p.starts + b + 1)) return;  // padding
-  } else {
-    b = tok / p.R;
-  }
+  const int b = tok / p.R;
   const long long per = __ldcg(p.plan);
   // the pieces of this row in segment s: CTAs from .. to, its first one's slot differing
   struct Pieces {
     int from, to, r, whole;  // r: the row in the item
   };
   auto pieces_of = [&](int s, const Segment& g) -> Pieces {
-    const int tiles = tiles_of<D>(p, g), rt = row_tiles<D>(p, g);
-    const int r = (tok - g.tok0) * p.G + head - kvh * p.G;
-    const int x = kvh * rt + r / attend_rows(D);
+    const int tiles = tiles_of<D>(p, g), rt = items_of<D>(p, g), tokens = p.tile_tokens * attend_row_tiles(D);
+    const int i = (tok - g.tok0) / tokens, x = kvh * rt + i;
     const long long u = __ldcg(p.plan + 2 + s) + (long long)x * (tiles + kItemCost) + kItemCost;
     Pieces z;
     z.from = (int)(u / per);
     z.to = (int)((u + tiles - 1) / per);
-    z.r = r % attend_rows(D);
+    z.r = (tok - g.tok0 - i * tokens) * p.G + head - kvh * p.G;
     z.whole = z.from == z.to;
     return z;
   };
@@ -1041,43 +1100,7 @@ __global__ void __launch_bounds__(256) merge_rows_kernel(const AttendParams p) {
     *ml = p.slot_ml + k;
     *acc = p.slot_acc + k * D;
   };
-  float top = -INFINITY;
-  for (int i = lane; i < n; i += 32) {
-    const float2* ml;
-    const float* acc;
-    at(i, &ml, &acc);
-    top = fmaxf(top, __ldcg(ml).x);
-  }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float sum = 0.f, v[V] = {};
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float2* ml;
-    const float* acc;
-    at(i, &ml, &acc);
-    const float2 x = __ldcg(ml);
-    const float w = x.x == -INFINITY ? 0.f : exp2_approx(x.x - top);
-    sum += w * x.y;
-#pragma unroll
-    for (int j = 0; j < V; j += 4) {
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(acc + 32 * j + 4 * lane));
-      if (w > 0.f) {  // a piece that saw no token of the row may hold anything
-        v[j] += w * y.x;
-        v[j + 1] += w * y.y;
-        v[j + 2] += w * y.z;
-        v[j + 3] += w * y.w;
-      }
-    }
-  }
-  const float f = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-  for (int j = 0; j < V; j += 4) {
-    uint2 y;
-    y.x = pack2<T>(v[j] * f, v[j + 1] * f);
-    y.y = pack2<T>(v[j + 2] * f, v[j + 3] * f);
-    *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * D + 32 * j + 4 * lane) = y;
-  }
+  merge_pieces<T, D>(n, at, static_cast<T*>(p.out) + row * D);
 }
 
 // ------------------------------------------------------------------ launch
@@ -1108,9 +1131,13 @@ cudaError_t launch_attend_load(const AttendParams& p, const AttendMaps& maps, cu
   cfg.dynamicSmemBytes = C::SMEM;
   e = cudaLaunchKernelEx(&cfg, kern, p, maps);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(((long long)p.T * p.Hq + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
+  if (!p.shared) {
+    cfg.gridDim = dim3(p.ctas, (p.slot_rows + 7) / 8);
+    return cudaLaunchKernelEx(&cfg, merge_items_kernel<T, D>, p);
+  }
+  cfg.gridDim = dim3((unsigned)(((long long)p.T * p.Hq + 7) / 8));
   return cudaLaunchKernelEx(&cfg, merge_rows_kernel<T, D>, p);
 }
 template <typename T, int D>

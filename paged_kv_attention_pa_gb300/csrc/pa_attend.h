@@ -11,6 +11,12 @@ namespace pa {
 // tensor copies, other 16-bit caches and fp8 ones through a staging ring.
 enum AttendLoad { kLoadTensor = 0, kLoad16 = 1, kLoadFp8 = 2 };
 
+// An item whose pieces several CTAs hold.
+struct SplitItem {
+  int tok, rows, kvh;  // first query token, rows (token and head of the group)
+  int pieces;          // 0: none
+};
+
 struct AttendParams {
   const void* q;
   void* out;
@@ -24,16 +30,18 @@ struct AttendParams {
   uint32_t* err;             // device error word
   // workspace (see attend_workspace)
   long long* plan;           // units per CTA, units in all, then the first unit of every segment
+  SplitItem* split;          // [CTAs] the item that begins in a CTA and ends in a later one
   float2* slot_ml;           // [CTAs][2][slot_rows] reference and sum of the pieces of items that
                              // CTAs share: 0 the end of one, 1 the start of the next
   float* slot_acc;           // [CTAs][2][slot_rows][D] their unnormalised outputs
   float2* row_ml;            // [2][T * Hq] the same of whole items whose rows have two contexts
   float* row_acc;            // [2][T * Hq][D]
-  long long q_stride;        // elements between query rows
   int B, N, T, R;            // sequences, groups (cross: 0), query rows, rows per sequence
   int shared;                // pa_decode_shared
   int Hq, Hkv, G;
-  uint32_t g_magic;          // r / G = umulhi(r, g_magic) for r < 2^28, G > 1
+  uint32_t g_magic;          // r / G = umulhi(r, g_magic) for r < 2^16, G > 1
+  int tile_tokens;           // query tokens of a row tile of the tensor cores, 128 / G
+  int out_wide;              // out is 32-byte aligned
   int block_size, num_blocks, max_blocks, cap;
   uint32_t bs_magic;         // t / block_size as in DecodeParams
   int bs_shift;
@@ -44,12 +52,12 @@ struct AttendParams {
   int negate;                // the scale is negative
 };
 
-// Query rows (token and head of a KV head's group) of an item, tokens of a tile.
-__host__ __device__ constexpr int attend_rows(int D) { return D == 128 ? 256 : 128; }
+// Row tiles of an item; tokens of the context in a tile.
+__host__ __device__ constexpr int attend_row_tiles(int D) { return D == 128 ? 2 : 1; }
 __host__ __device__ constexpr int attend_tile(int D) { return D == 128 ? 128 : 64; }
 
 struct AttendMaps {
-  CUtensorMap k, v;
+  CUtensorMap k, v, q;
 };
 
 // One launcher per type and head_dim: the attention grid and the grid that merges its pieces.

@@ -132,6 +132,13 @@ __device__ __forceinline__ void mma_commit(uint32_t on, uint32_t bar) {
       : "memory");
 }
 
+// 32 bytes to global memory (aligned to 32).
+__device__ __forceinline__ void store32(void* at, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // ---------------------------------------------------------------- pairs of fp32
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
