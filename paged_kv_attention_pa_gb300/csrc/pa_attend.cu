@@ -51,7 +51,7 @@ pa_status check_sizes(const Call& c, int* cap) {
 }
 
 struct Layout {
-  size_t plan, split, slot_ml, slot_acc, row_ml, row_acc, total;
+  size_t plan, segments, split, slot_ml, slot_acc, row_ml, row_acc, total;
   int slot_rows;
 };
 // both: rows may have two contexts
@@ -66,7 +66,8 @@ Layout layout_of(const Call& c, int ctas, int segments, bool both) {
     off += align256(bytes);
     return at;
   };
-  w.plan = take((size_t)(2 + (int64_t)segments) * 8);
+  w.plan = take(2 * 8);
+  w.segments = take(both ? (size_t)segments * sizeof(SegmentRecord) : 0);
   w.split = take((size_t)ctas * sizeof(SplitItem));
   w.slot_ml = take(slots * 8);
   w.slot_acc = take(slots * c.D * 4);
@@ -127,6 +128,7 @@ pa_status run(const Call& c, AttendParams& p, int cap, void* workspace, size_t b
   p.seq_lens = c.seq_lens;
   p.err = reinterpret_cast<uint32_t*>(ws);
   p.plan = reinterpret_cast<long long*>(ws + w.plan);
+  p.segments = reinterpret_cast<SegmentRecord*>(ws + w.segments);
   p.split = reinterpret_cast<SplitItem*>(ws + w.split);
   p.slot_ml = reinterpret_cast<float2*>(ws + w.slot_ml);
   p.slot_acc = reinterpret_cast<float*>(ws + w.slot_acc);

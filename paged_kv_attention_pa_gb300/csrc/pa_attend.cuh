@@ -7,12 +7,13 @@
 // of the group) pairs, whole tokens to a row tile of at most 128, cut into items of two row tiles at
 // head_dim 128 and of one at 256.
 //
-// Division of the work. An item of n token tiles counts n + 1 units (the start and end of an item
-// cost about one tile). Every CTA, one per SM, takes an equal run of the units of all items in
-// order, found from the lengths on the device: runs begin and end inside items, and the pieces of
-// an item that several CTAs hold, as well as the two contexts of a row with a shared prefix, leave
-// (reference, sum, unnormalised output) in the workspace, which a second grid joins. The
-// division depends on the sizes alone, so repeated calls give the same bits.
+// Division of the work. An item's time is taken as a number of units: 5, and for every token tile 2,
+// or 3 with two row tiles (GB300, by a fit over the CTAs of eight calls: 2.1 to 4.3 us an item, 0.9 to
+// 1.2 us a tile of one row tile, 1.6 to 1.9 us of two). Every CTA, one per SM, takes an equal run of
+// the units of all items in order, found from the lengths on the device: runs begin and end inside
+// items, and the pieces of an item that several CTAs hold, as well as the two contexts of a row with
+// a shared prefix, leave (reference, sum, unnormalised output) in the workspace, which a second grid
+// joins. The division depends on the sizes alone, so repeated calls give the same bits.
 //
 // Roles of the warps of a CTA:
 //   softmax   one or two groups of four warps, a thread per row
@@ -85,86 +86,108 @@ struct Segment {
   int lo, hi;     // its context
   int table;      // row of the block tables
   int partial;    // 0: the rows' only context; 1, 2: the shared, the own part of two
+  int group;      // partial == 2: whose prefix
+};
+// Sequences [first, end) share their first `tokens` tokens: none in a group of one.
+struct Group {
+  int first, end, tokens;
 };
 
 __device__ __forceinline__ int clamp_len(const AttendParams& p, int b) {
   const int L = __ldg(p.seq_lens + b);
   return L < 0 ? 0 : min(L, p.cap);
 }
-// The group that sequence b is in: the last n with groups[n] <= b, -1 for none.
-__device__ __forceinline__ int group_of(const AttendParams& p, int b) {
-  if (p.N == 0) return -1;
-  int lo = 0, hi = p.N + 1;  // the answer + 1 is in [lo, hi]
+__device__ __forceinline__ Group read_group(const AttendParams& p, int n) {
+  Group g;
+  const int a = __ldg(p.groups + n), b = __ldg(p.groups + n + 1), x = __ldg(p.prefix + n);
+  g.first = min(max(a, 0), p.B);
+  g.end = min(max(b, g.first), p.B);
+  g.tokens = g.end - g.first < 2 ? 0 : max(0, min(x, clamp_len(p, g.first)));
+  return g;
+}
+// The group that sequence b is in: the last n of [0, N) that begins at or before it, -1 for none.
+template <typename Begin>
+__device__ __forceinline__ int group_of(const AttendParams& p, int b, const Begin& begin) {
+  int lo = 0, hi = p.N;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(p.groups + mid) <= b)
+    if (begin(mid) <= b)
       lo = mid + 1;
     else
       hi = mid;
   }
-  const int n = lo - 1;
-  return n >= 0 && n < p.N && b < __ldg(p.groups + n + 1) ? n : -1;
-}
-// Tokens that group n shares: none in a group of one sequence.
-__device__ __forceinline__ int shared_tokens(const AttendParams& p, int n, int* first, int* end) {
-  const int g0 = min(max(__ldg(p.groups + n), 0), p.B), g1 = min(max(__ldg(p.groups + n + 1), g0), p.B);
-  *first = g0;
-  *end = g1;
-  if (g1 - g0 < 2) return 0;
-  return max(0, min(__ldg(p.prefix + n), clamp_len(p, g0)));
+  return lo - 1;
 }
 __device__ __forceinline__ int segment_count(const AttendParams& p) { return p.N + p.B; }
-__device__ __forceinline__ Segment segment_of(const AttendParams& p, int s) {
-  Segment g{};
-  if (s < p.N) {
-    int a, b;
-    g.hi = shared_tokens(p, s, &a, &b);
-    g.tok0 = a * p.R;
-    g.n = g.hi > 0 ? (b - a) * p.R : 0;
-    g.table = a;
-    g.partial = 1;
-    return g;
-  }
-  const int b = s - p.N;
-  g.table = b;
-  g.hi = clamp_len(p, b);
-  if (p.starts) {
-    g.tok0 = min(max(__ldg(p.starts + b), 0), p.T);
-    g.n = min(max(__ldg(p.starts + b + 1), g.tok0), p.T) - g.tok0;
-  } else {
-    g.tok0 = b * p.R;
-    g.n = p.R;
-  }
-  if (p.shared) {
-    const int n = group_of(p, b);
-    int a, e;
-    if (n >= 0) g.lo = shared_tokens(p, n, &a, &e);
-    g.partial = g.lo > 0 ? 2 : 0;
-  }
-  return g;
+__device__ __forceinline__ Segment prefix_segment(const AttendParams& p, const Group& g) {
+  Segment s{};
+  s.hi = g.tokens;
+  s.tok0 = g.first * p.R;
+  s.n = g.tokens > 0 ? (g.end - g.first) * p.R : 0;
+  s.table = g.first;
+  s.partial = 1;
+  return s;
 }
-// Where its tiles start (tensor copies start at a multiple of the box), how many there are (one,
-// without a token, for an empty context), items and units.
+// n, g: the group that begins at or before sequence b (n = -1: none)
+__device__ __forceinline__ Segment own_segment(const AttendParams& p, int b, int n, const Group& g) {
+  Segment s{};
+  s.table = b;
+  s.hi = clamp_len(p, b);
+  if (p.starts) {
+    s.tok0 = min(max(__ldg(p.starts + b), 0), p.T);
+    s.n = min(max(__ldg(p.starts + b + 1), s.tok0), p.T) - s.tok0;
+  } else {
+    s.tok0 = b * p.R;
+    s.n = p.R;
+  }
+  if (n >= 0 && b >= g.first && b < g.end && g.tokens > 0) {
+    s.lo = g.tokens;
+    s.partial = 2;
+    s.group = n;
+  }
+  return s;
+}
+
+// A segment's items and units. Its tiles start at a multiple of a tensor copy's box; an empty
+// context has one tile without a token. A KV head's items are equal but for the last.
+constexpr int kItemUnits = 5;
+// A CTA's run is at least two tiles, one for each softmax group. (With less than a tile's units a
+// CTA amid an item's pieces could hold none of it.)
+constexpr int kLeastUnits = 4;
+__host__ __device__ constexpr int tile_units(int row_tiles) { return row_tiles == 2 ? 3 : 2; }
+struct Shape {
+  int tiles, items;   // of an item, of a KV head
+  int full, last;     // units of a tile
+  long long head;     // units of a KV head
+};
 __device__ __forceinline__ int first_token(const AttendParams& p, const Segment& g) { return g.lo & -p.box; }
 template <int D>
 __device__ __forceinline__ int tiles_of(const AttendParams& p, const Segment& g) {
   return max(1, (g.hi - first_token(p, g) + attend_tile(D) - 1) / attend_tile(D));
 }
 template <int D>
-__device__ __forceinline__ int items_of(const AttendParams& p, const Segment& g) {  // of a KV head
-  const int tokens = p.tile_tokens * attend_row_tiles(D);
-  return (int)(((unsigned)g.n + tokens - 1) / tokens);
+__device__ __forceinline__ Shape shape_of(const AttendParams& p, int tiles, int n) {
+  Shape z;
+  const unsigned tokens = p.tile_tokens * attend_row_tiles(D);
+  z.tiles = tiles;
+  z.items = (int)(((unsigned)n + tokens - 1) / tokens);
+  z.full = tile_units(attend_row_tiles(D));
+  z.last = n - (z.items - 1) * (int)tokens > p.tile_tokens ? z.full : tile_units(1);
+  z.head = z.items == 0 ? 0 : (long long)z.items * kItemUnits + ((long long)(z.items - 1) * z.full + z.last) * tiles;
+  return z;
 }
-constexpr int kItemCost = 1;  // units of an item beside its tiles
-template <int D>
-__device__ __forceinline__ long long units_of(const AttendParams& p, const Segment& g) {
-  return (long long)items_of<D>(p, g) * p.Hkv * (tiles_of<D>(p, g) + kItemCost);
+// First unit of an item's first tile, in its segment.
+__device__ __forceinline__ long long units_before(const Shape& z, int kvh, int item) {
+  return kvh * z.head + (long long)item * (kItemUnits + z.full * z.tiles) + kItemUnits;
 }
 __device__ __forceinline__ int div_group(const AttendParams& p, int r) {
   return p.G == 1 ? r : (int)__umulhi((uint32_t)r, p.g_magic);
 }
 __device__ __forceinline__ int div_block(const AttendParams& p, int t) {
   return p.bs_magic == 0 ? t >> p.bs_shift : (int)(__umulhi((uint32_t)t, p.bs_magic) >> p.bs_shift);
+}
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (a | b) >> 32 == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // A piece of an item: the tiles of it that a CTA computes.
@@ -175,6 +198,7 @@ struct Item {
   int lo, hi;     // the segment's context
   int table, kvh;
   int tok, rows;  // its first query token, its rows
+  int of_prefix;  // rows of several sequences
   int dest;
 };
 
@@ -222,16 +246,39 @@ struct AttendShared {
 
 // ------------------------------------------------------------------ plan
 // Every CTA finds the first unit of its run: a sum over the segments' units. CTA 0 writes what the
-// merge reads and reports lengths and groups that are out of range.
+// merge reads and reports lengths, groups and starts that are out of range. `groups`: room for
+// kGroupTable groups in shared memory; with more they are read from global memory as needed.
+constexpr int kGroupTable = 8192;
 template <typename C, int D>
-__device__ __forceinline__ void plan_work(const AttendParams& p, AttendShared<C>& sh) {
+__device__ __forceinline__ void plan_work(const AttendParams& p, AttendShared<C>& sh, Group* groups) {
+  static_assert(kGroupTable * sizeof(Group) <= C::NS * C::STAGE, "groups in the ring's memory");
   const int n = segment_count(p), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool report = blockIdx.x == 0, table = p.N <= kGroupTable;
+  if (table && p.N > 0) {
+    for (int i = tid; i < p.N; i += C::THREADS) groups[i] = read_group(p, i);
+    __syncthreads();
+  }
+  auto group_at = [&](int i) { return table ? groups[i] : read_group(p, i); };
+  auto segment_of = [&](int s) -> Segment {
+    if (s < p.N) return prefix_segment(p, group_at(s));
+    const int b = s - p.N;
+    int g = -1;
+    if (p.N > 0)
+      g = table ? group_of(p, b, [&](int i) { return groups[i].first; })
+                : group_of(p, b, [&](int i) { return __ldg(p.groups + i); });
+    return own_segment(p, b, g, g >= 0 ? group_at(g) : Group{});
+  };
+  auto shape = [&](const Segment& g) { return shape_of<D>(p, tiles_of<D>(p, g), g.n); };
   const int each = (n + C::THREADS - 1) / C::THREADS;
   const int s0 = min(n, tid * each), s1 = min(n, s0 + each);
   long long mine = 0;
+  Segment only{};  // with one segment a thread, it
+  long long only_units = 0;
   for (int s = s0; s < s1; ++s) {
-    mine += units_of<D>(p, segment_of(p, s));
-    if (blockIdx.x == 0) {
+    only = segment_of(s);
+    only_units = shape(only).head * p.Hkv;
+    mine += only_units;
+    if (report) {
       uint32_t bad = 0;
       if (s < p.N) {
         const int a = __ldg(p.groups + s), b = __ldg(p.groups + s + 1), x = __ldg(p.prefix + s);
@@ -263,34 +310,37 @@ __device__ __forceinline__ void plan_work(const AttendParams& p, AttendShared<C>
     if (w < warp) upto += x;
     total += x;
   }
-  const long long per = (total + p.ctas - 1) / p.ctas;
+  const long long per = max((long long)kLeastUnits, quotient(total + p.ctas - 1, p.ctas));
   const long long from = per * blockIdx.x;
-  long long at = upto - mine;
   if (tid == 0) {
     sh.per = per;
     sh.total = total;
     if (from >= total) sh.first_segment = n;
-  }
-  if (from >= at && from < upto) {
-    for (int s = s0; s < s1; ++s) {
-      const long long u = units_of<D>(p, segment_of(p, s));
-      if (from < at + u) {
-        sh.first_segment = s;
-        sh.first_unit = at;
-        break;
-      }
-      at += u;
-    }
-    at = upto - mine;
-  }
-  if (blockIdx.x == 0) {
-    if (tid == 0) {
+    if (report) {
       p.plan[0] = per;
       p.plan[1] = total;
     }
+  }
+  long long at = upto - mine;
+  const bool here = from >= at && from < upto, write = report && p.shared;
+  if (here || write) {
     for (int s = s0; s < s1; ++s) {
-      p.plan[2 + s] = at;
-      at += units_of<D>(p, segment_of(p, s));
+      const Segment g = each == 1 ? only : segment_of(s);
+      const long long u = each == 1 ? only_units : shape(g).head * p.Hkv;
+      if (from >= at && from < at + u) {
+        sh.first_segment = s;
+        sh.first_unit = at;
+      }
+      if (write) {
+        SegmentRecord r{};
+        r.first = at;
+        r.tiles = tiles_of<D>(p, g);
+        r.tok0 = g.tok0;
+        r.n = g.n;
+        r.group = g.partial == 2 ? g.group : -1;
+        p.segments[s] = r;
+      }
+      at += u;
     }
   }
 }
@@ -301,49 +351,69 @@ __device__ __forceinline__ void plan_role(const AttendParams& p, AttendShared<C>
   const int lane = threadIdx.x & 31;
   const long long lo = sh.per * blockIdx.x, hi = min(lo + sh.per, sh.total);
   uint32_t count = 0;
-  int s = sh.first_segment;
   const int n = segment_count(p);
   long long at = sh.first_unit;
   bool first = true, split = false;
-  while (s < n && at < hi) {
-    const Segment g = segment_of(p, s);
-    const int tiles = tiles_of<D>(p, g), rt = items_of<D>(p, g), cost = tiles + kItemCost;
-    const int items = rt * p.Hkv;
-    int x = first && items > 0 ? (int)((lo - at) / cost) : 0;
-    first = false;
-    for (; x < items; ++x) {
-      const long long u = at + (long long)x * cost + kItemCost;  // the unit of the first tile
-      if (u - kItemCost >= hi) break;
-      const int ta = (int)max(0ll, lo - u), tb = (int)min((long long)tiles, hi - u);
-      if (ta >= tb) continue;
-      const int slot = count % C::ITEMS;
-      PA_WAIT(sh.item_empty[slot], ((count / C::ITEMS) & 1) ^ 1);
-      if (lane == 0) {
-        Item& it = sh.items[slot];
-        const int kvh = x / rt, r = x - kvh * rt;
-        it.tiles = tb - ta;
-        it.t0 = first_token(p, g) + ta * C::TN;
-        it.lo = g.lo;
-        it.hi = g.hi;
-        it.table = g.table;
-        it.kvh = kvh;
-        const int t0 = r * C::NWG * p.tile_tokens;
-        it.tok = g.tok0 + t0;
-        it.rows = min(C::NWG * p.tile_tokens, g.n - t0) * p.G;
-        it.dest = ta > 0 ? kSlotNext
-                  : tb < tiles ? kSlotFirst
-                  : g.partial == 1 ? kRowShared : g.partial == 2 ? kRowOwn : kDirect;
-        mbar_arrive(smem_addr(&sh.item_full[slot]));
-        if (it.dest == kSlotFirst) {
-          p.split[blockIdx.x] = SplitItem{it.tok, it.rows, kvh, (int)((u + tiles - 1) / sh.per) - (int)blockIdx.x + 1};
-          split = true;
-        }
+  int held = -2;  // the group read last
+  Group group{};
+  for (int s = sh.first_segment; s < n && at < hi; ++s) {
+    Segment g;
+    if (s < p.N) {
+      g = prefix_segment(p, read_group(p, s));
+    } else {
+      const int b = s - p.N;
+      if (held == -2 || b >= group.end) {  // sequences ascend
+        held = p.N > 0 ? group_of(p, b, [&](int i) { return __ldg(p.groups + i); }) : -1;
+        group = held >= 0 ? read_group(p, held) : Group{};
       }
-      __syncwarp();
-      ++count;
+      g = own_segment(p, b, held, group);
     }
-    at += (long long)items * cost;
-    ++s;
+    const Shape z = shape_of<D>(p, tiles_of<D>(p, g), g.n);
+    int kvh = 0, r = 0;
+    if (first && z.items > 0) {  // the item that holds unit lo
+      kvh = (int)quotient(lo - at, z.head);
+      r = (int)min((long long)z.items - 1, quotient(lo - at - kvh * z.head, kItemUnits + z.full * z.tiles));
+    }
+    first = false;
+    for (; kvh < p.Hkv && z.items > 0; ++kvh, r = 0) {
+      for (; r < z.items; ++r) {
+        const long long u = at + units_before(z, kvh, r);
+        if (u - kItemUnits >= hi) break;
+        // tile t, from unit u + w t on, is the CTA's whose run holds that unit
+        const int w = r == z.items - 1 ? z.last : z.full;
+        const int ta = u >= lo ? 0 : (int)quotient(lo - u + w - 1, w);
+        const int tb = hi <= u ? 0 : (int)min((long long)z.tiles, quotient(hi - u + w - 1, w));
+        if (ta >= tb) continue;
+        const int slot = count % C::ITEMS;
+        PA_WAIT(sh.item_empty[slot], ((count / C::ITEMS) & 1) ^ 1);
+        if (lane == 0) {
+          Item& it = sh.items[slot];
+          it.tiles = tb - ta;
+          it.t0 = first_token(p, g) + ta * C::TN;
+          it.lo = g.lo;
+          it.hi = g.hi;
+          it.table = g.table;
+          it.kvh = kvh;
+          const int t0 = r * C::NWG * p.tile_tokens;
+          it.tok = g.tok0 + t0;
+          it.rows = min(C::NWG * p.tile_tokens, g.n - t0) * p.G;
+          it.of_prefix = g.partial == 1;
+          it.dest = ta > 0 ? kSlotNext
+                    : tb < z.tiles ? kSlotFirst
+                    : g.partial == 1 ? kRowShared : g.partial == 2 ? kRowOwn : kDirect;
+          mbar_arrive(smem_addr(&sh.item_full[slot]));
+          if (it.dest == kSlotFirst) {
+            const long long last = min((long long)p.ctas - 1, quotient(u + (long long)w * (z.tiles - 1), sh.per));
+            p.split[blockIdx.x] = SplitItem{it.tok, it.rows, kvh, (int)last - (int)blockIdx.x + 1};
+            split = true;
+          }
+        }
+        __syncwarp();
+        ++count;
+      }
+      if (at + (kvh + 1) * z.head >= hi) break;
+    }
+    at += z.head * p.Hkv;
   }
   const int slot = count % C::ITEMS;
   PA_WAIT(sh.item_empty[slot], ((count / C::ITEMS) & 1) ^ 1);
@@ -448,6 +518,15 @@ __device__ __forceinline__ void staged_load_role(const AttendParams& p, AttendSh
   bool more = next_item(sh, count, it);
   int lead = more ? lead_of<C>(p, it) : 0, k = 0, v = 0;  // tiles of K and V issued
   uint32_t issued = 0, done = 0;
+  // lane l resolves row l of its warp; V of a tile has the rows of its K, at most two tiles before
+  auto entry = [&](int t) -> int {
+    const int tok = it.t0 + t * C::TN + warp * RW + lane;
+    return t < it.tiles && lane < RW && tok >= it.lo && tok < it.hi
+               ? __ldg(p.block_tables + (size_t)it.table * p.max_blocks + div_block(p, tok))
+               : 0;
+  };
+  int phys = more ? entry(0) : 0;  // of the next K tile
+  uint32_t even = 0, odd = 0;      // rows of K tiles
   // issue the next tile, if there is one
   auto issue = [&]() {
     if (more) {
@@ -455,19 +534,21 @@ __device__ __forceinline__ void staged_load_role(const AttendParams& p, AttendSh
       const int t = is_k ? k++ : v++;
       const int t0 = it.t0 + t * C::TN;
       const uint8_t* cache = static_cast<const uint8_t*>(is_k ? p.k_cache : p.v_cache);
-      const int tok = t0 + warp * RW + lane;
-      const bool live = lane < RW && tok >= it.lo && tok < it.hi;
-      uint32_t ridx = 0;
-      if (live) {
-        const int blk = div_block(p, tok);
-        int phys = __ldg(p.block_tables + (size_t)it.table * p.max_blocks + blk);
+      if (is_k) {
         if ((unsigned)phys >= (unsigned)p.num_blocks) {
           atomicOr(p.err, PA_DEVERR_BLOCK_INDEX);
           phys = 0;
         }
-        ridx = ((uint32_t)phys * (uint32_t)p.block_size + (uint32_t)(tok - blk * p.block_size)) * (uint32_t)p.Hkv +
-               (uint32_t)it.kvh;
+        const int tok = t0 + warp * RW + lane, slot = tok - div_block(p, tok) * p.block_size;
+        const uint32_t row =
+            ((uint32_t)phys * (uint32_t)p.block_size + (uint32_t)slot) * (uint32_t)p.Hkv + (uint32_t)it.kvh;
+        if (t & 1)
+          odd = row;
+        else
+          even = row;
+        phys = entry(t + 1);
       }
+      const uint32_t ridx = t & 1 ? odd : even;
       const int c0 = max(0, min(C::TN, it.lo - t0)), c1 = max(0, min(C::TN, it.hi - t0));
       const int slot = issued % C::NR;
       if (lane == 0) sh.staged[slot][warp] = make_int2(c0, c1);
@@ -487,6 +568,7 @@ __device__ __forceinline__ void staged_load_role(const AttendParams& p, AttendSh
         more = next_item(sh, count, it);
         lead = lead_of<C>(p, it);
         k = v = 0;
+        phys = more ? entry(0) : 0;
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -503,10 +585,14 @@ __device__ __forceinline__ void staged_load_role(const AttendParams& p, AttendSh
     if (!wait_for(smem_addr(&sh.kv_empty[stage]), ((done / C::NS) & 1) ^ 1, &sh.give_up)) break;
     const uint32_t src = raw_lane + slot * C::RAW;
     const uint32_t tile = smem_addr(stages) + stage * C::STAGE;
+    uint4 chunk[CH < 8 ? CH : 8];  // eight loads in flight
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
+      if (i % 8 == 0)
+#pragma unroll
+        for (int j = 0; j < 8 && i + j < CH; ++j) chunk[j] = lds128(src + (i + j) * 512);
       const int f = i * 32 + lane, r = warp * RW + f / CPR, c = f % CPR;
-      uint4 x = lds128(src + i * 512);
+      uint4 x = chunk[i % 8];
       if (r < rows.x || r >= rows.y) x = make_uint4(0u, 0u, 0u, 0u);
       auto put = [&](int chunk, const uint4& y) {  // chunk: 8 elements of the row
         const uint32_t a = tile + (chunk >> 3) * (C::TN * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
@@ -685,9 +771,10 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
     const int tok = live ? it.tok + div_group(p, r) : 0;
     const int head = it.kvh * p.G + r - div_group(p, r) * p.G;
     int end = it.hi;  // this row sees tokens in [lo, end)
-    if (p.shared && live) {
-      const int b = tok / p.R;
-      end = min(end, clamp_len(p, b) - p.R + 1 + (tok - b * p.R));
+    if (p.shared && live) {  // causal among the new rows
+      const int b = p.R == 1 ? tok : tok / p.R;
+      const int L = it.of_prefix ? clamp_len(p, b) : it.hi;  // the end of its own segment
+      end = min(end, L - p.R + 1 + (tok - b * p.R));
     }
     if (!live) end = it.lo;
     float ref = -INFINITY, sum = 0.f;
@@ -945,7 +1032,7 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
   tc_fence_before();
   // inputs may come from the kernel before in the stream
   pdl_wait();
-  plan_work<C, D>(p, sh);
+  plan_work<C, D>(p, sh, reinterpret_cast<Group*>(stages));
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
@@ -994,28 +1081,42 @@ __device__ __forceinline__ void merge_pieces(int n, const At& at, T* out) {
   const int lane = threadIdx.x & 31;
   const float2* ml;
   const float* acc;
-  float top = -INFINITY;
-  for (int i = lane; i < n; i += 32) {
-    at(i, &ml, &acc);
-    top = fmaxf(top, __ldcg(ml).x);
-  }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float sum = 0.f, v[V] = {};
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    at(i, &ml, &acc);
-    const float2 x = __ldcg(ml);
-    const float w = x.x == -INFINITY ? 0.f : exp2_approx(x.x - top);
-    sum += w * x.y;
+  float top = -INFINITY;
+  // kBatch pieces at a time, their states and outputs in one round trip
+  constexpr int kBatch = D == 128 ? 8 : 4;
+  for (int first = 0; first < n; first += kBatch) {
+    float2 x[kBatch];
+    float4 y[kBatch][V / 4];
+    float most = top;
 #pragma unroll
-    for (int j = 0; j < V; j += 4) {
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(acc + 32 * j + 4 * lane));
-      if (w > 0.f) {  // a piece that saw no token of the row may hold anything
-        v[j] += w * y.x;
-        v[j + 1] += w * y.y;
-        v[j + 2] += w * y.z;
-        v[j + 3] += w * y.w;
+    for (int i = 0; i < kBatch; ++i) {
+      x[i] = make_float2(-INFINITY, 0.f);
+      if (first + i < n) {
+        at(first + i, &ml, &acc);
+        x[i] = __ldcg(ml);
+#pragma unroll
+        for (int j = 0; j < V / 4; ++j) y[i][j] = __ldcg(reinterpret_cast<const float4*>(acc + 128 * j + 4 * lane));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) most = fmaxf(most, x[i].x);
+    const float f = top == -INFINITY ? 0.f : exp2_approx(top - most);
+    top = most;
+    sum *= f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] *= f;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (x[i].x == -INFINITY) continue;  // none, or it saw no token of the row: its output may be anything
+      const float w = exp2_approx(x[i].x - top);
+      sum += w * x[i].y;
+#pragma unroll
+      for (int j = 0; j < V / 4; ++j) {
+        v[4 * j] += w * y[i][j].x;
+        v[4 * j + 1] += w * y[i][j].y;
+        v[4 * j + 2] += w * y[i][j].z;
+        v[4 * j + 3] += w * y[i][j].w;
       }
     }
   }
@@ -1058,49 +1159,53 @@ __global__ void __launch_bounds__(256) merge_rows_kernel(const AttendParams p) {
   pdl_launch_dependents();
   if (row >= (long long)p.T * p.Hq) return;
   const int tok = (int)(row / p.Hq), head = (int)(row - (long long)tok * p.Hq);
-  const int kvh = head / p.G;
-  const int b = tok / p.R;
+  const int kvh = head / p.G, b = p.R == 1 ? tok : tok / p.R;
+  auto record = [&](int s) -> SegmentRecord {
+    union {
+      int4 x[2];
+      SegmentRecord r;
+    } y;
+    y.x[0] = __ldcg(reinterpret_cast<const int4*>(p.segments + s));
+    y.x[1] = __ldcg(reinterpret_cast<const int4*>(p.segments + s) + 1);
+    return y.r;
+  };
   const long long per = __ldcg(p.plan);
-  // the pieces of this row in segment s: CTAs from .. to, its first one's slot differing
+  const SegmentRecord own = record(p.N + b);
+  // the pieces of this row in a segment: CTAs from .. to
   struct Pieces {
-    int from, to, r, whole;  // r: the row in the item
+    int from, to, r;  // r: the row in the item
   };
-  auto pieces_of = [&](int s, const Segment& g) -> Pieces {
-    const int tiles = tiles_of<D>(p, g), rt = items_of<D>(p, g), tokens = p.tile_tokens * attend_row_tiles(D);
-    const int i = (tok - g.tok0) / tokens, x = kvh * rt + i;
-    const long long u = __ldcg(p.plan + 2 + s) + (long long)x * (tiles + kItemCost) + kItemCost;
-    Pieces z;
-    z.from = (int)(u / per);
-    z.to = (int)((u + tiles - 1) / per);
-    z.r = (tok - g.tok0 - i * tokens) * p.G + head - kvh * p.G;
-    z.whole = z.from == z.to;
-    return z;
+  auto pieces_of = [&](const SegmentRecord& g) -> Pieces {
+    const Shape z = shape_of<D>(p, g.tiles, g.n);
+    const int tokens = p.tile_tokens * attend_row_tiles(D), i = (tok - g.tok0) / tokens;
+    const long long u = g.first + units_before(z, kvh, i);
+    Pieces y;
+    y.from = (int)quotient(u, per);
+    y.to = (int)quotient(u + (long long)(i == z.items - 1 ? z.last : z.full) * (z.tiles - 1), per);
+    y.r = (tok - g.tok0 - i * tokens) * p.G + head - kvh * p.G;
+    return y;
   };
-  const Segment own = segment_of(p, p.N + b);
-  const Pieces po = pieces_of(p.N + b, own);
-  if (own.partial == 0 && po.whole) return;  // written by the attention grid
-  Pieces ps{0, -1, 0, 0};
-  if (own.partial) {
-    const int n = group_of(p, b);
-    ps = pieces_of(n, segment_of(p, n));
-  }
+  const Pieces po = pieces_of(own);
+  if (own.group < 0 && po.from == po.to) return;  // written by the attention grid
+  Pieces ps{0, -1, 0};
+  if (own.group >= 0) ps = pieces_of(record(own.group));
   const int n_shared = ps.to - ps.from + 1, n = n_shared + po.to - po.from + 1;
-  auto at = [&](int i, const float2** ml, const float** acc) {
-    const bool mine = i >= n_shared;
-    const Pieces& z = mine ? po : ps;
-    size_t k;
-    if (z.whole) {
-      k = (mine ? (size_t)p.T * p.Hq : 0) + row;
-      *ml = p.row_ml + k;
-      *acc = p.row_acc + k * D;
-      return;
-    }
-    const int c = z.from + (mine ? i - n_shared : i);
-    k = ((size_t)c * 2 + (c == z.from ? 1 : 0)) * p.slot_rows + z.r;
-    *ml = p.slot_ml + k;
-    *acc = p.slot_acc + k * D;
-  };
-  merge_pieces<T, D>(n, at, static_cast<T*>(p.out) + row * D);
+  merge_pieces<T, D>(
+      n,
+      [&](int i, const float2** ml, const float** acc) {
+        const bool mine = i >= n_shared;
+        const int from = mine ? po.from : ps.from, c = mine ? from + i - n_shared : from + i;
+        if (from == (mine ? po.to : ps.to)) {  // a whole item
+          const size_t k = (mine ? (size_t)p.T * p.Hq : 0) + row;
+          *ml = p.row_ml + k;
+          *acc = p.row_acc + k * D;
+        } else {
+          const size_t k = ((size_t)c * 2 + (c == from ? 1 : 0)) * p.slot_rows + (mine ? po.r : ps.r);
+          *ml = p.slot_ml + k;
+          *acc = p.slot_acc + k * D;
+        }
+      },
+      static_cast<T*>(p.out) + row * D);
 }
 
 // ------------------------------------------------------------------ launch

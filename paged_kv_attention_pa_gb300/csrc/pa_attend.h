@@ -11,6 +11,13 @@ namespace pa {
 // tensor copies, other 16-bit caches and fp8 ones through a staging ring.
 enum AttendLoad { kLoadTensor = 0, kLoad16 = 1, kLoadFp8 = 2 };
 
+// What the merge of rows with two contexts needs of a segment (see pa_attend.cuh).
+struct SegmentRecord {
+  long long first;     // its first unit
+  int tiles, tok0, n;  // of its context; its query tokens
+  int group;           // own segments: the group whose prefix the sequence shares, -1 for none
+  int pad[2];
+};
 // An item whose pieces several CTAs hold.
 struct SplitItem {
   int tok, rows, kvh;  // first query token, rows (token and head of the group)
@@ -29,7 +36,8 @@ struct AttendParams {
   const int32_t* prefix;     // [N]
   uint32_t* err;             // device error word
   // workspace (see attend_workspace)
-  long long* plan;           // units per CTA, units in all, then the first unit of every segment
+  long long* plan;           // units per CTA, units in all
+  SegmentRecord* segments;
   SplitItem* split;          // [CTAs] the item that begins in a CTA and ends in a later one
   float2* slot_ml;           // [CTAs][2][slot_rows] reference and sum of the pieces of items that
                              // CTAs share: 0 the end of one, 1 the start of the next
