@@ -1074,81 +1074,113 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
 
 // ------------------------------------------------------------------ merge
 // The pieces of a row, weighed by 2^(reference - largest), their sums and outputs added in order; a
-// warp per row. at(i) gives the addresses of piece i's (reference, sum) and output.
-template <typename T, int D, typename At>
-__device__ __forceinline__ void merge_pieces(int n, const At& at, T* out) {
-  constexpr int V = D / 32;  // elements of a lane
-  const int lane = threadIdx.x & 31;
-  const float2* ml;
-  const float* acc;
-  float sum = 0.f, v[V] = {};
-  float top = -INFINITY;
-  // kBatch pieces at a time, their states and outputs in one round trip
-  constexpr int kBatch = D == 128 ? 8 : 4;
-  for (int first = 0; first < n; first += kBatch) {
-    float2 x[kBatch];
-    float4 y[kBatch][V / 4];
-    float most = top;
+// warp per row. at(i) gives the addresses of piece i's (reference, sum) and output. BATCH pieces at
+// a time, their states and outputs in one round trip.
+template <int D>
+struct Merged {
+  static constexpr int V = D / 128;  // 16-byte vectors of a lane
+  float top = -INFINITY, sum = 0.f;
+  float4 v[V];
+  __device__ Merged() {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int j = 0; j < V; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  template <int BATCH, typename At>
+  __device__ __forceinline__ void load(float2 (&x)[BATCH], float4 (&y)[BATCH][V], int first, int n, const At& at) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
       x[i] = make_float2(-INFINITY, 0.f);
       if (first + i < n) {
+        const float2* ml;
+        const float* acc;
         at(first + i, &ml, &acc);
         x[i] = __ldcg(ml);
 #pragma unroll
-        for (int j = 0; j < V / 4; ++j) y[i][j] = __ldcg(reinterpret_cast<const float4*>(acc + 128 * j + 4 * lane));
+        for (int j = 0; j < V; ++j) y[i][j] = __ldcg(reinterpret_cast<const float4*>(acc + 128 * j + 4 * lane));
       }
     }
+  }
+  template <int BATCH>
+  __device__ __forceinline__ void add(const float2 (&x)[BATCH], const float4 (&y)[BATCH][V]) {
+    float most = top;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) most = fmaxf(most, x[i].x);
+    for (int i = 0; i < BATCH; ++i) most = fmaxf(most, x[i].x);
     const float f = top == -INFINITY ? 0.f : exp2_approx(top - most);
     top = most;
     sum *= f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] *= f;
+    for (int j = 0; j < V; ++j) v[j] = make_float4(v[j].x * f, v[j].y * f, v[j].z * f, v[j].w * f);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < BATCH; ++i) {
       if (x[i].x == -INFINITY) continue;  // none, or it saw no token of the row: its output may be anything
       const float w = exp2_approx(x[i].x - top);
       sum += w * x[i].y;
 #pragma unroll
-      for (int j = 0; j < V / 4; ++j) {
-        v[4 * j] += w * y[i][j].x;
-        v[4 * j + 1] += w * y[i][j].y;
-        v[4 * j + 2] += w * y[i][j].z;
-        v[4 * j + 3] += w * y[i][j].w;
+      for (int j = 0; j < V; ++j) {
+        v[j].x += w * y[i][j].x;
+        v[j].y += w * y[i][j].y;
+        v[j].z += w * y[i][j].z;
+        v[j].w += w * y[i][j].w;
       }
     }
   }
-  const float f = sum > 0.f ? 1.f / sum : 0.f;
+  template <typename T>
+  __device__ __forceinline__ void store(T* out) const {
+    const float f = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-  for (int j = 0; j < V; j += 4) {
-    uint2 y;
-    y.x = pack2<T>(v[j] * f, v[j + 1] * f);
-    y.y = pack2<T>(v[j + 2] * f, v[j + 3] * f);
-    *reinterpret_cast<uint2*>(out + 32 * j + 4 * lane) = y;
+    for (int j = 0; j < V; ++j)
+      *reinterpret_cast<uint2*>(out + 128 * j + 4 * (threadIdx.x & 31)) =
+          make_uint2(pack2<T>(v[j].x * f, v[j].y * f), pack2<T>(v[j].z * f, v[j].w * f));
   }
+};
+template <typename T, int D, int BATCH, typename At>
+__device__ __forceinline__ void merge_pieces(int n, const At& at, T* out) {
+  Merged<D> m;
+  for (int first = 0; first < n; first += BATCH) {
+    float2 x[BATCH];
+    float4 y[BATCH][Merged<D>::V];
+    m.load(x, y, first, n, at);
+    m.add(x, y);
+  }
+  m.store(out);
 }
 
-// Rows with one context: grid (CTAs, rows of an item / 8), the item that CTA blockIdx.x begins and
-// others end.
-template <typename T, int D>
+// Rows with one context: grid (CTAs, rows of an item / (8 ROWS)), the item that CTA blockIdx.x begins
+// and others end. A warp takes ROWS rows: one where items have few rows but many pieces, four,
+// their first pieces loaded together, where they have many (six packed prompts, 152 items of up to
+// 256 rows in two pieces: MEASURED us with one row a warp, MEASURED with four).
+template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(256) merge_items_kernel(const AttendParams p) {
-  const int c = blockIdx.x, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  constexpr int BATCH = ROWS == 1 ? (D == 128 ? 8 : 4) : 2;
+  const int c = blockIdx.x, r0 = blockIdx.y * 8 * ROWS + (threadIdx.x >> 5);
   pdl_wait();
   pdl_launch_dependents();
   const int4 x = __ldcg(reinterpret_cast<const int4*>(p.split + c));
   const SplitItem it{x.x, x.y, x.z, x.w};
-  if (it.pieces == 0 || r >= it.rows) return;
-  const int tok = div_group(p, r);
-  merge_pieces<T, D>(
-      it.pieces,
-      [&](int i, const float2** ml, const float** acc) {
-        const size_t k = ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * p.slot_rows + r;
-        *ml = p.slot_ml + k;
-        *acc = p.slot_acc + k * D;
-      },
-      static_cast<T*>(p.out) + ((size_t)(it.tok + tok) * p.Hq + it.kvh * p.G + r - tok * p.G) * D);
+  if (it.pieces == 0 || r0 >= it.rows) return;
+  Merged<D> m[ROWS];
+  for (int first = 0; first < it.pieces; first += BATCH) {
+    float2 ml[ROWS][BATCH];
+    float4 acc[ROWS][BATCH][Merged<D>::V];
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const int r = r0 + 8 * k;
+      m[k].load(ml[k], acc[k], first, r < it.rows ? it.pieces : 0, [&](int i, const float2** a, const float** b) {
+        const size_t at = ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * p.slot_rows + r;
+        *a = p.slot_ml + at;
+        *b = p.slot_acc + at * D;
+      });
+    }
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) m[k].add(ml[k], acc[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    const int r = r0 + 8 * k, tok = div_group(p, r);
+    if (r < it.rows)
+      m[k].store(static_cast<T*>(p.out) + ((size_t)(it.tok + tok) * p.Hq + it.kvh * p.G + r - tok * p.G) * D);
+  }
 }
 
 // Rows with two contexts, and others: every row finds its pieces.
@@ -1190,7 +1222,7 @@ __global__ void __launch_bounds__(256) merge_rows_kernel(const AttendParams p) {
   Pieces ps{0, -1, 0};
   if (own.group >= 0) ps = pieces_of(record(own.group));
   const int n_shared = ps.to - ps.from + 1, n = n_shared + po.to - po.from + 1;
-  merge_pieces<T, D>(
+  merge_pieces<T, D, D == 128 ? 8 : 4>(
       n,
       [&](int i, const float2** ml, const float** acc) {
         const bool mine = i >= n_shared;
@@ -1239,8 +1271,10 @@ cudaError_t launch_attend_load(const AttendParams& p, const AttendMaps& maps, cu
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   if (!p.shared) {
-    cfg.gridDim = dim3(p.ctas, (p.slot_rows + 7) / 8);
-    return cudaLaunchKernelEx(&cfg, merge_items_kernel<T, D>, p);
+    const int rows = p.slot_rows > 64 ? 4 : 1;
+    cfg.gridDim = dim3(p.ctas, (p.slot_rows + 8 * rows - 1) / (8 * rows));
+    return rows == 4 ? cudaLaunchKernelEx(&cfg, merge_items_kernel<T, D, 4>, p)
+                     : cudaLaunchKernelEx(&cfg, merge_items_kernel<T, D, 1>, p);
   }
   cfg.gridDim = dim3((unsigned)(((long long)p.T * p.Hq + 7) / 8));
   return cudaLaunchKernelEx(&cfg, merge_rows_kernel<T, D>, p);
