@@ -511,6 +511,7 @@ __device__ __forceinline__ void staged_load_role(const AttendParams& p, AttendSh
   constexpr int CPR = D * C::KVB / 16;  // chunks of a row
   constexpr int RW = C::TN / 4;         // rows of a warp
   constexpr int CH = RW * CPR / 32;     // chunks of a lane
+  constexpr int RPI = 32 / CPR;         // rows of a warp's i-th chunks
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - C::W_LOAD;
   const uint32_t raw_lane = smem_addr(raw) + warp * (C::RAW / 4) + lane * 16;
   uint32_t count = 0;
@@ -553,15 +554,23 @@ __device__ __forceinline__ void staged_load_role(const AttendParams& p, AttendSh
       const int slot = issued % C::NR;
       if (lane == 0) sh.staged[slot][warp] = make_int2(c0, c1);
       const uint32_t dst = raw_lane + slot * C::RAW;
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int f = i * 32 + lane, r = f / CPR, c = f % CPR;
-        const uint32_t rr = __shfl_sync(0xffffffffu, ridx, r);
-        const int row = warp * RW + r;
-        if (row >= c0 && row < c1)
+      const uint8_t* const src = cache + lane % CPR * 16;
+      auto copy = [&](int i, bool here) {
+        const uint32_t rr = __shfl_sync(0xffffffffu, ridx, i * RPI + lane / CPR);
+        if (here)
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 512),
-                       "l"(cache + (size_t)rr * (D * C::KVB) + c * 16)
+                       "l"(src + (size_t)rr * (D * C::KVB))
                        : "memory");
+      };
+      if (c0 == 0 && c1 == C::TN) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) copy(i, true);
+      } else {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int row = warp * RW + i * RPI + lane / CPR;
+          copy(i, row >= c0 && row < c1);
+        }
       }
       ++issued;
       if (v == it.tiles) {
@@ -584,35 +593,50 @@ __device__ __forceinline__ void staged_load_role(const AttendParams& p, AttendSh
     const int2 rows = sh.staged[slot][warp];
     if (!wait_for(smem_addr(&sh.kv_empty[stage]), ((done / C::NS) & 1) ^ 1, &sh.give_up)) break;
     const uint32_t src = raw_lane + slot * C::RAW;
-    const uint32_t tile = smem_addr(stages) + stage * C::STAGE;
-    uint4 chunk[CH < 8 ? CH : 8];  // eight loads in flight
+    // Chunk h (8 elements) of row r goes to chunk (h % 8) ^ (r % 8) of its panel's row. Rows i RPI + j
+    // of the warp, j < RPI: r % 8 is (i RPI % 8) | j, so that the address is xored with a constant.
+    const int j = lane / CPR, h = lane % CPR * (FP8 ? 2 : 1);
+    const uint32_t at = smem_addr(stages) + stage * C::STAGE + (h >> 3) * (C::TN * 128) + (warp * RW + j) * 128 +
+                        (((h & 7) ^ j) << 4);
+    auto put = [&](uint32_t a, const uint4& y) {
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                   : "memory");
+    };
+    const bool all = rows.x == 0 && rows.y == C::TN;
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      if (i % 8 == 0)
+    for (int i0 = 0; i0 < CH; i0 += 8) {
+      uint4 chunk[8];  // eight loads in flight
 #pragma unroll
-        for (int j = 0; j < 8 && i + j < CH; ++j) chunk[j] = lds128(src + (i + j) * 512);
-      const int f = i * 32 + lane, r = warp * RW + f / CPR, c = f % CPR;
-      uint4 x = chunk[i % 8];
-      if (r < rows.x || r >= rows.y) x = make_uint4(0u, 0u, 0u, 0u);
-      auto put = [&](int chunk, const uint4& y) {  // chunk: 8 elements of the row
-        const uint32_t a = tile + (chunk >> 3) * (C::TN * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
-                     : "memory");
-      };
-      if constexpr (FP8) {
-        uint4 lo, hi;
-        lo.x = e4m3x2_to_half2(x.x & 0xffff);
-        lo.y = e4m3x2_to_half2(x.x >> 16);
-        lo.z = e4m3x2_to_half2(x.y & 0xffff);
-        lo.w = e4m3x2_to_half2(x.y >> 16);
-        hi.x = e4m3x2_to_half2(x.z & 0xffff);
-        hi.y = e4m3x2_to_half2(x.z >> 16);
-        hi.z = e4m3x2_to_half2(x.w & 0xffff);
-        hi.w = e4m3x2_to_half2(x.w >> 16);
-        put(2 * c, lo);
-        put(2 * c + 1, hi);
-      } else {
-        put(c, x);
+      for (int k = 0; k < 8; ++k) chunk[k] = lds128(src + (i0 + k) * 512);
+      if (!all) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = warp * RW + (i0 + k) * RPI + j;
+          if (r < rows.x || r >= rows.y) chunk[k] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k;
+        const uint4 x = chunk[k];
+        const uint32_t a = (at ^ ((i * RPI & 7) << 4)) + i * RPI * 128;
+        if constexpr (FP8) {
+          uint4 lo, hi;
+          lo.x = e4m3x2_to_half2(x.x & 0xffff);
+          lo.y = e4m3x2_to_half2(x.x >> 16);
+          lo.z = e4m3x2_to_half2(x.y & 0xffff);
+          lo.w = e4m3x2_to_half2(x.y >> 16);
+          hi.x = e4m3x2_to_half2(x.z & 0xffff);
+          hi.y = e4m3x2_to_half2(x.z >> 16);
+          hi.z = e4m3x2_to_half2(x.w & 0xffff);
+          hi.w = e4m3x2_to_half2(x.w >> 16);
+          // lanes of odd panels write their upper half first: eight lanes of a row then fill a row
+          const bool odd = (h >> 3) & 1;
+          put(a ^ (odd ? 16 : 0), odd ? hi : lo);
+          put(a ^ (odd ? 0 : 16), odd ? lo : hi);
+        } else {
+          put(a, x);
+        }
       }
     }
     async_proxy_fence();
