@@ -783,35 +783,41 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
   const uint32_t lanes = (uint32_t)((threadIdx.x >> 5) & 3) << 21;  // 32 (warp % 4) in the upper half
   const uint32_t own_o = tmem + C::O_COL + group * D + lanes;
   const float sl2 = p.scale_log2;
-  uint32_t count = 0, used[2] = {0, 0}, pairs = 0, tiles_before = 0;
-  Item it;
-  while (next_item(sh, count, it)) {
-    const bool two = two_row_tiles<C>(p, it);
-    const int dup = two ? 1 : 0, steps = it.tiles << dup;
+  // Registers are short here (a spilled one comes back from L2): the item stays in its slot of the
+  // ring, and what is needed of it after its steps is read again; parities are bits of one word, 0 and
+  // 1 the score buffers', 2 the pair barrier's.
+  uint32_t count = 0, parities = 0, tiles_before = 0;
+  for (;; ++count) {
+    const Item& it = sh.items[count % C::ITEMS];
+    PA_WAIT(sh.item_full[count % C::ITEMS], (count / C::ITEMS) & 1);
+    const int tiles = it.tiles;
+    if (tiles == 0) return;
     const int tile_rows = p.tile_tokens * p.G;
+    const bool two = two_row_tiles<C>(p, it);
+    const int dup = two ? 1 : 0;
     const int r = (two ? group * tile_rows : 0) + at;  // the item's row of this thread
     const bool live = at < tile_rows && r < it.rows;
     const bool warp_live = at - lane < tile_rows && r - lane < it.rows;
-    const int tok = live ? it.tok + div_group(p, r) : 0;
-    const int head = it.kvh * p.G + r - div_group(p, r) * p.G;
-    int end = it.hi;  // this row sees tokens in [lo, end)
+    const int lo = it.lo;
+    int end = live ? it.hi : lo;  // this row sees tokens in [lo, end)
     if (p.shared && live) {  // causal among the new rows
-      const int b = p.R == 1 ? tok : tok / p.R;
-      const int L = it.of_prefix ? clamp_len(p, b) : it.hi;  // the end of its own segment
+      const int tok = it.tok + div_group(p, r), b = p.R == 1 ? tok : tok / p.R;
+      const int L = it.of_prefix ? clamp_len(p, b) : end;  // the end of its own segment
       end = min(end, L - p.R + 1 + (tok - b * p.R));
     }
-    if (!live) end = it.lo;
     float ref = -INFINITY, sum = 0.f;
-    int mine = 0;  // steps of this group in the item
-    for (int i = C::NWG == 2 ? group : 0; i < steps; i += C::NWG, ++mine) {
-      const int buf = i & 1, t = i >> dup;
+    int t0 = it.t0;
+    int i = C::NWG == 2 ? group : 0;
+    const bool any = i < tiles << dup;  // a step for this group
+    if (C::NWG == 2 && !dup) t0 += group * C::TN;
+    for (; i < tiles << dup; i += C::NWG, t0 += C::NWG == 2 && !dup ? 2 * C::TN : C::TN) {
+      const int buf = C::NWG == 2 ? group : i & 1;
       const uint32_t s_at = tmem + C::S_COL + buf * C::TN + lanes;
-      PA_WAIT(sh.s_full[buf], used[buf] & 1);
-      ++used[buf];
-      const int t0 = it.t0 + t * C::TN;
+      PA_WAIT(sh.s_full[buf], (parities >> buf) & 1);
+      parities ^= 1u << buf;
       if (warp_live) {
         tc_fence_after();
-        const int c0 = it.lo - t0, c1 = end - t0;  // columns [c0, c1) are seen
+        const int c0 = lo - t0, c1 = end - t0;  // columns [c0, c1) are seen
         uint32_t x[2][32];
         if (!__all_sync(0xffffffffu, !live || (c0 <= 0 && c1 >= C::TN))) {
           // scores of tokens that the row does not see become -inf, whatever they are
@@ -847,11 +853,10 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
           const float f = now == -INFINITY ? 1.f : exp2_approx(ref - now);
           ref = now;
           sum *= f;
-          if (mine > 0) {  // the accumulator of the steps before
+          if (i >= C::NWG) {  // the accumulator of the steps before
             const int last = C::NWG == 2 ? buf : buf ^ 1;
-            PA_WAIT(sh.pv_done[last], (used[last] - (C::NWG == 2 ? 2 : 1)) & 1);
+            PA_WAIT(sh.pv_done[last], (parities >> last & 1) ^ (C::NWG == 2 ? 0 : 1));
             tc_fence_after();
-            tmem_loaded(x[NC & 1]);
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -861,6 +866,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
               for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
               tmem_store32(own_o + 32 * c, o);
             }
+            tmem_load32(x[NC & 1], s_at);  // read again rather than kept across the wait
           }
         }
         const float sub = ref == -INFINITY ? 0.f : -ref;
@@ -871,17 +877,20 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
           uint32_t(&y)[32] = x[(NC + c) & 1];
           tmem_loaded(y);
           if (c + 1 < NC) tmem_load32(x[(NC + c + 1) & 1], s_at + 32 * (c + 1));
-          uint32_t w[16];
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float2 e = fma2(make_float2(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), by, plus);
-            e.x = exp2_approx(e.x);
-            e.y = exp2_approx(e.y);
-            part[(j / 2) & 1] = add2(part[(j / 2) & 1], e);
-            w[j / 2] = pack2<TM>(e.x, e.y);
+          for (int k = 0; k < 32; k += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              float2 e = fma2(make_float2(__uint_as_float(y[k + j]), __uint_as_float(y[k + j + 1])), by, plus);
+              e.x = exp2_approx(e.x);
+              e.y = exp2_approx(e.y);
+              part[(j / 2) & 1] = add2(part[(j / 2) & 1], e);
+              w[j / 2] = pack2<TM>(e.x, e.y);
+            }
+            // over columns of scores that are in registers already
+            tmem_store8(s_at + 16 * c + k / 2, w);
           }
-          // over columns of scores that are in registers already
-          tmem_store16(s_at + 16 * c, w);
         }
         const float2 both = add2(part[0], part[1]);
         sum += both.x + both.y;
@@ -890,12 +899,12 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
       if constexpr (ZERO_V) {
         // V rows outside the context hold whatever the cache or an earlier tile left: zeros there,
         // so that weights of 0 meet 0
-        if ((t0 < it.lo || t0 + C::TN > it.hi) && !(dup && group)) {
-          const uint32_t n = tiles_before + place_v(t, lead_of<C>(p, it), it.tiles);
+        if ((t0 < lo || t0 + C::TN > it.hi) && !(dup && group)) {
+          const uint32_t n = tiles_before + place_v(i >> dup, lead_of<C>(p, it), tiles);
           PA_WAIT(sh.kv_full[n % C::NS], (n / C::NS) & 1);
           const uint32_t tile = smem_addr(stages) + (n % C::NS) * C::STAGE;
           for (int row = at; row < C::TN; row += 128)
-            if (t0 + row < it.lo || t0 + row >= it.hi)
+            if (t0 + row < lo || t0 + row >= it.hi)
 #pragma unroll
               for (int c = 0; c < D / 8; ++c) sts128_zero(tile + (c >> 3) * (C::TN * 128) + row * 128 + (c & 7) * 16);
           async_proxy_fence();
@@ -905,12 +914,12 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[buf]));
     }
-    tiles_before += 2 * it.tiles;
+    tiles_before += 2 * tiles;
 
     // ---- the item's rows: O / sum, or (reference, sum, O) of a piece
-    if (mine > 0) {
-      const int last = C::NWG == 2 ? group : (steps - 1) & 1;
-      PA_WAIT(sh.pv_done[last], (used[last] - 1) & 1);
+    if (any) {
+      const int last = C::NWG == 2 ? group : (tiles - 1) & 1;
+      PA_WAIT(sh.pv_done[last], (parities >> last & 1) ^ 1);
     }
     tc_fence_after();
     const bool joint = C::NWG == 2 && !two;  // two states of the same rows
@@ -921,8 +930,8 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.pair));
-        PA_WAIT(sh.pair, pairs & 1);
-        ++pairs;
+        PA_WAIT(sh.pair, parities >> 2 & 1);
+        parities ^= 4;
         tc_fence_after();
         const float2 other = sh.state[group ^ 1][at];
         const float m = fmaxf(ref, other.x);
@@ -935,7 +944,8 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
     if (warp_live) {
       const bool whole = it.dest == kDirect;
       const float mul = whole ? (sum > 0.f ? p.v_scale / sum : 0.f) : p.v_scale;
-      const size_t row = (size_t)tok * p.Hq + head;
+      const int tok = it.tok + div_group(p, r), head = it.kvh * p.G + r - div_group(p, r) * p.G;
+      const size_t row = live ? (size_t)tok * p.Hq + head : 0;
       size_t part = 0;  // row of the partials
       float* acc = nullptr;
       float2* ml = nullptr;
@@ -1006,10 +1016,12 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.pair));
-        PA_WAIT(sh.pair, pairs & 1);
-        ++pairs;
+        PA_WAIT(sh.pair, parities >> 2 & 1);
+        parities ^= 4;
       }
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&sh.item_empty[count % C::ITEMS]));
   }
 }
 
