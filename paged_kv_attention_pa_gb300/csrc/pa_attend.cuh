@@ -20,7 +20,7 @@
 //   products  one warp, whose lane 0 issues the tensor core products
 //   plan      one warp that writes the items into a ring
 //   queries   one warp that copies the items' queries
-//   load      four warps that issue tensor copies of K and V, or stage and widen them
+//   load      four warps that issue tensor copies of K and V, or eight that copy their rows and widen fp8
 // S = Q K^T goes to tensor memory, a thread reads its row's scores, writes the weights over them
 // as the A operand of O += P V, and O stays in tensor memory. Step i of an item uses score buffer
 // i % 2, so that the tensor cores work on one while the softmax of the other runs (barriers are kept
@@ -57,19 +57,26 @@ struct AttendCfg {
   static constexpr int PANELS = D / 64;
   static constexpr int QTILE = 128 * D * 2, NQ = D == 128 ? 2 : 1;
   static constexpr int STAGE = TN * D * 2;
-  static constexpr int NS = LOAD == kLoadTensor ? 5 : 3;
+  static constexpr int NS = LOAD == kLoadFp8 ? 3 : 5;
   static constexpr int KVB = LOAD == kLoadFp8 ? 1 : 2;
-  static constexpr int RAW = LOAD == kLoadTensor ? 0 : TN * D * KVB;  // a staged tile
-  static constexpr int NR = LOAD == kLoadTensor ? 0 : LOAD == kLoadFp8 ? 4 : 2;
+  static constexpr int RAW = LOAD == kLoadFp8 ? TN * D : 0;  // a staged tile
+  static constexpr int NR = 2;                               // of K and of V
   static constexpr int NSW = 4 * NWG;
   static constexpr int W_MMA = NSW, W_PLAN = NSW + 1, W_Q = NSW + 2, W_LOAD = NSW + 3;
-  static constexpr int NLOAD = 4;
-  static constexpr int WARPS = NSW + 3 + NLOAD, THREADS = WARPS * 32;
-  static constexpr int READERS = WARPS - 1;  // warps that read the ring of items
+  static constexpr int NLOAD = LOAD == kLoadTensor ? 4 : 8;
+  static constexpr int READERS = NSW + 2 + NLOAD;  // warps that read the ring of items
+  // Registers: a CTA of 480 threads starts with 128 each. One with eight load warps and two groups of
+  // softmax warps (20 warps, the last idle) starts with 96, and its other warps give some to the
+  // softmax warps.
+  static constexpr bool kShift = LOAD != kLoadTensor && NWG == 2;
+  static constexpr int WARPS = LOAD == kLoadTensor ? NSW + 3 + NLOAD : (NSW + 3 + NLOAD + 3) / 4 * 4;
+  static constexpr int THREADS = WARPS * 32;
+  static constexpr int kStartRegs = 96, kSoftmaxRegs = 128, kOtherRegs = 72;
+  static_assert(!kShift || NSW * kSoftmaxRegs + (WARPS - NSW) * kOtherRegs <= WARPS * kStartRegs, "registers");
   static constexpr int ITEMS = 4;            // slots of that ring
   static constexpr int OFF_STAGE = NQ * QTILE;
   static constexpr int OFF_RAW = OFF_STAGE + NS * STAGE;
-  static constexpr int OFF_SYNC = OFF_RAW + NR * RAW;
+  static constexpr int OFF_SYNC = OFF_RAW + 2 * NR * RAW;
   static constexpr int SYNC_BYTES = 3072;
   static constexpr int SMEM = OFF_SYNC + SYNC_BYTES;
   static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
@@ -204,8 +211,10 @@ struct Item {
 
 // ------------------------------------------------------------------ waits
 // Wait for a phase of a barrier; false when it took over two seconds or another warp gave up. The
-// whole warp together.
-static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* give_up) {
+// whole warp together. The slow part is a function of its own where the kernel has one register count
+// (inlined everywhere it cost 2%: 4096 rows over 8192 tokens 345 us, 352), and inlined where register
+// counts change, which function calls do not go with.
+__device__ __forceinline__ bool wait_loop(uint32_t bar, uint32_t parity, volatile int* give_up) {
   const uint64_t t0 = global_ns();
   for (;;) {
     const bool over = global_ns() - t0 >= 2000000000ull || *give_up != 0;
@@ -217,9 +226,13 @@ static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, vol
     }
   }
 }
+static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* give_up) {
+  return wait_loop(bar, parity, give_up);
+}
+template <bool INLINE>
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* give_up) {
   if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
-  return wait_long(bar, parity, give_up);
+  return INLINE ? wait_loop(bar, parity, give_up) : wait_long(bar, parity, give_up);
 }
 
 // ------------------------------------------------------------------ shared memory
@@ -237,12 +250,11 @@ struct AttendShared {
   long long first_unit, per, total;
   Item items[C::ITEMS];
   float2 state[2][128];    // (reference, sum) of the two softmax groups
-  int2 staged[4][4];       // [slot][load warp] rows of a staged tile that hold tokens
   long long scan[32];
 };
 
 #define PA_WAIT(bar, parity) \
-  if (!wait_for(smem_addr(&(bar)), (parity), &sh.give_up)) return
+  if (!wait_for<C::kShift>(smem_addr(&(bar)), (parity), &sh.give_up)) return
 
 // ------------------------------------------------------------------ plan
 // Every CTA finds the first unit of its run: a sum over the segments' units. CTA 0 writes what the
@@ -428,7 +440,7 @@ __device__ __forceinline__ void plan_role(const AttendParams& p, AttendShared<C>
 template <typename C>
 __device__ __forceinline__ bool next_item(AttendShared<C>& sh, uint32_t& count, Item& it) {
   const int slot = count % C::ITEMS;
-  if (!wait_for(smem_addr(&sh.item_full[slot]), (count / C::ITEMS) & 1, &sh.give_up)) return false;
+  if (!wait_for<C::kShift>(smem_addr(&sh.item_full[slot]), (count / C::ITEMS) & 1, &sh.give_up)) return false;
   it = sh.items[slot];
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&sh.item_empty[slot]));
@@ -503,145 +515,183 @@ __device__ __forceinline__ void tensor_load_role(const AttendParams& p, const CU
   }
 }
 
-// Staged copies: each lane copies 16-byte chunks of its warp's rows into a ring of raw tiles with
-// cp.async, and later widens its own chunks into the swizzled tile. Rows without a token are zero.
+// Where cp.async brings a tile: four warps for K and four for V, a warp for a quarter of the rows. Lane
+// l resolves the warp's row l and the lanes copy 16-byte chunks. 16-bit chunks go to their place in the
+// tile, with zeros for rows without a token; fp8 chunks to a ring of raw tiles, from which each lane
+// later widens those it copied. A warp takes some 1400 cycles for an fp8 tile, most of them latencies
+// between its few instructions, so that K and V side by side take half the time of one after the other.
 template <typename C, int D, bool FP8>
-__device__ __forceinline__ void staged_load_role(const AttendParams& p, AttendShared<C>& sh, uint8_t* stages,
-                                                 uint8_t* raw) {
-  constexpr int CPR = D * C::KVB / 16;  // chunks of a row
-  constexpr int RW = C::TN / 4;         // rows of a warp
-  constexpr int CH = RW * CPR / 32;     // chunks of a lane
-  constexpr int RPI = 32 / CPR;         // rows of a warp's i-th chunks
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - C::W_LOAD;
-  const uint32_t raw_lane = smem_addr(raw) + warp * (C::RAW / 4) + lane * 16;
-  uint32_t count = 0;
-  Item it;
-  bool more = next_item(sh, count, it);
-  int lead = more ? lead_of<C>(p, it) : 0, k = 0, v = 0;  // tiles of K and V issued
-  uint32_t issued = 0, done = 0;
-  // lane l resolves row l of its warp; V of a tile has the rows of its K, at most two tiles before
-  auto entry = [&](int t) -> int {
-    const int tok = it.t0 + t * C::TN + warp * RW + lane;
-    return t < it.tiles && lane < RW && tok >= it.lo && tok < it.hi
-               ? __ldg(p.block_tables + (size_t)it.table * p.max_blocks + div_block(p, tok))
-               : 0;
-  };
-  int phys = more ? entry(0) : 0;  // of the next K tile
-  uint32_t even = 0, odd = 0;      // rows of K tiles
-  // issue the next tile, if there is one
-  auto issue = [&]() {
-    if (more) {
-      const bool is_k = k < it.tiles && k < v + lead;
-      const int t = is_k ? k++ : v++;
-      const int t0 = it.t0 + t * C::TN;
-      const uint8_t* cache = static_cast<const uint8_t*>(is_k ? p.k_cache : p.v_cache);
-      if (is_k) {
-        if ((unsigned)phys >= (unsigned)p.num_blocks) {
-          atomicOr(p.err, PA_DEVERR_BLOCK_INDEX);
-          phys = 0;
-        }
-        const int tok = t0 + warp * RW + lane, slot = tok - div_block(p, tok) * p.block_size;
-        const uint32_t row =
-            ((uint32_t)phys * (uint32_t)p.block_size + (uint32_t)slot) * (uint32_t)p.Hkv + (uint32_t)it.kvh;
-        if (t & 1)
-          odd = row;
-        else
-          even = row;
-        phys = entry(t + 1);
-      }
-      const uint32_t ridx = t & 1 ? odd : even;
-      const int c0 = max(0, min(C::TN, it.lo - t0)), c1 = max(0, min(C::TN, it.hi - t0));
-      const int slot = issued % C::NR;
-      if (lane == 0) sh.staged[slot][warp] = make_int2(c0, c1);
-      const uint32_t dst = raw_lane + slot * C::RAW;
-      const uint8_t* const src = cache + lane % CPR * 16;
-      auto copy = [&](int i, bool here) {
-        const uint32_t rr = __shfl_sync(0xffffffffu, ridx, i * RPI + lane / CPR);
-        if (here)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 512),
-                       "l"(src + (size_t)rr * (D * C::KVB))
-                       : "memory");
-      };
-      if (c0 == 0 && c1 == C::TN) {
-#pragma unroll
-        for (int i = 0; i < CH; ++i) copy(i, true);
-      } else {
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int row = warp * RW + i * RPI + lane / CPR;
-          copy(i, row >= c0 && row < c1);
-        }
-      }
-      ++issued;
-      if (v == it.tiles) {
-        more = next_item(sh, count, it);
-        lead = lead_of<C>(p, it);
-        k = v = 0;
-        phys = more ? entry(0) : 0;
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-#pragma unroll
-  for (int i = 0; i < C::NR - 1; ++i) issue();
-  for (;;) {
-    issue();
-    if (done == issued) break;
-    asm volatile("cp.async.wait_group %0;" ::"n"(C::NR - 1) : "memory");
-    __syncwarp();
-    const int slot = done % C::NR, stage = done % C::NS;
-    const int2 rows = sh.staged[slot][warp];
-    if (!wait_for(smem_addr(&sh.kv_empty[stage]), ((done / C::NS) & 1) ^ 1, &sh.give_up)) break;
-    const uint32_t src = raw_lane + slot * C::RAW;
+struct RowLoader {
+  static constexpr int CPR = D * C::KVB / 16;  // chunks of a row
+  static constexpr int RW = C::TN / 4;         // rows of a warp
+  static constexpr int CH = RW * CPR / 32;     // chunks of a lane
+  static constexpr int RPI = 32 / CPR;         // rows of a warp's i-th chunks
+  const AttendParams& p;
+  AttendShared<C>& sh;
+  const bool is_k;
+  const int warp, lane;
+  const uint8_t* const src;
+  uint32_t at;                           // this lane's first chunk in a tile
+  uint32_t count = 0, before = 0;        // items; tiles of the items before
+  Item it{};
+  int t = 0, phys = 0;                   // the tile to issue, lane l's block of its row l
+  bool more;
+
+  __device__ __forceinline__ RowLoader(const AttendParams& p, AttendShared<C>& sh, bool is_k, int warp)
+      : p(p), sh(sh), is_k(is_k), warp(warp), lane(threadIdx.x & 31),
+        src(static_cast<const uint8_t*>(is_k ? p.k_cache : p.v_cache) + (threadIdx.x & 31) % CPR * 16) {
     // Chunk h (8 elements) of row r goes to chunk (h % 8) ^ (r % 8) of its panel's row. Rows i RPI + j
     // of the warp, j < RPI: r % 8 is (i RPI % 8) | j, so that the address is xored with a constant.
     const int j = lane / CPR, h = lane % CPR * (FP8 ? 2 : 1);
-    const uint32_t at = smem_addr(stages) + stage * C::STAGE + (h >> 3) * (C::TN * 128) + (warp * RW + j) * 128 +
-                        (((h & 7) ^ j) << 4);
-    auto put = [&](uint32_t a, const uint4& y) {
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
-                   : "memory");
-    };
-    const bool all = rows.x == 0 && rows.y == C::TN;
+    at = (h >> 3) * (C::TN * 128) + (warp * RW + j) * 128 + (((h & 7) ^ j) << 4);
+    more = next_item(sh, count, it);
+    if (more) phys = entry(0);
+  }
+  __device__ __forceinline__ uint32_t place_in(uint32_t tile, int i) const {
+    return ((tile + at) ^ ((i * RPI & 7) << 4)) + i * RPI * 128;
+  }
+  __device__ __forceinline__ int entry(int tile) const {
+    const int tok = it.t0 + tile * C::TN + warp * RW + lane;
+    return tile < it.tiles && lane < RW && tok >= it.lo && tok < it.hi
+               ? __ldg(p.block_tables + (size_t)it.table * p.max_blocks + div_block(p, tok))
+               : 0;
+  }
+  __device__ __forceinline__ uint32_t place() const {  // of the tile to issue in the ring
+    return before + (is_k ? place_k(t, lead_of<C>(p, it)) : place_v(t, lead_of<C>(p, it), it.tiles));
+  }
+  __device__ __forceinline__ int2 rows() const {  // of that tile that hold tokens
+    const int t0 = it.t0 + t * C::TN;
+    return make_int2(max(0, min(C::TN, it.lo - t0)), max(0, min(C::TN, it.hi - t0)));
+  }
+  // Chunk i goes to to(i). Then the next tile is the one to issue.
+  template <typename To>
+  __device__ __forceinline__ void issue(const int2& r01, const To& to) {
+    const int tok = it.t0 + t * C::TN + warp * RW + lane;
+    if ((unsigned)phys >= (unsigned)p.num_blocks) {
+      atomicOr(p.err, PA_DEVERR_BLOCK_INDEX);
+      phys = 0;
+    }
+    const int off = tok - div_block(p, tok) * p.block_size;
+    const uint32_t row =
+        ((uint32_t)phys * (uint32_t)p.block_size + (uint32_t)off) * (uint32_t)p.Hkv + (uint32_t)it.kvh;
+    phys = entry(t + 1);
+    const bool all = r01.x == 0 && r01.y == C::TN;
+    if (all) {
 #pragma unroll
-    for (int i0 = 0; i0 < CH; i0 += 8) {
-      uint4 chunk[8];  // eight loads in flight
-#pragma unroll
-      for (int k = 0; k < 8; ++k) chunk[k] = lds128(src + (i0 + k) * 512);
-      if (!all) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = warp * RW + (i0 + k) * RPI + j;
-          if (r < rows.x || r >= rows.y) chunk[k] = make_uint4(0u, 0u, 0u, 0u);
-        }
+      for (int i = 0; i < CH; ++i) {
+        const uint32_t rr = __shfl_sync(0xffffffffu, row, i * RPI + lane / CPR);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to(i)), "l"(src + (size_t)rr * (D * C::KVB))
+                     : "memory");
       }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int i = i0 + k;
-        const uint4 x = chunk[k];
-        const uint32_t a = (at ^ ((i * RPI & 7) << 4)) + i * RPI * 128;
-        if constexpr (FP8) {
-          uint4 lo, hi;
-          lo.x = e4m3x2_to_half2(x.x & 0xffff);
-          lo.y = e4m3x2_to_half2(x.x >> 16);
-          lo.z = e4m3x2_to_half2(x.y & 0xffff);
-          lo.w = e4m3x2_to_half2(x.y >> 16);
-          hi.x = e4m3x2_to_half2(x.z & 0xffff);
-          hi.y = e4m3x2_to_half2(x.z >> 16);
-          hi.z = e4m3x2_to_half2(x.w & 0xffff);
-          hi.w = e4m3x2_to_half2(x.w >> 16);
-          // lanes of odd panels write their upper half first: eight lanes of a row then fill a row
-          const bool odd = (h >> 3) & 1;
-          put(a ^ (odd ? 16 : 0), odd ? hi : lo);
-          put(a ^ (odd ? 0 : 16), odd ? lo : hi);
-        } else {
-          put(a, x);
-        }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < CH; ++i) {
+        const uint32_t rr = __shfl_sync(0xffffffffu, row, i * RPI + lane / CPR);
+        const int r = warp * RW + i * RPI + lane / CPR;
+        const bool here = r >= r01.x && r < r01.y;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to(i)),
+                     "l"(here ? src + (size_t)rr * (D * C::KVB) : src), "r"(here ? 16 : 0)
+                     : "memory");
       }
     }
+    if (++t == it.tiles) {
+      before += 2 * it.tiles;
+      more = next_item(sh, count, it);
+      t = 0;
+      if (more) phys = entry(0);
+    }
+  }
+  __device__ __forceinline__ void landed(uint32_t place) {  // this lane's part of a tile is in its place
     async_proxy_fence();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_addr(&sh.kv_full[stage]));
+    if (lane == 0) mbar_arrive(smem_addr(&sh.kv_full[place % C::NS]));
+  }
+  __device__ __forceinline__ bool room(uint32_t place) {
+    return wait_for<C::kShift>(smem_addr(&sh.kv_empty[place % C::NS]), ((place / C::NS) & 1) ^ 1, &sh.give_up);
+  }
+};
+
+template <typename C, int D>
+__device__ __forceinline__ void row_load_role(const AttendParams& p, bool is_k, int warp, AttendShared<C>& sh,
+                                              uint8_t* stages) {
+  RowLoader<C, D, false> L(p, sh, is_k, warp);
+  const uint32_t base = smem_addr(stages);
+  uint32_t last = 0;
+  bool pending = false;  // a tile is on its way
+  while (L.more) {
+    const uint32_t n = L.place();
+    if (!L.room(n)) break;
+    const uint32_t tile = base + n % C::NS * C::STAGE;
+    L.issue(L.rows(), [&](int i) { return L.place_in(tile, i); });
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (pending) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      L.landed(last);
+    }
+    last = n;
+    pending = true;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (pending) L.landed(last);
+}
+
+template <typename C, int D>
+__device__ __forceinline__ void fp8_load_role(const AttendParams& p, bool is_k, int warp, AttendShared<C>& sh,
+                                              uint8_t* stages, uint8_t* raw) {
+  using Loader = RowLoader<C, D, true>;
+  Loader L(p, sh, is_k, warp);
+  const int lane = threadIdx.x & 31;
+  const uint32_t raw_lane = smem_addr(raw) + (is_k ? 0 : C::NR * C::RAW) + warp * (C::RAW / 4) + lane * 16;
+  static_assert(C::NR == 2, "one tile on its way while another is widened");
+  uint32_t issued = 0, done = 0, place[2];
+  int2 rows[2];
+  auto issue = [&](int k) {  // the next tile, if there is one
+    if (L.more) {
+      place[k] = L.place();
+      rows[k] = L.rows();
+      const uint32_t dst = raw_lane + issued % 2 * C::RAW;
+      ++issued;
+      L.issue(rows[k], [&](int i) { return dst + i * 512; });
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  issue(0);
+  for (;;) {
+    issue(1);
+    if (done == issued) break;
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const uint32_t n = place[0];
+    place[0] = place[1];
+    rows[0] = rows[1];
+    if (!L.room(n)) break;
+    const uint32_t from = raw_lane + done % 2 * C::RAW, tile = smem_addr(stages) + n % C::NS * C::STAGE;
+    static_assert(Loader::CH == 8, "a tile's chunks of a lane");
+    uint4 chunk[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) chunk[i] = lds128(from + i * 512);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 x = chunk[i];
+      const uint32_t a = L.place_in(tile, i);
+      uint4 lo, hi;
+      lo.x = e4m3x2_to_half2(x.x & 0xffff);
+      lo.y = e4m3x2_to_half2(x.x >> 16);
+      lo.z = e4m3x2_to_half2(x.y & 0xffff);
+      lo.w = e4m3x2_to_half2(x.y >> 16);
+      hi.x = e4m3x2_to_half2(x.z & 0xffff);
+      hi.y = e4m3x2_to_half2(x.z >> 16);
+      hi.z = e4m3x2_to_half2(x.w & 0xffff);
+      hi.w = e4m3x2_to_half2(x.w >> 16);
+      // lanes of odd panels write their upper half first: eight lanes of a row then fill a row
+      const bool odd = lane % Loader::CPR * 2 >> 3 & 1;
+      auto put = [&](uint32_t a, const uint4& y) {
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                     : "memory");
+      };
+      put(a ^ (odd ? 16 : 0), odd ? hi : lo);
+      put(a ^ (odd ? 0 : 16), odd ? lo : hi);
+    }
+    L.landed(n);
     ++done;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -718,7 +768,7 @@ __device__ __forceinline__ void product_role(const AttendParams& p, AttendShared
   Item it;
   auto next_tile = [&](uint32_t& which) -> bool {
     which = stage;
-    if (!wait_for(smem_addr(&sh.kv_full[stage]), lap, &sh.give_up)) return false;
+    if (!wait_for<C::kShift>(smem_addr(&sh.kv_full[stage]), lap, &sh.give_up)) return false;
     if (++stage == C::NS) {
       stage = 0;
       lap ^= 1;
@@ -1044,7 +1094,7 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
     auto init = [](uint64_t* bars, int n, int count) {
       for (int i = 0; i < n; ++i) mbar_init_count(smem_addr(bars + i), count);
     };
-    init(sh.kv_full, C::NS, LOAD == kLoadTensor ? 2 : C::NLOAD);
+    init(sh.kv_full, C::NS, LOAD == kLoadTensor ? 2 : 4);
     init(sh.kv_empty, C::NS, 1);
     init(sh.q_raw, C::NQ, 1);
     init(sh.q_full, C::NQ, 1);
@@ -1073,8 +1123,16 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
+  if constexpr (C::kShift) {
+    if (warp < C::NSW)
+      take_registers<C::kSoftmaxRegs>();
+    else
+      give_registers<C::kOtherRegs>();
+  }
   if (warp < C::NSW)
     softmax_role<C, T, D, LOAD == kLoadTensor>(p, sh, stages, tmem);
+  else if (warp >= C::W_LOAD + C::NLOAD)
+    ;  // fills the last group of four
   else if (warp == C::W_MMA)
     product_role<C, D>(p, sh, q_tiles, stages, tmem);
   else if (warp == C::W_PLAN)
@@ -1084,8 +1142,10 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
   else if constexpr (LOAD == kLoadTensor)
     tensor_load_role<C, D>(p, warp < C::W_LOAD + 2 ? &maps.k : &maps.v, warp < C::W_LOAD + 2,
                            (warp - C::W_LOAD) & 1, sh, stages);
+  else if constexpr (LOAD == kLoadFp8)
+    fp8_load_role<C, D>(p, warp < C::W_LOAD + 4, (warp - C::W_LOAD) & 3, sh, stages, raw);
   else
-    staged_load_role<C, D, LOAD == kLoadFp8>(p, sh, stages, raw);
+    row_load_role<C, D>(p, warp < C::W_LOAD + 4, (warp - C::W_LOAD) & 3, sh, stages);
 
   __syncwarp();
   pdl_launch_dependents();
@@ -1288,6 +1348,12 @@ cudaError_t launch_attend_load(const AttendParams& p, const AttendMaps& maps, cu
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & bit)) {
+    if constexpr (C::kShift) {  // registers that the CTA does not start with would be waited for without end
+      cudaFuncAttributes attrs{};
+      e = cudaFuncGetAttributes(&attrs, kern);
+      if (e != cudaSuccess) return e;
+      if (attrs.numRegs < C::kStartRegs) return cudaErrorInvalidKernelImage;
+    }
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&done_mask, bit, __ATOMIC_ACQ_REL);

@@ -8,7 +8,7 @@
 namespace pa {
 
 // How K and V reach shared memory: 16-bit caches whose blocks are whole groups of eight tokens by
-// tensor copies, other 16-bit caches and fp8 ones through a staging ring.
+// tensor copies, other 16-bit caches row by row, fp8 ones likewise and through a ring of raw tiles.
 enum AttendLoad { kLoadTensor = 0, kLoad16 = 1, kLoadFp8 = 2 };
 
 // What the merge of rows with two contexts needs of a segment (see pa_attend.cuh).

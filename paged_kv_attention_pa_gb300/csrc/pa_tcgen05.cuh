@@ -136,6 +136,18 @@ __device__ __forceinline__ void store32(void* at, const uint32_t (&w)[8]) {
                : "memory");
 }
 
+// ---------------------------------------------------------------- registers
+// A group of four warps takes registers of its CTA that others gave up (waits until there are
+// enough), or gives its own up.
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ---------------------------------------------------------------- pairs of fp32
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
