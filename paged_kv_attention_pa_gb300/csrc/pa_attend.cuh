@@ -1242,40 +1242,43 @@ __device__ __forceinline__ void merge_pieces(int n, const At& at, T* out) {
   m.store(out);
 }
 
-// Rows with one context: grid (CTAs, rows of an item / (8 ROWS)), the item that CTA blockIdx.x begins
-// and others end. A warp takes ROWS rows: one where items have few rows but many pieces, four,
-// their first pieces loaded together, where they have many (six packed prompts, 152 items of up to
-// 256 rows in two pieces: MEASURED us with one row a warp, MEASURED with four).
+// Rows with one context: grid (CTAs, parts of an item's rows), the item that CTA blockIdx.x begins and
+// others end. A warp takes ROWS rows at a time: one where items have few rows but many pieces, two, their
+// first pieces loaded together, where they have many, and then enough rows that every block is resident
+// (each starts with a round trip to find its item).
+constexpr int kMergeParts = 4;
 template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(256) merge_items_kernel(const AttendParams p) {
   constexpr int BATCH = ROWS == 1 ? (D == 128 ? 8 : 4) : 2;
-  const int c = blockIdx.x, r0 = blockIdx.y * 8 * ROWS + (threadIdx.x >> 5);
+  const int c = blockIdx.x;
   pdl_wait();
   pdl_launch_dependents();
   const int4 x = __ldcg(reinterpret_cast<const int4*>(p.split + c));
   const SplitItem it{x.x, x.y, x.z, x.w};
-  if (it.pieces == 0 || r0 >= it.rows) return;
-  Merged<D> m[ROWS];
-  for (int first = 0; first < it.pieces; first += BATCH) {
-    float2 ml[ROWS][BATCH];
-    float4 acc[ROWS][BATCH][Merged<D>::V];
+  if (it.pieces == 0) return;
+  for (int r0 = blockIdx.y * 8 * ROWS + (threadIdx.x >> 5); r0 < it.rows; r0 += gridDim.y * 8 * ROWS) {
+    Merged<D> m[ROWS];
+    for (int first = 0; first < it.pieces; first += BATCH) {
+      float2 ml[ROWS][BATCH];
+      float4 acc[ROWS][BATCH][Merged<D>::V];
 #pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-      const int r = r0 + 8 * k;
-      m[k].load(ml[k], acc[k], first, r < it.rows ? it.pieces : 0, [&](int i, const float2** a, const float** b) {
-        const size_t at = ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * p.slot_rows + r;
-        *a = p.slot_ml + at;
-        *b = p.slot_acc + at * D;
-      });
+      for (int k = 0; k < ROWS; ++k) {
+        const int r = r0 + 8 * k;
+        m[k].load(ml[k], acc[k], first, r < it.rows ? it.pieces : 0, [&](int i, const float2** a, const float** b) {
+          const size_t at = ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * p.slot_rows + r;
+          *a = p.slot_ml + at;
+          *b = p.slot_acc + at * D;
+        });
+      }
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) m[k].add(ml[k], acc[k]);
     }
 #pragma unroll
-    for (int k = 0; k < ROWS; ++k) m[k].add(ml[k], acc[k]);
-  }
-#pragma unroll
-  for (int k = 0; k < ROWS; ++k) {
-    const int r = r0 + 8 * k, tok = div_group(p, r);
-    if (r < it.rows)
-      m[k].store(static_cast<T*>(p.out) + ((size_t)(it.tok + tok) * p.Hq + it.kvh * p.G + r - tok * p.G) * D);
+    for (int k = 0; k < ROWS; ++k) {
+      const int r = r0 + 8 * k, tok = div_group(p, r);
+      if (r < it.rows)
+        m[k].store(static_cast<T*>(p.out) + ((size_t)(it.tok + tok) * p.Hq + it.kvh * p.G + r - tok * p.G) * D);
+    }
   }
 }
 
@@ -1373,10 +1376,10 @@ cudaError_t launch_attend_load(const AttendParams& p, const AttendMaps& maps, cu
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   if (!p.shared) {
-    const int rows = p.slot_rows > 64 ? 4 : 1;
-    cfg.gridDim = dim3(p.ctas, (p.slot_rows + 8 * rows - 1) / (8 * rows));
-    return rows == 4 ? cudaLaunchKernelEx(&cfg, merge_items_kernel<T, D, 4>, p)
-                     : cudaLaunchKernelEx(&cfg, merge_items_kernel<T, D, 1>, p);
+    const int parts = (p.slot_rows + 7) / 8;
+    cfg.gridDim = dim3(p.ctas, p.slot_rows > 64 ? kMergeParts : parts);
+    return p.slot_rows > 64 ? cudaLaunchKernelEx(&cfg, merge_items_kernel<T, D, 2>, p)
+                            : cudaLaunchKernelEx(&cfg, merge_items_kernel<T, D, 1>, p);
   }
   cfg.gridDim = dim3((unsigned)(((long long)p.T * p.Hq + 7) / 8));
   return cudaLaunchKernelEx(&cfg, merge_rows_kernel<T, D>, p);
