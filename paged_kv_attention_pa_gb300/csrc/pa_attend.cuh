@@ -65,14 +65,10 @@ struct AttendCfg {
   static constexpr int W_MMA = NSW, W_PLAN = NSW + 1, W_Q = NSW + 2, W_LOAD = NSW + 3;
   static constexpr int NLOAD = LOAD == kLoadTensor ? 4 : 8;
   static constexpr int READERS = NSW + 2 + NLOAD;  // warps that read the ring of items
-  // Registers: a CTA of 480 threads starts with 128 each. One with eight load warps and two groups of
-  // softmax warps (20 warps, the last idle) starts with 96, and its other warps give some to the
-  // softmax warps.
-  static constexpr bool kShift = LOAD != kLoadTensor && NWG == 2;
-  static constexpr int WARPS = LOAD == kLoadTensor ? NSW + 3 + NLOAD : (NSW + 3 + NLOAD + 3) / 4 * 4;
-  static constexpr int THREADS = WARPS * 32;
-  static constexpr int kStartRegs = 96, kSoftmaxRegs = 128, kOtherRegs = 72;
-  static_assert(!kShift || NSW * kSoftmaxRegs + (WARPS - NSW) * kOtherRegs <= WARPS * kStartRegs, "registers");
+  static constexpr int WARPS = NSW + 3 + NLOAD, THREADS = WARPS * 32;
+  // Scores that a softmax thread reads at a time: a CTA of 480 threads has 128 registers for each, one of
+  // 608 has 96.
+  static constexpr int CHUNK = NWG == 2 && NLOAD == 8 ? 16 : 32;
   static constexpr int ITEMS = 4;            // slots of that ring
   static constexpr int OFF_STAGE = NQ * QTILE;
   static constexpr int OFF_RAW = OFF_STAGE + NS * STAGE;
@@ -83,6 +79,12 @@ struct AttendCfg {
   // tensor memory: score buffers, then accumulators
   static constexpr int S_COL = 0, O_COL = 256;
   static_assert(2 * TN <= 256 && O_COL + NWG * D <= (int)kTmemColumns, "tensor memory");
+  // At head_dim 256 Q lies beside the score buffers, and the products take it from there: with 64 tokens
+  // a tile, a product of 128 x 64 x 16 from shared memory reads 6 KB in the time of 4, and took 55 cycles
+  // instead of 32 (500 rows over 3000 to 6500 tokens: MEASURED us, from tensor memory MEASURED).
+  static constexpr bool kQInTmem = D == 256;
+  static constexpr int Q_COL = 2 * TN;
+  static_assert(!kQInTmem || Q_COL + D / 2 <= O_COL, "Q in tensor memory");
   static constexpr float kSlack = 8.f;  // log2 units
   static constexpr float kLift = std::is_same_v<TM, __half> ? 6.f : 0.f;
 };
@@ -211,10 +213,9 @@ struct Item {
 
 // ------------------------------------------------------------------ waits
 // Wait for a phase of a barrier; false when it took over two seconds or another warp gave up. The
-// whole warp together. The slow part is a function of its own where the kernel has one register count
-// (inlined everywhere it cost 2%: 4096 rows over 8192 tokens 345 us, 352), and inlined where register
-// counts change, which function calls do not go with.
-__device__ __forceinline__ bool wait_loop(uint32_t bar, uint32_t parity, volatile int* give_up) {
+// whole warp together. (The slow part is a function of its own: inlined everywhere it cost 2%, 4096 rows
+// over 8192 tokens 352 us instead of 345.)
+static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* give_up) {
   const uint64_t t0 = global_ns();
   for (;;) {
     const bool over = global_ns() - t0 >= 2000000000ull || *give_up != 0;
@@ -226,20 +227,16 @@ __device__ __forceinline__ bool wait_loop(uint32_t bar, uint32_t parity, volatil
     }
   }
 }
-static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* give_up) {
-  return wait_loop(bar, parity, give_up);
-}
-template <bool INLINE>
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* give_up) {
   if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
-  return INLINE ? wait_loop(bar, parity, give_up) : wait_long(bar, parity, give_up);
+  return wait_long(bar, parity, give_up);
 }
 
 // ------------------------------------------------------------------ shared memory
 template <typename C>
 struct AttendShared {
   uint64_t kv_full[C::NS], kv_empty[C::NS];
-  uint64_t q_raw[C::NQ], q_full[C::NQ], q_empty[C::NQ];
+  uint64_t q_raw[C::NQ], q_full[C::NQ], q_empty[C::NQ], q_tmem;
   uint64_t s_full[2], p_full[2];
   uint64_t pv_done[2];  // by the step's score buffer
   uint64_t item_full[C::ITEMS], item_empty[C::ITEMS];
@@ -253,8 +250,10 @@ struct AttendShared {
   long long scan[32];
 };
 
-#define PA_WAIT(bar, parity) \
-  if (!wait_for<C::kShift>(smem_addr(&(bar)), (parity), &sh.give_up)) return
+#define PA_WAIT(bar, parity)                                          \
+  do {                                                                \
+    if (!wait_for(smem_addr(&(bar)), (parity), &sh.give_up)) return;  \
+  } while (0)
 
 // ------------------------------------------------------------------ plan
 // Every CTA finds the first unit of its run: a sum over the segments' units. CTA 0 writes what the
@@ -315,13 +314,15 @@ __device__ __forceinline__ void plan_work(const AttendParams& p, AttendShared<C>
   }
   if (lane == 31) sh.scan[warp] = upto;
   __syncthreads();
-  long long total = 0;
+  long long total = lane < C::WARPS ? sh.scan[lane] : 0;  // then the inclusive sum over the warps
 #pragma unroll
-  for (int w = 0; w < C::WARPS; ++w) {
-    const long long x = sh.scan[w];
-    if (w < warp) upto += x;
-    total += x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, total, o);
+    if (lane >= o) total += x;
   }
+  const long long warps_before = __shfl_sync(0xffffffffu, total, warp - 1 & 31);
+  if (warp > 0) upto += warps_before;
+  total = __shfl_sync(0xffffffffu, total, 31);
   const long long per = max((long long)kLeastUnits, quotient(total + p.ctas - 1, p.ctas));
   const long long from = per * blockIdx.x;
   if (tid == 0) {
@@ -440,7 +441,7 @@ __device__ __forceinline__ void plan_role(const AttendParams& p, AttendShared<C>
 template <typename C>
 __device__ __forceinline__ bool next_item(AttendShared<C>& sh, uint32_t& count, Item& it) {
   const int slot = count % C::ITEMS;
-  if (!wait_for<C::kShift>(smem_addr(&sh.item_full[slot]), (count / C::ITEMS) & 1, &sh.give_up)) return false;
+  if (!wait_for(smem_addr(&sh.item_full[slot]), (count / C::ITEMS) & 1, &sh.give_up)) return false;
   it = sh.items[slot];
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&sh.item_empty[slot]));
@@ -607,7 +608,7 @@ struct RowLoader {
     if (lane == 0) mbar_arrive(smem_addr(&sh.kv_full[place % C::NS]));
   }
   __device__ __forceinline__ bool room(uint32_t place) {
-    return wait_for<C::kShift>(smem_addr(&sh.kv_empty[place % C::NS]), ((place / C::NS) & 1) ^ 1, &sh.give_up);
+    return wait_for(smem_addr(&sh.kv_empty[place % C::NS]), ((place / C::NS) & 1) ^ 1, &sh.give_up);
   }
 };
 
@@ -759,7 +760,7 @@ __device__ __forceinline__ void product_role(const AttendParams& p, AttendShared
                  v_lo = (uint32_t)by_n + (smem_addr(stages) >> 4);
   const uint32_t k_hi = (uint32_t)(by_k >> 32), v_hi = (uint32_t)(by_n >> 32);
   // a negative scale: the scores of -Q
-  const uint32_t for_scores = mma_desc<TM>(C::TN, false) | (p.negate ? kNegateA : 0u);
+  const uint32_t for_scores = mma_desc<TM>(C::TN, false) | (p.negate && !C::kQInTmem ? kNegateA : 0u);
   constexpr uint32_t kForValues = mma_desc<TM>(D, true);
   const uint32_t on = elected();
   uint32_t count = 0, used = 0;  // items, query tiles
@@ -768,7 +769,7 @@ __device__ __forceinline__ void product_role(const AttendParams& p, AttendShared
   Item it;
   auto next_tile = [&](uint32_t& which) -> bool {
     which = stage;
-    if (!wait_for<C::kShift>(smem_addr(&sh.kv_full[stage]), lap, &sh.give_up)) return false;
+    if (!wait_for(smem_addr(&sh.kv_full[stage]), lap, &sh.give_up)) return false;
     if (++stage == C::NS) {
       stage = 0;
       lap ^= 1;
@@ -780,7 +781,11 @@ __device__ __forceinline__ void product_role(const AttendParams& p, AttendShared
     const int dup = __any_sync(0xffffffffu, two_row_tiles<C>(p, it)) ? 1 : 0;
     const int steps = tiles << dup;
     const uint32_t q0 = used % C::NQ, q1 = (used + dup) % C::NQ;
-    for (int i = 0; i <= dup; ++i) PA_WAIT(sh.q_full[(used + i) % C::NQ], ((used + i) / C::NQ) & 1);
+    if constexpr (C::kQInTmem) {
+      PA_WAIT(sh.q_tmem, used & 1);
+    } else {
+      for (int i = 0; i <= dup; ++i) PA_WAIT(sh.q_full[(used + i) % C::NQ], ((used + i) / C::NQ) & 1);
+    }
     used += 1 + dup;
     uint32_t k_stage = 0, v_stage = 0;
     auto scores = [&](int i) -> bool {  // step i: S = Q K^T
@@ -790,12 +795,17 @@ __device__ __forceinline__ void product_role(const AttendParams& p, AttendShared
       const uint32_t a = q_lo + q_tile * (C::QTILE >> 4), b = k_lo + k_stage * (C::STAGE >> 4);
       const uint32_t d = tmem + C::S_COL + (i & 1) * C::TN;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss(on, d, a + (((kk / 4) * (128 * 128) + (kk % 4) * 32) >> 4), k_hi,
-               b + (((kk / 4) * (C::TN * 128) + (kk % 4) * 32) >> 4), k_hi, for_scores, kk > 0);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t bk = b + (((kk / 4) * (C::TN * 128) + (kk % 4) * 32) >> 4);
+        if constexpr (C::kQInTmem)
+          mma_ts(on, d, tmem + C::Q_COL + kk * 8, bk, k_hi, for_scores, kk > 0);
+        else
+          mma_ss(on, d, a + (((kk / 4) * (128 * 128) + (kk % 4) * 32) >> 4), k_hi, bk, k_hi, for_scores, kk > 0);
+      }
       mma_commit(on, smem_addr(&sh.s_full[i & 1]));
       if (dup == 0 || (i & 1)) mma_commit(on, smem_addr(&sh.kv_empty[k_stage]));
-      if (i >= steps - 1 - dup) mma_commit(on, smem_addr(&sh.q_empty[q_tile]));  // its row tile's last
+      if (!C::kQInTmem && i >= steps - 1 - dup)  // its row tile's last
+        mma_commit(on, smem_addr(&sh.q_empty[q_tile]));
       return true;
     };
     for (int i = 0; i < 2 && i < steps; ++i)
@@ -825,10 +835,10 @@ __device__ __forceinline__ void product_role(const AttendParams& p, AttendShared
 // ------------------------------------------------------------------ softmax
 // One thread per row of a row tile.
 template <typename C, typename T, int D, bool ZERO_V>
-__device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared<C>& sh, uint8_t* stages,
-                                             uint32_t tmem) {
+__device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared<C>& sh, uint8_t* q_tiles,
+                                             uint8_t* stages, uint32_t tmem) {
   using TM = typename C::TM;
-  constexpr int NC = C::TN / 32;
+  constexpr int W = C::CHUNK, NC = C::TN / W;
   const int lane = threadIdx.x & 31, group = threadIdx.x >> 7, at = threadIdx.x & 127;
   const uint32_t lanes = (uint32_t)((threadIdx.x >> 5) & 3) << 21;  // 32 (warp % 4) in the upper half
   const uint32_t own_o = tmem + C::O_COL + group * D + lanes;
@@ -837,6 +847,38 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
   // ring, and what is needed of it after its steps is read again; parities are bits of one word, 0 and
   // 1 the score buffers', 2 the pair barrier's.
   uint32_t count = 0, parities = 0, tiles_before = 0;
+  // The queries of item n, if there is one, into tensor memory: when no product reads those of the item
+  // before any more. A negative scale negates them.
+  auto place_queries = [&](uint32_t n) -> bool {
+    if (!wait_for(smem_addr(&sh.item_full[n % C::ITEMS]), (n / C::ITEMS) & 1, &sh.give_up)) return false;
+    if (sh.items[n % C::ITEMS].tiles == 0) return true;
+    if (!wait_for(smem_addr(&sh.q_full[0]), n & 1, &sh.give_up)) return false;
+    const uint32_t row = smem_addr(q_tiles) + at * 128, sign = p.negate ? 0x80008000u : 0u;
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = 0; c < D / 8; c += 4) {
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 x = lds128(row + (c >> 3) * (128 * 128) + ((((c & 7) + j) ^ (at & 7)) << 4));
+        w[4 * j] = x.x ^ sign;
+        w[4 * j + 1] = x.y ^ sign;
+        w[4 * j + 2] = x.z ^ sign;
+        w[4 * j + 3] = x.w ^ sign;
+      }
+      tmem_store(tmem + C::Q_COL + 4 * c + lanes, w);
+    }
+    tmem_stored();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(smem_addr(&sh.q_tmem));
+      mbar_arrive(smem_addr(&sh.q_empty[0]));
+    }
+    return true;
+  };
+  if constexpr (C::kQInTmem)
+    if (!place_queries(0)) return;
   for (;; ++count) {
     const Item& it = sh.items[count % C::ITEMS];
     PA_WAIT(sh.item_full[count % C::ITEMS], (count / C::ITEMS) & 1);
@@ -868,30 +910,30 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
       if (warp_live) {
         tc_fence_after();
         const int c0 = lo - t0, c1 = end - t0;  // columns [c0, c1) are seen
-        uint32_t x[2][32];
+        uint32_t x[2][W];
         if (!__all_sync(0xffffffffu, !live || (c0 <= 0 && c1 >= C::TN))) {
           // scores of tokens that the row does not see become -inf, whatever they are
 #pragma unroll 1
-          for (int c = 0; c < C::TN; c += 32) {
-            tmem_load32(x[0], s_at + c);
+          for (int c = 0; c < C::TN; c += W) {
+            tmem_load(x[0], s_at + c);
             tmem_loaded(x[0]);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < W; ++j)
               if (c + j < c0 || c + j >= c1) x[0][j] = 0xff800000u;
-            tmem_store32(s_at + c, x[0]);
+            tmem_store(s_at + c, x[0]);
           }
           tmem_stored();
         }
         // the largest score, scaled
         float most[2] = {-INFINITY, -INFINITY};
-        tmem_load32(x[0], s_at);
+        tmem_load(x[0], s_at);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          uint32_t(&y)[32] = x[c & 1];
+          uint32_t(&y)[W] = x[c & 1];
           tmem_loaded(y);
-          tmem_load32(x[(c + 1) & 1], s_at + 32 * ((c + 1) % NC));  // the last one: the first columns again
+          tmem_load(x[(c + 1) & 1], s_at + W * ((c + 1) % NC));  // the last one: the first columns again
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
+          for (int j = 0; j < W; j += 4) {
             most[0] = fmaxf(fmaxf(most[0], __uint_as_float(y[j])), __uint_as_float(y[j + 1]));
             most[1] = fmaxf(fmaxf(most[1], __uint_as_float(y[j + 2])), __uint_as_float(y[j + 3]));
           }
@@ -908,15 +950,15 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
             PA_WAIT(sh.pv_done[last], (parities >> last & 1) ^ (C::NWG == 2 ? 0 : 1));
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_load32(o, own_o + 32 * c);
+            for (int c = 0; c < D; c += W) {
+              uint32_t o[W];
+              tmem_load(o, own_o + c);
               tmem_loaded(o);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_store32(own_o + 32 * c, o);
+              for (int j = 0; j < W; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_store(own_o + c, o);
             }
-            tmem_load32(x[NC & 1], s_at);  // read again rather than kept across the wait
+            tmem_load(x[NC & 1], s_at);  // read again rather than kept across the wait
           }
         }
         const float sub = ref == -INFINITY ? 0.f : -ref;
@@ -924,11 +966,11 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
         float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          uint32_t(&y)[32] = x[(NC + c) & 1];
+          uint32_t(&y)[W] = x[(NC + c) & 1];
           tmem_loaded(y);
-          if (c + 1 < NC) tmem_load32(x[(NC + c + 1) & 1], s_at + 32 * (c + 1));
+          if (c + 1 < NC) tmem_load(x[(NC + c + 1) & 1], s_at + W * (c + 1));
 #pragma unroll
-          for (int k = 0; k < 32; k += 16) {
+          for (int k = 0; k < W; k += 16) {
             uint32_t w[8];
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
@@ -939,7 +981,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
               w[j / 2] = pack2<TM>(e.x, e.y);
             }
             // over columns of scores that are in registers already
-            tmem_store8(s_at + 16 * c + k / 2, w);
+            tmem_store(s_at + (W * c + k) / 2, w);
           }
         }
         const float2 both = add2(part[0], part[1]);
@@ -965,6 +1007,8 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
       if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[buf]));
     }
     tiles_before += 2 * tiles;
+    if constexpr (C::kQInTmem)  // while the last product runs
+      if (!place_queries(count + 1)) return;
 
     // ---- the item's rows: O / sum, or (reference, sum, O) of a piece
     if (any) {
@@ -1015,16 +1059,16 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
       const int from = joint ? group * (D / 2) : 0, to = joint ? from + D / 2 : D;
       const uint32_t other_o = tmem + C::O_COL + (group ^ 1) * D + lanes;
 #pragma unroll 1
-      for (int c = from; c < to; c += 32) {
-        uint32_t o[32];
-        tmem_load32(o, own_o + c);
+      for (int c = from; c < to; c += W) {
+        uint32_t o[W];
+        tmem_load(o, own_o + c);
         tmem_loaded(o);
         if (joint) {
-          uint32_t o2[32];
-          tmem_load32(o2, other_o + c);
+          uint32_t o2[W];
+          tmem_load(o2, other_o + c);
           tmem_loaded(o2);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {  // an accumulator that saw no token may hold anything
+          for (int j = 0; j < W; ++j) {  // an accumulator that saw no token may hold anything
             const float a = f_own > 0.f ? __uint_as_float(o[j]) * f_own : 0.f;
             const float b = f_other > 0.f ? __uint_as_float(o2[j]) * f_other : 0.f;
             o[j] = __float_as_uint(a + b);
@@ -1034,7 +1078,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
           if (whole) {
             T* dst = static_cast<T*>(p.out) + row * D + c;
 #pragma unroll
-            for (int j = 0; j < 32; j += 16) {
+            for (int j = 0; j < W; j += 16) {
               uint32_t w[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -1051,7 +1095,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
           } else {
             float* dst = acc + part * D + c;
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
+            for (int j = 0; j < W; j += 8) {
               uint32_t w[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__uint_as_float(o[j + i]) * mul);
@@ -1098,7 +1142,8 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
     init(sh.kv_empty, C::NS, 1);
     init(sh.q_raw, C::NQ, 1);
     init(sh.q_full, C::NQ, 1);
-    init(sh.q_empty, C::NQ, 1);
+    init(sh.q_empty, C::NQ, C::kQInTmem ? 4 : 1);
+    init(&sh.q_tmem, 1, 4);
     init(sh.s_full, 2, 1);
     init(sh.p_full, 2, 4);
     init(sh.pv_done, 2, 1);
@@ -1123,16 +1168,8 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  if constexpr (C::kShift) {
-    if (warp < C::NSW)
-      take_registers<C::kSoftmaxRegs>();
-    else
-      give_registers<C::kOtherRegs>();
-  }
   if (warp < C::NSW)
-    softmax_role<C, T, D, LOAD == kLoadTensor>(p, sh, stages, tmem);
-  else if (warp >= C::W_LOAD + C::NLOAD)
-    ;  // fills the last group of four
+    softmax_role<C, T, D, LOAD == kLoadTensor>(p, sh, q_tiles, stages, tmem);
   else if (warp == C::W_MMA)
     product_role<C, D>(p, sh, q_tiles, stages, tmem);
   else if (warp == C::W_PLAN)
@@ -1351,12 +1388,6 @@ cudaError_t launch_attend_load(const AttendParams& p, const AttendMaps& maps, cu
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & bit)) {
-    if constexpr (C::kShift) {  // registers that the CTA does not start with would be waited for without end
-      cudaFuncAttributes attrs{};
-      e = cudaFuncGetAttributes(&attrs, kern);
-      if (e != cudaSuccess) return e;
-      if (attrs.numRegs < C::kStartRegs) return cudaErrorInvalidKernelImage;
-    }
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&done_mask, bit, __ATOMIC_ACQ_REL);
