@@ -98,7 +98,8 @@ typedef enum pa_kv_dtype {
 /* Bits of the device error word (workspace header). */
 #define PA_DEVERR_BLOCK_INDEX 1u /* a live token's block table entry was outside [0, num_blocks) */
 #define PA_DEVERR_SEQ_LEN 2u     /* a seq_len < 0, > max_seq_len or > max_blocks_per_seq*block_size */
-#define PA_DEVERR_COPY 4u        /* a copy into shared memory took over two seconds: no meaningful output */
+#define PA_DEVERR_COPY 4u        /* a copy into shared memory, or a wait for another part of the kernel,
+                                    took over two seconds: no meaningful output */
 #define PA_DEVERR_ROWS 8u        /* pa_cross, pa_decode_shared: starts or groups that do not ascend, or
                                     reach past the call's rows or sequences */
 
@@ -436,8 +437,8 @@ pa_status pa_gather(const pa_gather_args* args, void* workspace, size_t workspac
  *             least Hq * D), the heads of a row are dense
  *   starts    as for pa_append: NULL, and sequence b has the `rows` rows b * rows + i; or [B + 1]
  *             ascending int32 on the device, and `rows` is the number of rows in all. Rows of no
- *             sequence are padding: neither read nor written in out
- *   out       dense [rows, Hq, D]; rows over an empty context (seq_lens[b] = 0) are zero
+ *             sequence are padding, left alone in out
+ *   out       dense [rows, Hq, D], apart from q; rows over an empty context (seq_lens[b] = 0) are zero
  *   k_cache, v_cache, block_tables, seq_lens, max_seq_len, kv_dtype, k_scale, v_scale
  *             as for pa_decode_ex, with 16-bit and fp8 caches (with fp8 the queries are rounded to
  *             fp16: |x| <= 65504). 4-bit caches: PA_ERR_UNSUPPORTED
@@ -475,7 +476,8 @@ pa_status pa_cross(const pa_cross_args* args, void* workspace, size_t workspace_
 /*
  * Decode for sequences that share prefixes: pa_decode_ex's result, with the keys and values of a
  * shared prefix read once for all sequences of its group.
- *   args         as for pa_decode_ex, with q_len causal query rows per sequence (any number);
+ *   args         as for pa_decode_ex, with q_len causal query rows per sequence (any number) and out
+ *                apart from q;
  *                16-bit and fp8 caches (4 bits: PA_ERR_UNSUPPORTED); splits and window must be 0
  *   groups       [num_groups + 1] ascending int32 on the device: sequences groups[n] to
  *                groups[n + 1] - 1 are group n. Sequences of no group share nothing

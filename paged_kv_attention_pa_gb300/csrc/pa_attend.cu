@@ -114,6 +114,10 @@ bool make_map(CUtensorMap* map, const Call& c, const void* at, int64_t rows, int
 pa_status run(const Call& c, AttendParams& p, int cap, void* workspace, size_t bytes, pa_stream_t stream) {
   if (!c.q || !c.k_cache || !c.v_cache || !c.block_tables || !c.seq_lens || !c.out) return PA_ERR_INVALID_ARG;
   if (!aligned16(c.q) || !aligned16(c.k_cache) || !aligned16(c.v_cache) || !aligned16(c.out)) return PA_ERR_INVALID_ARG;
+  // rows of out are written while other rows' queries are still read
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(c.q), o0 = reinterpret_cast<uintptr_t>(c.out);
+  const uintptr_t row = (uintptr_t)c.Hq * c.D * 2, q1 = q0 + (uintptr_t)(c.T - 1) * c.q_stride * 2 + row;
+  if (q0 < o0 + (uintptr_t)c.T * row && o0 < q1) return PA_ERR_INVALID_ARG;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PA_ERR_WORKSPACE;
   const int sms = current_sm_count();
   if (sms <= 0) return PA_ERR_CUDA;

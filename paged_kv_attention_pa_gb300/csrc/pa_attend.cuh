@@ -1037,7 +1037,8 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
     }
     if (warp_live) {
       const bool whole = it.dest == kDirect;
-      const float mul = whole ? (sum > 0.f ? p.v_scale / sum : 0.f) : p.v_scale;
+      // a row that sees no token is zero (and whatever its accumulator holds); one with a NaN is NaN
+      const float mul = whole ? (sum == 0.f ? 0.f : p.v_scale / sum) : p.v_scale;
       const int tok = it.tok + div_group(p, r), head = it.kvh * p.G + r - div_group(p, r) * p.G;
       const size_t row = live ? (size_t)tok * p.Hq + head : 0;
       size_t part = 0;  // row of the partials
@@ -1083,7 +1084,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const float a = __uint_as_float(o[j + 2 * i]), b = __uint_as_float(o[j + 2 * i + 1]);
-                w[i] = pack2<T>(sum > 0.f ? a * mul : 0.f, sum > 0.f ? b * mul : 0.f);
+                w[i] = pack2<T>(sum == 0.f ? 0.f : a * mul, sum == 0.f ? 0.f : b * mul);
               }
               if (p.out_wide) {
                 store32(dst + j, w);
@@ -1246,7 +1247,7 @@ struct Merged {
     for (int j = 0; j < V; ++j) v[j] = make_float4(v[j].x * f, v[j].y * f, v[j].z * f, v[j].w * f);
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      if (x[i].x == -INFINITY) continue;  // none, or it saw no token of the row: its output may be anything
+      if (x[i].y == 0.f) continue;  // none, or it saw no token of the row: its output may be anything
       const float w = exp2_approx(x[i].x - top);
       sum += w * x[i].y;
 #pragma unroll
@@ -1260,7 +1261,7 @@ struct Merged {
   }
   template <typename T>
   __device__ __forceinline__ void store(T* out) const {
-    const float f = sum > 0.f ? 1.f / sum : 0.f;
+    const float f = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int j = 0; j < V; ++j)
       *reinterpret_cast<uint2*>(out + 128 * j + 4 * (threadIdx.x & 31)) =
