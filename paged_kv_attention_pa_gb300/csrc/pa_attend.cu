@@ -146,6 +146,7 @@ pa_status run(const Call& c, AttendParams& p, int cap, void* workspace, size_t b
   // r (m G - 2^32) < 2^16 * 16 < 2^32 with m = ceil(2^32 / G): floor(r m / 2^32) = floor(r / G)
   p.g_magic = p.G == 1 ? 0u : (uint32_t)(((1ull << 32) + p.G - 1) / p.G);
   p.tile_tokens = 128 / p.G;
+  p.spread_tokens = 32 / p.G;
   p.out_wide = (reinterpret_cast<uintptr_t>(c.out) & 31u) == 0;
   p.block_size = c.block_size;
   p.num_blocks = c.num_blocks;
@@ -167,7 +168,9 @@ pa_status run(const Call& c, AttendParams& p, int cap, void* workspace, size_t b
   const AttendLoad load =
       fp8 ? kLoadFp8 : p.box >= 8 && (int64_t)c.num_blocks * c.block_size <= INT_MAX ? kLoadTensor : kLoad16;
   AttendMaps maps{};
-  if (!make_map(&maps.q, c, c.q, c.T, c.T > 1 ? c.q_stride : (int64_t)c.Hq * c.D, c.Hq, p.tile_tokens, p.G))
+  const int64_t q_stride = c.T > 1 ? c.q_stride : (int64_t)c.Hq * c.D;
+  if (!make_map(&maps.q, c, c.q, c.T, q_stride, c.Hq, p.tile_tokens, p.G) ||
+      !make_map(&maps.q_spread, c, c.q, c.T, q_stride, c.Hq, p.spread_tokens, p.G))
     return PA_ERR_CUDA;
   if (load == kLoadTensor) {
     const int64_t tokens = (int64_t)c.num_blocks * c.block_size, stride = (int64_t)c.Hkv * c.D;

@@ -81,10 +81,12 @@ struct AttendCfg {
   static_assert(2 * TN <= 256 && O_COL + NWG * D <= (int)kTmemColumns, "tensor memory");
   // At head_dim 256 Q lies beside the score buffers, and the products take it from there: with 64 tokens
   // a tile, a product of 128 x 64 x 16 from shared memory reads 6 KB in the time of 4, and took 55 cycles
-  // instead of 32 (500 rows over 3000 to 6500 tokens: MEASURED us, from tensor memory MEASURED).
+  // instead of 32 (500 rows of 24 heads over 3000 to 6500 tokens, two sequences: 106 us, from tensor memory 96).
   static constexpr bool kQInTmem = D == 256;
   static constexpr int Q_COL = 2 * TN;
   static_assert(!kQInTmem || Q_COL + D / 2 <= O_COL, "Q in tensor memory");
+  static constexpr bool kSpread = LOAD == kLoadFp8;        // items of few rows, see spread_rows
+  static constexpr int kSpreadTiles = D == 128 ? 6 : 1;
   static constexpr float kSlack = 8.f;  // log2 units
   static constexpr float kLift = std::is_same_v<TM, __half> ? 6.f : 0.f;
 };
@@ -326,6 +328,7 @@ __device__ __forceinline__ void plan_work(const AttendParams& p, AttendShared<C>
   const long long per = max((long long)kLeastUnits, quotient(total + p.ctas - 1, p.ctas));
   const long long from = per * blockIdx.x;
   if (tid == 0) {
+    p.split[blockIdx.x].pieces = 0;  // until the plan warp finds one
     sh.per = per;
     sh.total = total;
     if (from >= total) sh.first_segment = n;
@@ -366,7 +369,7 @@ __device__ __forceinline__ void plan_role(const AttendParams& p, AttendShared<C>
   uint32_t count = 0;
   const int n = segment_count(p);
   long long at = sh.first_unit;
-  bool first = true, split = false;
+  bool first = true;
   int held = -2;  // the group read last
   Group group{};
   for (int s = sh.first_segment; s < n && at < hi; ++s) {
@@ -418,7 +421,6 @@ __device__ __forceinline__ void plan_role(const AttendParams& p, AttendShared<C>
           if (it.dest == kSlotFirst) {
             const long long last = min((long long)p.ctas - 1, quotient(u + (long long)w * (z.tiles - 1), sh.per));
             p.split[blockIdx.x] = SplitItem{it.tok, it.rows, kvh, (int)last - (int)blockIdx.x + 1};
-            split = true;
           }
         }
         __syncwarp();
@@ -431,7 +433,6 @@ __device__ __forceinline__ void plan_role(const AttendParams& p, AttendShared<C>
   const int slot = count % C::ITEMS;
   PA_WAIT(sh.item_empty[slot], ((count / C::ITEMS) & 1) ^ 1);
   if (lane == 0) {
-    if (!split) p.split[blockIdx.x].pieces = 0;
     sh.items[slot].tiles = 0;
     mbar_arrive(smem_addr(&sh.item_full[slot]));
   }
@@ -453,6 +454,19 @@ __device__ __forceinline__ bool next_item(AttendShared<C>& sh, uint32_t& count, 
 template <typename C>
 __device__ __forceinline__ bool two_row_tiles(const AttendParams& p, const Item& it) {
   return C::NWG == 2 && it.rows > p.tile_tokens * p.G;
+}
+
+// An fp8 item whose rows fit in a warp is spread: the row tile holds them four times, and each of a
+// group's four warps, which reach 32 rows each, sees a quarter of a tile's tokens: the weights of the others
+// are zero in its rows. One warp for all tokens, while three have nothing to do, is slower than fp8 tiles come
+// in: 24 sequences of 14 rows a KV head over 1000 to 6000 tokens took 102 us, 93 spread, 16 of 6 rows of 256
+// behind two prefixes 63 and 47. 16-bit tiles take twice as long to come: 64 sequences 67.3 us, 69.1 spread.
+// The states of the warps are joined behind an item's last tile, which costs more than it saves in short ones:
+// 128 contexts of 16 to 700 tokens behind a document took 118.0 us with all of them spread, 116.6 with those of
+// 6 tiles and more.
+template <typename C>
+__device__ __forceinline__ bool spread_rows(const AttendParams& p, const Item& it) {
+  return C::kSpread && it.rows <= p.spread_tokens * p.G && it.tiles >= C::kSpreadTiles;
 }
 
 // ------------------------------------------------------------------ load
@@ -685,12 +699,8 @@ __device__ __forceinline__ void fp8_load_role(const AttendParams& p, bool is_k, 
       hi.w = e4m3x2_to_half2(x.w >> 16);
       // lanes of odd panels write their upper half first: eight lanes of a row then fill a row
       const bool odd = lane % Loader::CPR * 2 >> 3 & 1;
-      auto put = [&](uint32_t a, const uint4& y) {
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
-                     : "memory");
-      };
-      put(a ^ (odd ? 16 : 0), odd ? hi : lo);
-      put(a ^ (odd ? 0 : 16), odd ? lo : hi);
+      sts128(a ^ (odd ? 16 : 0), odd ? hi : lo);
+      sts128(a ^ (odd ? 0 : 16), odd ? lo : hi);
     }
     L.landed(n);
     ++done;
@@ -701,17 +711,21 @@ __device__ __forceinline__ void fp8_load_role(const AttendParams& p, bool is_k, 
 // ------------------------------------------------------------------ queries
 // A tensor copy per panel brings 128 / G tokens with the G heads of the KV head, token after token
 // (those past the item's rows are other sequences', or zeros behind the last one: rows nobody reads).
-// bf16 queries of an fp8 cache are then rounded to fp16 in place.
+// bf16 queries of an fp8 cache are then rounded to fp16 in place. Spread items have smaller copies, four
+// of them where the products read the tile (at head_dim 256 its rows go to tensor memory first).
 template <typename C, typename T, int D>
-__device__ __forceinline__ void query_role(const AttendParams& p, const CUtensorMap* map, AttendShared<C>& sh,
+__device__ __forceinline__ void query_role(const AttendParams& p, const AttendMaps& maps, AttendShared<C>& sh,
                                            uint8_t* tiles) {
   constexpr bool kConvert = !std::is_same_v<T, typename C::TM>;
+  constexpr int kTimes = C::kQInTmem ? 1 : 4;  // a spread item's rows in the tile
   const int lane = threadIdx.x & 31;
-  const uint32_t bytes = p.tile_tokens * p.G * D * 2;
   uint32_t count = 0, used = 0;
   Item it;
   while (next_item(sh, count, it)) {
     const int n = two_row_tiles<C>(p, it) ? 2 : 1;
+    const bool spread = spread_rows<C>(p, it);
+    const int times = spread && !kConvert ? kTimes : 1;
+    const uint32_t bytes = (spread ? p.spread_tokens : p.tile_tokens) * p.G * D * 2 * times;
     for (int i = 0; i < n; ++i, ++used) {
       const int slot = used % C::NQ;
       const uint32_t lap = (used / C::NQ) & 1;
@@ -720,15 +734,18 @@ __device__ __forceinline__ void query_role(const AttendParams& p, const CUtensor
       const uint32_t tile = smem_addr(tiles) + slot * C::QTILE;
       if (lane == 0) mbar_expect(smem_addr(bar), bytes);
       __syncwarp();
-      if (lane < C::PANELS)
-        tensor_load3(tile + lane * (128 * 128), map, smem_addr(bar), lane * 64, it.kvh * p.G,
-                     it.tok + i * p.tile_tokens);
+      if (lane < C::PANELS * times) {
+        const int c = lane % C::PANELS;
+        tensor_load3(tile + c * (128 * 128) + lane / C::PANELS * (32 * 128), spread ? &maps.q_spread : &maps.q,
+                     smem_addr(bar), c * 64, it.kvh * p.G, it.tok + i * p.tile_tokens);
+      }
       if constexpr (kConvert) {
         PA_WAIT(*bar, lap);
-        const int rows = p.tile_tokens * p.G;
+        const int tile_rows = p.tile_tokens * p.G, rows = min(tile_rows, it.rows - i * tile_rows);
 #pragma unroll 4
         for (int f = lane; f < rows * (D / 8); f += 32) {
-          const uint32_t a = tile + (f / (rows * 8)) * (128 * 128) + (f % (rows * 8)) * 16;
+          const int c = f % (D / 8);
+          const uint32_t a = tile + (c / 8) * (128 * 128) + f / (D / 8) * 128 + c % 8 * 16;
           uint4 x = lds128(a);
           uint32_t* w = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
@@ -736,8 +753,7 @@ __device__ __forceinline__ void query_role(const AttendParams& p, const CUtensor
             const float2 y = unpack2<T>(w[j]);
             w[j] = pack2<typename C::TM>(y.x, y.y);
           }
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
-                       : "memory");
+          for (int k = 0; k < (spread ? kTimes : 1); ++k) sts128(a + k * (32 * 128), x);
         }
         async_proxy_fence();
         __syncwarp();
@@ -780,6 +796,7 @@ __device__ __forceinline__ void product_role(const AttendParams& p, AttendShared
     const int tiles = __reduce_max_sync(0xffffffffu, it.tiles);
     const int dup = __any_sync(0xffffffffu, two_row_tiles<C>(p, it)) ? 1 : 0;
     const int steps = tiles << dup;
+    const int spread = __any_sync(0xffffffffu, spread_rows<C>(p, it));
     const uint32_t q0 = used % C::NQ, q1 = (used + dup) % C::NQ;
     if constexpr (C::kQInTmem) {
       PA_WAIT(sh.q_tmem, used & 1);
@@ -804,7 +821,7 @@ __device__ __forceinline__ void product_role(const AttendParams& p, AttendShared
       }
       mma_commit(on, smem_addr(&sh.s_full[i & 1]));
       if (dup == 0 || (i & 1)) mma_commit(on, smem_addr(&sh.kv_empty[k_stage]));
-      if (!C::kQInTmem && i >= steps - 1 - dup)  // its row tile's last
+      if (!C::kQInTmem && i >= steps - 1 - dup && !spread)  // its row tile's last
         mma_commit(on, smem_addr(&sh.q_empty[q_tile]));
       return true;
     };
@@ -833,6 +850,209 @@ __device__ __forceinline__ void product_role(const AttendParams& p, AttendShared
 }
 
 // ------------------------------------------------------------------ softmax
+__host__ __device__ constexpr int ilog2(int x) { return x <= 1 ? 0 : 1 + ilog2(x / 2); }
+
+// All softmax warps of the CTA meet. Bit 2 of parities is the barrier's.
+template <typename C>
+__device__ __forceinline__ bool meet(AttendShared<C>& sh, uint32_t& parities) {
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&sh.pair));
+  if (!wait_for(smem_addr(&sh.pair), parities >> 2 & 1, &sh.give_up)) return false;
+  parities ^= 4;
+  tc_fence_after();
+  return true;
+}
+
+// The end of the context that query row r of an item sees, of a live row: causal among the new rows.
+__device__ __forceinline__ int seen_to(const AttendParams& p, const Item& it, int r) {
+  if (!p.shared) return it.hi;
+  const int tok = it.tok + div_group(p, r), b = p.R == 1 ? tok : tok / p.R;
+  const int L = it.of_prefix ? clamp_len(p, b) : it.hi;  // the end of its own segment
+  return min(it.hi, L - p.R + 1 + (tok - b * p.R));
+}
+
+// A spread item: a thread has a row's scores over a quarter of each tile of its group.
+template <typename C, typename T, int D, typename Next>
+__device__ __forceinline__ bool spread_item(const AttendParams& p, AttendShared<C>& sh, const Item& it, uint8_t* q_tiles,
+                                          uint32_t tmem, uint32_t& parities, const Next& place_next) {
+  using TM = typename C::TM;
+  static_assert(!C::kSpread || C::KVB == 1, "V rows outside the context are zeros already");
+  constexpr int N = C::TN / 4;      // the warp's columns of a tile
+  constexpr int HALF = D / C::NWG;  // the group's columns of the output
+  constexpr int W = 16;
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 7, at = threadIdx.x & 127, quarter = at >> 5;
+  const uint32_t lanes = (uint32_t)quarter << 21;
+  const uint32_t own_o = tmem + C::O_COL + group * D + lanes, other_o = tmem + C::O_COL + (group ^ 1) * D + lanes;
+  const float sl2 = p.scale_log2;
+  const bool live = lane < it.rows;
+  const int end = live ? seen_to(p, it, lane) : it.lo;
+  float ref = -INFINITY, sum = 0.f;
+  int i = C::NWG == 2 ? group : 0;
+  const bool any = i < it.tiles;
+  for (; i < it.tiles; i += C::NWG) {
+    const int buf = i & 1;
+    const uint32_t s_at = tmem + C::S_COL + buf * C::TN + lanes;
+    if (!wait_for(smem_addr(&sh.s_full[buf]), (parities >> buf) & 1, &sh.give_up)) return false;
+    parities ^= 1u << buf;
+    tc_fence_after();
+    uint32_t x[N];
+    tmem_load(x, s_at + quarter * N);
+    tmem_loaded(x);
+    const uint32_t none[N / 2] = {};
+#pragma unroll
+    for (int k = 1; k < 4; ++k) tmem_store(s_at + (quarter + k) % 4 * (N / 2), none);
+    const int t0 = it.t0 + i * C::TN + quarter * N, c0 = it.lo - t0, c1 = end - t0;  // columns [c0, c1) are seen
+    if (!__all_sync(0xffffffffu, !live || (c0 <= 0 && c1 >= N))) {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (j < c0 || j >= c1) x[j] = 0xff800000u;
+    }
+    float most[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      most[0] = fmaxf(fmaxf(most[0], __uint_as_float(x[j])), __uint_as_float(x[j + 1]));
+      most[1] = fmaxf(fmaxf(most[1], __uint_as_float(x[j + 2])), __uint_as_float(x[j + 3]));
+    }
+    const float top = fmaxf(most[0], most[1]) * sl2 - C::kLift;
+    const bool raise = live && top > ref + C::kSlack;
+    if (__any_sync(0xffffffffu, raise)) {
+      const float now = raise ? top : ref;
+      const float f = now == -INFINITY ? 1.f : exp2_approx(ref - now);
+      ref = now;
+      sum *= f;
+      if (i >= C::NWG) {  // the accumulator of the steps before
+        const int last = C::NWG == 2 ? buf : buf ^ 1;
+        if (!wait_for(smem_addr(&sh.pv_done[last]), (parities >> last & 1) ^ (C::NWG == 2 ? 0 : 1), &sh.give_up))
+          return false;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += W) {
+          uint32_t o[W];
+          tmem_load(o, own_o + c);
+          tmem_loaded(o);
+#pragma unroll
+          for (int j = 0; j < W; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+          tmem_store(own_o + c, o);
+        }
+      }
+    }
+    const float sub = ref == -INFINITY ? 0.f : -ref;
+    const float2 by = make_float2(sl2, sl2), plus = make_float2(sub, sub);
+    float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+      float2 e = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), by, plus);
+      e.x = exp2_approx(e.x);
+      e.y = exp2_approx(e.y);
+      part[(j / 2) & 1] = add2(part[(j / 2) & 1], e);
+      w[j / 2] = pack2<TM>(e.x, e.y);
+    }
+    tmem_store(s_at + quarter * (N / 2), w);
+    const float2 both = add2(part[0], part[1]);
+    sum += both.x + both.y;
+    tmem_stored();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[buf]));
+  }
+
+  if (!place_next()) return false;  // while the last product runs
+
+  // ---- the states of a row, of four warps in each group
+  if (any) {
+    const int last = C::NWG == 2 ? group : (it.tiles - 1) & 1;
+    if (!wait_for(smem_addr(&sh.pv_done[last]), (parities >> last & 1) ^ 1, &sh.give_up)) return false;
+  }
+  sh.state[group][at] = make_float2(ref, sum);
+  if (!meet(sh, parities)) return false;
+  float m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 4 * C::NWG; ++k) m = fmaxf(m, sh.state[k >> 2][(k & 3) * 32 + lane].x);
+  auto factor = [&](float of) { return of == -INFINITY ? 0.f : exp2_approx(of - m); };
+  sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4 * C::NWG; ++k) {
+    const float2 y = sh.state[k >> 2][(k & 3) * 32 + lane];
+    sum += y.y * factor(y.x);
+  }
+  const float f_own = factor(ref), f_other = C::NWG == 2 ? factor(sh.state[group ^ 1][at].x) : 0.f;
+
+  // ---- the rows: the warps' parts are added through the item's query tile, which no product reads any
+  // more: [warp][row][column], the group's columns or half of them, 16-byte chunks swizzled by the row
+  const bool whole = it.dest == kDirect, by_row = it.dest == kRowShared || it.dest == kRowOwn;
+  const float mul = whole ? (sum == 0.f ? 0.f : p.v_scale / sum) : p.v_scale;
+  const size_t first_slot = ((size_t)blockIdx.x * 2 + (it.dest == kSlotFirst ? 1 : 0)) * p.slot_rows;
+  auto of_call = [&](int r) {  // the row's place among the call's
+    const int tok = div_group(p, r);
+    return (size_t)(it.tok + tok) * p.Hq + it.kvh * p.G + r - tok * p.G;
+  };
+  auto of_partials = [&](int r) {
+    return by_row ? (it.dest == kRowOwn ? (size_t)p.T * p.Hq : 0) + of_call(r) : first_slot + r;
+  };
+  if (!whole && live && group == 0 && quarter == 0)
+    (by_row ? p.row_ml : p.slot_ml)[of_partials(lane)] = make_float2(m, sum);
+  static_assert(C::NWG * 4 * 16 * HALF * 4 == C::QTILE, "16 rows of all columns");
+  const bool few = it.rows <= 16;
+  const int room = few ? 16 : 32, cols = few ? HALF : HALF / 2;
+  const uint32_t area = smem_addr(q_tiles) + (C::kQInTmem ? 0 : parities >> 3 & 1) * C::QTILE + group * (C::QTILE / C::NWG);
+  for (int c0 = 0; c0 < HALF; c0 += cols) {
+    if (c0 > 0 && !meet(sh, parities)) return false;
+#pragma unroll 1
+    for (int c = 0; c < cols; c += W) {
+      uint32_t o[W], o2[W];
+      tmem_load(o, own_o + group * HALF + c0 + c);
+      if constexpr (C::NWG == 2) {
+        tmem_load(o2, other_o + group * HALF + c0 + c);
+        tmem_loaded(o2);
+      }
+      tmem_loaded(o);
+      const uint32_t to = area + (quarter * room + lane) * cols * 4;
+#pragma unroll
+      for (int j = 0; j < W; j += 4) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // an accumulator that saw no token may hold anything
+          float a = f_own > 0.f ? __uint_as_float(o[j + k]) * f_own : 0.f;
+          if constexpr (C::NWG == 2) a += f_other > 0.f ? __uint_as_float(o2[j + k]) * f_other : 0.f;
+          w[k] = __float_as_uint(a * mul);
+        }
+        if (live) sts128(to + (((c + j) / 4 ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+      }
+    }
+    if (!meet(sh, parities)) return false;
+    const int shift = few ? ilog2(HALF / 8) : ilog2(HALF / 16);
+    for (int u = at; u < it.rows << shift; u += 128) {  // 8 columns of a row
+      const int r = u >> shift, c = u - (r << shift);
+      float e[8] = {};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 x = lds128(area + (k * room + r) * cols * 4 + ((2 * c + h ^ (r & 7)) << 4));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) e[4 * h + j] += __uint_as_float(word_of(x, j));
+        }
+      const int column = group * HALF + c0 + 8 * c;
+      if (whole) {
+        *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + of_call(r) * D + column) =
+            make_uint4(pack2<T>(e[0], e[1]), pack2<T>(e[2], e[3]), pack2<T>(e[4], e[5]), pack2<T>(e[6], e[7]));
+      } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(e[j]);
+        store32((by_row ? p.row_acc : p.slot_acc) + of_partials(r) * D + column, w);
+      }
+    }
+  }
+  async_proxy_fence();  // the next copy of queries comes after these reads
+  // accumulators, states and the tile are read before the next ones come
+  if (!meet(sh, parities)) return false;
+  if (!C::kQInTmem && threadIdx.x == 0) mbar_arrive(smem_addr(&sh.q_empty[parities >> 3 & 1]));
+  return true;
+}
+
 // One thread per row of a row tile.
 template <typename C, typename T, int D, bool ZERO_V>
 __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared<C>& sh, uint8_t* q_tiles,
@@ -845,7 +1065,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
   const float sl2 = p.scale_log2;
   // Registers are short here (a spilled one comes back from L2): the item stays in its slot of the
   // ring, and what is needed of it after its steps is read again; parities are bits of one word, 0 and
-  // 1 the score buffers', 2 the pair barrier's.
+  // 1 the score buffers', 2 the pair barrier's; 3 is the query tile of the next item of one row tile.
   uint32_t count = 0, parities = 0, tiles_before = 0;
   // The queries of item n, if there is one, into tensor memory: when no product reads those of the item
   // before any more. A negative scale negates them.
@@ -853,7 +1073,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
     if (!wait_for(smem_addr(&sh.item_full[n % C::ITEMS]), (n / C::ITEMS) & 1, &sh.give_up)) return false;
     if (sh.items[n % C::ITEMS].tiles == 0) return true;
     if (!wait_for(smem_addr(&sh.q_full[0]), n & 1, &sh.give_up)) return false;
-    const uint32_t row = smem_addr(q_tiles) + at * 128, sign = p.negate ? 0x80008000u : 0u;
+    const uint32_t row = smem_addr(q_tiles) + (spread_rows<C>(p, sh.items[n % C::ITEMS]) ? lane : at) * 128, sign = p.negate ? 0x80008000u : 0u;
     tc_fence_after();
 #pragma unroll 1
     for (int c = 0; c < D / 8; c += 4) {
@@ -873,17 +1093,37 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
     __syncwarp();
     if (lane == 0) {
       mbar_arrive(smem_addr(&sh.q_tmem));
-      mbar_arrive(smem_addr(&sh.q_empty[0]));
+      if (!C::kSpread) mbar_arrive(smem_addr(&sh.q_empty[0]));
     }
     return true;
   };
-  if constexpr (C::kQInTmem)
+  auto end_item = [&](bool two) {
+    if (!two) parities ^= 8;
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(smem_addr(&sh.item_empty[count % C::ITEMS]));
+      if (C::kQInTmem && C::kSpread) mbar_arrive(smem_addr(&sh.q_empty[0]));
+    }
+  };
+  if constexpr (C::kQInTmem) {
     if (!place_queries(0)) return;
+    // later ones when the item before is out, which may need the tile to add its rows' parts
+    if (C::kSpread && lane == 0) mbar_arrive(smem_addr(&sh.q_empty[0]));
+  }
   for (;; ++count) {
     const Item& it = sh.items[count % C::ITEMS];
     PA_WAIT(sh.item_full[count % C::ITEMS], (count / C::ITEMS) & 1);
     const int tiles = it.tiles;
     if (tiles == 0) return;
+    if constexpr (C::kSpread) {
+      if (spread_rows<C>(p, it)) {
+        if (!spread_item<C, T, D>(p, sh, it, q_tiles, tmem, parities,
+                                  [&] { return !C::kQInTmem || place_queries(count + 1); }))
+          return;
+        end_item(false);
+        continue;
+      }
+    }
     const int tile_rows = p.tile_tokens * p.G;
     const bool two = two_row_tiles<C>(p, it);
     const int dup = two ? 1 : 0;
@@ -891,12 +1131,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
     const bool live = at < tile_rows && r < it.rows;
     const bool warp_live = at - lane < tile_rows && r - lane < it.rows;
     const int lo = it.lo;
-    int end = live ? it.hi : lo;  // this row sees tokens in [lo, end)
-    if (p.shared && live) {  // causal among the new rows
-      const int tok = it.tok + div_group(p, r), b = p.R == 1 ? tok : tok / p.R;
-      const int L = it.of_prefix ? clamp_len(p, b) : end;  // the end of its own segment
-      end = min(end, L - p.R + 1 + (tok - b * p.R));
-    }
+    const int end = live ? seen_to(p, it, r) : lo;  // this row sees tokens in [lo, end)
     float ref = -INFINITY, sum = 0.f;
     int t0 = it.t0;
     int i = C::NWG == 2 ? group : 0;
@@ -1021,12 +1256,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
     if constexpr (C::NWG == 2) {
       if (joint) {
         sh.state[group][at] = make_float2(ref, sum);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sh.pair));
-        PA_WAIT(sh.pair, parities >> 2 & 1);
-        parities ^= 4;
-        tc_fence_after();
+        if (!meet(sh, parities)) return;
         const float2 other = sh.state[group ^ 1][at];
         const float m = fmaxf(ref, other.x);
         f_own = ref == -INFINITY ? 0.f : exp2_approx(ref - m);
@@ -1106,17 +1336,9 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
         }
       }
     }
-    if constexpr (C::NWG == 2) {
-      if (joint) {  // both accumulators are read before either group's next weights
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sh.pair));
-        PA_WAIT(sh.pair, parities >> 2 & 1);
-        parities ^= 4;
-      }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_addr(&sh.item_empty[count % C::ITEMS]));
+    if constexpr (C::NWG == 2)
+      if (joint && !meet(sh, parities)) return;  // both accumulators are read before either group's next weights
+    end_item(two);
   }
 }
 
@@ -1127,7 +1349,12 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
   using C = AttendCfg<T, D, LOAD>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_addr(smem) & 1023) {  // the swizzle counts on it
-    if (threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_COPY);
+    pdl_wait();
+    if (threadIdx.x == 0) {
+      atomicOr(p.err, PA_DEVERR_COPY);
+      p.split[blockIdx.x].pieces = 0;
+      if (blockIdx.x == 0) p.plan[0] = 0;  // nothing to merge
+    }
     return;
   }
   uint8_t *q_tiles = smem, *stages = smem + C::OFF_STAGE, *raw = smem + C::OFF_RAW;
@@ -1176,7 +1403,7 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
   else if (warp == C::W_PLAN)
     plan_role<C, D>(p, sh);
   else if (warp == C::W_Q)
-    query_role<C, T, D>(p, &maps.q, sh, q_tiles);
+    query_role<C, T, D>(p, maps, sh, q_tiles);
   else if constexpr (LOAD == kLoadTensor)
     tensor_load_role<C, D>(p, warp < C::W_LOAD + 2 ? &maps.k : &maps.v, warp < C::W_LOAD + 2,
                            (warp - C::W_LOAD) & 1, sh, stages);
@@ -1339,6 +1566,7 @@ __global__ void __launch_bounds__(256) merge_rows_kernel(const AttendParams p) {
     return y.r;
   };
   const long long per = __ldcg(p.plan);
+  if (per == 0) return;
   const SegmentRecord own = record(p.N + b);
   // the pieces of this row in a segment: CTAs from .. to
   struct Pieces {

@@ -49,6 +49,7 @@ struct AttendParams {
   int Hq, Hkv, G;
   uint32_t g_magic;          // r / G = umulhi(r, g_magic) for r < 2^16, G > 1
   int tile_tokens;           // query tokens of a row tile of the tensor cores, 128 / G
+  int spread_tokens;         // of an item whose rows fit in a warp, 32 / G
   int out_wide;              // out is 32-byte aligned
   int block_size, num_blocks, max_blocks, cap;
   uint32_t bs_magic;         // t / block_size as in DecodeParams
@@ -65,7 +66,7 @@ __host__ __device__ constexpr int attend_row_tiles(int D) { return D == 128 ? 2 
 __host__ __device__ constexpr int attend_tile(int D) { return D == 128 ? 128 : 64; }
 
 struct AttendMaps {
-  CUtensorMap k, v, q;
+  CUtensorMap k, v, q, q_spread;
 };
 
 // One launcher per type and head_dim: the attention grid and the grid that merges its pieces.
