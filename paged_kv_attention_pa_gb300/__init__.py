@@ -1,5 +1,6 @@
-"""Python binding of libpa.so: single-query paged-attention decode on GB300, and the
-rows of its paged cache (append with rotary positions, gather).
+"""Python binding of libpa.so: single-query paged-attention decode on GB300, the rows of its
+paged cache (append with rotary positions, gather), and attention of many rows over it (cross,
+decode_shared).
 
 Argument marshalling only (the hot calls' in csrc/binding.cpp): every step of the
 computation runs in the CUDA kernels behind the C ABI declared in include/pa.h. PyTorch provides device
