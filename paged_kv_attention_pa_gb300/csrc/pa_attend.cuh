@@ -1225,15 +1225,17 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
       }
       if constexpr (ZERO_V) {
         // V rows outside the context hold whatever the cache or an earlier tile left: zeros there,
-        // so that weights of 0 meet 0
+        // so that weights of 0 meet 0. (Eight lanes a row: with a row for each lane, lanes met in the banks.)
         if ((t0 < lo || t0 + C::TN > it.hi) && !(dup && group)) {
           const uint32_t n = tiles_before + place_v(i >> dup, lead_of<C>(p, it), tiles);
           PA_WAIT(sh.kv_full[n % C::NS], (n / C::NS) & 1);
-          const uint32_t tile = smem_addr(stages) + (n % C::NS) * C::STAGE;
-          for (int row = at; row < C::TN; row += 128)
-            if (t0 + row < lo || t0 + row >= it.hi)
+          const uint32_t tile = smem_addr(stages) + (n % C::NS) * C::STAGE + at * 16;
+          const int from = lo - t0 - (at >> 3), to = it.hi - t0 - (at >> 3);
 #pragma unroll
-              for (int c = 0; c < D / 8; ++c) sts128_zero(tile + (c >> 3) * (C::TN * 128) + row * 128 + (c & 7) * 16);
+          for (int row = 0; row < C::TN; row += 16)
+            if (row < from || row >= to)
+#pragma unroll
+              for (int c = 0; c < C::PANELS; ++c) sts128_zero(tile + c * (C::TN * 128) + row * 128);
           async_proxy_fence();
         }
       }
