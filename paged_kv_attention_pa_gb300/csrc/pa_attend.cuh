@@ -742,18 +742,27 @@ __device__ __forceinline__ void query_role(const AttendParams& p, const AttendMa
       if constexpr (kConvert) {
         PA_WAIT(*bar, lap);
         const int tile_rows = p.tile_tokens * p.G, rows = min(tile_rows, it.rows - i * tile_rows);
-#pragma unroll 4
-        for (int f = lane; f < rows * (D / 8); f += 32) {
+        constexpr int BATCH = 8;  // loads of a lane on their way together
+        auto place = [&](int f) -> uint32_t {
           const int c = f % (D / 8);
-          const uint32_t a = tile + (c / 8) * (128 * 128) + f / (D / 8) * 128 + c % 8 * 16;
-          uint4 x = lds128(a);
-          uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+          return tile + (c / 8) * (128 * 128) + f / (D / 8) * 128 + c % 8 * 16;
+        };
+        for (int f0 = lane; f0 < rows * (D / 8); f0 += 32 * BATCH) {
+          uint4 x[BATCH];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 y = unpack2<T>(w[j]);
-            w[j] = pack2<typename C::TM>(y.x, y.y);
+          for (int j = 0; j < BATCH; ++j)
+            if (f0 + 32 * j < rows * (D / 8)) x[j] = lds128(place(f0 + 32 * j));
+#pragma unroll
+          for (int j = 0; j < BATCH; ++j) {
+            if (f0 + 32 * j >= rows * (D / 8)) break;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&x[j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 y = unpack2<T>(w[i]);
+              w[i] = pack2<typename C::TM>(y.x, y.y);
+            }
+            for (int k = 0; k < (spread ? kTimes : 1); ++k) sts128(place(f0 + 32 * j) + k * (32 * 128), x[j]);
           }
-          for (int k = 0; k < (spread ? kTimes : 1); ++k) sts128(a + k * (32 * 128), x);
         }
         async_proxy_fence();
         __syncwarp();
