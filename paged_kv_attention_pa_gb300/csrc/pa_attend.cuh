@@ -742,7 +742,8 @@ __device__ __forceinline__ void query_role(const AttendParams& p, const AttendMa
       if constexpr (kConvert) {
         PA_WAIT(*bar, lap);
         const int tile_rows = p.tile_tokens * p.G, rows = min(tile_rows, it.rows - i * tile_rows);
-        constexpr int BATCH = 8;  // loads of a lane on their way together
+        // loads of a lane on their way together (one by one, six packed prompts took 119 us instead of 113)
+        constexpr int BATCH = 8;
         auto place = [&](int f) -> uint32_t {
           const int c = f % (D / 8);
           return tile + (c / 8) * (128 * 128) + f / (D / 8) * 128 + c % 8 * 16;
@@ -1236,7 +1237,8 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
       }
       if constexpr (ZERO_V) {
         // V rows outside the context hold whatever the cache or an earlier tile left: zeros there,
-        // so that weights of 0 meet 0. (Eight lanes a row: with a row for each lane, lanes met in the banks.)
+        // so that weights of 0 meet 0. (Eight lanes a row: with a row for each lane, eight lanes met in a bank,
+        // and six packed prompts of 128-token tiles took 89 us instead of 84.)
         if ((t0 < lo || t0 + C::TN > it.hi) && !(dup && group)) {
           const uint32_t n = tiles_before + place_v(i >> dup, lead_of<C>(p, it), tiles);
           PA_WAIT(sh.kv_full[n % C::NS], (n / C::NS) & 1);
