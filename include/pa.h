@@ -97,7 +97,8 @@ typedef enum pa_kv_dtype {
 
 /* Bits of the device error word (workspace header). */
 #define PA_DEVERR_BLOCK_INDEX 1u /* a live token's block table entry was outside [0, num_blocks) */
-#define PA_DEVERR_SEQ_LEN 2u     /* a seq_len < 0, > max_seq_len or > max_blocks_per_seq*block_size */
+#define PA_DEVERR_SEQ_LEN 2u     /* a seq_len < 0, > max_seq_len or > max_blocks_per_seq*block_size
+                                    (pa_decode_shared: or a prefix_len) */
 #define PA_DEVERR_COPY 4u        /* a copy into shared memory, or a wait for another part of the kernel,
                                     took over two seconds: no meaningful output */
 #define PA_DEVERR_ROWS 8u        /* pa_cross, pa_decode_shared: starts or groups that do not ascend, or

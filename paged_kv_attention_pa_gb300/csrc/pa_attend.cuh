@@ -73,7 +73,7 @@ struct AttendCfg {
   static constexpr int OFF_STAGE = NQ * QTILE;
   static constexpr int OFF_RAW = OFF_STAGE + NS * STAGE;
   static constexpr int OFF_SYNC = OFF_RAW + 2 * NR * RAW;
-  static constexpr int SYNC_BYTES = 3072;
+  static constexpr int SYNC_BYTES = 3 * 1024;
   static constexpr int SMEM = OFF_SYNC + SYNC_BYTES;
   static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
   // tensor memory: score buffers, then accumulators

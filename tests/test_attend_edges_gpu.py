@@ -303,3 +303,24 @@ def test_a_decoder_layer_of_beams(cuda_lib, cache):
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(bits(t), w) for t, w in zip(outs, before))
+
+
+@pytest.mark.parametrize("D,cache", [(128, "same"), (256, "same"), (128, "fp8"), (256, "fp8")])
+def test_workspaces_that_hold_anything(cuda_lib, D, cache):
+    # only the header has to be zero before a call, and is after it
+    lens = [1500, 1100, 2300, 0, 17, 900]
+    pool = ah.Pool(lens, 4, D, 16, "f16", cache, seed=6, prefixes=[(0, 3, 1000)])
+    kc, vc, bt, sl = pool.cuda()
+    scales = dict(k_scale=pool.scale, v_scale=pool.scale)
+    many, few = (ah.queries((6, n, 16, D), "f16", n).cuda() for n in (37, 2))
+    groups, prefix = i32([0, 3]), i32([1000])
+    calls = [lambda ws: cuda_lib.cross(many, kc, vc, bt, sl, 0.08, workspace=ws, **scales),
+             lambda ws: cuda_lib.cross(few, kc, vc, bt, sl, 0.08, workspace=ws, **scales),
+             lambda ws: cuda_lib.decode_shared(few, kc, vc, bt, sl, 0.08, groups, prefix, workspace=ws, **scales)]
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    want = [call(ws) for call in calls]
+    for byte in (0xff, 0x7f, 0x01):
+        for call, w in zip(calls, want):
+            ws[cuda_lib.PA_WORKSPACE_HEADER_BYTES:] = byte
+            assert torch.equal(bits(call(ws)), bits(w))
+    assert not ws[:cuda_lib.PA_WORKSPACE_HEADER_BYTES].any()
