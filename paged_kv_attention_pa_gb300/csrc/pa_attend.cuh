@@ -1158,10 +1158,16 @@ __device__ __forceinline__ void softmax_role(const AttendParams& p, AttendShared
         uint32_t x[2][W];
         if (!__all_sync(0xffffffffu, !live || (c0 <= 0 && c1 >= C::TN))) {
           // scores of tokens that the row does not see become -inf, whatever they are
-          const int all = __reduce_min_sync(0xffffffffu, live ? c1 : C::TN);
+          const int all = __reduce_min_sync(0xffffffffu, live ? c1 : C::TN), none = __reduce_max_sync(0xffffffffu, c1);
 #pragma unroll 1
           for (int c = 0; c < C::TN; c += W) {
             if (c >= c0 && c + W <= all) continue;
+            if (c >= none) {  // not read either
+#pragma unroll
+              for (int j = 0; j < W; ++j) x[0][j] = 0xff800000u;
+              tmem_store(s_at + c, x[0]);
+              continue;
+            }
             tmem_load(x[0], s_at + c);
             tmem_loaded(x[0]);
 #pragma unroll
