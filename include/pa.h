@@ -100,7 +100,8 @@ typedef enum pa_kv_dtype {
 #define PA_DEVERR_SEQ_LEN 2u     /* a seq_len < 0, > max_seq_len or > max_blocks_per_seq*block_size
                                     (pa_decode_shared: or a prefix_len) */
 #define PA_DEVERR_COPY 4u        /* a copy into shared memory, or a wait for another part of the kernel,
-                                    took over two seconds: no meaningful output */
+                                    took over two seconds (pa_cross, pa_decode_shared: and some time for
+                                    every token): no meaningful output */
 #define PA_DEVERR_ROWS 8u        /* pa_cross, pa_decode_shared: starts or groups that do not ascend, or
                                     reach past the call's rows or sequences */
 

@@ -214,22 +214,29 @@ struct Item {
 };
 
 // ------------------------------------------------------------------ waits
-// Wait for a phase of a barrier; false when it took over two seconds or another warp gave up. The
+// Waits end after two seconds, and 5 us for each unit of the CTA's run: warps may wait for a whole item, and
+// one of 10^8 tokens takes seconds.
+struct GiveUp {
+  volatile int now;
+  volatile unsigned long long after;  // ns
+};
+constexpr unsigned long long kGiveUpAfter = 2000000000ull, kGiveUpUnit = 5000ull;
+// Wait for a phase of a barrier; false when it took too long or another warp gave up. The
 // whole warp together. (The slow part is a function of its own: inlined everywhere it cost 2%, 4096 rows
 // over 8192 tokens 352 us instead of 345.)
-static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* give_up) {
-  const uint64_t t0 = global_ns();
+static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, GiveUp* give_up) {
+  const uint64_t t0 = global_ns(), after = give_up->after;
   for (;;) {
-    const bool over = global_ns() - t0 >= 2000000000ull || *give_up != 0;
+    const bool over = global_ns() - t0 >= after || give_up->now != 0;
     const bool done = mbar_try(bar, parity);
     if (__all_sync(0xffffffffu, done)) return true;
     if (__any_sync(0xffffffffu, over)) {
-      *give_up = 1;
+      give_up->now = 1;
       return false;
     }
   }
 }
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* give_up) {
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, GiveUp* give_up) {
   if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
   return wait_long(bar, parity, give_up);
 }
@@ -244,7 +251,7 @@ struct AttendShared {
   uint64_t item_full[C::ITEMS], item_empty[C::ITEMS];
   uint64_t pair, drain;
   uint32_t tmem;
-  int give_up;
+  GiveUp give_up;
   int first_segment;
   long long first_unit, per, total;
   Item items[C::ITEMS];
@@ -330,6 +337,7 @@ __device__ __forceinline__ void plan_work(const AttendParams& p, AttendShared<C>
   if (tid == 0) {
     p.split[blockIdx.x].pieces = 0;  // until the plan warp finds one
     sh.per = per;
+    sh.give_up.after = kGiveUpAfter + kGiveUpUnit * per;
     sh.total = total;
     if (from >= total) sh.first_segment = n;
     if (report) {
@@ -1400,7 +1408,8 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
     init(sh.item_empty, C::ITEMS, C::READERS);
     init(&sh.pair, 1, C::NSW);
     init(&sh.drain, 1, 1);
-    sh.give_up = 0;
+    sh.give_up.now = 0;
+    sh.give_up.after = kGiveUpAfter;
     mbar_init_fence();
     tensor_prefetch(&maps.q);
     if constexpr (LOAD == kLoadTensor) {
@@ -1437,8 +1446,8 @@ __global__ void __launch_bounds__(AttendCfg<T, D, LOAD>::THREADS, 1)
   pdl_launch_dependents();
   tc_fence_before();
   __syncthreads();
-  if (sh.give_up) {
-    // some wait took over two seconds: copies and products in flight are waited for, with a limit,
+  if (sh.give_up.now) {
+    // some wait took too long: copies and products in flight are waited for, with a limit,
     // before the CTA gives its memory back
     if (threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_COPY);
     if (warp == C::W_MMA) {
