@@ -9,7 +9,8 @@
 //
 // Division of the work. An item's time is taken as a number of units: 5, and for every token tile 2,
 // or 3 with two row tiles (GB300, by a fit over the CTAs of eight calls: 2.1 to 4.3 us an item, 0.9 to
-// 1.2 us a tile of one row tile, 1.6 to 1.9 us of two). Every CTA, one per SM, takes an equal run of
+// 1.2 us a tile of one row tile, 1.6 to 1.9 us of two; items have become cheaper since, but 3 or 4 units
+// are 0.9% and 0.3% slower over 36 calls). Every CTA, one per SM, takes an equal run of
 // the units of all items in order, found from the lengths on the device: runs begin and end inside
 // items, and the pieces of an item that several CTAs hold, as well as the two contexts of a row with
 // a shared prefix, leave (reference, sum, unnormalised output) in the workspace, which a second grid
@@ -468,7 +469,8 @@ __device__ __forceinline__ bool two_row_tiles(const AttendParams& p, const Item&
 // group's four warps, which reach 32 rows each, sees a quarter of a tile's tokens: the weights of the others
 // are zero in its rows. One warp for all tokens, while three have nothing to do, is slower than fp8 tiles come
 // in: 24 sequences of 14 rows a KV head over 1000 to 6000 tokens took 102 us, 93 spread, 16 of 6 rows of 256
-// behind two prefixes 63 and 47. 16-bit tiles take twice as long to come: 64 sequences 67.3 us, 69.1 spread.
+// behind two prefixes 63 and 47. 16-bit tiles take twice as long to come: 64 sequences 67.3 us, 69.1 spread, and
+// at head_dim 256 57.3 and 58.0.
 // The states of the warps are joined behind an item's last tile, which costs more than it saves in short ones:
 // 128 contexts of 16 to 700 tokens behind a document took 118.0 us with all of them spread, 116.6 with those of
 // 6 tiles and more.
