@@ -368,6 +368,9 @@ __device__ __forceinline__ void plan_work(const AttendParams& p, AttendShared<C>
       at += u;
     }
   }
+  // Tensor copies will write where the groups lay: a fence of every thread orders its accesses, which
+  // are ordinary ones, before them (with the barrier of the CTA that follows).
+  if (table && p.N > 0) async_proxy_fence();
 }
 
 // The plan warp: the pieces of this CTA's run, in order.
