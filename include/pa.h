@@ -188,7 +188,9 @@ typedef struct pa_decode_args {
  * splits of a sequence share out the tail of its context; every call leaves the
  * counters zero again. After the header come the fp32 split partials (m, l, acc),
  * which every call writes before it reads them. One workspace serves calls of
- * any shape that fit its size; calls that overlap on the GPU must not share one.
+ * any shape that fit its size; calls that overlap on the GPU must not share one. (Host
+ * threads that call on one stream may: the kernels of a call are queued one behind the
+ * other.)
  * Returns 0 for invalid sizes (max_seq_len must be > 0 here).
  */
 #define PA_WORKSPACE_HEADER_BYTES 8448u

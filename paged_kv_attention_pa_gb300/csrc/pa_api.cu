@@ -11,6 +11,7 @@
 
 #include "pa.h"
 #include "pa_internal.h"
+#include "pa_launch.h"
 #include "pa_params.h"
 
 namespace {
@@ -273,6 +274,12 @@ int current_sm_count() {
   return n;
 }
 
+std::mutex& launch_mutex(const void* workspace) {
+  static std::mutex mutexes[64];
+  const uint64_t at = reinterpret_cast<uintptr_t>(workspace);  // a multiple of 256
+  return mutexes[at * 0x9e3779b97f4a7c15ull >> 58];
+}
+
 // Division by the block size as a multiply-high and a shift (division by invariant
 // integers using multiplication, Granlund and Montgomery, 1994): for d not a power
 // of two, with l = ceil(log2 d), s = l - 1 and m = ceil(2^(32+s) / d) < 2^32,
@@ -468,6 +475,8 @@ static pa_status decode_ex(const pa_decode_args* a, void* workspace, size_t work
   cudaStream_t cs = (cudaStream_t)stream;
   cudaError_t e;
   const bool bf16 = a->dtype == PA_BF16;
+  std::unique_lock<std::mutex> lock;
+  if (!kernels) lock = std::unique_lock<std::mutex>(pa::launch_mutex(workspace));
   if (kv == pa::kKvInt4) {
     if (a->D == 128)
       e = bf16 ? pa::launch_decode_int4_bf16_d128(p, cs, kernels) : pa::launch_decode_int4_f16_d128(p, cs, kernels);

@@ -9,6 +9,7 @@
 
 #include "pa.h"
 #include "pa_attend.h"
+#include "pa_launch.h"
 #include "pa_params.h"
 
 namespace pa {
@@ -182,6 +183,7 @@ pa_status run(const Call& c, AttendParams& p, int cap, void* workspace, size_t b
   }
   const bool bf16 = c.dtype == PA_BF16;
   cudaStream_t st = (cudaStream_t)stream;
+  std::lock_guard<std::mutex> lock(launch_mutex(workspace));
   const cudaError_t e = c.D == 128 ? (bf16 ? launch_attend_bf16_d128(p, maps, load, st) : launch_attend_f16_d128(p, maps, load, st))
                                    : (bf16 ? launch_attend_bf16_d256(p, maps, load, st) : launch_attend_f16_d256(p, maps, load, st));
   if (e != cudaSuccess) {
