@@ -288,6 +288,7 @@ def make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale: float,
 _workspaces = {}
 _captured = {}  # (device, stream) -> (id of its last capture, that capture's workspace)
 _outgrown = []
+_workspaces_lock = threading.Lock()  # held while one is made
 
 
 def _capture_of(stream_handle: int) -> int:
@@ -309,22 +310,23 @@ def _default_workspace(dev: int, stream_handle: int) -> Optional[torch.Tensor]:
 
 def _workspace(need: int, device: torch.device, stream_handle: int, stream=None) -> torch.Tensor:
     key, capture = (device.index, stream_handle), _capture_of(stream_handle)
-    ws = _kept(key, capture)
-    if ws is not None and ws.numel() >= need:
-        return ws
-    if ws is not None:
-        need = max(need, 2 * ws.numel())
-    with torch.cuda.stream(stream):  # zeroed in the order of the call's stream
-        new = torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
-    if ws is not None:
-        new.outgrown = ws  # its error word is read with the new one's
-    if capture:
-        _captured[key] = (capture, new)
+    with _workspaces_lock:
+        ws = _kept(key, capture)
+        if ws is not None and ws.numel() >= need:
+            return ws
+        if ws is not None:
+            need = max(need, 2 * ws.numel())
+        with torch.cuda.stream(stream):  # zeroed in the order of the call's stream
+            new = torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
+        if ws is not None:
+            new.outgrown = ws  # its error word is read with the new one's
+        if capture:
+            _captured[key] = (capture, new)
+            return new
+        if ws is not None:
+            _outgrown.append(ws)
+        _workspaces[key] = new
         return new
-    if ws is not None:
-        _outgrown.append(ws)
-    _workspaces[key] = new
-    return new
 
 
 def workspace_for(args: DecodeArgs, device: torch.device, stream_handle: int,
