@@ -512,7 +512,8 @@ __device__ __forceinline__ void tensor_load_role(const AttendParams& p, const CU
     const int32_t* row = p.block_tables + (size_t)it.table * p.max_blocks;
     const int lead = lead_of<C>(p, it);
     int tok = it.t0 + lane * p.box;  // the box's first token
-    auto holds = [&](int tk) { return lane < boxes && tk < it.hi && tk + p.box > it.lo; };
+    // (a sequence that ends within its group's prefix, in the box where that ends, has none of its own)
+    auto holds = [&](int tk) { return lane < boxes && max(tk, it.lo) < min(tk + p.box, it.hi); };
     auto entry = [&](int t, int tk) -> int { return t < it.tiles && holds(tk) ? __ldg(row + div_block(p, tk)) : 0; };
     int phys = entry(0, tok);
     for (int t = 0; t < it.tiles; ++t, tok += C::TN) {
