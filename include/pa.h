@@ -438,7 +438,7 @@ pa_status pa_gather(const pa_gather_args* args, void* workspace, size_t workspac
  * Any number of rows: one (a decode step), a few (the beams of a search, which share their
  * source), or a prompt's thousands.
  *   q         [rows, Hq, D] (dtype); row r starts at element r * q_stride (a multiple of 8, at
- *             least Hq * D), the heads of a row are dense
+ *             least Hq * D, below 2^39), the heads of a row are dense
  *   starts    as for pa_append: NULL, and sequence b has the `rows` rows b * rows + i; or [B + 1]
  *             ascending int32 on the device, and `rows` is the number of rows in all. Rows of no
  *             sequence are padding, left alone in out

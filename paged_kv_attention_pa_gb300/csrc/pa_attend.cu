@@ -43,7 +43,9 @@ pa_status check_sizes(const Call& c, int* cap) {
       !(c.k_scale > 0.f && c.v_scale > 0.f && c.k_scale < INFINITY && c.v_scale < INFINITY))
     return PA_ERR_INVALID_ARG;
   if ((int64_t)c.num_blocks * c.block_size * c.Hkv > (int64_t)UINT32_MAX) return PA_ERR_UNSUPPORTED;
-  if (c.T * c.Hq > INT_MAX) return PA_ERR_UNSUPPORTED;  // rows of the output
+  if (c.T > INT_MAX / c.Hq) return PA_ERR_UNSUPPORTED;  // rows of the output
+  // a tensor copy's strides are below 2^40 bytes, and all queries lie below 2^62
+  if (c.T > 1 && (c.q_stride >= 1ll << 39 || c.q_stride > (INT64_MAX >> 2) / (c.T - 1))) return PA_ERR_UNSUPPORTED;
   const int64_t all = (int64_t)c.max_blocks * c.block_size;
   const int64_t len = c.max_seq_len <= 0 ? all : c.max_seq_len;
   if (len > all || len > INT_MAX - 1024) return PA_ERR_OUT_OF_RANGE;  // 1024: tiles past the end
