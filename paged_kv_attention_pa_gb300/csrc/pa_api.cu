@@ -219,8 +219,7 @@ pa_status check_sizes(const pa_decode_args* a, int64_t* max_len) {
       !(a->k_scale > 0.f && a->v_scale > 0.f && a->k_scale < INFINITY && a->v_scale < INFINITY))
     return PA_ERR_INVALID_ARG;
   if (a->B > 65535 || a->Hkv > 65535) return PA_ERR_INVALID_ARG;  // grid limits
-  // kernels address cache rows with 32-bit row indices
-  if ((int64_t)a->num_blocks * a->block_size * a->Hkv > (int64_t)UINT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (pa::rows_beyond_32_bits(a->num_blocks, a->block_size, a->Hkv)) return PA_ERR_UNSUPPORTED;
   const int64_t cap = (int64_t)a->max_blocks_per_seq * a->block_size;
   int64_t ml = a->max_seq_len <= 0 ? cap : a->max_seq_len;
   if (ml > cap) return PA_ERR_OUT_OF_RANGE;

@@ -42,7 +42,7 @@ pa_status check_sizes(const Call& c, int* cap) {
   if (c.kv_dtype == PA_KV_FP8_E4M3 &&
       !(c.k_scale > 0.f && c.v_scale > 0.f && c.k_scale < INFINITY && c.v_scale < INFINITY))
     return PA_ERR_INVALID_ARG;
-  if ((int64_t)c.num_blocks * c.block_size * c.Hkv > (int64_t)UINT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (rows_beyond_32_bits(c.num_blocks, c.block_size, c.Hkv)) return PA_ERR_UNSUPPORTED;
   if (c.T > INT_MAX / c.Hq) return PA_ERR_UNSUPPORTED;  // rows of the output
   // a tensor copy's strides are below 2^40 bytes, and all queries lie below 2^62
   if (c.T > 1 && (c.q_stride >= 1ll << 39 || c.q_stride > (INT64_MAX >> 2) / (c.T - 1))) return PA_ERR_UNSUPPORTED;

@@ -145,6 +145,10 @@ struct DecodeParams {
 
 // Host helpers shared by the entry points (pa_api.cu).
 int current_sm_count();
+// Kernels number the rows of a cache with 32 bits. (By division: the product can pass 64.)
+inline bool rows_beyond_32_bits(int num_blocks, int block_size, int Hkv) {
+  return (int64_t)num_blocks * block_size > (int64_t)UINT32_MAX / Hkv;
+}
 void set_block_division(int d, uint32_t* magic, int* shift);
 
 // One launcher per (dtype, head_dim); each dispatches on the GQA group size. With

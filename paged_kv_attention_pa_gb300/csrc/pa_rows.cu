@@ -603,7 +603,7 @@ pa_status check_rows(int B, int rows, const int32_t* starts, int Hkv, int D, int
     return PA_ERR_INVALID_ARG;
   if (kv_dtype != PA_KV_AS_DTYPE && !(good_scale(k_scale) && good_scale(v_scale)))
     return PA_ERR_INVALID_ARG;
-  if ((int64_t)num_blocks * block_size * Hkv > (int64_t)UINT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (rows_beyond_32_bits(num_blocks, block_size, Hkv)) return PA_ERR_UNSUPPORTED;
   const int64_t c = (int64_t)max_blocks * block_size;
   if (c > INT_MAX) return PA_ERR_OUT_OF_RANGE;
   *cap = (int)c;
