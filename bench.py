@@ -254,14 +254,14 @@ def load_peaks():
 # A capture holds only for the kernel code it was taken on: when the SHA-256 of that
 # code (comments and blank space removed) differs from the one recorded here, the
 # bench reports traffic as null.
-TRAFFIC_SOURCES_SHA256 = "498f27ecbbdef6e23fd7c88cdea4f7eb936925859bb6c8422c848169fda294c4"
+TRAFFIC_SOURCES_SHA256 = "2cf2d2c02012bfd0fb392b4bec7bd4bcaaecf024a053a83f695b9a30a39f9825"
 TRAFFIC_CAPTURES = {
     # 32q/8kv, block 16, batch 8, 16384 tokens: three launches
-    (128, "bf16"): {"alg_bytes": 536870912, "dram_bytes": 537045419 + 985173},
+    (128, "bf16"): {"alg_bytes": 536870912, "dram_bytes": 537056000 + 1036117},
     # 24q/4kv, block 784, batch 1, 32768 tokens: three launches
-    (256, "bf16"): {"alg_bytes": 134217728, "dram_bytes": 134300160 + 963328},
+    (256, "bf16"): {"alg_bytes": 134217728, "dram_bytes": 134303488 + 983893},
     # 32q/8kv fp8 E4M3 KV, block 16, batch 8, 16384 tokens: three launches
-    (128, "fp8"): {"alg_bytes": 268435456, "dram_bytes": 268605867 + 965205},
+    (128, "fp8"): {"alg_bytes": 268435456, "dram_bytes": 268607488 + 967595},
 }
 
 
@@ -274,18 +274,32 @@ def code_tokens(src: str) -> str:
 
 
 def kernel_sources_sha256(csrc=None) -> str:
-    """SHA-256 of the device code (comments and blank space removed): the kernel
-    headers, the launch parameters and the instantiation units (host-side planning
-    and the C API are not part of it)."""
+    """SHA-256 of the decode kernel's device code (comments and blank space removed): the
+    units that instantiate it and the headers in csrc that they include (host-side planning,
+    the C API and the other kernels are not part of it)."""
     import hashlib
-    h = hashlib.sha256()
     csrc = csrc or os.path.join(ROOT, "paged_kv_attention_pa_gb300", "csrc")
-    files = sorted(f for f in os.listdir(csrc)
-                   if f.endswith(".cuh") or f == "pa_params.h" or f.startswith("pa_inst_"))
-    for f in files:
-        h.update(f.encode())
+
+    def read(f):
         with open(os.path.join(csrc, f), encoding="utf-8") as fh:
-            h.update(code_tokens(fh.read()).encode())
+            return code_tokens(fh.read())
+
+    def included(src):
+        names = re.findall(r'#\s*include "([^"]+)"', src)
+        return [f for f in names if os.path.exists(os.path.join(csrc, f))]
+
+    code = {}
+    todo = [f for f in sorted(os.listdir(csrc)) if f.startswith("pa_inst_")
+            and "pa_decode_kernel.cuh" in included(read(f))]
+    while todo:
+        f = todo.pop()
+        if f not in code:
+            code[f] = read(f)
+            todo += included(code[f])
+    h = hashlib.sha256()
+    for f in sorted(code):
+        h.update(f.encode())
+        h.update(code[f].encode())
     return h.hexdigest()
 
 
