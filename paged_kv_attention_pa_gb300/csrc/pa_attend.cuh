@@ -8,9 +8,8 @@
 // head_dim 128 and of one at 256.
 //
 // Division of the work. An item's time is taken as a number of units: 5, and for every token tile 2,
-// or 3 with two row tiles (GB300, by a fit over the CTAs of eight calls: 2.1 to 4.3 us an item, 0.9 to
-// 1.2 us a tile of one row tile, 1.6 to 1.9 us of two; items have become cheaper since, but 3 or 4 units
-// are 0.9% and 0.3% slower over 36 calls). Every CTA, one per SM, takes an equal run of
+// or 3 with two row tiles (GB300: a tile of two takes about 1.6 times one of one; 3 or 4 units an item are
+// 0.9% and 0.3% slower over 36 calls). Every CTA, one per SM, takes an equal run of
 // the units of all items in order, found from the lengths on the device: runs begin and end inside
 // items, and the pieces of an item that several CTAs hold, as well as the two contexts of a row with
 // a shared prefix, leave (reference, sum, unnormalised output) in the workspace, which a second grid
@@ -673,14 +672,12 @@ __device__ __forceinline__ void fp8_load_role(const AttendParams& p, bool is_k, 
   const uint32_t raw_lane = smem_addr(raw) + (is_k ? 0 : C::NR * C::RAW) + warp * (C::RAW / 4) + lane * 16;
   static_assert(C::NR == 2, "one tile on its way while another is widened");
   uint32_t issued = 0, done = 0, place[2];
-  int2 rows[2];
   auto issue = [&](int k) {  // the next tile, if there is one
     if (L.more) {
       place[k] = L.place();
-      rows[k] = L.rows();
       const uint32_t dst = raw_lane + issued % 2 * C::RAW;
       ++issued;
-      L.issue(rows[k], [&](int i) { return dst + i * 512; });
+      L.issue(L.rows(), [&](int i) { return dst + i * 512; });
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -691,7 +688,6 @@ __device__ __forceinline__ void fp8_load_role(const AttendParams& p, bool is_k, 
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     const uint32_t n = place[0];
     place[0] = place[1];
-    rows[0] = rows[1];
     if (!L.room(n)) break;
     const uint32_t from = raw_lane + done % 2 * C::RAW, tile = smem_addr(stages) + n % C::NS * C::STAGE;
     static_assert(Loader::CH == 8, "a tile's chunks of a lane");

@@ -35,7 +35,7 @@ struct AttendParams {
   const int32_t* groups;     // shared prefixes: [N + 1]
   const int32_t* prefix;     // [N]
   uint32_t* err;             // device error word
-  // workspace (see attend_workspace)
+  // workspace (see layout_of in pa_attend.cu)
   long long* plan;           // units per CTA, units in all
   SegmentRecord* segments;
   SplitItem* split;          // [CTAs] the item that begins in a CTA and ends in a later one
