@@ -288,7 +288,7 @@ def make_args(q, k_cache, v_cache, block_tables, seq_lens, out, scale: float,
 _workspaces = {}
 _captured = {}  # (device, stream) -> (id of its last capture, that capture's workspace)
 _outgrown = []
-_workspaces_lock = threading.Lock()  # held while one is made
+_workspaces_lock = threading.RLock()  # held while one is made (a finalizer run amid that may call)
 
 
 def _capture_of(stream_handle: int) -> int:
@@ -565,7 +565,8 @@ def cross(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     sequence b; others are padding, left alone in out and uninitialised in an out made here). It may
     be a slice of a projection: the heads of a row contiguous, the rows evenly spaced. The caches,
     tables and max_seq_len are as in decode(), 16-bit or float8_e4m3fn. An empty context gives
-    zeros. out must be contiguous. Repeated calls are bitwise identical. Asynchronous on the current
+    zeros. One row per sequence is what decode() computes, in about half the time where calls are
+    small. out must be contiguous. Repeated calls are bitwise identical. Asynchronous on the current
     (or given) stream; workspace as in decode().
     """
     dev, sh, stream = _call_on(q, stream)
@@ -584,6 +585,8 @@ def decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """decode() for sequences that share prefixes (a system prompt, several answers to one
     question): the keys and values of a shared prefix are read once for all sequences of a group.
+    It is the faster of the two once that saves reading about 100 MB of 16-bit keys and values
+    (16 sequences behind 2048 tokens of 8 heads of 128), 200 MB of fp8 ones.
 
     groups [N + 1] int32, ascending: sequences groups[n] to groups[n + 1] - 1 are group n; sequences
     of no group share nothing. prefix_lens [N] int32: how many of their leading tokens they share

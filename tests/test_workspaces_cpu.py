@@ -35,3 +35,21 @@ def test_threads_that_call_first_share_one_workspace(host_workspaces, monkeypatc
     assert len(made) == 1 and got[0] is got[1]
     got[0][0] = pa.PA_DEVERR_SEQ_LEN
     assert pa.read_device_errors(host_workspaces(1 << 16), FakeStream) == pa.PA_DEVERR_SEQ_LEN
+
+
+def test_a_call_amid_the_making_of_a_workspace(host_workspaces, monkeypatch):  # noqa: F811
+    # a finalizer that an allocation sets off calls on the same thread
+    zeros, amid, calls = torch.zeros, [], []
+
+    def again(*args, **kw):
+        if not amid:
+            amid.append(1)
+            calls.append(host_workspaces(pa.PA_WORKSPACE_HEADER_BYTES))
+        return zeros(*args, **kw)
+
+    monkeypatch.setattr(torch, "zeros", again)
+    got = []
+    t = threading.Thread(target=lambda: got.append(host_workspaces(1 << 17)), daemon=True)
+    t.start()
+    t.join(20)
+    assert got and got[0].numel() >= 1 << 17 and calls[0] is not got[0]
